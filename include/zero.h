@@ -86,7 +86,16 @@ typedef enum {
                               its scalar table */
 } zero_status;
 
-typedef enum { ZERO_F16 = 1, ZERO_BF16 = 2 } zero_dtype;
+/* Element types.  The step's calls take ZERO_F16 and ZERO_BF16; the others are
+ * for the matrices of the layer operators (zero_mat). */
+typedef enum {
+    ZERO_F16 = 1,
+    ZERO_BF16 = 2,
+    ZERO_F32 = 3,
+    ZERO_E4M3 = 4,         /* 8-bit floating point, 4 exponent bits, no infinities */
+    ZERO_I32 = 5,
+    ZERO_I64 = 6
+} zero_dtype;
 
 typedef enum {
     ZERO_PLAN_PADDED = 0,   /* pad to a multiple of 2*world_size, then split (the walkthrough's rule) */
@@ -629,6 +638,164 @@ int zero_shard_step_host(const void* const* host_grad_slices, int n_slices, int 
                          void* staging, size_t staging_bytes,
                          void* workspace, size_t workspace_bytes,
                          zero_result* result, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Layer operators: what the layers around a ZeRO-3 unit's gathers compute.
+ * The pages stop at the unit's gather before its forward, the gather before
+ * its backward and the reduce of its gradients (reading notes 7 and 9); these
+ * calls are the forward and backward of such a unit's norm, products and
+ * loss, with the gradients written where the bucket reduce reads them and the
+ * loss scale taken from where the chained step keeps it.
+ *
+ * They follow the conventions above (caller's buffers, stream-ordered, no
+ * allocation, argument errors before any work) and these:
+ *  - A matrix is a zero_mat: element (r, c) at data + (r * ld + c) elements.
+ *    Any row distance and any alignment to the element is taken; rows that all
+ *    start on 16-byte boundaries run with 16-byte accesses.  ld may be
+ *    anything (0 included) when there is at most one row.
+ *  - A matrix of no rows or no columns is allowed and gives an empty result.
+ *  - Sums are held in fp32 or more, each output is rounded once to its type,
+ *    and results do not depend on timing: no sum uses atomics.
+ *  - "may be X" means: the very same data pointer and ld as X.  No other
+ *    output may overlap an input or another output.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void* data;
+    int64_t ld;            /* elements between the starts of two rows */
+    int32_t dtype;         /* zero_dtype */
+    int32_t reserved;
+} zero_mat;
+
+/* Root-mean-square norm of a residual stream.
+ *   h = round(x + residual);  rstd = 1 / sqrt(mean(h^2) + eps);  y = h rstd weight
+ * per row.  The norm is taken of h as it is stored, so that y and the backward
+ * pass can be computed again from h alone.
+ * x          rows x cols, ZERO_F16, ZERO_BF16 or ZERO_F32
+ * residual   the same, or ZERO_F32 (the residual stream then stays in fp32);
+ *            NULL: h = x
+ * weight     cols values (fp16, bf16 or fp32, e.g. in a gathered unit); NULL: 1
+ * h_out      in the residual's type (x's without one); NULL: not stored; may
+ *            be residual or x
+ * y          in x's type, or ZERO_E4M3: y is then divided by a scale, s = the
+ *            largest |y| of its block (at least 2^-100) / 448, and rounded to
+ *            nearest; a NaN or an infinity in a block makes the scale so
+ * y_scale    ZERO_E4M3 only: the scales, rows x 1 (scale_block 0: a block is a
+ *            row) or rows x ceil(cols / 128) (scale_block 128)
+ * rstd       rows values, NULL: not stored
+ * A row of NaN or infinities gives NaN in its own row only.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ELIMIT (more than 1048576 columns),
+ * ZERO_ECUDA. */
+int zero_norm_forward(const zero_mat* x, const zero_mat* residual, const zero_mat* weight, int64_t rows, int64_t cols,
+                      float eps, const zero_mat* h_out, const zero_mat* y, float* y_scale, int64_t scale_block,
+                      float* rstd, void* stream);
+
+/* Its backward pass, with xh = h rstd and g = dy weight:
+ *   dx = rstd (g - xh mean(g xh)) + dh      the gradient of x and of residual
+ *   dw = sum over rows of dy xh
+ * dy         the gradient of y, rows x cols (ZERO_F16, ZERO_BF16, ZERO_F32; of
+ *            an e4m3 y: with respect to the values before they were scaled)
+ * h, rstd    from the forward pass; h in dy's type or ZERO_F32
+ * dh         the gradient that reaches h by the residual stream, in h's type;
+ *            NULL: none
+ * dx         in h's type; may be dy (of the same type) or dh
+ * dw         cols values (fp16, bf16 or fp32, e.g. in a gradient bucket); NULL:
+ *            not wanted; accumulate nonzero: added to what is there, in fp32,
+ *            and rounded once
+ * workspace  zero_norm_workspace_bytes(cols) bytes, 4-byte aligned, contents
+ *            irrelevant (NULL if dw is)
+ * With no rows dw is 0 (or unchanged).  Errors as zero_norm_forward, and
+ * ZERO_EWORKSPACE. */
+int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* weight, int64_t rows, int64_t cols,
+                       const float* rstd, const zero_mat* dh, const zero_mat* dx, const zero_mat* dw, int accumulate,
+                       void* workspace, size_t workspace_bytes, void* stream);
+size_t zero_norm_workspace_bytes(int64_t cols);
+
+/* Distillation from a teacher's largest logits: per row, with temperature T,
+ *   q = softmax(logits / T) over the cols columns
+ *   p = softmax(teacher / T) over the row's entries, or, with teacher_lse,
+ *       p_i = exp(teacher_i / T - teacher_lse) (the teacher's log-sum-exp over
+ *       its whole vocabulary at T; the p then add up to P <= 1)
+ *   loss = w T^2 sum_i p_i (log p_i - log q[id_i])
+ *   dlogits[v] = w T grad_scale S (P q[v] - sum of p_i with id_i = v)
+ * logits     rows x cols, ZERO_F16, ZERO_BF16 or ZERO_F32; -inf masks a column
+ * ids        rows x k, ZERO_I32 or ZERO_I64, in any order; an id outside
+ *            0 .. cols - 1 (-1 by custom) is no entry; an id may come twice
+ * teacher    rows x k (any float type); -inf is no entry
+ * row_weight w, rows values; NULL: 1.  A row of weight 0 or without entries has
+ *            loss 0 and gradient 0 whatever its logits hold
+ * grad_scale, chain   the gradient's factor (1 / tokens, say), and, if chain is
+ *            not NULL, S = chain->loss_scale read on the device when the kernel
+ *            runs (1 otherwise): the scale that the chained step divides by
+ * loss, lse  rows values each (lse of logits / T, for the backward call);
+ *            NULL: not wanted
+ * dlogits    in the logits' type; may be logits; NULL: not wanted
+ * k <= 1024.  Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ELIMIT, ZERO_ECUDA. */
+int zero_distill_loss(const zero_mat* logits, int64_t rows, int64_t cols, const zero_mat* ids, const zero_mat* teacher,
+                      int k, const float* teacher_lse, float temperature, const float* row_weight, float grad_scale,
+                      const zero_chain* chain, float* loss, float* lse, const zero_mat* dlogits, void* stream);
+
+/* The gradient alone, when the rows' upstream gradients are known only after
+ * the loss (row_weight carries them): dlogits from lse as zero_distill_loss
+ * stored it, the rest as there. */
+int zero_distill_backward(const zero_mat* logits, int64_t rows, int64_t cols, const zero_mat* ids,
+                          const zero_mat* teacher, int k, const float* teacher_lse, float temperature,
+                          const float* row_weight, float grad_scale, const zero_chain* chain, const float* lse,
+                          const zero_mat* dlogits, void* stream);
+
+/* A microscaled 4-bit matrix (OCP Microscaling Formats v1.0, MXFP4): values
+ * +-{0, .5, 1, 1.5, 2, 3, 4, 6} times a power of two per 32 consecutive
+ * elements of a row.
+ * data    16-byte aligned; row r at r * ld bytes, ld a multiple of 16 and at
+ *         least 16 ceil(cols / 32); two elements a byte, the even one in the
+ *         low half; the last block of a row is filled up with zeros
+ * scales  the exponents + 127 (255: NaN).  ZERO_MX4_ROWS: rows x ceil(cols / 32)
+ *         bytes.  With cols a multiple of 32 and ld its minimum, a range of
+ *         whole blocks of the flattened matrix is one range of data (half a
+ *         byte an element) and one of scales: a ZeRO-3 part can be quantised by
+ *         its owner and gathered by zero3_gather_* (as 16-bit elements).
+ *         ZERO_MX4_TILES (16-byte aligned): what zero_mx4_matmul reads.  Tiles
+ *         of 128 rows by 4 blocks, 512 bytes each, (r, b) of a tile at byte
+ *         (r % 32) * 16 + (r / 32) * 4 + b; the tiles of 128 rows follow one
+ *         another along the blocks; rows padded to 128, blocks to 8, the
+ *         padding's bytes 0. */
+typedef enum { ZERO_MX4_ROWS = 0, ZERO_MX4_TILES = 1 } zero_mx4_layout;
+typedef struct {
+    void* data;
+    void* scales;
+    int64_t rows, cols, ld;
+    int32_t layout;        /* zero_mx4_layout of scales */
+    int32_t reserved;
+} zero_mx4;
+
+/* Smallest ld and the sizes of both buffers, in bytes.  Host only. */
+int zero_mx4_bytes(int64_t rows, int64_t cols, int layout, int64_t* ld, int64_t* data_bytes, int64_t* scale_bytes);
+
+/* Quantise src (rows x cols; fp16, bf16, fp32): out along its rows (rows x
+ * cols), out_t along its columns (cols x rows: the transpose, quantised along
+ * its own rows); either may be NULL, both come from one read of src.  A block's
+ * exponent is floor(log2 max|x|) - 2, at least -127; values are rounded to
+ * nearest (ties to even) and clipped at 6; an infinity or NaN makes the block's
+ * scale NaN.  Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ECUDA. */
+int zero_mx4_quantize(const zero_mat* src, int64_t rows, int64_t cols, const zero_mx4* out, const zero_mx4* out_t,
+                      void* stream);
+
+/* The values src stands for, rounded to dst's type (exact in bf16 and fp32
+ * within their range). */
+int zero_mx4_dequantize(const zero_mx4* src, const zero_mat* dst, void* stream);
+
+/* src's scales (ZERO_MX4_ROWS, as gathered) into dst's (ZERO_MX4_TILES, of the
+ * same size).  Only the scales are touched. */
+int zero_mx4_tile_scales(const zero_mx4* src, const zero_mx4* dst, void* stream);
+
+/* d = alpha a b^T: d[m][n] = alpha sum_k a[m][k] b[n][k], fp32 sums, d (a->rows
+ * x b->rows) rounded to fp16, bf16 or fp32.  Scales in ZERO_MX4_TILES.  A NaN
+ * scale gives NaN in the rows or columns of d that its block belongs to.
+ * status: device int32 the caller zero-fills; a block whose bounded wait runs
+ * out sets bit 0, and d is then incomplete (ZERO_GB300_SPIN_LIMIT as for
+ * zero3_gather_bulk).
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ELIMIT (more than 2^30 rows or
+ * columns), ZERO_ECUDA. */
+int zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, float alpha, const zero_mat* d, int32_t* status, void* stream);
 
 /* Message of the last error on this thread ("" if none). */
 const char* zero_last_error(void);

@@ -1,0 +1,172 @@
+"""CPU tests of the layer operators' argument checks: each refusal comes before
+any device work (no GPU is touched here), and the host-only sizes."""
+import ctypes
+
+import pytest
+import torch
+
+FAKE = 0x10000      # an aligned address that is never dereferenced: every case fails validation first
+
+
+@pytest.fixture(scope="module")
+def Z():
+    import __graft_entry__
+    __graft_entry__.build()
+    import zero_dp_partitioned_gb300 as Z
+    return Z
+
+
+def refused(Z, code, f, *args):
+    with pytest.raises(Z.ZeroError) as e:
+        f(*args, stream=0)
+    assert e.value.code == code, str(e.value)
+    assert str(e.value)
+
+
+def m(Z, ld=64, dtype=2, data=FAKE):
+    return Z.mat(data, ld, dtype)
+
+
+def test_struct_sizes(Z):
+    assert ctypes.sizeof(Z.zero_mat) == 24 and ctypes.sizeof(Z.zero_mx4) == 48
+
+
+def test_norm_forward_refusals(Z):
+    def call(code, **kw):
+        a = dict(x=m(Z), residual=m(Z), weight=m(Z), rows=4, cols=64, eps=1e-5, h_out=m(Z), y=m(Z), y_scale=None,
+                 scale_block=0, rstd=FAKE)
+        a.update(kw)
+        refused(Z, code, Z.zero_norm_forward, *a.values())
+
+    call(Z.ZERO_EINVAL, rows=-1)
+    call(Z.ZERO_EINVAL, cols=-1)
+    call(Z.ZERO_ELIMIT, cols=(1 << 20) + 1)
+    for eps in (-1.0, float("nan"), float("inf")):
+        call(Z.ZERO_EINVAL, eps=eps)
+    call(Z.ZERO_EINVAL, x=None)
+    call(Z.ZERO_EINVAL, x=m(Z, data=0))
+    call(Z.ZERO_EINVAL, x=m(Z, dtype=4))
+    call(Z.ZERO_EINVAL, x=m(Z, dtype=99))
+    call(Z.ZERO_EINVAL, x=m(Z, dtype=-1))
+    call(Z.ZERO_EINVAL, x=m(Z, ld=63))
+    call(Z.ZERO_EALIGN, x=m(Z, data=FAKE + 1))
+    call(Z.ZERO_EINVAL, residual=m(Z, dtype=1))              # fp16 beside bf16
+    call(Z.ZERO_EINVAL, h_out=m(Z, dtype=3))                 # not the residual's type
+    call(Z.ZERO_EINVAL, y=m(Z, dtype=3))
+    call(Z.ZERO_EINVAL, y=None)
+    call(Z.ZERO_EINVAL, y=m(Z, dtype=4))                     # no y_scale
+    call(Z.ZERO_EINVAL, y=m(Z, dtype=4), y_scale=FAKE, scale_block=64)
+    call(Z.ZERO_EALIGN, y=m(Z, dtype=4), y_scale=FAKE + 2)
+    call(Z.ZERO_EALIGN, rstd=FAKE + 1)
+    call(Z.ZERO_EINVAL, weight=m(Z, dtype=5))
+    call(Z.ZERO_EALIGN, weight=m(Z, data=FAKE + 1))
+    call(Z.ZERO_EINVAL, x=torch.zeros(4, 63, dtype=torch.bfloat16))          # another shape
+    call(Z.ZERO_EINVAL, x=torch.zeros(64, 4, dtype=torch.bfloat16).t())      # columns apart
+    call(Z.ZERO_EINVAL, rstd=torch.zeros(3))
+    call(Z.ZERO_EINVAL, weight=torch.zeros(64, dtype=torch.float64))
+
+
+def test_norm_backward_refusals(Z):
+    ws = Z.zero_norm_workspace_bytes(64)
+    assert ws >= 64 * 4 and Z.zero_norm_workspace_bytes(0) == 0
+
+    def call(code, **kw):
+        a = dict(dy=m(Z), h=m(Z), weight=m(Z), rows=4, cols=64, rstd=FAKE, dh=m(Z), dx=m(Z), dw=m(Z), accumulate=0,
+                 workspace=FAKE, workspace_bytes=ws)
+        a.update(kw)
+        refused(Z, code, Z.zero_norm_backward, *a.values())
+
+    call(Z.ZERO_EINVAL, rows=-1)
+    call(Z.ZERO_EINVAL, dy=None)
+    call(Z.ZERO_EINVAL, rstd=None)
+    call(Z.ZERO_EINVAL, h=m(Z, dtype=1))
+    call(Z.ZERO_EINVAL, dx=m(Z, dtype=3))
+    call(Z.ZERO_EINVAL, dh=m(Z, dtype=3))
+    call(Z.ZERO_EINVAL, dw=m(Z, dtype=4))
+    call(Z.ZERO_EALIGN, dw=m(Z, data=FAKE + 1))
+    call(Z.ZERO_EWORKSPACE, workspace=None)
+    call(Z.ZERO_EWORKSPACE, workspace_bytes=ws - 1)
+    call(Z.ZERO_ELIMIT, cols=(1 << 20) + 1)
+
+
+def test_distill_refusals(Z):
+    def call(code, f=None, **kw):
+        a = dict(logits=m(Z), rows=4, cols=64, ids=m(Z, 8, 6), teacher=m(Z, 8), k=8, teacher_lse=None, temperature=1.0,
+                 row_weight=None, grad_scale=1.0, chain_dev=None, loss=FAKE, lse=FAKE, dlogits=m(Z))
+        a.update(kw)
+        refused(Z, code, Z.zero_distill_loss, *a.values())
+        del a["loss"]
+        if kw.get("loss") is None:
+            refused(Z, code, Z.zero_distill_backward, *a.values())
+
+    call(Z.ZERO_EINVAL, rows=-1)
+    call(Z.ZERO_EINVAL, cols=-1)
+    call(Z.ZERO_EINVAL, k=-1)
+    call(Z.ZERO_ELIMIT, k=1025)
+    call(Z.ZERO_ELIMIT, cols=1 << 31)
+    for t in (0.0, -1.0, float("nan"), float("inf")):
+        call(Z.ZERO_EINVAL, temperature=t)
+    call(Z.ZERO_EINVAL, grad_scale=float("inf"))
+    call(Z.ZERO_EINVAL, logits=m(Z, dtype=4))
+    call(Z.ZERO_EINVAL, ids=m(Z, 8, 2))
+    call(Z.ZERO_EALIGN, ids=m(Z, 8, 6, FAKE + 4))
+    call(Z.ZERO_EINVAL, ids=m(Z, 7, 6))
+    call(Z.ZERO_EINVAL, teacher=None)
+    call(Z.ZERO_EINVAL, dlogits=m(Z, dtype=3))
+    call(Z.ZERO_EALIGN, row_weight=FAKE + 2)
+    call(Z.ZERO_EALIGN, chain_dev=FAKE + 4)
+    call(Z.ZERO_EALIGN, loss=FAKE + 1)
+    call(Z.ZERO_EALIGN, lse=FAKE + 1)
+    call(Z.ZERO_EINVAL, row_weight=torch.zeros(3))
+    args = (m(Z), 4, 64, m(Z, 8, 6), m(Z, 8), 8, None, 1.0, None, 1.0, None)
+    refused(Z, Z.ZERO_EINVAL, Z.zero_distill_backward, *args, None, m(Z))            # no lse
+    refused(Z, Z.ZERO_EINVAL, Z.zero_distill_backward, *args, FAKE, None)            # no dlogits
+
+
+def test_mx4_sizes(Z):
+    assert Z.zero_mx4_bytes(1, 1, Z.ZERO_MX4_ROWS) == (16, 16, 1)
+    assert Z.zero_mx4_bytes(1, 1) == (16, 16, 1024)
+    assert Z.zero_mx4_bytes(129, 257) == (144, 129 * 144, 2 * 2 * 1024)
+    assert Z.zero_mx4_bytes(14336, 4096) == (2048, 14336 * 2048, 14336 * 128)
+    assert Z.zero_mx4_bytes(14336, 4096, Z.ZERO_MX4_ROWS) == (2048, 14336 * 2048, 14336 * 128)
+    assert Z.zero_mx4_bytes(0, 5) == (16, 0, 0)
+    for bad in ((-1, 4, 0), (4, -1, 1), (4, 4, 2)):
+        with pytest.raises(Z.ZeroError):
+            Z.zero_mx4_bytes(*bad)
+    q = Z.mx4(3, 70, device="cpu")
+    assert (q.rows, q.cols, q.ld) == (3, 70, 48) and q.scales == q.data + 3 * 48
+    with pytest.raises(Z.ZeroError):
+        Z.mx4(3, 70, torch.zeros(3 * 48 - 1, dtype=torch.uint8), torch.zeros(1024, dtype=torch.uint8))
+
+
+def test_mx4_refusals(Z):
+    def q(rows=4, cols=64, ld=32, data=FAKE, scales=FAKE, layout=1):
+        return Z.zero_mx4(data, scales, rows, cols, ld, layout, 0)
+
+    f = Z.zero_mx4_quantize
+    refused(Z, Z.ZERO_EINVAL, f, m(Z), -1, 64, q(), None)
+    refused(Z, Z.ZERO_EINVAL, f, m(Z, dtype=4), 4, 64, q(), None)
+    refused(Z, Z.ZERO_EINVAL, f, m(Z), 4, 64, q(rows=5), None)
+    refused(Z, Z.ZERO_EINVAL, f, m(Z), 4, 64, None, q())                  # the transpose is 64 x 4
+    refused(Z, Z.ZERO_EINVAL, f, m(Z), 4, 64, q(ld=16), None)
+    refused(Z, Z.ZERO_EINVAL, f, m(Z), 4, 64, q(ld=40), None)
+    refused(Z, Z.ZERO_EALIGN, f, m(Z), 4, 64, q(data=FAKE + 8), None)
+    refused(Z, Z.ZERO_EALIGN, f, m(Z), 4, 64, q(scales=FAKE + 4), None)
+    refused(Z, Z.ZERO_EINVAL, f, m(Z), 4, 64, q(scales=0), None)
+    refused(Z, Z.ZERO_EINVAL, f, m(Z), 4, 64, q(layout=2), None)
+    refused(Z, Z.ZERO_EINVAL, Z.zero_mx4_dequantize, None, m(Z))
+    refused(Z, Z.ZERO_EINVAL, Z.zero_mx4_dequantize, q(), m(Z, dtype=6))
+    refused(Z, Z.ZERO_EINVAL, Z.zero_mx4_dequantize, q(), m(Z, ld=63))
+    t = Z.zero_mx4_tile_scales
+    refused(Z, Z.ZERO_EINVAL, t, q(), q())
+    refused(Z, Z.ZERO_EINVAL, t, q(layout=0), q(rows=5))
+    mm = Z.zero_mx4_matmul
+    refused(Z, Z.ZERO_EINVAL, mm, q(), q(cols=32), 1.0, m(Z), FAKE)
+    refused(Z, Z.ZERO_EINVAL, mm, q(layout=0), q(), 1.0, m(Z), FAKE)
+    refused(Z, Z.ZERO_EINVAL, mm, q(), q(), 1.0, m(Z, ld=3), FAKE)
+    refused(Z, Z.ZERO_EINVAL, mm, q(), q(), 1.0, m(Z, dtype=4), FAKE)
+    refused(Z, Z.ZERO_EINVAL, mm, q(), q(), 1.0, m(Z), None)
+    refused(Z, Z.ZERO_EINVAL, mm, q(), q(), 1.0, m(Z), FAKE + 2)
+    refused(Z, Z.ZERO_EINVAL, mm, q(), q(), float("nan"), m(Z), FAKE)
+    refused(Z, Z.ZERO_ELIMIT, mm, q(rows=1 << 31), q(), 1.0, m(Z), FAKE)
+    Z.zero_mx4_matmul(q(rows=0), q(), 1.0, m(Z), FAKE, stream=0)          # nothing to do: no launch

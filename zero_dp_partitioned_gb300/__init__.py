@@ -19,7 +19,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libzero_gb300.so")
 
 ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_EWORKSPACE, ZERO_ECUDA, ZERO_ELIMIT = 0, -1, -2, -3, -4, -5
-ZERO_F16, ZERO_BF16 = 1, 2
+ZERO_F16, ZERO_BF16, ZERO_F32, ZERO_E4M3, ZERO_I32, ZERO_I64 = 1, 2, 3, 4, 5, 6
+ZERO_MX4_ROWS, ZERO_MX4_TILES = 0, 1
 ZERO_PLAN_PADDED, ZERO_PLAN_UNPADDED = 0, 1
 ZERO_MAX_SLICES = ZERO_MAX_SHARDS = 64
 
@@ -65,6 +66,18 @@ class zero_result(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_ if not k.startswith("reserved")}
 
 
+class zero_mat(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class zero_mx4(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("layout", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+assert ctypes.sizeof(zero_mat) == 24 and ctypes.sizeof(zero_mx4) == 48
 assert ctypes.sizeof(zero_hyper) == 32 and ctypes.sizeof(zero_shard) == 80
 assert ctypes.sizeof(zero_stats) == 16 and ctypes.sizeof(zero_result) == 48 and ctypes.sizeof(zero_chain) == 56
 
@@ -98,6 +111,18 @@ _SIGS = {
     "zero_shard_step_commit": (_I, [_P, _I, _P, _I, ctypes.c_float, _I64, _I64, _P, _P, ctypes.c_double, _I, _P, _P]),
     "zero_shard_step_host": (_I, [_P, _I, _I, _P, _I, _P, _I, _P, _P, ctypes.c_float, ctypes.c_double, _I, _P,
                                   ctypes.c_size_t, _P, ctypes.c_size_t, _P, _P]),
+    "zero_norm_forward": (_I, [_P, _P, _P, _I64, _I64, ctypes.c_float, _P, _P, _P, _I64, _P, _P]),
+    "zero_norm_backward": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P]),
+    "zero_norm_workspace_bytes": (ctypes.c_size_t, [_I64]),
+    "zero_distill_loss": (_I, [_P, _I64, _I64, _P, _P, _I, _P, ctypes.c_float, _P, ctypes.c_float, _P, _P, _P, _P,
+                               _P]),
+    "zero_distill_backward": (_I, [_P, _I64, _I64, _P, _P, _I, _P, ctypes.c_float, _P, ctypes.c_float, _P, _P, _P,
+                                   _P]),
+    "zero_mx4_bytes": (_I, [_I64, _I64, _I, _P, _P, _P]),
+    "zero_mx4_quantize": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "zero_mx4_dequantize": (_I, [_P, _P, _P]),
+    "zero_mx4_tile_scales": (_I, [_P, _P, _P]),
+    "zero_mx4_matmul": (_I, [_P, _P, ctypes.c_float, _P, _P, _P]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
 # every symbol include/zero.h declares
@@ -371,3 +396,156 @@ def read_result(t) -> zero_result:
 def read_stats(t) -> zero_stats:
     b = bytes(t.detach().cpu().view(-1).numpy().tobytes())
     return zero_stats.from_buffer_copy(b[:ctypes.sizeof(zero_stats)])
+
+
+# ------------------------------------------------------------------ layer operators
+_MAT_DTYPES = {"torch.float16": ZERO_F16, "torch.bfloat16": ZERO_BF16, "torch.float32": ZERO_F32,
+               "torch.float8_e4m3fn": ZERO_E4M3, "torch.int32": ZERO_I32, "torch.int64": ZERO_I64}
+
+
+def mat(data, ld=None, dtype=None) -> zero_mat:
+    """A zero_mat of a torch tensor (two dimensions with adjacent columns, or
+    one: a single row), or of an address with its row distance and dtype."""
+    if not hasattr(data, "data_ptr"):
+        return zero_mat(_ptr(data), ld or 0, dtype or 0, 0)
+    code = _MAT_DTYPES.get(str(data.dtype))
+    if code is None:
+        raise ZeroError(ZERO_EINVAL, f"no zero_mat of {data.dtype}")
+    if data.dim() not in (1, 2) or (data.shape[-1] > 1 and data.stride(-1) != 1):
+        raise ZeroError(ZERO_EINVAL, "a zero_mat has one or two dimensions and adjacent columns")
+    m = zero_mat(data.data_ptr(), data.stride(0) if data.dim() == 2 else data.shape[0], code, 0)
+    m.tensor = data                        # kept alive with the argument
+    return m
+
+
+def _mat(x):
+    if x is None:
+        return None
+    return ctypes.byref(x if isinstance(x, zero_mat) else mat(x))
+
+
+def _shape(x, rows, cols, what):
+    """A tensor argument holds the rows x cols that the call will touch."""
+    if hasattr(x, "data_ptr"):
+        have = tuple(x.shape) if x.dim() == 2 else (1, x.shape[0]) if x.dim() == 1 else None
+        if have != (rows, cols):
+            raise ZeroError(ZERO_EINVAL, f"{what} is {tuple(x.shape)}, not {rows} x {cols}")
+
+
+def _count(x, n, what):
+    """A tensor argument is a contiguous fp32 array of at least n values."""
+    if hasattr(x, "data_ptr") and (x.numel() < n or str(x.dtype) != "torch.float32" or not x.is_contiguous()):
+        raise ZeroError(ZERO_EINVAL, f"{what} must be {n} contiguous float32 values")
+
+
+def zero_norm_forward(x, residual, weight, rows, cols, eps, h_out, y, y_scale, scale_block, rstd, stream=None):
+    """h = x + residual, y = RMSnorm(h) * weight per row; y in x's type, or
+    float8_e4m3fn with a scale per row (scale_block 0) or per 128 columns."""
+    for t, what in ((x, "x"), (residual, "residual"), (h_out, "h_out"), (y, "y")):
+        _shape(t, rows, cols, what)
+    _shape(weight, 1, cols, "weight")
+    _count(rstd, rows, "rstd")
+    _count(y_scale, rows * (-(-cols // scale_block) if scale_block > 0 else 1), "y_scale")
+    _check(lib.zero_norm_forward(_mat(x), _mat(residual), _mat(weight), rows, cols, eps, _mat(h_out), _mat(y),
+                                 _ptr(y_scale), scale_block, _ptr(rstd), _stream(stream)))
+
+
+def zero_norm_workspace_bytes(cols):
+    return lib.zero_norm_workspace_bytes(cols)
+
+
+def zero_norm_backward(dy, h, weight, rows, cols, rstd, dh, dx, dw, accumulate, workspace, workspace_bytes,
+                       stream=None):
+    """dx (of x and residual alike) and dw of zero_norm_forward."""
+    for t, what in ((dy, "dy"), (h, "h"), (dh, "dh"), (dx, "dx")):
+        _shape(t, rows, cols, what)
+    for t, what in ((weight, "weight"), (dw, "dw")):
+        _shape(t, 1, cols, what)
+    _count(rstd, rows, "rstd")
+    _check(lib.zero_norm_backward(_mat(dy), _mat(h), _mat(weight), rows, cols, _ptr(rstd), _mat(dh), _mat(dx),
+                                  _mat(dw), int(accumulate), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def _distill_shapes(logits, rows, cols, ids, teacher, k, teacher_lse, row_weight, lse, dlogits):
+    for t, n, what in ((logits, cols, "logits"), (dlogits, cols, "dlogits"), (ids, k, "ids"), (teacher, k, "teacher")):
+        _shape(t, rows, n, what)
+    for t, what in ((teacher_lse, "teacher_lse"), (row_weight, "row_weight"), (lse, "lse")):
+        _count(t, rows, what)
+
+
+def zero_distill_loss(logits, rows, cols, ids, teacher, k, teacher_lse, temperature, row_weight, grad_scale, chain_dev,
+                      loss, lse, dlogits, stream=None):
+    """The rows' losses against the teacher's k logits and, with dlogits, the
+    gradient, scaled by grad_scale and by the loss scale of the device chain."""
+    _distill_shapes(logits, rows, cols, ids, teacher, k, teacher_lse, row_weight, lse, dlogits)
+    _count(loss, rows, "loss")
+    _check(lib.zero_distill_loss(_mat(logits), rows, cols, _mat(ids), _mat(teacher), k, _ptr(teacher_lse), temperature,
+                                 _ptr(row_weight), grad_scale, _ptr(chain_dev), _ptr(loss), _ptr(lse), _mat(dlogits),
+                                 _stream(stream)))
+
+
+def zero_distill_backward(logits, rows, cols, ids, teacher, k, teacher_lse, temperature, row_weight, grad_scale,
+                          chain_dev, lse, dlogits, stream=None):
+    """The gradient alone, from the lse that zero_distill_loss stored."""
+    _distill_shapes(logits, rows, cols, ids, teacher, k, teacher_lse, row_weight, lse, dlogits)
+    _check(lib.zero_distill_backward(_mat(logits), rows, cols, _mat(ids), _mat(teacher), k, _ptr(teacher_lse),
+                                     temperature, _ptr(row_weight), grad_scale, _ptr(chain_dev), _ptr(lse),
+                                     _mat(dlogits), _stream(stream)))
+
+
+def zero_mx4_bytes(rows, cols, layout=ZERO_MX4_TILES):
+    """(ld, data bytes, scale bytes) of a 4-bit matrix."""
+    ld, data, scales = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
+    _check(lib.zero_mx4_bytes(rows, cols, layout, ctypes.byref(ld), ctypes.byref(data), ctypes.byref(scales)))
+    return ld.value, data.value, scales.value
+
+
+def mx4(rows, cols, data=None, scales=None, layout=ZERO_MX4_TILES, device=None) -> zero_mx4:
+    """A zero_mx4 over given buffers (torch uint8 tensors or addresses), or over
+    new ones on `device`; rows follow one another without gaps."""
+    ld, n_data, n_scales = zero_mx4_bytes(rows, cols, layout)
+    if data is None or scales is None:
+        import torch
+        buf = torch.empty((n_data if data is None else 0) + (n_scales if scales is None else 0), dtype=torch.uint8,
+                          device=device)
+        if data is None:
+            data, buf = buf[:n_data], buf[n_data:]
+        if scales is None:
+            scales = buf
+    for t, n, what in ((data, n_data, "data"), (scales, n_scales, "scales")):
+        if hasattr(t, "data_ptr") and (t.numel() * t.element_size() < n or not t.is_contiguous()):
+            raise ZeroError(ZERO_EINVAL, f"{what} must be at least {n} contiguous bytes")
+    m = zero_mx4(_ptr(data), _ptr(scales), rows, cols, ld, layout, 0)
+    m.tensors = (data, scales)             # kept alive with the argument
+    return m
+
+
+def _mx4(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def zero_mx4_quantize(src, rows, cols, out, out_t, stream=None):
+    """src to 4 bits along its rows (out) and along its columns (out_t: cols x
+    rows); either may be None."""
+    _shape(src, rows, cols, "src")
+    _check(lib.zero_mx4_quantize(_mat(src), rows, cols, _mx4(out), _mx4(out_t), _stream(stream)))
+
+
+def zero_mx4_dequantize(src, dst, stream=None):
+    """The values of a 4-bit matrix in dst's type."""
+    if src is not None:
+        _shape(dst, src.rows, src.cols, "dst")
+    _check(lib.zero_mx4_dequantize(_mx4(src), _mat(dst), _stream(stream)))
+
+
+def zero_mx4_tile_scales(src, dst, stream=None):
+    """Scales gathered row by row (ZERO_MX4_ROWS) to the product's tiles."""
+    _check(lib.zero_mx4_tile_scales(_mx4(src), _mx4(dst), _stream(stream)))
+
+
+def zero_mx4_matmul(a, b, alpha, d, status, stream=None):
+    """d = alpha a b^T of two 4-bit matrices; status: device int32 (zero-filled by
+    the caller), bit 0 set if a wait ran out."""
+    if a is not None and b is not None:
+        _shape(d, a.rows, b.rows, "d")
+    _check(lib.zero_mx4_matmul(_mx4(a), _mx4(b), alpha, _mat(d), _ptr(status), _stream(stream)))

@@ -1,0 +1,172 @@
+// zero_layer.cuh -- what the layer operators (norm, distillation, 4-bit
+// matrices) share: element types, row access of any alignment, block
+// reductions, and the host checks of a zero_mat.
+//
+// A row is walked in units of E elements per thread.  V8: 8 consecutive
+// elements, one 16-byte access (two for fp32), taken when every row of every
+// matrix starts on a 16-byte boundary and the columns are a multiple of 8.
+// Otherwise 4 elements 32 apart, one per warp-wide coalesced access: rows
+// that start anywhere still read whole sectors.  Either way 128 consecutive
+// columns belong to 16 (V8) or 32 consecutive lanes of one warp, so a scale
+// per 128 columns needs no shared memory.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "zero_internal.h"
+
+namespace zdp {
+
+template <int DT> struct Elem;
+template <> struct Elem<ZERO_F16> { static constexpr int SIZE = 2; };
+template <> struct Elem<ZERO_BF16> { static constexpr int SIZE = 2; };
+template <> struct Elem<ZERO_F32> { static constexpr int SIZE = 4; };
+
+__host__ __device__ __forceinline__ int elem_size(int dt) {
+    return dt == ZERO_F32 || dt == ZERO_I32 ? 4 : dt == ZERO_I64 ? 8 : dt == ZERO_E4M3 ? 1 : 2;
+}
+
+// ---------------------------------------------------------------- elements
+template <int DT>
+__device__ __forceinline__ float ld1(const void* p, int64_t i) {
+    if constexpr (DT == ZERO_F32) return static_cast<const float*>(p)[i];
+    else return Half16<DT>::widen(static_cast<const uint16_t*>(p)[i]);
+}
+template <int DT>
+__device__ __forceinline__ void st1(void* p, int64_t i, float v) {
+    if constexpr (DT == ZERO_F32) static_cast<float*>(p)[i] = v;
+    else static_cast<uint16_t*>(p)[i] = (uint16_t)Half16<DT>::narrow(v);
+}
+__device__ __forceinline__ float ld1_any(const void* p, int64_t i, int dt) {
+    return dt == ZERO_F32 ? ld1<ZERO_F32>(p, i) : dt == ZERO_BF16 ? ld1<ZERO_BF16>(p, i) : ld1<ZERO_F16>(p, i);
+}
+__device__ __forceinline__ void st1_any(void* p, int64_t i, float v, int dt) {
+    if (dt == ZERO_F32) st1<ZERO_F32>(p, i, v);
+    else if (dt == ZERO_BF16) st1<ZERO_BF16>(p, i, v);
+    else st1<ZERO_F16>(p, i, v);
+}
+
+// Eight packed elements as they lie in memory: one 16-byte word, or two.
+template <int DT> struct Raw8 { uint4 w[DT == ZERO_F32 ? 2 : 1]; };
+
+template <int DT>
+__device__ __forceinline__ Raw8<DT> ld8(const void* p, int64_t i) {
+    Raw8<DT> r;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * Elem<DT>::SIZE);
+    r.w[0] = q[0];
+    if constexpr (DT == ZERO_F32) r.w[1] = q[1];
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ Raw8<DT> ld8_stream(const void* p, int64_t i) {
+    Raw8<DT> r;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * Elem<DT>::SIZE);
+    r.w[0] = __ldcs(q);
+    if constexpr (DT == ZERO_F32) r.w[1] = __ldcs(q + 1);
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw8<DT>& r, float (&v)[8]) {
+    if constexpr (DT == ZERO_F32) {
+        const uint32_t u[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[e]);
+    } else {
+        const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[2 * q] = Half16<DT>::widen(u[q] & 0xFFFFu);
+            v[2 * q + 1] = Half16<DT>::widen(u[q] >> 16);
+        }
+    }
+}
+template <int DT>
+__device__ __forceinline__ Raw8<DT> narrow8(const float (&v)[8]) {
+    Raw8<DT> r;
+    if constexpr (DT == ZERO_F32) {
+        r.w[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        r.w[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+    } else {
+        r.w[0] = make_uint4(Half16<DT>::narrow2(v[0], v[1]), Half16<DT>::narrow2(v[2], v[3]),
+                            Half16<DT>::narrow2(v[4], v[5]), Half16<DT>::narrow2(v[6], v[7]));
+    }
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ void st8(void* p, int64_t i, const Raw8<DT>& r) {
+    uint4* q = reinterpret_cast<uint4*>(static_cast<char*>(p) + i * Elem<DT>::SIZE);
+    q[0] = r.w[0];
+    if constexpr (DT == ZERO_F32) q[1] = r.w[1];
+}
+// Eight elements of a vector that other rows read too (a weight), whatever its alignment.
+__device__ __forceinline__ void ld8_any(const void* p, int64_t i, int dt, bool aligned16, float (&v)[8]) {
+    if (!aligned16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = ld1_any(p, i + e, dt);
+    } else if (dt == ZERO_F32) {
+        widen8<ZERO_F32>(ld8<ZERO_F32>(p, i), v);
+    } else if (dt == ZERO_BF16) {
+        widen8<ZERO_BF16>(ld8<ZERO_BF16>(p, i), v);
+    } else {
+        widen8<ZERO_F16>(ld8<ZERO_F16>(p, i), v);
+    }
+}
+
+// ---------------------------------------------------------------- reductions
+// |x| as an unsigned integer orders as |x| does, with NaN above infinity: the
+// largest of a block keeps a NaN, where fmaxf would drop it.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// The block's sum, the same in every thread and every run (a butterfly in
+// each warp, then the warps in order).  s: 32 floats of shared memory that no
+// call in flight uses; the caller alternates two of them between calls.
+__device__ __forceinline__ float block_sum(float v, float* s) {
+    v = warp_sum(v);
+    if (blockDim.x <= 32) return v;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int nw = blockDim.x >> 5;
+    float t = 0.f;
+    for (int w = 0; w < nw; ++w) t += s[w];
+    return t;
+}
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s) {
+    v = lanes_max<32>(v);
+    if (blockDim.x <= 32) return v;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int nw = blockDim.x >> 5;
+    uint32_t t = 0;
+    for (int w = 0; w < nw; ++w) t = max(t, s[w]);
+    return t;
+}
+
+// ---------------------------------------------------------------- host
+// A matrix argument: not NULL, one of the types in `types` (a bit per code),
+// rows at least `cols` apart, aligned to its element.
+int check_mat(const zero_mat* m, int64_t rows, int64_t cols, unsigned types, const char* what);
+constexpr unsigned FLOAT_TYPES = 1u << ZERO_F16 | 1u << ZERO_BF16 | 1u << ZERO_F32;
+// Whether every row starts on a 16-byte boundary.
+inline bool rows_aligned(const zero_mat& m, int64_t rows) {
+    return aligned(m.data, 16) && (rows <= 1 || (m.ld * elem_size(m.dtype)) % 16 == 0);
+}
+// SM count of the current device (0 and an error message if it cannot be had).
+int sm_count();
+
+}  // namespace zdp

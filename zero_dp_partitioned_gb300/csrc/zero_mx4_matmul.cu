@@ -1,0 +1,456 @@
+// zero_mx4_matmul.cu -- D[m][n] = alpha * sum_k A[m][k] B[n][k] of two
+// microscaled 4-bit matrices on the block-scaled tensor cores
+// (tcgen05.mma kind::mxf4, a scale for 32 elements of each operand).
+//
+// A persistent block per SM walks tiles of 128 rows of one operand (X) by BN
+// rows of the other (Y).  Warp 0's first lane copies stages of 256 elements
+// of k into shared memory (TMA tiles of 128-byte rows, 128-byte swizzle; the
+// scales' tiles as plain bulk copies), warp 1's first lane moves the scales
+// to tensor memory and issues the four products of a stage, and warps 2 to 5
+// read the fp32 accumulator back, scale it and store it.  With BN = 256 the
+// two accumulators of 256 columns and the scales do not fit the 512 columns
+// of tensor memory side by side, so the accumulators overlap by 32 columns:
+// a tile's epilogue reads those 32 first and then lets the next tile start.
+//
+// X is A, and Y is B, unless A has few rows (tokens): then X is B, the
+// weights, so that the 128 rows of a tile are all used, and the accumulator
+// is stored transposed.
+//
+// Every wait is bounded.  A block whose wait runs out sets bit 0 of *status,
+// its roles stop, what they have in flight is waited for (bounded again), the
+// tensor memory is freed, and the block leaves; D is then incomplete.
+#include <cuda.h>
+
+#include <cstdlib>
+#include <mutex>
+
+#include "zero_layer.cuh"
+#include "zero_mx4.cuh"
+#include "zero_tma.cuh"
+
+namespace zdp {
+
+constexpr int MM_THREADS = 192;
+constexpr int MM_BX = 128;
+constexpr int MM_KB = 128;                    // bytes of k in a stage: 256 elements
+constexpr int MM_HEADER = 1024;
+constexpr int MM_SF_COL = 480;                // tensor-memory column of the scales
+constexpr int MM_MAX_STAGES = 8;
+
+template <int BN>
+struct MmShape {
+    static constexpr int Y_TILES = (BN + 127) / 128;           // 128-row scale tiles of Y
+    static constexpr int X_BYTES = MM_BX * MM_KB, Y_BYTES = BN * MM_KB;
+    static constexpr int XS_BYTES = 1024, YS_BYTES = 1024 * Y_TILES;
+    static constexpr int STAGE = X_BYTES + Y_BYTES + XS_BYTES + YS_BYTES;
+    // a stage starts on 1024 bytes (the swizzle's period)
+    static constexpr int STRIDE = (STAGE + 1023) / 1024 * 1024;
+    static constexpr int STAGES = (232448 - 2048) / STRIDE < MM_MAX_STAGES ? (232448 - 2048) / STRIDE : MM_MAX_STAGES;
+    static constexpr int SMEM = STAGES * STRIDE + 2048;
+    static constexpr bool OVERLAP = BN == 256;
+    static constexpr int ACC1 = OVERLAP ? 224 : BN;            // column of the second accumulator
+};
+
+struct MmArgs {
+    const uint8_t *xs, *ys;                   // tiled scales
+    void* d;
+    int64_t ldd;
+    int x_rows, y_rows;                       // rows of X and Y
+    int x_tiles, y_tiles, k_steps;            // tiles of 128 and BN rows, stages of 256 elements
+    int dt, swap, wide_store;
+    float alpha;
+    int32_t* status;
+    unsigned spin_limit, drain_limit;
+};
+
+// ---------------------------------------------------------------- PTX
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                       bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((int)add)
+        : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 32 lanes by 16 columns: a thread gets its lane's 16 consecutive columns.
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Shared-memory descriptors.  Operand tiles: rows of 128 bytes in the 128-byte
+// swizzle, 8 rows (1024 bytes) from one group to the next.  Scale tiles: 32
+// rows of 16 bytes as they lie, 8 rows (128 bytes) to a group.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(128 >> 4) << 32 | 1ull << 46;
+}
+// Instruction descriptor: both operands e2m1, scales e8m0, the shape, and
+// which half of a 4-byte word of scales is used.
+__device__ __forceinline__ constexpr uint32_t mma_desc(int bn, int half) {
+    return (uint32_t)(half * 2) << 4 | 1u << 7 | 1u << 10 | (uint32_t)(bn >> 3) << 17 | 1u << 23 |
+           (uint32_t)(MM_BX >> 4) << 24 | (uint32_t)(half * 2) << 29;
+}
+
+// A bounded wait that also ends when another role of the block has given up.
+__device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, unsigned limit, volatile int* stop) {
+    for (unsigned it = 0; it < limit; it += 256) {
+        const unsigned n = limit - it < 256 ? limit - it : 256;
+        if (mbar_wait(bar, parity, n)) return true;
+        if (*stop) return false;
+    }
+    return false;
+}
+
+// Tiles in order, in groups of 8 tiles of Y so that the blocks that run
+// together share both operands in L2.
+__device__ __forceinline__ void tile_at(const MmArgs& a, int t, int& x, int& y) {
+    const int per = 8 * a.x_tiles, g = t / per, y0 = g * 8;
+    const int w = min(8, a.y_tiles - y0), r = t - g * per;
+    x = r / w;
+    y = y0 + r % w;
+}
+
+template <int BN>
+__global__ void __launch_bounds__(MM_THREADS, 1)
+    k_mx4_matmul(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap ymap,
+                 const __grid_constant__ MmArgs a) {
+    using S = MmShape<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023) & ~1023u;
+    uint8_t* head = smem_raw + (base - raw);
+    // header: full[8], empty[8], acc_full[2], acc_free[2], drained, then the tensor-memory address, stop flag and count
+    const uint32_t full = base, empty = base + 64, acc_full = base + 128, acc_free = base + 144, drained = base + 160;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 168);
+    volatile int* stop = reinterpret_cast<volatile int*>(head + 172);
+    volatile int* loaded = reinterpret_cast<volatile int*>(head + 176);   // stages whose loads were issued
+    const uint32_t stages = base + MM_HEADER;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::STAGES; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_full + 8, 1);
+        mbar_init(acc_free, 4);
+        mbar_init(acc_free + 8, 4);
+        mbar_init(drained, 1);
+        fence_mbar_init();
+        *stop = 0;
+        *loaded = 0;
+    }
+    if (warp == 1)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + 168) : "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch_next();
+
+    const int n_tiles = a.x_tiles * a.y_tiles, K = a.k_steps;
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            int st = 0, count = 0;
+            uint32_t phase = 0;
+            for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+                int x, y;
+                tile_at(a, t, x, y);
+                for (int k = 0; k < K; ++k) {
+                    if (count >= S::STAGES && !mm_wait(empty + 8 * st, phase ^ 1, a.spin_limit, stop)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = full + 8 * st, at = stages + st * S::STRIDE;
+                    mbar_expect_tx(bar, S::STAGE);
+                    tma_tile(at, &xmap, k * MM_KB, x * MM_BX, bar);
+                    tma_tile(at + S::X_BYTES, &ymap, k * MM_KB, y * BN, bar);
+                    bulk_load(at + S::X_BYTES + S::Y_BYTES, a.xs + ((int64_t)x * K + k) * 1024, 1024, bar);
+#pragma unroll
+                    for (int q = 0; q < S::Y_TILES; ++q) {
+                        // the last tile of Y may have fewer than BN rows: its last scale tile again, for rows that are 0
+                        const int yt = min(BN >= 128 ? y * S::Y_TILES + q : y * BN / 128, (a.y_rows + 127) / 128 - 1);
+                        bulk_load(at + S::X_BYTES + S::Y_BYTES + 1024 + 1024 * q, a.ys + ((int64_t)yt * K + k) * 1024, 1024,
+                                  bar);
+                    }
+                    *loaded = ++count;
+                    if (++st == S::STAGES) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int st = 0, n = 0;
+            uint32_t phase = 0;
+            for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x, ++n) {
+                // the accumulator of tile n was last used by tile n - 2; overlapping ones wait for tile n - 1's first
+                // columns (its epilogue began after tile n - 2's ended)
+                const int need = S::OVERLAP ? n - 1 : n - 2;
+                if (need >= 0 && !mm_wait(acc_free + 8 * (need & 1), (need >> 1) & 1, a.spin_limit, stop)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + (n & 1 ? S::ACC1 : 0);
+                for (int k = 0; k < K; ++k) {
+                    if (!mm_wait(full + 8 * st, phase, a.spin_limit, stop)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = stages + st * S::STRIDE, sx = at + S::X_BYTES + S::Y_BYTES, sy = sx + 1024;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tc_copy_scales(tmem + MM_SF_COL + 4 * h, scale_desc(sx + 512 * h));
+#pragma unroll
+                        for (int q = 0; q < S::Y_TILES; ++q)
+                            tc_copy_scales(tmem + MM_SF_COL + 8 + 4 * (h * S::Y_TILES + q), scale_desc(sy + 1024 * q + 512 * h));
+                    }
+                    const uint64_t dx = operand_desc(at), dy = operand_desc(at + S::X_BYTES);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        tc_mma(d, dx + 2 * q, dy + 2 * q, mma_desc(BN, q & 1), tmem + MM_SF_COL + 4 * (q >> 1),
+                               tmem + MM_SF_COL + 8 + 4 * S::Y_TILES * (q >> 1), k > 0 || q > 0);
+                    tc_commit(empty + 8 * st);
+                    if (++st == S::STAGES) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (ok) tc_commit(acc_full + 8 * (n & 1));
+            }
+            tc_commit(drained);
+        }
+    } else {
+        const int quarter = warp & 3;                        // the 32 lanes of tensor memory this warp can read
+        int n = 0;
+        for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, ++n) {
+            int x, y;
+            tile_at(a, t, x, y);
+            const int acc = n & 1;
+            ok = mm_wait(acc_full + 8 * acc, (n >> 1) & 1, a.spin_limit, stop);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + (acc ? S::ACC1 : 0) + ((uint32_t)(quarter * 32) << 16);
+            const int64_t xr = (int64_t)x * MM_BX + quarter * 32 + lane;
+            const int64_t y0 = (int64_t)y * BN;
+            // 16 columns at a time; the overlapping 32 first: the last of accumulator 0, the first of accumulator 1
+            for (int c = 0; c < BN / 16; ++c) {
+                const int col = S::OVERLAP && !acc ? ((c + 14) & 15) * 16 : c * 16;
+                uint32_t v[16];
+                __syncwarp();
+                tc_ld16(d + col, v);
+                tc_wait_ld();
+                if (c == (S::OVERLAP ? 1 : BN / 16 - 1)) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_free + 8 * acc);
+                }
+                if (xr >= a.x_rows) continue;
+                if (a.swap) {
+                    // a lane holds one column of D: the warp stores 32 consecutive ones of each row
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (y0 + col + e < a.y_rows)
+                            st1_any(a.d, (y0 + col + e) * a.ldd + xr, __uint_as_float(v[e]) * a.alpha, a.dt);
+                } else {
+                    const int64_t at = xr * a.ldd + y0 + col;
+                    if (a.wide_store && y0 + col + 16 <= a.y_rows) {
+                        float lo[8], hi[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            lo[e] = __uint_as_float(v[e]) * a.alpha;
+                            hi[e] = __uint_as_float(v[8 + e]) * a.alpha;
+                        }
+                        if (a.dt == ZERO_F32) {
+                            st8<ZERO_F32>(a.d, at, narrow8<ZERO_F32>(lo));
+                            st8<ZERO_F32>(a.d, at + 8, narrow8<ZERO_F32>(hi));
+                        } else if (a.dt == ZERO_BF16) {
+                            st8<ZERO_BF16>(a.d, at, narrow8<ZERO_BF16>(lo));
+                            st8<ZERO_BF16>(a.d, at + 8, narrow8<ZERO_BF16>(hi));
+                        } else {
+                            st8<ZERO_F16>(a.d, at, narrow8<ZERO_F16>(lo));
+                            st8<ZERO_F16>(a.d, at + 8, narrow8<ZERO_F16>(hi));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (y0 + col + e < a.y_rows) st1_any(a.d, at + e, __uint_as_float(v[e]) * a.alpha, a.dt);
+                    }
+                }
+            }
+        }
+    }
+    if (!ok && lane == 0) {
+        *stop = 1;
+        atomicOr(a.status, 1);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // what was issued and not waited for: the products (their shared and tensor memory), and after a stop the loads
+    if (threadIdx.x == 32) {
+        mbar_wait(drained, 0, a.drain_limit);
+        if (*stop)
+            for (int c = max(0, *loaded - S::STAGES); c < *loaded; ++c)
+                mbar_wait(full + 8 * (c % S::STAGES), (uint32_t)(c / S::STAGES) & 1, a.drain_limit);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+// ---------------------------------------------------------------- host
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn encode_fn() {
+    static EncodeFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(p);
+        else
+            cudaGetLastError();
+    });
+    return fn;
+}
+
+// Packed rows as bytes: boxes of 128 bytes by box_rows rows, 128-byte swizzle;
+// bytes and rows past the end read as 0.
+static int make_map(CUtensorMap* map, const zero_mx4& m, int box_rows) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return fail(ZERO_ECUDA, "zero_mx4_matmul: the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t dims[2] = {(cuuint64_t)(mx4_blocks(m.cols) * 16), (cuuint64_t)m.rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)m.ld};
+    const cuuint32_t box[2] = {MM_KB, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m.data, dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_ECUDA, "zero_mx4_matmul: cuTensorMapEncodeTiled failed");
+}
+
+template <int BN>
+static int launch_matmul(const CUtensorMap& xm, const CUtensorMap& ym, const MmArgs& a, int grid, cudaStream_t s) {
+    const void* f = (const void*)k_mx4_matmul<BN>;
+    int rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, MmShape<BN>::SMEM),
+                       "zero_mx4_matmul shared-memory size");
+    if (rc != ZERO_OK) return rc;
+    void* args[] = {const_cast<CUtensorMap*>(&xm), const_cast<CUtensorMap*>(&ym), const_cast<MmArgs*>(&a)};
+    return cuda_fail(launch_after_previous(f, grid, MM_THREADS, args, MmShape<BN>::SMEM, s), "zero_mx4_matmul launch");
+}
+
+__global__ void k_fill_zero(void* d, int64_t ld, int64_t rows, int64_t cols, int dt) {
+    pdl_wait();
+    pdl_launch_next();
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * cols; i += (int64_t)gridDim.x * blockDim.x)
+        st1_any(d, i / cols * ld + i % cols, 0.f, dt);
+}
+
+}  // namespace zdp
+
+using namespace zdp;
+
+extern "C" {
+
+int zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, float alpha, const zero_mat* d, int32_t* status, void* stream) {
+    int rc = check_mx4(a, "zero_mx4_matmul: a");
+    if (rc == ZERO_OK) rc = check_mx4(b, "zero_mx4_matmul: b");
+    if (rc != ZERO_OK) return rc;
+    if (a->cols != b->cols) return fail(ZERO_EINVAL, "zero_mx4_matmul: a and b have as many columns");
+    if (a->layout != ZERO_MX4_TILES || b->layout != ZERO_MX4_TILES)
+        return fail(ZERO_EINVAL, "zero_mx4_matmul: scales in ZERO_MX4_TILES (zero_mx4_tile_scales)");
+    if (a->rows > INT32_MAX / 2 || b->rows > INT32_MAX / 2 || a->cols > INT32_MAX / 2)
+        return fail(ZERO_ELIMIT, "zero_mx4_matmul: more than 2^30 rows or columns");
+    rc = check_mat(d, a->rows, b->rows, FLOAT_TYPES, "zero_mx4_matmul: d");
+    if (rc != ZERO_OK) return rc;
+    if (!status || !aligned(status, 4)) return fail(ZERO_EINVAL, "zero_mx4_matmul: status NULL or not 4-byte aligned");
+    if (!(alpha - alpha == 0.f)) return fail(ZERO_EINVAL, "zero_mx4_matmul: alpha must be finite");
+    if (a->rows == 0 || b->rows == 0) return ZERO_OK;
+    const int sms = sm_count();
+    if (!sms) return ZERO_ECUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a->cols == 0) {                      // a sum of nothing
+        void* dp = d->data;
+        int64_t ld = d->ld, rows = a->rows, cols = b->rows;
+        int dt = d->dtype;
+        void* args[] = {&dp, &ld, &rows, &cols, &dt};
+        return cuda_fail(launch_after_previous((const void*)k_fill_zero, sms * 4, 256, args, 0, s), "zero_mx4_matmul launch");
+    }
+    MmArgs m = {};
+    m.swap = a->rows <= 128;
+    const zero_mx4 &x = m.swap ? *b : *a, &y = m.swap ? *a : *b;
+    m.xs = static_cast<const uint8_t*>(x.scales);
+    m.ys = static_cast<const uint8_t*>(y.scales);
+    m.d = d->data;
+    m.ldd = d->ld;
+    m.x_rows = (int)x.rows;
+    m.y_rows = (int)y.rows;
+    m.x_tiles = (int)((x.rows + MM_BX - 1) / MM_BX);
+    m.k_steps = (int)((a->cols + 255) / 256);
+    m.dt = d->dtype;
+    m.wide_store = rows_aligned(*d, a->rows);
+    m.alpha = alpha;
+    m.status = status;
+    const char* e = std::getenv("ZERO_GB300_SPIN_LIMIT");
+    m.spin_limit = e ? (unsigned)std::strtoul(e, nullptr, 10) : SPIN_LIMIT;
+    m.drain_limit = SPIN_LIMIT;
+    const int bn = m.swap ? (y.rows <= 16 ? 16 : y.rows <= 64 ? 64 : 128) : 256;
+    m.y_tiles = (int)((y.rows + bn - 1) / bn);
+    if ((int64_t)m.x_tiles * m.y_tiles > INT32_MAX) return fail(ZERO_ELIMIT, "zero_mx4_matmul: too many tiles");
+    const int tiles = m.x_tiles * m.y_tiles, grid = tiles < sms ? tiles : sms;
+    CUtensorMap xm, ym;
+    rc = make_map(&xm, x, MM_BX);
+    if (rc == ZERO_OK) rc = make_map(&ym, y, bn);
+    if (rc != ZERO_OK) return rc;
+    switch (bn) {
+        case 16: return launch_matmul<16>(xm, ym, m, grid, s);
+        case 64: return launch_matmul<64>(xm, ym, m, grid, s);
+        case 128: return launch_matmul<128>(xm, ym, m, grid, s);
+        default: return launch_matmul<256>(xm, ym, m, grid, s);
+    }
+}
+
+}  // extern "C"

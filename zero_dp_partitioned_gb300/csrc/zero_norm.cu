@@ -1,0 +1,664 @@
+// zero_norm.cu -- the residual RMS norm of a layer, forward and backward.
+//
+//   h = round(x + r)      (r and h in x's type, or both in fp32)
+//   y = h w / sqrt(mean(h^2) + eps)
+// and, with xh = h rstd and g = dy w,
+//   dx = rstd (g - xh mean(g xh)) + dh        (of x and of r alike)
+//   dw = sum over rows of dy xh
+//
+// Bound: HBM.  Forward reads x and r and writes h and y (8 bytes an element
+// in 16 bits, 7 with an e4m3 y); backward reads dy, h and dh and writes dx.
+// A row is read once and kept in registers between the sum of squares and the
+// output, so one block owns a row and nothing is read again.
+#include "zero_layer.cuh"
+
+namespace zdp {
+
+constexpr int NORM_THREADS = 512;       // most threads that share a row
+constexpr int64_t NORM_MAX_COLS = 1 << 20;
+constexpr int NORM_MAX_GRID = 608;      // blocks of the backward pass, each with a partial dw
+constexpr float E4M3_MAX = 448.f;
+constexpr float SCALE_FLOOR = 7.888609052210118e-31f;   // 2^-100: a zero row still has a usable scale
+
+struct NormArgs {
+    const void *x, *r, *w;              // backward: dy, dh, w
+    const void* hin;                    // backward: the stored h
+    void *h, *y;                        // backward: y is dx
+    int64_t ldx, ldr, ldhin, ldh, ldy, rows, cols, n_scale;
+    float eps;
+    int wdt, w_aligned, y8, block128;
+    float *scale, *rstd;
+    float* part;                        // backward: [grid][cols] partial dw
+};
+
+// Columns of element e of unit u: V8 units are 8 consecutive columns, the
+// others 4 columns 32 apart inside a warp's 128.
+template <bool V8>
+struct Map {
+    static constexpr int E = V8 ? 8 : 4;
+    static constexpr int LANES = V8 ? 16 : 32;      // lanes that share 128 columns
+    // this thread's j-th unit
+    static __device__ __forceinline__ int64_t unit(int j) { return threadIdx.x + (int64_t)j * blockDim.x; }
+    static __device__ __forceinline__ int64_t col(int64_t u, int e) {
+        return V8 ? u * 8 + e : (u >> 5) * 128 + e * 32 + (u & 31);
+    }
+    static __device__ __forceinline__ bool any(int64_t u, int64_t cols) { return col(u, 0) < cols; }
+};
+
+// Loads of one unit of a row, kept as they lie until they are used, so that
+// every load of a row is in flight before the first is waited for.
+template <int DT, bool V8>
+struct Unit {
+    Raw8<DT> raw;                        // V8
+    float one[V8 ? 1 : 4];
+    __device__ __forceinline__ void load(const void* row, int64_t u, int64_t cols) {
+        if constexpr (V8) {
+            if (u * 8 < cols) raw = ld8<DT>(row, u * 8);
+            else
+#pragma unroll
+                for (auto& w : raw.w) w = make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t c = Map<V8>::col(u, e);
+                one[e] = c < cols ? ld1<DT>(row, c) : 0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[Map<V8>::E]) const {
+        if constexpr (V8) widen8<DT>(raw, v);
+        else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = one[e];
+    }
+};
+
+template <int DT, bool V8>
+__device__ __forceinline__ void store_unit(void* row, int64_t u, int64_t cols, const float (&v)[Map<V8>::E]) {
+    if constexpr (V8) {
+        if (u * 8 < cols) st8<DT>(row, u * 8, narrow8<DT>(v));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t c = Map<V8>::col(u, e);
+            if (c < cols) st1<DT>(row, c, v[e]);
+        }
+    }
+}
+
+template <bool V8>
+__device__ __forceinline__ void store_e4m3(void* row, int64_t u, int64_t cols, const float (&v)[Map<V8>::E]) {
+    uint8_t* p = static_cast<uint8_t*>(row);
+    if constexpr (V8) {
+        if (u * 8 >= cols) return;
+        uint32_t h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            h[q] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * q], v[2 * q + 1]), __NV_SATFINITE, __NV_E4M3);
+        *reinterpret_cast<uint2*>(p + u * 8) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t c = Map<V8>::col(u, e);
+            if (c < cols) p[c] = __nv_cvt_float_to_fp8(v[e], __NV_SATFINITE, __NV_E4M3);
+        }
+    }
+}
+
+template <bool V8>
+__device__ __forceinline__ void weights(const NormArgs& a, int64_t u, float (&w)[Map<V8>::E]) {
+    if (!a.w) {
+#pragma unroll
+        for (int e = 0; e < Map<V8>::E; ++e) w[e] = 1.f;
+    } else if constexpr (V8) {
+        if (u * 8 < a.cols) ld8_any(a.w, u * 8, a.wdt, a.w_aligned, w);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 0.f;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t c = Map<V8>::col(u, e);
+            w[e] = c < a.cols ? ld1_any(a.w, c, a.wdt) : 0.f;
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ const void* row_of(const void* p, int64_t ld, int64_t r) {
+    return static_cast<const char*>(p) + r * ld * Elem<DT>::SIZE;
+}
+template <int DT>
+__device__ __forceinline__ void* row_of(void* p, int64_t ld, int64_t r) {
+    return static_cast<char*>(p) + r * ld * Elem<DT>::SIZE;
+}
+
+// x + r of one unit, rounded to the type h is stored in.
+template <int XT, int RT, bool V8>
+__device__ __forceinline__ void add_unit(const Unit<XT, V8>& x, const Unit<RT, V8>& r, bool has_r,
+                                         float (&h)[Map<V8>::E]) {
+    x.values(h);
+    if (!has_r) return;
+    float b[Map<V8>::E];
+    r.values(b);
+#pragma unroll
+    for (int e = 0; e < Map<V8>::E; ++e) {
+        h[e] = __fadd_rn(h[e], b[e]);
+        if constexpr (RT != ZERO_F32) h[e] = Half16<RT>::widen(Half16<RT>::narrow(h[e]));
+    }
+}
+
+// A row in NV units per thread, in registers.
+template <int XT, int RT, bool V8, int NV>
+__global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_constant__ NormArgs a) {
+    constexpr int E = Map<V8>::E;
+    __shared__ float ssum[2][32];
+    __shared__ uint32_t smax[2][32];
+    pdl_wait();
+    pdl_launch_next();
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const void* X = row_of<XT>(a.x, a.ldx, row);
+        const void* R = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
+        Unit<XT, V8> x[NV];
+        Unit<RT, V8> r[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) x[j].load(X, Map<V8>::unit(j), a.cols);
+        if (R)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) r[j].load(R, Map<V8>::unit(j), a.cols);
+        float h[NV][E];
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            add_unit<XT, RT, V8>(x[j], r[j], R != nullptr, h[j]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) ss = fmaf(h[j][e], h[j][e], ss);
+            if (a.h) store_unit<RT, V8>(row_of<RT>(a.h, a.ldh, row), Map<V8>::unit(j), a.cols, h[j]);
+        }
+        ss = block_sum(ss, ssum[turn]);
+        const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
+        if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float w[E];
+            weights<V8>(a, Map<V8>::unit(j), w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                h[j][e] = h[j][e] * rstd * w[e];
+                if (a.y8) top = max(top, abs_bits(h[j][e]));
+            }
+            if (!a.y8) {
+                store_unit<XT, V8>(row_of<XT>(a.y, a.ldy, row), Map<V8>::unit(j), a.cols, h[j]);
+            } else if (a.block128) {
+                const uint32_t t = lanes_max<Map<V8>::LANES>(top);
+                top = 0;
+                const float m = fmaxf(__uint_as_float(t), SCALE_FLOOR);
+                const float mm = __uint_as_float(t) != __uint_as_float(t) ? __uint_as_float(t) : m;
+                const float inv = E4M3_MAX / mm;
+                float q[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) q[e] = h[j][e] * inv;
+                const int64_t u = Map<V8>::unit(j);
+                store_e4m3<V8>(static_cast<uint8_t*>(a.y) + row * a.ldy, u, a.cols, q);
+                if ((u & (Map<V8>::LANES - 1)) == 0 && Map<V8>::any(u, a.cols))
+                    a.scale[row * a.n_scale + u / Map<V8>::LANES] = mm / E4M3_MAX;
+            }
+        }
+        if (a.y8 && !a.block128) {
+            const uint32_t t = block_max(top, smax[turn]);
+            const float m = fmaxf(__uint_as_float(t), SCALE_FLOOR);
+            const float mm = __uint_as_float(t) != __uint_as_float(t) ? __uint_as_float(t) : m;
+            const float inv = E4M3_MAX / mm;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float q[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) q[e] = h[j][e] * inv;
+                store_e4m3<V8>(static_cast<uint8_t*>(a.y) + row * a.ldy, Map<V8>::unit(j), a.cols, q);
+            }
+            if (threadIdx.x == 0) a.scale[row * a.n_scale] = mm / E4M3_MAX;
+        }
+    }
+}
+
+// A row too long for the registers: the block walks it once for the sum of
+// squares (storing h, if it is wanted) and again for the output, the second
+// time from L2.
+template <int XT, int RT, bool V8>
+__global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid_constant__ NormArgs a) {
+    constexpr int E = Map<V8>::E;
+    __shared__ float ssum[2][32];
+    __shared__ uint32_t smax[2][32];
+    pdl_wait();
+    pdl_launch_next();
+    const int64_t units = V8 ? a.cols / 8 : (a.cols + 127) / 128 * 32;
+    const int64_t steps = (units + blockDim.x - 1) / blockDim.x;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const void* X = row_of<XT>(a.x, a.ldx, row);
+        const void* R = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
+        void* H = a.h ? row_of<RT>(a.h, a.ldh, row) : nullptr;
+        auto value = [&](int64_t u, float (&h)[E]) {      // h again, after it was stored over x or r
+            if (H) {
+                Unit<RT, V8> s;
+                s.load(H, u, a.cols);
+                s.values(h);
+            } else {
+                Unit<XT, V8> x;
+                Unit<RT, V8> r;
+                x.load(X, u, a.cols);
+                if (R) r.load(R, u, a.cols);
+                add_unit<XT, RT, V8>(x, r, R != nullptr, h);
+            }
+        };
+        float ss = 0.f;
+        for (int64_t j = 0; j < steps; ++j) {
+            const int64_t u = threadIdx.x + j * blockDim.x;
+            Unit<XT, V8> x;
+            Unit<RT, V8> r;
+            x.load(X, u, a.cols);
+            if (R) r.load(R, u, a.cols);
+            float h[E];
+            add_unit<XT, RT, V8>(x, r, R != nullptr, h);
+#pragma unroll
+            for (int e = 0; e < E; ++e) ss = fmaf(h[e], h[e], ss);
+            if (H) store_unit<RT, V8>(H, u, a.cols, h);
+        }
+        ss = block_sum(ss, ssum[turn]);
+        const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
+        if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+        float whole = 0.f;
+        if (a.y8 && !a.block128) {
+            uint32_t top = 0;
+            for (int64_t j = 0; j < steps; ++j) {
+                const int64_t u = threadIdx.x + j * blockDim.x;
+                float h[E], w[E];
+                value(u, h);
+                weights<V8>(a, u, w);
+#pragma unroll
+                for (int e = 0; e < E; ++e) top = max(top, abs_bits(h[e] * rstd * w[e]));
+            }
+            const uint32_t t = block_max(top, smax[turn]);
+            const float m = fmaxf(__uint_as_float(t), SCALE_FLOOR);
+            whole = __uint_as_float(t) != __uint_as_float(t) ? __uint_as_float(t) : m;
+            if (threadIdx.x == 0) a.scale[row * a.n_scale] = whole / E4M3_MAX;
+        }
+        for (int64_t j = 0; j < steps; ++j) {
+            const int64_t u = threadIdx.x + j * blockDim.x;
+            float h[E], w[E];
+            value(u, h);
+            weights<V8>(a, u, w);
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                h[e] = h[e] * rstd * w[e];
+                top = max(top, abs_bits(h[e]));
+            }
+            if (!a.y8) {
+                store_unit<XT, V8>(row_of<XT>(a.y, a.ldy, row), u, a.cols, h);
+                continue;
+            }
+            float mm = whole;
+            if (a.block128) {
+                const uint32_t t = lanes_max<Map<V8>::LANES>(top);
+                const float m = fmaxf(__uint_as_float(t), SCALE_FLOOR);
+                mm = __uint_as_float(t) != __uint_as_float(t) ? __uint_as_float(t) : m;
+                if ((u & (Map<V8>::LANES - 1)) == 0 && Map<V8>::any(u, a.cols))
+                    a.scale[row * a.n_scale + u / Map<V8>::LANES] = mm / E4M3_MAX;
+            }
+            const float inv = E4M3_MAX / mm;
+#pragma unroll
+            for (int e = 0; e < E; ++e) h[e] *= inv;
+            store_e4m3<V8>(static_cast<uint8_t*>(a.y) + row * a.ldy, u, a.cols, h);
+        }
+    }
+}
+
+// Backward: each block walks rows blockIdx.x, + grid, ...; a thread owns the
+// same columns of all of them, so its part of dw stays in registers and is
+// written once, as one row of `part`.
+template <int XT, int RT, bool V8, int NV>
+__global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_constant__ NormArgs a) {
+    constexpr int E = Map<V8>::E;
+    __shared__ float ssum[2][32];
+    pdl_wait();
+    pdl_launch_next();
+    float dw[NV][E];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e) dw[j][e] = 0.f;
+    const float inv_n = 1.f / (float)a.cols;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const void* DY = row_of<XT>(a.x, a.ldx, row);
+        const void* H = row_of<RT>(a.hin, a.ldhin, row);
+        const void* DH = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
+        Unit<XT, V8> dy[NV];
+        Unit<RT, V8> h[NV], dh[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            dy[j].load(DY, Map<V8>::unit(j), a.cols);
+            h[j].load(H, Map<V8>::unit(j), a.cols);
+        }
+        if (DH)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) dh[j].load(DH, Map<V8>::unit(j), a.cols);
+        const float rstd = a.rstd[row];
+        float dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float g[E], v[E], w[E];
+            dy[j].values(g);
+            h[j].values(v);
+            weights<V8>(a, Map<V8>::unit(j), w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float xh = v[e] * rstd;
+                dw[j][e] = fmaf(g[e], xh, dw[j][e]);
+                dot = fmaf(g[e] * w[e], xh, dot);
+            }
+        }
+        const float c = block_sum(dot, ssum[turn]) * inv_n;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float g[E], v[E], w[E], up[E];
+            dy[j].values(g);
+            h[j].values(v);
+            weights<V8>(a, Map<V8>::unit(j), w);
+            if (DH) dh[j].values(up);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float xh = v[e] * rstd;
+                g[e] = rstd * (g[e] * w[e] - xh * c);
+                if (DH) g[e] += up[e];
+            }
+            store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), Map<V8>::unit(j), a.cols, g);
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int64_t c = Map<V8>::col(Map<V8>::unit(j), e);
+            if (c < a.cols) a.part[(int64_t)blockIdx.x * a.cols + c] = dw[j][e];
+        }
+}
+
+// Rows too long for the registers: dx by walking the row twice, and dw by
+// blocks that own 128 columns and a share of the rows (gridDim.y shares).
+template <int XT, int RT, bool V8>
+__global__ void __launch_bounds__(NORM_THREADS) k_norm_backward_long(const __grid_constant__ NormArgs a) {
+    constexpr int E = Map<V8>::E;
+    __shared__ float ssum[2][32];
+    pdl_wait();
+    pdl_launch_next();
+    const int64_t units = V8 ? a.cols / 8 : (a.cols + 127) / 128 * 32;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const void* DY = row_of<XT>(a.x, a.ldx, row);
+        const void* H = row_of<RT>(a.hin, a.ldhin, row);
+        const void* DH = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
+        const float rstd = a.rstd[row];
+        float dot = 0.f;
+        for (int64_t u = threadIdx.x; u < units; u += blockDim.x) {
+            Unit<XT, V8> dy;
+            Unit<RT, V8> h;
+            dy.load(DY, u, a.cols);
+            h.load(H, u, a.cols);
+            float g[E], v[E], w[E];
+            dy.values(g);
+            h.values(v);
+            weights<V8>(a, u, w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) dot = fmaf(g[e] * w[e], v[e] * rstd, dot);
+        }
+        const float c = block_sum(dot, ssum[turn]) / (float)a.cols;
+        for (int64_t u = threadIdx.x; u < units; u += blockDim.x) {
+            Unit<XT, V8> dy;
+            Unit<RT, V8> h, dh;
+            dy.load(DY, u, a.cols);
+            h.load(H, u, a.cols);
+            if (DH) dh.load(DH, u, a.cols);
+            float g[E], v[E], w[E], up[E];
+            dy.values(g);
+            h.values(v);
+            weights<V8>(a, u, w);
+            if (DH) dh.values(up);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                g[e] = rstd * (g[e] * w[e] - v[e] * rstd * c);
+                if (DH) g[e] += up[e];
+            }
+            store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), u, a.cols, g);
+        }
+    }
+}
+
+// Launched before k_norm_backward_long, whose dx may overwrite dy or dh.
+template <int XT, int RT>
+__global__ void __launch_bounds__(128) k_norm_dw_long(const __grid_constant__ NormArgs a) {
+    pdl_wait();
+    pdl_launch_next();
+    const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (c >= a.cols) return;
+    float s = 0.f;
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y)
+        s = fmaf(ld1<XT>(row_of<XT>(a.x, a.ldx, row), c), ld1<RT>(row_of<RT>(a.hin, a.ldhin, row), c) * a.rstd[row], s);
+    a.part[(int64_t)blockIdx.y * a.cols + c] = s;
+}
+
+// dw[c] = sum of the n partial rows, in order in each of the block's 8 rows of
+// threads and then over those; added to what dw holds if accumulate.
+__global__ void __launch_bounds__(256) k_norm_dw(const float* part, int n, int64_t cols, void* dw, int dt,
+                                                 int accumulate) {
+    __shared__ float s[8][32];
+    pdl_wait();
+    pdl_launch_next();
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float t = 0.f;
+    if (c < cols)
+        for (int i = k; i < n; i += 8) t += part[(int64_t)i * cols + c];
+    s[k][lane] = t;
+    __syncthreads();
+    if (k || c >= cols) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t += s[i][lane];
+    if (accumulate) t += ld1_any(dw, c, dt);
+    st1_any(dw, c, t, dt);
+}
+
+// ---------------------------------------------------------------- choice of the launch
+template <int XT, int RT, bool V8>
+static const void* forward_fn(int nv) {
+    switch (nv) {
+        case 2: return (const void*)k_norm_forward<XT, RT, V8, 2>;
+        case 4: return (const void*)k_norm_forward<XT, RT, V8, 4>;
+        default: return (const void*)k_norm_forward_long<XT, RT, V8>;
+    }
+}
+template <int XT, int RT, bool V8>
+static const void* backward_fn(int nv) {
+    switch (nv) {
+        case 2: return (const void*)k_norm_backward<XT, RT, V8, 2>;
+        case 4: return (const void*)k_norm_backward<XT, RT, V8, 4>;
+        default: return (const void*)k_norm_backward_long<XT, RT, V8>;
+    }
+}
+template <int XT, int RT>
+static const void* pick(bool fwd, bool v8, int nv) {
+    if (fwd) return v8 ? forward_fn<XT, RT, true>(nv) : forward_fn<XT, RT, false>(nv);
+    return v8 ? backward_fn<XT, RT, true>(nv) : backward_fn<XT, RT, false>(nv);
+}
+static const void* norm_fn(bool fwd, int xt, int rt, bool v8, int nv) {
+    if (xt == ZERO_F32) return pick<ZERO_F32, ZERO_F32>(fwd, v8, nv);
+    if (xt == ZERO_BF16)
+        return rt == ZERO_F32 ? pick<ZERO_BF16, ZERO_F32>(fwd, v8, nv) : pick<ZERO_BF16, ZERO_BF16>(fwd, v8, nv);
+    return rt == ZERO_F32 ? pick<ZERO_F16, ZERO_F32>(fwd, v8, nv) : pick<ZERO_F16, ZERO_F16>(fwd, v8, nv);
+}
+
+// Units per thread (0 = the row does not fit the registers) and threads per row.
+static void shape_of(int64_t cols, bool v8, int* nv, int* threads) {
+    const int64_t per = v8 ? 8 : 4;
+    const int64_t units = v8 ? (cols + 7) / 8 : (cols + 127) / 128 * 32;
+    (void)per;
+    *nv = units <= 2 * NORM_THREADS ? 2 : units <= 4 * NORM_THREADS ? 4 : 0;
+    const int64_t t = *nv ? (units + *nv - 1) / *nv : NORM_THREADS;
+    *threads = (int)((t + 31) / 32 * 32);
+}
+
+static int check_weight(const zero_mat* w, int64_t cols, NormArgs& a) {
+    if (!w || !w->data) return ZERO_OK;
+    if (w->dtype != ZERO_F16 && w->dtype != ZERO_BF16 && w->dtype != ZERO_F32)
+        return fail(ZERO_EINVAL, "norm: unknown weight dtype");
+    if (!aligned(w->data, elem_size(w->dtype))) return fail(ZERO_EALIGN, "norm: weight not aligned to its element");
+    a.w = w->data;
+    a.wdt = w->dtype;
+    a.w_aligned = aligned(w->data, 16);
+    return ZERO_OK;
+}
+
+}  // namespace zdp
+
+using namespace zdp;
+
+extern "C" {
+
+int zero_norm_forward(const zero_mat* x, const zero_mat* residual, const zero_mat* weight, int64_t rows, int64_t cols,
+                      float eps, const zero_mat* h_out, const zero_mat* y, float* y_scale, int64_t scale_block,
+                      float* rstd, void* stream) {
+    if (rows < 0 || cols < 0) return fail(ZERO_EINVAL, "zero_norm_forward: negative rows or cols");
+    if (cols > NORM_MAX_COLS) return fail(ZERO_ELIMIT, "zero_norm_forward: more than 1048576 columns");
+    if (!(eps >= 0.f) || !(eps < INFINITY)) return fail(ZERO_EINVAL, "zero_norm_forward: eps must be finite and >= 0");
+    int rc = check_mat(x, rows, cols, FLOAT_TYPES, "zero_norm_forward: x");
+    if (rc == ZERO_OK) rc = check_mat(y, rows, cols, FLOAT_TYPES | 1u << ZERO_E4M3, "zero_norm_forward: y");
+    if (rc == ZERO_OK && residual) rc = check_mat(residual, rows, cols, FLOAT_TYPES, "zero_norm_forward: residual");
+    if (rc == ZERO_OK && h_out) rc = check_mat(h_out, rows, cols, FLOAT_TYPES, "zero_norm_forward: h_out");
+    if (rc != ZERO_OK) return rc;
+    const int rt = residual ? residual->dtype : x->dtype;
+    if (rt != x->dtype && rt != ZERO_F32)
+        return fail(ZERO_EINVAL, "zero_norm_forward: the residual is in x's type or fp32");
+    if (h_out && h_out->dtype != rt)
+        return fail(ZERO_EINVAL, "zero_norm_forward: h_out is in the residual's type (x's without one)");
+    const bool y8 = y->dtype == ZERO_E4M3;
+    if (!y8 && y->dtype != x->dtype) return fail(ZERO_EINVAL, "zero_norm_forward: y is in x's type or e4m3");
+    if (y8 && (scale_block != 0 && scale_block != 128))
+        return fail(ZERO_EINVAL, "zero_norm_forward: scale_block is 0 (a scale per row) or 128");
+    if (y8 && rows > 0 && cols > 0 && !y_scale) return fail(ZERO_EINVAL, "zero_norm_forward: e4m3 output needs y_scale");
+    if (!aligned(y_scale, 4) || !aligned(rstd, 4)) return fail(ZERO_EALIGN, "zero_norm_forward: y_scale or rstd not 4-byte aligned");
+    NormArgs a = {};
+    rc = check_weight(weight, cols, a);
+    if (rc != ZERO_OK || rows == 0 || cols == 0) return rc;
+    a.x = x->data;
+    a.ldx = x->ld;
+    a.r = residual ? residual->data : nullptr;
+    a.ldr = residual ? residual->ld : 0;
+    a.h = h_out ? h_out->data : nullptr;
+    a.ldh = h_out ? h_out->ld : 0;
+    a.y = y->data;
+    a.ldy = y->ld;
+    a.rows = rows;
+    a.cols = cols;
+    a.eps = eps;
+    a.y8 = y8;
+    a.block128 = y8 && scale_block == 128;
+    a.n_scale = a.block128 ? (cols + 127) / 128 : 1;
+    a.scale = y_scale;
+    a.rstd = rstd;
+    const bool y_ok = y8 ? aligned(y->data, 8) && (rows == 1 || y->ld % 8 == 0) : rows_aligned(*y, rows);
+    const bool v8 = cols % 8 == 0 && rows_aligned(*x, rows) && y_ok && (!residual || rows_aligned(*residual, rows)) &&
+                    (!h_out || rows_aligned(*h_out, rows));
+    int nv, threads;
+    shape_of(cols, v8, &nv, &threads);
+    void* args[] = {&a};
+    return cuda_fail(launch_after_previous(norm_fn(true, x->dtype, rt, v8, nv), (int)(rows < 1 << 30 ? rows : 1 << 30),
+                                           threads, args, 0, static_cast<cudaStream_t>(stream)),
+                     "zero_norm_forward launch");
+}
+
+size_t zero_norm_workspace_bytes(int64_t cols) {
+    return cols > 0 && cols <= NORM_MAX_COLS ? (size_t)NORM_MAX_GRID * (size_t)cols * 4 : 0;
+}
+
+int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* weight, int64_t rows, int64_t cols,
+                       const float* rstd, const zero_mat* dh, const zero_mat* dx, const zero_mat* dw, int accumulate,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    if (rows < 0 || cols < 0) return fail(ZERO_EINVAL, "zero_norm_backward: negative rows or cols");
+    if (cols > NORM_MAX_COLS) return fail(ZERO_ELIMIT, "zero_norm_backward: more than 1048576 columns");
+    int rc = check_mat(dy, rows, cols, FLOAT_TYPES, "zero_norm_backward: dy");
+    if (rc == ZERO_OK) rc = check_mat(h, rows, cols, FLOAT_TYPES, "zero_norm_backward: h");
+    if (rc == ZERO_OK) rc = check_mat(dx, rows, cols, FLOAT_TYPES, "zero_norm_backward: dx");
+    if (rc == ZERO_OK && dh) rc = check_mat(dh, rows, cols, FLOAT_TYPES, "zero_norm_backward: dh");
+    if (rc == ZERO_OK && dw) rc = check_mat(dw, 1, cols, FLOAT_TYPES, "zero_norm_backward: dw");
+    if (rc != ZERO_OK) return rc;
+    const int rt = h->dtype;
+    if (rt != dy->dtype && rt != ZERO_F32) return fail(ZERO_EINVAL, "zero_norm_backward: h is in dy's type or fp32");
+    if (dx->dtype != rt || (dh && dh->dtype != rt)) return fail(ZERO_EINVAL, "zero_norm_backward: dx and dh are in h's type");
+    if (rows > 0 && cols > 0 && (!rstd || !aligned(rstd, 4)))
+        return fail(ZERO_EINVAL, "zero_norm_backward: rstd NULL or not 4-byte aligned");
+    if (dw && cols > 0 && (!workspace || !aligned(workspace, 4) || workspace_bytes < zero_norm_workspace_bytes(cols)))
+        return fail(ZERO_EWORKSPACE, "zero_norm_backward: workspace smaller than zero_norm_workspace_bytes(cols)");
+    NormArgs a = {};
+    rc = check_weight(weight, cols, a);
+    if (rc != ZERO_OK || cols == 0) return rc;
+    const int sms = sm_count();
+    if (!sms) return ZERO_ECUDA;
+    a.x = dy->data;
+    a.ldx = dy->ld;
+    a.hin = h->data;
+    a.ldhin = h->ld;
+    a.r = dh ? dh->data : nullptr;
+    a.ldr = dh ? dh->ld : 0;
+    a.y = dx->data;
+    a.ldy = dx->ld;
+    a.rows = rows;
+    a.cols = cols;
+    a.rstd = const_cast<float*>(rstd);
+    a.part = dw ? static_cast<float*>(workspace) : nullptr;
+    const bool v8 = cols % 8 == 0 && rows_aligned(*dy, rows) && rows_aligned(*h, rows) && rows_aligned(*dx, rows) &&
+                    (!dh || rows_aligned(*dh, rows));
+    int nv, threads;
+    shape_of(cols, v8, &nv, &threads);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void* args[] = {&a};
+    int64_t g = 2 * (int64_t)sms;
+    if (g > NORM_MAX_GRID) g = NORM_MAX_GRID;
+    if (g > rows) g = rows;
+    const void* f = norm_fn(false, dy->dtype, rt, v8, nv);
+    int parts = (int)g;
+    if (nv == 0 && dw && rows > 0) {
+        // dw first: dx may be written over dy or dh
+        const int64_t chunks = (cols + 127) / 128;
+        int64_t shares = (8 * (int64_t)sms + chunks - 1) / chunks;
+        if (shares > NORM_MAX_GRID) shares = NORM_MAX_GRID;
+        if (shares > rows) shares = rows;
+        parts = (int)shares;
+        const dim3 grid((unsigned)chunks, (unsigned)shares);
+        const void* fw = dy->dtype == ZERO_F32 ? (const void*)k_norm_dw_long<ZERO_F32, ZERO_F32>
+                       : dy->dtype == ZERO_BF16 ? (rt == ZERO_F32 ? (const void*)k_norm_dw_long<ZERO_BF16, ZERO_F32>
+                                                                  : (const void*)k_norm_dw_long<ZERO_BF16, ZERO_BF16>)
+                                                : (rt == ZERO_F32 ? (const void*)k_norm_dw_long<ZERO_F16, ZERO_F32>
+                                                                  : (const void*)k_norm_dw_long<ZERO_F16, ZERO_F16>);
+        rc = cuda_fail(cudaLaunchKernel(fw, grid, dim3(128), args, 0, s), "zero_norm_backward dw launch");
+        if (rc != ZERO_OK) return rc;
+    }
+    if (rows > 0) {
+        if (nv == 0) g = rows < 1 << 30 ? rows : 1 << 30;
+        rc = cuda_fail(launch_after_previous(f, (int)g, threads, args, 0, s), "zero_norm_backward launch");
+        if (rc != ZERO_OK) return rc;
+    }
+    if (!dw) return ZERO_OK;
+    const float* part = a.part;
+    int n = rows > 0 ? parts : 0, dt = dw->dtype;
+    int64_t nc = cols;
+    void* out = dw->data;
+    void* wargs[] = {&part, &n, &nc, &out, &dt, &accumulate};
+    return cuda_fail(launch_after_previous((const void*)k_norm_dw, (int)((cols + 31) / 32), 256, wargs, 0, s),
+                     "zero_norm_backward dw reduction launch");
+}
+
+}  // extern "C"
