@@ -13,7 +13,9 @@ no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libzero_gb300.so")
@@ -75,6 +77,12 @@ class zero_mx4(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("layout", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+    @property
+    def tensors(self):
+        """The (data, scales) buffers that mx4() was given or made."""
+        data, scales, n = self.buffers
+        return (data, scales) if n is None else (data[:n], data[n:])
 
 
 assert ctypes.sizeof(zero_mat) == 24 and ctypes.sizeof(zero_mx4) == 48
@@ -154,8 +162,24 @@ def _ptr(x):
 def _stream(stream):
     if stream is not None:
         return _ptr(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
-    import torch
-    return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+    return _current_stream()
+
+
+_raw_stream = None
+
+
+def _current_stream():
+    """torch's current stream on the current device (None without a GPU), by the
+    calls under torch.cuda.current_stream(): its Stream object alone costs as
+    much as a small kernel (2.8 us on the host that drives a GB300)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        if not torch.cuda.is_available():
+            return None
+        torch.cuda.init()
+        _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    return _raw_stream[0](_raw_stream[1]())
 
 
 def _check(rc):
@@ -399,8 +423,21 @@ def read_stats(t) -> zero_stats:
 
 
 # ------------------------------------------------------------------ layer operators
+# Most calls of a layer take a few microseconds on the GPU, so the arguments
+# are marshalled with few Python operations: a tensor's zero_mat is packed as
+# bytes, whose address ctypes passes.
 _MAT_DTYPES = {"torch.float16": ZERO_F16, "torch.bfloat16": ZERO_BF16, "torch.float32": ZERO_F32,
                "torch.float8_e4m3fn": ZERO_E4M3, "torch.int32": ZERO_I32, "torch.int64": ZERO_I64}
+_codes = {}                                # torch dtype -> zero_dtype, filled as they are met
+_pack_mat = struct.Struct("=Qqii").pack
+
+
+def _code(dtype):
+    code = _MAT_DTYPES.get(str(dtype))
+    if code is None:
+        raise ZeroError(ZERO_EINVAL, f"no zero_mat of {dtype}")
+    _codes[dtype] = code
+    return code
 
 
 def mat(data, ld=None, dtype=None) -> zero_mat:
@@ -408,9 +445,7 @@ def mat(data, ld=None, dtype=None) -> zero_mat:
     one: a single row), or of an address with its row distance and dtype."""
     if not hasattr(data, "data_ptr"):
         return zero_mat(_ptr(data), ld or 0, dtype or 0, 0)
-    code = _MAT_DTYPES.get(str(data.dtype))
-    if code is None:
-        raise ZeroError(ZERO_EINVAL, f"no zero_mat of {data.dtype}")
+    code = _code(data.dtype)
     if data.dim() not in (1, 2) or (data.shape[-1] > 1 and data.stride(-1) != 1):
         raise ZeroError(ZERO_EINVAL, "a zero_mat has one or two dimensions and adjacent columns")
     m = zero_mat(data.data_ptr(), data.stride(0) if data.dim() == 2 else data.shape[0], code, 0)
@@ -418,36 +453,48 @@ def mat(data, ld=None, dtype=None) -> zero_mat:
     return m
 
 
-def _mat(x):
+def _mat(x, rows, cols, what):
+    """A matrix argument: None, a zero_mat, or a tensor of exactly rows x cols
+    (of one dimension: a single row) with adjacent columns."""
     if x is None:
         return None
-    return ctypes.byref(x if isinstance(x, zero_mat) else mat(x))
+    if isinstance(x, zero_mat):
+        return ctypes.byref(x)
+    code = _codes.get(x.dtype) or _code(x.dtype)
+    shape, step = x.shape, x.stride()
+    if len(shape) == 1:
+        shape, step = (1, shape[0]), (shape[0], step[0])
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ZeroError(ZERO_EINVAL, f"{what} is {tuple(x.shape)}, not {rows} x {cols}")
+    if step[1] != 1 and cols > 1:
+        raise ZeroError(ZERO_EINVAL, f"{what}: its columns are not adjacent")
+    if not x.is_cuda:
+        raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU")
+    return _pack_mat(x.data_ptr(), step[0], code, 0)
 
 
-def _shape(x, rows, cols, what):
-    """A tensor argument holds the rows x cols that the call will touch."""
+def _vec(x, n, what):
+    """An array argument: None, an address, or a tensor of at least n contiguous
+    fp32 values."""
+    if x is None or isinstance(x, int):
+        return x
     if hasattr(x, "data_ptr"):
-        have = tuple(x.shape) if x.dim() == 2 else (1, x.shape[0]) if x.dim() == 1 else None
-        if have != (rows, cols):
-            raise ZeroError(ZERO_EINVAL, f"{what} is {tuple(x.shape)}, not {rows} x {cols}")
-
-
-def _count(x, n, what):
-    """A tensor argument is a contiguous fp32 array of at least n values."""
-    if hasattr(x, "data_ptr") and (x.numel() < n or str(x.dtype) != "torch.float32" or not x.is_contiguous()):
-        raise ZeroError(ZERO_EINVAL, f"{what} must be {n} contiguous float32 values")
+        if x.numel() < n or (_codes.get(x.dtype) or _code(x.dtype)) != ZERO_F32 or not x.is_contiguous():
+            raise ZeroError(ZERO_EINVAL, f"{what} must be {n} contiguous float32 values")
+        if not x.is_cuda:
+            raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU")
+        return x.data_ptr()
+    return int(x)
 
 
 def zero_norm_forward(x, residual, weight, rows, cols, eps, h_out, y, y_scale, scale_block, rstd, stream=None):
     """h = x + residual, y = RMSnorm(h) * weight per row; y in x's type, or
     float8_e4m3fn with a scale per row (scale_block 0) or per 128 columns."""
-    for t, what in ((x, "x"), (residual, "residual"), (h_out, "h_out"), (y, "y")):
-        _shape(t, rows, cols, what)
-    _shape(weight, 1, cols, "weight")
-    _count(rstd, rows, "rstd")
-    _count(y_scale, rows * (-(-cols // scale_block) if scale_block > 0 else 1), "y_scale")
-    _check(lib.zero_norm_forward(_mat(x), _mat(residual), _mat(weight), rows, cols, eps, _mat(h_out), _mat(y),
-                                 _ptr(y_scale), scale_block, _ptr(rstd), _stream(stream)))
+    n = rows * (-(-cols // scale_block) if scale_block > 0 else 1)
+    _check(lib.zero_norm_forward(_mat(x, rows, cols, "x"), _mat(residual, rows, cols, "residual"),
+                                 _mat(weight, 1, cols, "weight"), rows, cols, eps, _mat(h_out, rows, cols, "h_out"),
+                                 _mat(y, rows, cols, "y"), _vec(y_scale, n, "y_scale"), scale_block,
+                                 _vec(rstd, rows, "rstd"), _stream(stream)))
 
 
 def zero_norm_workspace_bytes(cols):
@@ -457,42 +504,33 @@ def zero_norm_workspace_bytes(cols):
 def zero_norm_backward(dy, h, weight, rows, cols, rstd, dh, dx, dw, accumulate, workspace, workspace_bytes,
                        stream=None):
     """dx (of x and residual alike) and dw of zero_norm_forward."""
-    for t, what in ((dy, "dy"), (h, "h"), (dh, "dh"), (dx, "dx")):
-        _shape(t, rows, cols, what)
-    for t, what in ((weight, "weight"), (dw, "dw")):
-        _shape(t, 1, cols, what)
-    _count(rstd, rows, "rstd")
-    _check(lib.zero_norm_backward(_mat(dy), _mat(h), _mat(weight), rows, cols, _ptr(rstd), _mat(dh), _mat(dx),
-                                  _mat(dw), int(accumulate), _ptr(workspace), workspace_bytes, _stream(stream)))
-
-
-def _distill_shapes(logits, rows, cols, ids, teacher, k, teacher_lse, row_weight, lse, dlogits):
-    for t, n, what in ((logits, cols, "logits"), (dlogits, cols, "dlogits"), (ids, k, "ids"), (teacher, k, "teacher")):
-        _shape(t, rows, n, what)
-    for t, what in ((teacher_lse, "teacher_lse"), (row_weight, "row_weight"), (lse, "lse")):
-        _count(t, rows, what)
+    _check(lib.zero_norm_backward(_mat(dy, rows, cols, "dy"), _mat(h, rows, cols, "h"),
+                                  _mat(weight, 1, cols, "weight"), rows, cols, _vec(rstd, rows, "rstd"),
+                                  _mat(dh, rows, cols, "dh"), _mat(dx, rows, cols, "dx"), _mat(dw, 1, cols, "dw"),
+                                  int(accumulate), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def zero_distill_loss(logits, rows, cols, ids, teacher, k, teacher_lse, temperature, row_weight, grad_scale, chain_dev,
                       loss, lse, dlogits, stream=None):
     """The rows' losses against the teacher's k logits and, with dlogits, the
     gradient, scaled by grad_scale and by the loss scale of the device chain."""
-    _distill_shapes(logits, rows, cols, ids, teacher, k, teacher_lse, row_weight, lse, dlogits)
-    _count(loss, rows, "loss")
-    _check(lib.zero_distill_loss(_mat(logits), rows, cols, _mat(ids), _mat(teacher), k, _ptr(teacher_lse), temperature,
-                                 _ptr(row_weight), grad_scale, _ptr(chain_dev), _ptr(loss), _ptr(lse), _mat(dlogits),
-                                 _stream(stream)))
+    _check(lib.zero_distill_loss(_mat(logits, rows, cols, "logits"), rows, cols, _mat(ids, rows, k, "ids"),
+                                 _mat(teacher, rows, k, "teacher"), k, _vec(teacher_lse, rows, "teacher_lse"),
+                                 temperature, _vec(row_weight, rows, "row_weight"), grad_scale, _ptr(chain_dev),
+                                 _vec(loss, rows, "loss"), _vec(lse, rows, "lse"),
+                                 _mat(dlogits, rows, cols, "dlogits"), _stream(stream)))
 
 
 def zero_distill_backward(logits, rows, cols, ids, teacher, k, teacher_lse, temperature, row_weight, grad_scale,
                           chain_dev, lse, dlogits, stream=None):
     """The gradient alone, from the lse that zero_distill_loss stored."""
-    _distill_shapes(logits, rows, cols, ids, teacher, k, teacher_lse, row_weight, lse, dlogits)
-    _check(lib.zero_distill_backward(_mat(logits), rows, cols, _mat(ids), _mat(teacher), k, _ptr(teacher_lse),
-                                     temperature, _ptr(row_weight), grad_scale, _ptr(chain_dev), _ptr(lse),
-                                     _mat(dlogits), _stream(stream)))
+    _check(lib.zero_distill_backward(_mat(logits, rows, cols, "logits"), rows, cols, _mat(ids, rows, k, "ids"),
+                                     _mat(teacher, rows, k, "teacher"), k, _vec(teacher_lse, rows, "teacher_lse"),
+                                     temperature, _vec(row_weight, rows, "row_weight"), grad_scale, _ptr(chain_dev),
+                                     _vec(lse, rows, "lse"), _mat(dlogits, rows, cols, "dlogits"), _stream(stream)))
 
 
+@functools.lru_cache(maxsize=1024)
 def zero_mx4_bytes(rows, cols, layout=ZERO_MX4_TILES):
     """(ld, data bytes, scale bytes) of a 4-bit matrix."""
     ld, data, scales = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
@@ -504,19 +542,20 @@ def mx4(rows, cols, data=None, scales=None, layout=ZERO_MX4_TILES, device=None) 
     """A zero_mx4 over given buffers (torch uint8 tensors or addresses), or over
     new ones on `device`; rows follow one another without gaps."""
     ld, n_data, n_scales = zero_mx4_bytes(rows, cols, layout)
-    if data is None or scales is None:
+    if data is None and scales is None:
         import torch
-        buf = torch.empty((n_data if data is None else 0) + (n_scales if scales is None else 0), dtype=torch.uint8,
-                          device=device)
-        if data is None:
-            data, buf = buf[:n_data], buf[n_data:]
-        if scales is None:
-            scales = buf
+        buf = torch.empty(n_data + n_scales, dtype=torch.uint8, device=device)
+        at = buf.data_ptr()
+        m = zero_mx4(at, at + n_data, rows, cols, ld, layout, 0)
+        m.buffers = (buf, None, n_data)    # kept alive with the argument
+        return m
+    if data is None or scales is None:
+        raise ZeroError(ZERO_EINVAL, "data and scales: both or neither")
     for t, n, what in ((data, n_data, "data"), (scales, n_scales, "scales")):
         if hasattr(t, "data_ptr") and (t.numel() * t.element_size() < n or not t.is_contiguous()):
             raise ZeroError(ZERO_EINVAL, f"{what} must be at least {n} contiguous bytes")
     m = zero_mx4(_ptr(data), _ptr(scales), rows, cols, ld, layout, 0)
-    m.tensors = (data, scales)             # kept alive with the argument
+    m.buffers = (data, scales, None)
     return m
 
 
@@ -527,15 +566,13 @@ def _mx4(x):
 def zero_mx4_quantize(src, rows, cols, out, out_t, stream=None):
     """src to 4 bits along its rows (out) and along its columns (out_t: cols x
     rows); either may be None."""
-    _shape(src, rows, cols, "src")
-    _check(lib.zero_mx4_quantize(_mat(src), rows, cols, _mx4(out), _mx4(out_t), _stream(stream)))
+    _check(lib.zero_mx4_quantize(_mat(src, rows, cols, "src"), rows, cols, _mx4(out), _mx4(out_t), _stream(stream)))
 
 
 def zero_mx4_dequantize(src, dst, stream=None):
     """The values of a 4-bit matrix in dst's type."""
-    if src is not None:
-        _shape(dst, src.rows, src.cols, "dst")
-    _check(lib.zero_mx4_dequantize(_mx4(src), _mat(dst), _stream(stream)))
+    d = None if src is None else _mat(dst, src.rows, src.cols, "dst")
+    _check(lib.zero_mx4_dequantize(_mx4(src), d, _stream(stream)))
 
 
 def zero_mx4_tile_scales(src, dst, stream=None):
@@ -546,6 +583,5 @@ def zero_mx4_tile_scales(src, dst, stream=None):
 def zero_mx4_matmul(a, b, alpha, d, status, stream=None):
     """d = alpha a b^T of two 4-bit matrices; status: device int32 (zero-filled by
     the caller), bit 0 set if a wait ran out."""
-    if a is not None and b is not None:
-        _shape(d, a.rows, b.rows, "d")
-    _check(lib.zero_mx4_matmul(_mx4(a), _mx4(b), alpha, _mat(d), _ptr(status), _stream(stream)))
+    m = None if a is None or b is None else _mat(d, a.rows, b.rows, "d")
+    _check(lib.zero_mx4_matmul(_mx4(a), _mx4(b), alpha, m, _ptr(status), _stream(stream)))

@@ -20,7 +20,9 @@
 namespace zdp {
 
 constexpr int DISTILL_THREADS = 512;
-constexpr int DISTILL_VECS = 8;          // vectors a thread keeps
+constexpr int DISTILL_BLOCKS = 2;        // resident blocks of a multiprocessor
+constexpr int DISTILL_BATCH = 8;         // vectors a thread has in flight
+constexpr int DISTILL_KEEP = 8;          // most vectors a thread keeps in shared memory (a multiple of the batch)
 constexpr int DISTILL_CLUSTER = 8;       // most blocks that share a row (the portable cluster size)
 constexpr int DISTILL_MAX_K = 1024;
 
@@ -31,14 +33,15 @@ struct DistillArgs {
     float *loss, *lse;
     const zero_chain* chain;
     int64_t ldz, lddz, ldt, ldi, rows, cols;
-    int k, t_dt, id64, split;
+    int k, t_dt, id64, split, keep;
     float k2, temperature, grad_scale;   // k2 = log2(e) / T
 };
 
-// One entry of the row's teacher list, in shared memory.
+// One entry of the row's teacher list, in shared memory: the column (-1: no
+// entry), the teacher's logit times k2, and the student's logit.
 struct Entry {
-    int id;          // -1: no entry
-    float p, lp, z;  // p_i (before the division by the sum: e_i), log2 p_i, and the student's logit
+    int id;
+    float t, z;
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -47,89 +50,98 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// The row as 16-byte vectors: vector i holds elements i W - off .. + W - 1, so
-// that every vector but the first and the last is whole and aligned wherever
-// the row starts.
+__device__ __forceinline__ uint64_t exp2_2(uint64_t v) {
+    const float2 x = unpack2(v);
+    return pack2(exp2_fast(x.x), exp2_fast(x.y));
+}
+
+// A row between 16-byte boundaries: `n` whole aligned vectors of W elements
+// from element `head`, and fewer than W elements at either end (the edges).
 template <int DT>
 struct RowVec {
-    static constexpr int W = 16 / Elem<DT>::SIZE;
-    static constexpr uint32_t NEG_INF = DT == ZERO_F32 ? 0xFF800000u : DT == ZERO_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
-    const char* base;       // the row's first element
-    int off;                // elements between the 16-byte boundary at or before it and it
-    int64_t cols, n;
-    __device__ __forceinline__ RowVec(const void* p, int64_t cols_)
-        : base(static_cast<const char*>(p)), cols(cols_) {
-        off = (int)(reinterpret_cast<uintptr_t>(p) & 15u) / Elem<DT>::SIZE;
-        n = (cols + off + W - 1) / W;
+    static constexpr int W = 16 / Elem<DT>::SIZE, PAIRS = W / 2;
+    const char *base, *vec;   // element 0, vector 0
+    int head, n, cols;
+    __device__ __forceinline__ RowVec(const void* p, int cols_) : base(static_cast<const char*>(p)), cols(cols_) {
+        const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15u) / Elem<DT>::SIZE;
+        head = min(off ? W - off : 0, cols);
+        n = (cols - head) / W;
+        vec = base + (int64_t)head * Elem<DT>::SIZE;
     }
-    __device__ __forceinline__ bool whole(int64_t i) const { return (i > 0 || off == 0) && (i + 1) * W - off <= cols; }
-    __device__ __forceinline__ uint4 load(int64_t i) const {
-        const int64_t c0 = i * W - off;
-        if (whole(i)) return __ldcs(reinterpret_cast<const uint4*>(base + c0 * Elem<DT>::SIZE));
-        uint32_t u[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+    // the e-th edge element's column, -1 past the last; there are at most 2 (W - 1) <= 14
+    __device__ __forceinline__ int edge(int e) const {
+        const int c = e < head ? e : e + n * W;
+        return c < cols ? c : -1;
+    }
+    // which of the row's vectors holds column c (-1: an edge)
+    __device__ __forceinline__ int vector_of(int c) const {
+        const int v = c < head ? -1 : (c - head) / W;
+        return v < n ? v : -1;
+    }
+    // plain loads (the gradient may be in the logits' place): the first walk's lines should stay for the second
+    __device__ __forceinline__ uint4 load(int i) const { return reinterpret_cast<const uint4*>(vec)[i]; }
+    __device__ __forceinline__ uint4 load_last(int i) const { return __ldcs(reinterpret_cast<const uint4*>(vec) + i); }
+    // elements 2 q and 2 q + 1
+    static __device__ __forceinline__ uint64_t pair(const uint4& r, int q) {
+        const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+        if constexpr (DT == ZERO_F32) return pack2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]));
+        else if constexpr (DT == ZERO_BF16) return pack2(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xFFFF0000u));
+        else return pack2(Half16<DT>::widen(u[q] & 0xFFFFu), Half16<DT>::widen(u[q] >> 16));
+    }
+    static __device__ __forceinline__ float top(const uint4& r) {
+        if constexpr (DT == ZERO_F32) {
+            return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+        } else if constexpr (DT == ZERO_BF16) {
+            const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
+            const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+            return fmaxf(__low2float(m), __high2float(m));
+        } else {
+            const __half2* h = reinterpret_cast<const __half2*>(&r);
+            const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+            return fmaxf(__low2float(m), __high2float(m));
+        }
+    }
+    // sum of 2^(z k - m k) of a vector's pairs, added to s
+    static __device__ __forceinline__ uint64_t sum(const uint4& r, uint64_t k, uint64_t neg_mk, uint64_t s) {
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            const int64_t c = c0 + e;
-            if (c < 0 || c >= cols) continue;
+        for (int q = 0; q < PAIRS; ++q) s = add2(s, exp2_2(fma2(pair(r, q), k, neg_mk)));
+        return s;
+    }
+    // g 2^(z k - m k) of a vector, rounded and stored
+    static __device__ __forceinline__ void grad(char* dst, bool aligned16, const uint4& r, uint64_t k, uint64_t neg_mk,
+                                                uint64_t g) {
+        float2 v[PAIRS];
+#pragma unroll
+        for (int q = 0; q < PAIRS; ++q) v[q] = unpack2(mul2(exp2_2(fma2(pair(r, q), k, neg_mk)), g));
+        put(dst, aligned16, v);
+    }
+    static __device__ __forceinline__ void put(char* dst, bool aligned16, const float2 (&v)[PAIRS]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int q = 0; q < PAIRS; ++q) {
             if constexpr (DT == ZERO_F32) {
-                u[e] = reinterpret_cast<const uint32_t*>(base)[c];
+                u[2 * q] = __float_as_uint(v[q].x);
+                u[2 * q + 1] = __float_as_uint(v[q].y);
             } else {
-                const uint32_t h = reinterpret_cast<const uint16_t*>(base)[c];
-                u[e / 2] = e % 2 ? (u[e / 2] & 0xFFFFu) | h << 16 : (u[e / 2] & 0xFFFF0000u) | h;
+                u[q] = Half16<DT>::narrow2(v[q].x, v[q].y);
             }
         }
-        return make_uint4(u[0], u[1], u[2], u[3]);
-    }
-    __device__ __forceinline__ void store(void* row, bool same_phase, int64_t i, const float (&v)[W]) const {
-        const int64_t c0 = i * W - off;
-        if (same_phase && whole(i)) {
-            uint4 o;
-            if constexpr (DT == ZERO_F32)
-                o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                               __float_as_uint(v[3]));
-            else
-                o = make_uint4(Half16<DT>::narrow2(v[0], v[1]), Half16<DT>::narrow2(v[2], v[3]),
-                               Half16<DT>::narrow2(v[4], v[5]), Half16<DT>::narrow2(v[6], v[7]));
-            __stcs(reinterpret_cast<uint4*>(static_cast<char*>(row) + c0 * Elem<DT>::SIZE), o);
-            return;
-        }
+        if (aligned16) {
+            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(u[0], u[1], u[2], u[3]));
+        } else {
 #pragma unroll
-        for (int e = 0; e < W; ++e)
-            if (c0 + e >= 0 && c0 + e < cols) st1<DT>(row, c0 + e, v[e]);
+            for (int e = 0; e < W; ++e) {
+                if constexpr (DT == ZERO_F32) reinterpret_cast<uint32_t*>(dst)[e] = u[e];
+                else reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
+            }
+        }
     }
 };
 
-template <int DT>
-__device__ __forceinline__ void widen(const uint4& r, float (&v)[RowVec<DT>::W]) {
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        if constexpr (DT == ZERO_F32) {
-            v[q] = __uint_as_float(u[q]);
-        } else {
-            v[2 * q] = Half16<DT>::widen(u[q] & 0xFFFFu);
-            v[2 * q + 1] = Half16<DT>::widen(u[q] >> 16);
-        }
-    }
-}
-
-// Two values of the block at once: their maxima or sums, in every thread.
-template <bool MAX>
-__device__ __forceinline__ float2 block_pair(float x, float y, float2* s) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float a = __shfl_xor_sync(0xFFFFFFFFu, x, o), b = __shfl_xor_sync(0xFFFFFFFFu, y, o);
-        x = MAX ? fmaxf(x, a) : x + a;
-        y = MAX ? fmaxf(y, b) : y + b;
-    }
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(x, y);
-    __syncthreads();
-    float2 t = s[0];
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) {
-        t.x = MAX ? fmaxf(t.x, s[w].x) : t.x + s[w].x;
-        t.y = MAX ? fmaxf(t.y, s[w].y) : t.y + s[w].y;
-    }
-    return t;
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
 }
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -145,183 +157,211 @@ __device__ __forceinline__ void store_remote(float2* local, int rank, float2 v) 
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(r), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// RES: the block's share of the row stays in registers (DISTILL_VECS vectors a
-// thread); otherwise the row is walked twice.  BWD: the row's log-sum-exp is
-// given (lse_in) and nothing crosses the cluster.
-template <int DT, bool RES, bool BWD>
-__global__ void __launch_bounds__(DISTILL_THREADS, 2) k_distill(const __grid_constant__ DistillArgs a) {
-    constexpr int W = RowVec<DT>::W;
-    extern __shared__ Entry entry[];
-    __shared__ float2 red[2][16], peer[DISTILL_CLUSTER];
+// A maximum and the sum of 2^(x - it) of several parts, one a lane and step,
+// to those of the whole.  A part whose maximum is -inf has a sum of 0, or of
+// NaN, which is kept (a maximum drops it).
+__device__ __forceinline__ float2 merge(const float2* part, int n) {
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, part[i].x);
+    m = warp_max(m);
+    float s = 0.f;
+    for (int i = lane; i < n; i += 32) {
+        const float2 p = part[i];
+        s += p.x == -INFINITY ? p.y : p.y * exp2f(p.x - m);
+    }
+    return make_float2(m, warp_sum(s));
+}
+
+// BWD: the row's log-sum-exp is given (lse_in), so that only the gradient is
+// walked and nothing crosses the cluster.
+//
+// Every warp reduces its own part to a maximum and a sum and sends the pair to
+// all blocks of the cluster: one barrier, and each warp merges all pairs.
+template <int DT, bool BWD>
+__global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(const __grid_constant__ DistillArgs a) {
+    using R = RowVec<DT>;
+    constexpr int MAX_WARPS = DISTILL_THREADS / 32, U = DISTILL_BATCH;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    uint4* kept = reinterpret_cast<uint4*>(dyn);            // [keep][T]
+    __shared__ float2 zpart[DISTILL_CLUSTER * MAX_WARPS], tpart[MAX_WARPS];
     pdl_wait();
     pdl_launch_next();
-    const int C = a.split, rank = (int)(blockIdx.x % (unsigned)C);
-    const int64_t row = blockIdx.x / (unsigned)C;
+    Entry* entry = reinterpret_cast<Entry*>(dyn + (size_t)a.keep * blockDim.x * 16);
+    const int C = a.split, T = blockDim.x, rank = C == 1 ? 0 : (int)(blockIdx.x % (unsigned)C);
+    const int64_t row = C == 1 ? blockIdx.x : blockIdx.x / (unsigned)C;
     if (!BWD && C > 1) cluster_arrive();          // this block runs: its shared memory may be written
-    const RowVec<DT> rv(static_cast<const char*>(a.z) + row * a.ldz * Elem<DT>::SIZE, a.cols);
-    const int64_t step = (int64_t)C * blockDim.x, first = (int64_t)rank * blockDim.x + threadIdx.x;
+    const R rv(static_cast<const char*>(a.z) + row * a.ldz * Elem<DT>::SIZE, (int)a.cols);
+    const int step = C * T, first = rank * T + threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // whether column c is written by this block (the edges are the first block's)
+    auto mine = [&](int c) {
+        if (C == 1) return true;
+        const int v = rv.vector_of(c);
+        return (v < 0 ? 0 : v / T % C) == rank;
+    };
 
-    uint4 raw[RES ? DISTILL_VECS : 1];
-    if constexpr (RES && !BWD) {
-#pragma unroll
-        for (int j = 0; j < DISTILL_VECS; ++j)
-            if (first + j * step < rv.n) raw[j] = rv.load(first + j * step);
-    }
+    // the edges: one element in each of the first lanes of the row's first block
+    const int edge = rank == 0 && threadIdx.x < 16 ? rv.edge(threadIdx.x) : -1;
+    const float edge_z = edge >= 0 ? ld1<DT>(rv.base, edge) : -INFINITY;
     // the teacher's entries, and the student's logits at them (read before any
     // gradient is written, which may be in their place)
     float tmax = -INFINITY;
-    for (int i = threadIdx.x; i < a.k; i += blockDim.x) {
+    for (int i = threadIdx.x; i < a.k; i += T) {
         const int64_t at = row * a.ldi + i;
         const int64_t id = a.id64 ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
         const float t = ld1_any(a.t, row * a.ldt + i, a.t_dt);
         const bool have = id >= 0 && id < a.cols && t != -INFINITY;
-        Entry en;
-        en.id = have ? (int)id : -1;
-        en.lp = have ? t * a.k2 : -INFINITY;
+        Entry en = {have ? (int)id : -1, have ? t * a.k2 : -INFINITY, 0.f};
         // the backward pass alone has no barrier between its blocks: it reads what it itself will write
-        const bool mine = have && (!BWD || (int)((id + rv.off) / W / blockDim.x % C) == rank);
-        en.z = mine ? ld1<DT>(rv.base, id) : 0.f;
-        en.p = 0.f;
+        if (have && (!BWD || mine(en.id))) en.z = ld1<DT>(rv.base, en.id);
         entry[i] = en;
-        if (have) tmax = fmaxf(tmax, t != t ? 0.f : en.lp);     // a NaN entry makes the sum NaN, not the row empty
+        if (have) tmax = fmaxf(tmax, t != t ? 0.f : en.t);      // a NaN entry makes the sum NaN, not the row empty
     }
     const float k2 = a.k2;
-    float zmax = -INFINITY;
+    const uint64_t kk = pack2(k2, k2);
+    float m = -INFINITY, s = 0.f;                 // this thread's m k and sum
     if constexpr (!BWD) {
-        if constexpr (RES) {
-#pragma unroll
-            for (int j = 0; j < DISTILL_VECS; ++j)
-                if (first + j * step < rv.n) {
-                    float v[W];
-                    widen<DT>(raw[j], v);
-#pragma unroll
-                    for (int e = 0; e < W; ++e) zmax = fmaxf(zmax, v[e]);
-                }
-        } else {
-            for (int64_t i = first; i < rv.n; i += step) {
-                float v[W];
-                widen<DT>(rv.load(i), v);
-#pragma unroll
-                for (int e = 0; e < W; ++e) zmax = fmaxf(zmax, v[e]);
+        uint64_t s2 = 0;
+        auto take = [&](float t) {                // bring the sum to a larger maximum
+            if (t > m) {
+                const float f = exp2_fast(m - t);
+                s2 = mul2(s2, pack2(f, f));
+                m = t;
             }
-        }
-    }
-    float2 top = block_pair<true>(zmax, tmax, red[0]);
-    // a share that holds nothing but -inf adds nothing: its exponents are taken from 0
-    const float own_mk = top.x == -INFINITY ? 0.f : top.x * k2;
-    float zsum = 0.f, tsum = 0.f;
-    if constexpr (!BWD) {
-        if constexpr (RES) {
+        };
+        auto neg = [&] { return m == -INFINITY ? 0.f : -m; };   // nothing but -inf so far: exponents from 0
+        int i = first, j = 0;
+        for (; i + (U - 1) * step < rv.n; i += U * step, j += U) {
+            uint4 r[U];
+            if (j < a.keep) {
 #pragma unroll
-            for (int j = 0; j < DISTILL_VECS; ++j)
-                if (first + j * step < rv.n) {
-                    float v[W];
-                    widen<DT>(raw[j], v);
+                for (int u = 0; u < U; ++u) r[u] = rv.load_last(i + u * step);
 #pragma unroll
-                    for (int e = 0; e < W; ++e) zsum += exp2_fast(fmaf(v[e], k2, -own_mk));
-                }
-        } else {
-            for (int64_t i = first; i < rv.n; i += step) {
-                float v[W];
-                widen<DT>(rv.load(i), v);
+                for (int u = 0; u < U; ++u) kept[(j + u) * T + threadIdx.x] = r[u];
+            } else {
 #pragma unroll
-                for (int e = 0; e < W; ++e) zsum += exp2_fast(fmaf(v[e], k2, -own_mk));
+                for (int u = 0; u < U; ++u) r[u] = rv.load(i + u * step);
             }
+            float t = R::top(r[0]);
+#pragma unroll
+            for (int u = 1; u < U; ++u) t = fmaxf(t, R::top(r[u]));
+            take(t * k2);
+            const uint64_t nm = pack2(neg(), neg());
+#pragma unroll
+            for (int u = 0; u < U; ++u) s2 = R::sum(r[u], kk, nm, s2);
         }
+        for (; i < rv.n; i += step, ++j) {
+            const uint4 r = rv.load(i);
+            if (j < a.keep) kept[j * T + threadIdx.x] = r;
+            take(R::top(r) * k2);
+            s2 = R::sum(r, kk, pack2(neg(), neg()), s2);
+        }
+        if (edge >= 0) {
+            take(edge_z * k2);
+            s2 = add2(s2, pack2(exp2_fast(fmaf(edge_z, k2, neg())), 0.f));
+        }
+        const float2 p = unpack2(s2);
+        s = p.x + p.y;
+        const float wm = warp_max(m);
+        s = warp_sum(m == -INFINITY ? s : s * exp2f(m - wm));
+        m = wm;
     }
-    // with the teacher's own log-sum-exp the entries' exponents are taken from it
-    const float tm = a.t_lse ? a.t_lse[row] * 1.4426950408889634f : top.y;
-    for (int i = threadIdx.x; i < a.k; i += blockDim.x)
-        if (entry[i].id >= 0) tsum += (entry[i].p = exp2f(entry[i].lp - tm));
-    float2 sum = block_pair<false>(zsum, tsum, red[1]);
-    const bool none = top.y == -INFINITY;           // no teacher entry in the row
-    const float pscale = a.t_lse ? 1.f : 1.f / sum.y, P = none ? 0.f : sum.y * pscale;
-    const float lpoff = tm + (a.t_lse ? 0.f : log2f(sum.y));
-
-    // m k and the sum of the whole row
-    float mk, total;
+    {
+        const float tm = warp_max(tmax);
+        float ts = 0.f;
+        if (warp * 32 < a.k)
+            for (int i = threadIdx.x; i < a.k; i += T)
+                if (entry[i].id >= 0) ts += exp2f(entry[i].t - tm);
+        ts = warp_sum(ts);
+        if (lane == 0) tpart[warp] = make_float2(tm, ts);
+    }
+    float mk, total;                              // m k and the sum over the whole row
     if constexpr (BWD) {
+        __syncthreads();
         mk = a.lse_in[row] * 1.4426950408889634f;
         total = 1.f;
-    } else if (C == 1) {
-        mk = own_mk;
-        total = sum.x;
     } else {
-        cluster_wait();                            // every block of the cluster runs
-        if (threadIdx.x < (unsigned)C)
-            store_remote(&peer[rank], threadIdx.x, make_float2(top.x == -INFINITY ? -INFINITY : own_mk, sum.x));
-        __syncwarp();
-        cluster_arrive();
-        cluster_wait();                            // every block's pair is here; no block leaves before its last arrives
-        mk = -INFINITY;
-        for (int c = 0; c < C; ++c) mk = fmaxf(mk, peer[c].x);
-        total = 0.f;
-        for (int c = 0; c < C; ++c)
-            total += peer[c].x == -INFINITY ? 0.f : peer[c].y * exp2f(peer[c].x - mk);
-        if (mk == -INFINITY) mk = 0.f;
-        for (int c = 0; c < C; ++c)                // a maximum drops NaN; the sums keep it
-            if (peer[c].y != peer[c].y) total = peer[c].y;
+        const int nw = T >> 5;
+        if (C == 1) {
+            if (lane == 0) zpart[warp] = make_float2(m, s);
+            __syncthreads();
+        } else {
+            cluster_wait();                        // every block of the cluster runs
+            if (lane < C) store_remote(&zpart[rank * nw + warp], lane, make_float2(m, s));
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();                        // every pair is here; no block leaves before its last arrives
+        }
+        const float2 whole = merge(zpart, C * nw);
+        mk = whole.x == -INFINITY ? 0.f : whole.x;
+        total = whole.y;
     }
-    const float lg = BWD ? 0.f : log2f(total);
+    const float2 tw = merge(tpart, T >> 5);
+    const bool none = tw.x == -INFINITY;          // no teacher entry in the row
+    // p_i = 2^(t_i - tm) pscale
+    const float tl = a.t_lse ? a.t_lse[row] * 1.4426950408889634f : 0.f;
+    const float tm = tw.x, pscale = a.t_lse ? exp2f(tm - tl) : 1.f / tw.y, P = none ? 0.f : tw.y * pscale;
     const float w = a.w ? a.w[row] : 1.f;
     const bool dead = none || w == 0.f;
-    if (!BWD && a.lse && rank == 0 && threadIdx.x == 0) a.lse[row] = (mk + lg) * 0.6931471805599453f;
-    if (!BWD && a.loss && rank == 0) {
-        float l = 0.f;
-        if (!dead)
-            for (int i = threadIdx.x; i < a.k; i += blockDim.x) {
-                const Entry en = entry[i];
-                if (en.id >= 0 && en.p != 0.f)
-                    l += en.p * pscale * ((en.lp - lpoff) - (fmaf(en.z, k2, -mk) - lg));
-            }
-        const float2 s = block_pair<false>(l, 0.f, red[0]);
-        if (threadIdx.x == 0)
-            a.loss[row] = dead ? 0.f : s.x * 0.6931471805599453f * a.temperature * a.temperature * w;
+    if constexpr (!BWD) {
+        const float lg = log2f(total);
+        if (a.lse && rank == 0 && threadIdx.x == 0) a.lse[row] = (mk + lg) * 0.6931471805599453f;
+        if (a.loss && rank == 0 && warp == 0) {
+            const float lpoff = a.t_lse ? tl : tm + log2f(tw.y);
+            float l = 0.f;
+            if (!dead)
+                for (int i = lane; i < a.k; i += 32) {
+                    const Entry en = entry[i];
+                    const float p = en.id >= 0 ? exp2f(en.t - tm) * pscale : 0.f;
+                    if (p != 0.f) l += p * ((en.t - lpoff) - (fmaf(en.z, k2, -mk) - lg));
+                }
+            l = warp_sum(l);
+            if (lane == 0) a.loss[row] = dead ? 0.f : l * 0.6931471805599453f * a.temperature * a.temperature * w;
+        }
     }
     if (!a.dz) return;
     float coef = w * a.temperature * a.grad_scale;
     if (a.chain) coef *= (float)a.chain->loss_scale;
-    const float g = dead ? 0.f : coef * P / total;
     char* drow = static_cast<char*>(a.dz) + row * a.lddz * Elem<DT>::SIZE;
-    const bool same = ((reinterpret_cast<uintptr_t>(drow) ^ reinterpret_cast<uintptr_t>(rv.base)) & 15u) == 0;
-    if constexpr (RES && !BWD) {
-#pragma unroll
-        for (int j = 0; j < DISTILL_VECS; ++j)
-            if (first + j * step < rv.n) {
-                float v[W];
-                widen<DT>(raw[j], v);
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[e] = dead ? 0.f : g * exp2_fast(fmaf(v[e], k2, -mk));
-                rv.store(drow, same, first + j * step, v);
-            }
-    } else {
-        for (int64_t i = first; i < rv.n; i += step) {
-            float v[W];
-            widen<DT>(rv.load(i), v);
-#pragma unroll
-            for (int e = 0; e < W; ++e) v[e] = dead ? 0.f : g * exp2_fast(fmaf(v[e], k2, -mk));
-            rv.store(drow, same, i, v);
-        }
+    char* dvec = drow + (int64_t)rv.head * Elem<DT>::SIZE;
+    const bool al = (reinterpret_cast<uintptr_t>(dvec) & 15u) == 0;
+    if (dead) {
+        const float2 zero[R::PAIRS] = {};
+        for (int i = first; i < rv.n; i += step) R::put(dvec + (int64_t)i * 16, al, zero);
+        if (edge >= 0) st1<DT>(drow, edge, 0.f);
+        return;
     }
-    if (dead) return;
-    // the entries that lie in this block's vectors, written over after it
-    // wrote those: the same id twice gives the same value twice
+    const float g = coef * P / total;
+    const uint64_t gg = pack2(g, g), nm = pack2(-mk, -mk);
+    int i = first;
+    if constexpr (!BWD)
+        for (int j = 0; j < a.keep && i < rv.n; ++j, i += step)
+            R::grad(dvec + (int64_t)i * 16, al, kept[j * T + threadIdx.x], kk, nm, gg);
+    for (; i + (U - 1) * step < rv.n; i += U * step) {
+        uint4 r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u] = rv.load_last(i + u * step);
+#pragma unroll
+        for (int u = 0; u < U; ++u) R::grad(dvec + (int64_t)(i + u * step) * 16, al, r[u], kk, nm, gg);
+    }
+    for (; i < rv.n; i += step) R::grad(dvec + (int64_t)i * 16, al, rv.load_last(i), kk, nm, gg);
+    if (edge >= 0) st1<DT>(drow, edge, g * exp2_fast(fmaf(edge_z, k2, -mk)));
+    // the entries that lie in this block's part, written over after it wrote
+    // that: the same id twice gives the same value twice
     __syncthreads();
-    for (int i = threadIdx.x; i < a.k; i += blockDim.x) {
-        const Entry en = entry[i];
-        if (en.id < 0) continue;
-        const int64_t v = (en.id + rv.off) / W;
-        if ((int)(v / blockDim.x % C) != rank) continue;
+    for (int j = threadIdx.x; j < a.k; j += T) {
+        const Entry en = entry[j];
+        if (en.id < 0 || !mine(en.id)) continue;
         float p = 0.f;
-        for (int j = 0; j < a.k; ++j) p += entry[j].id == en.id ? entry[j].p : 0.f;
+        for (int o = 0; o < a.k; ++o)
+            if (entry[o].id == en.id) p += exp2f(entry[o].t - tm);
         st1<DT>(drow, en.id, fmaf(g, exp2_fast(fmaf(en.z, k2, -mk)), -coef * p * pscale));
     }
 }
 
 template <int DT>
-static const void* distill_fn(bool res, bool bwd) {
-    if (bwd) return (const void*)k_distill<DT, false, true>;
-    return res ? (const void*)k_distill<DT, true, false> : (const void*)k_distill<DT, false, false>;
+static const void* distill_fn(bool bwd) {
+    return bwd ? (const void*)k_distill<DT, true> : (const void*)k_distill<DT, false>;
 }
 
 static int distill(const char* who, const zero_mat* logits, int64_t rows, int64_t cols, const zero_mat* ids,
@@ -337,11 +377,10 @@ static int distill(const char* who, const zero_mat* logits, int64_t rows, int64_
     if (cols > INT32_MAX / 2 || rows > INT32_MAX / DISTILL_CLUSTER) return bad(ZERO_ELIMIT, "too many rows or columns");
     if (!(temperature > 0.f) || !(temperature < INFINITY)) return bad(ZERO_EINVAL, "temperature must be finite and > 0");
     if (!(grad_scale - grad_scale == 0.f)) return bad(ZERO_EINVAL, "grad_scale must be finite");
-    const std::string w(who);
-    int rc = check_mat(logits, rows, cols, FLOAT_TYPES, (w + ": logits").c_str());
-    if (rc == ZERO_OK) rc = check_mat(ids, rows, k, 1u << ZERO_I32 | 1u << ZERO_I64, (w + ": ids").c_str());
-    if (rc == ZERO_OK) rc = check_mat(teacher, rows, k, FLOAT_TYPES, (w + ": teacher").c_str());
-    if (rc == ZERO_OK && (dlogits || bwd)) rc = check_mat(dlogits, rows, cols, FLOAT_TYPES, (w + ": dlogits").c_str());
+    int rc = check_mat(logits, rows, cols, FLOAT_TYPES, who, "logits");
+    if (rc == ZERO_OK) rc = check_mat(ids, rows, k, 1u << ZERO_I32 | 1u << ZERO_I64, who, "ids");
+    if (rc == ZERO_OK) rc = check_mat(teacher, rows, k, FLOAT_TYPES, who, "teacher");
+    if (rc == ZERO_OK && (dlogits || bwd)) rc = check_mat(dlogits, rows, cols, FLOAT_TYPES, who, "dlogits");
     if (rc != ZERO_OK) return rc;
     if (dlogits && dlogits->dtype != logits->dtype) return bad(ZERO_EINVAL, "dlogits is in the logits' type");
     if (bwd && rows > 0 && cols > 0 && !lse_in) return bad(ZERO_EINVAL, "NULL lse");
@@ -376,18 +415,17 @@ static int distill(const char* who, const zero_mat* logits, int64_t rows, int64_
     a.temperature = temperature;
     a.grad_scale = grad_scale;
 
-    // Vectors of a row, with the one that an unaligned start adds; threads so
-    // that a short row leaves none idle; then the fewest blocks that hold a
-    // row in registers, and more while the rows alone do not fill the GPU.
+    // Threads so that a short row leaves none idle; a block to a row, and a
+    // cluster of more while the rows alone do not fill the GPU.
     const int W = 16 / elem_size(logits->dtype);
-    const int64_t n = (cols + W - 1) / W + 1;
-    const int threads = n <= 1024 ? 128 : n <= 2048 ? 256 : DISTILL_THREADS;
-    const int64_t per = (int64_t)threads * DISTILL_VECS;
+    const int64_t n = cols / W + 1;          // whole vectors of a row, at most
+    const int threads = n <= 1024 ? 128 : DISTILL_THREADS;
     int split = 1;
-    while (split < DISTILL_CLUSTER && split * per < n) split *= 2;
-    const bool res = split * per >= n;
     while (split < DISTILL_CLUSTER && rows * split < 2 * (int64_t)sms && split * threads < n) split *= 2;
     a.split = split;
+    // what a thread keeps: all its vectors if they are few, in whole batches
+    const int64_t own = (n + (int64_t)split * threads - 1) / ((int64_t)split * threads);
+    a.keep = bwd || !dlogits ? 0 : own >= DISTILL_KEEP ? DISTILL_KEEP : (int)((own + DISTILL_BATCH - 1) / DISTILL_BATCH * DISTILL_BATCH);
 
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -398,12 +436,16 @@ static int distill(const char* who, const zero_mat* logits, int64_t rows, int64_
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * split));
     cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = sizeof(Entry) * (size_t)k;
+    cfg.dynamicSmemBytes = (size_t)a.keep * (size_t)threads * 16 + sizeof(Entry) * (size_t)k;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = bwd ? 1 : 2;
-    const void* f = logits->dtype == ZERO_F32 ? distill_fn<ZERO_F32>(res, bwd)
-                  : logits->dtype == ZERO_BF16 ? distill_fn<ZERO_BF16>(res, bwd) : distill_fn<ZERO_F16>(res, bwd);
+    const void* f = logits->dtype == ZERO_F32 ? distill_fn<ZERO_F32>(bwd)
+                  : logits->dtype == ZERO_BF16 ? distill_fn<ZERO_BF16>(bwd) : distill_fn<ZERO_F16>(bwd);
+    if (cfg.dynamicSmemBytes > 40 * 1024) {
+        rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes), who);
+        if (rc != ZERO_OK) return rc;
+    }
     void* args[] = {&a};
     return cuda_fail(cudaLaunchKernelExC(&cfg, f, args), who);
 }

@@ -6,16 +6,20 @@
 
 namespace zdp {
 
-int check_mat(const zero_mat* m, int64_t rows, int64_t cols, unsigned types, const char* what) {
-    const std::string w(what);
-    if (!m) return fail(ZERO_EINVAL, (w + " is NULL").c_str());
+int refuse(int code, const char* call, const char* what, const char* why) {
+    set_error(std::string(call) + ": " + what + why);
+    return code;
+}
+
+int check_mat(const zero_mat* m, int64_t rows, int64_t cols, unsigned types, const char* call, const char* what) {
+    if (!m) return refuse(ZERO_EINVAL, call, what, " is NULL");
     if (m->dtype < 0 || m->dtype > 31 || !(types >> m->dtype & 1u))
-        return fail(ZERO_EINVAL, (w + ": unknown or unsupported dtype").c_str());
+        return refuse(ZERO_EINVAL, call, what, ": unknown or unsupported dtype");
     if (rows == 0 || cols == 0) return ZERO_OK;
-    if (!m->data) return fail(ZERO_EINVAL, (w + ": NULL data").c_str());
-    if (rows > 1 && m->ld < cols) return fail(ZERO_EINVAL, (w + ": rows closer than their columns").c_str());
+    if (!m->data) return refuse(ZERO_EINVAL, call, what, ": NULL data");
+    if (rows > 1 && m->ld < cols) return refuse(ZERO_EINVAL, call, what, ": rows closer than their columns");
     if (!aligned(m->data, (size_t)elem_size(m->dtype)))
-        return fail(ZERO_EALIGN, (w + ": not aligned to its element").c_str());
+        return refuse(ZERO_EALIGN, call, what, ": not aligned to its element");
     return ZERO_OK;
 }
 

@@ -116,7 +116,53 @@ __device__ __forceinline__ void ld8_any(const void* p, int64_t i, int dt, bool a
     }
 }
 
+// ---------------------------------------------------------------- pairs
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// elements 2 q and 2 q + 1 of eight packed ones, as fp32
+template <int DT>
+__device__ __forceinline__ uint64_t pair8(const Raw8<DT>& r, int q) {
+    if constexpr (DT == ZERO_F32) {
+        const uint4 w = r.w[q / 2];
+        return q % 2 ? pack2(__uint_as_float(w.z), __uint_as_float(w.w)) : pack2(__uint_as_float(w.x), __uint_as_float(w.y));
+    } else {
+        const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+        if constexpr (DT == ZERO_BF16) return pack2(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xFFFF0000u));
+        else return pack2(Half16<DT>::widen(u[q] & 0xFFFFu), Half16<DT>::widen(u[q] >> 16));
+    }
+}
+
 // ---------------------------------------------------------------- reductions
+// The largest of three that keeps a NaN.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // |x| as an unsigned integer orders as |x| does, with NaN above infinity: the
 // largest of a block keeps a NaN, where fmaxf would drop it.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
@@ -160,7 +206,9 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s) {
 // ---------------------------------------------------------------- host
 // A matrix argument: not NULL, one of the types in `types` (a bit per code),
 // rows at least `cols` apart, aligned to its element.
-int check_mat(const zero_mat* m, int64_t rows, int64_t cols, unsigned types, const char* what);
+int check_mat(const zero_mat* m, int64_t rows, int64_t cols, unsigned types, const char* call, const char* what);
+// Sets the message "call: what" + why and returns code.
+int refuse(int code, const char* call, const char* what, const char* why);
 constexpr unsigned FLOAT_TYPES = 1u << ZERO_F16 | 1u << ZERO_BF16 | 1u << ZERO_F32;
 // Whether every row starts on a 16-byte boundary.
 inline bool rows_aligned(const zero_mat& m, int64_t rows) {

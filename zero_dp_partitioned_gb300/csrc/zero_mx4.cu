@@ -255,18 +255,17 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_tile(const uint8_t* src, ui
     }
 }
 
-int check_mx4(const zero_mx4* m, const char* what) {
-    const std::string w(what);
-    if (!m) return fail(ZERO_EINVAL, (w + " is NULL").c_str());
-    if (m->rows < 0 || m->cols < 0) return fail(ZERO_EINVAL, (w + ": negative size").c_str());
+int check_mx4(const zero_mx4* m, const char* call, const char* what) {
+    if (!m) return refuse(ZERO_EINVAL, call, what, " is NULL");
+    if (m->rows < 0 || m->cols < 0) return refuse(ZERO_EINVAL, call, what, ": negative size");
     if (m->layout != ZERO_MX4_ROWS && m->layout != ZERO_MX4_TILES)
-        return fail(ZERO_EINVAL, (w + ": unknown scale layout").c_str());
+        return refuse(ZERO_EINVAL, call, what, ": unknown scale layout");
     if (m->rows == 0 || m->cols == 0) return ZERO_OK;
-    if (!m->data || !m->scales) return fail(ZERO_EINVAL, (w + ": NULL data or scales").c_str());
+    if (!m->data || !m->scales) return refuse(ZERO_EINVAL, call, what, ": NULL data or scales");
     if (!aligned(m->data, 16) || (m->layout == ZERO_MX4_TILES && !aligned(m->scales, 16)))
-        return fail(ZERO_EALIGN, (w + ": data and tiled scales must be 16-byte aligned").c_str());
+        return refuse(ZERO_EALIGN, call, what, ": data and tiled scales must be 16-byte aligned");
     if (m->ld % 16 != 0 || m->ld < mx4_blocks(m->cols) * 16)
-        return fail(ZERO_EINVAL, (w + ": ld is a multiple of 16 bytes, at least 16 for every 32 columns").c_str());
+        return refuse(ZERO_EINVAL, call, what, ": ld is a multiple of 16 bytes, at least 16 for every 32 columns");
     return ZERO_OK;
 }
 
@@ -299,9 +298,9 @@ int zero_mx4_bytes(int64_t rows, int64_t cols, int layout, int64_t* ld, int64_t*
 int zero_mx4_quantize(const zero_mat* src, int64_t rows, int64_t cols, const zero_mx4* out, const zero_mx4* out_t,
                       void* stream) {
     if (rows < 0 || cols < 0) return fail(ZERO_EINVAL, "zero_mx4_quantize: negative size");
-    int rc = check_mat(src, rows, cols, FLOAT_TYPES, "zero_mx4_quantize: src");
-    if (rc == ZERO_OK && out) rc = check_mx4(out, "zero_mx4_quantize: out");
-    if (rc == ZERO_OK && out_t) rc = check_mx4(out_t, "zero_mx4_quantize: out_t");
+    int rc = check_mat(src, rows, cols, FLOAT_TYPES, "zero_mx4_quantize", "src");
+    if (rc == ZERO_OK && out) rc = check_mx4(out, "zero_mx4_quantize", "out");
+    if (rc == ZERO_OK && out_t) rc = check_mx4(out_t, "zero_mx4_quantize", "out_t");
     if (rc != ZERO_OK) return rc;
     if (out && (out->rows != rows || out->cols != cols)) return fail(ZERO_EINVAL, "zero_mx4_quantize: out is rows x cols");
     if (out_t && (out_t->rows != cols || out_t->cols != rows))
@@ -337,8 +336,8 @@ int zero_mx4_quantize(const zero_mat* src, int64_t rows, int64_t cols, const zer
 }
 
 int zero_mx4_dequantize(const zero_mx4* src, const zero_mat* dst, void* stream) {
-    int rc = check_mx4(src, "zero_mx4_dequantize: src");
-    if (rc == ZERO_OK) rc = check_mat(dst, src->rows, src->cols, FLOAT_TYPES, "zero_mx4_dequantize: dst");
+    int rc = check_mx4(src, "zero_mx4_dequantize", "src");
+    if (rc == ZERO_OK) rc = check_mat(dst, src->rows, src->cols, FLOAT_TYPES, "zero_mx4_dequantize", "dst");
     if (rc != ZERO_OK || src->rows == 0 || src->cols == 0) return rc;
     if (!sm_count()) return ZERO_ECUDA;
     DequantArgs a = {};
@@ -358,8 +357,8 @@ int zero_mx4_dequantize(const zero_mx4* src, const zero_mat* dst, void* stream) 
 }
 
 int zero_mx4_tile_scales(const zero_mx4* src, const zero_mx4* dst, void* stream) {
-    int rc = check_mx4(src, "zero_mx4_tile_scales: src");
-    if (rc == ZERO_OK) rc = check_mx4(dst, "zero_mx4_tile_scales: dst");
+    int rc = check_mx4(src, "zero_mx4_tile_scales", "src");
+    if (rc == ZERO_OK) rc = check_mx4(dst, "zero_mx4_tile_scales", "dst");
     if (rc != ZERO_OK) return rc;
     if (src->layout != ZERO_MX4_ROWS || dst->layout != ZERO_MX4_TILES || src->rows != dst->rows || src->cols != dst->cols)
         return fail(ZERO_EINVAL, "zero_mx4_tile_scales: from ZERO_MX4_ROWS to ZERO_MX4_TILES of the same size");

@@ -31,6 +31,6 @@ __host__ __device__ __forceinline__ int64_t mx4_tiled_at(int64_t r, int64_t b, i
     return ((r >> 7) * tiles + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
 }
 
-int check_mx4(const zero_mx4* m, const char* what);
+int check_mx4(const zero_mx4* m, const char* call, const char* what);
 
 }  // namespace zdp

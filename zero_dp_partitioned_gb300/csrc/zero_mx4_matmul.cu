@@ -396,15 +396,15 @@ using namespace zdp;
 extern "C" {
 
 int zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, float alpha, const zero_mat* d, int32_t* status, void* stream) {
-    int rc = check_mx4(a, "zero_mx4_matmul: a");
-    if (rc == ZERO_OK) rc = check_mx4(b, "zero_mx4_matmul: b");
+    int rc = check_mx4(a, "zero_mx4_matmul", "a");
+    if (rc == ZERO_OK) rc = check_mx4(b, "zero_mx4_matmul", "b");
     if (rc != ZERO_OK) return rc;
     if (a->cols != b->cols) return fail(ZERO_EINVAL, "zero_mx4_matmul: a and b have as many columns");
     if (a->layout != ZERO_MX4_TILES || b->layout != ZERO_MX4_TILES)
         return fail(ZERO_EINVAL, "zero_mx4_matmul: scales in ZERO_MX4_TILES (zero_mx4_tile_scales)");
     if (a->rows > INT32_MAX / 2 || b->rows > INT32_MAX / 2 || a->cols > INT32_MAX / 2)
         return fail(ZERO_ELIMIT, "zero_mx4_matmul: more than 2^30 rows or columns");
-    rc = check_mat(d, a->rows, b->rows, FLOAT_TYPES, "zero_mx4_matmul: d");
+    rc = check_mat(d, a->rows, b->rows, FLOAT_TYPES, "zero_mx4_matmul", "d");
     if (rc != ZERO_OK) return rc;
     if (!status || !aligned(status, 4)) return fail(ZERO_EINVAL, "zero_mx4_matmul: status NULL or not 4-byte aligned");
     if (!(alpha - alpha == 0.f)) return fail(ZERO_EINVAL, "zero_mx4_matmul: alpha must be finite");

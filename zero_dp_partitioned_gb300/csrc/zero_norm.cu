@@ -16,6 +16,9 @@ namespace zdp {
 
 constexpr int NORM_THREADS = 512;       // most threads that share a row
 constexpr int64_t NORM_MAX_COLS = 1 << 20;
+constexpr int NORM_MAX_STAGES = 4;      // rows a thread has on their way or at hand
+constexpr int NORM_SM_SMEM = 216 * 1024;
+constexpr int NORM_FORWARD_THREADS = 1024, NORM_BACKWARD_THREADS = 512;   // of a multiprocessor, walking rows
 constexpr int NORM_MAX_GRID = 608;      // blocks of the backward pass, each with a partial dw
 constexpr float E4M3_MAX = 448.f;
 constexpr float SCALE_FLOOR = 7.888609052210118e-31f;   // 2^-100: a zero row still has a usable scale
@@ -24,9 +27,10 @@ struct NormArgs {
     const void *x, *r, *w;              // backward: dy, dh, w
     const void* hin;                    // backward: the stored h
     void *h, *y;                        // backward: y is dx
-    int64_t ldx, ldr, ldhin, ldh, ldy, rows, cols, n_scale;
+    int64_t ldx, ldr, ldhin, ldh, ldy, rows, n_scale;
+    int cols;
     float eps;
-    int wdt, w_aligned, y8, block128;
+    int wdt, w_aligned, y8, block128, stages;
     float *scale, *rstd;
     float* part;                        // backward: [grid][cols] partial dw
 };
@@ -38,11 +42,11 @@ struct Map {
     static constexpr int E = V8 ? 8 : 4;
     static constexpr int LANES = V8 ? 16 : 32;      // lanes that share 128 columns
     // this thread's j-th unit
-    static __device__ __forceinline__ int64_t unit(int j) { return threadIdx.x + (int64_t)j * blockDim.x; }
-    static __device__ __forceinline__ int64_t col(int64_t u, int e) {
+    static __device__ __forceinline__ int unit(int j) { return threadIdx.x + j * blockDim.x; }
+    static __device__ __forceinline__ int col(int u, int e) {
         return V8 ? u * 8 + e : (u >> 5) * 128 + e * 32 + (u & 31);
     }
-    static __device__ __forceinline__ bool any(int64_t u, int64_t cols) { return col(u, 0) < cols; }
+    static __device__ __forceinline__ bool any(int u, int cols) { return col(u, 0) < cols; }
 };
 
 // Loads of one unit of a row, kept as they lie until they are used, so that
@@ -51,7 +55,7 @@ template <int DT, bool V8>
 struct Unit {
     Raw8<DT> raw;                        // V8
     float one[V8 ? 1 : 4];
-    __device__ __forceinline__ void load(const void* row, int64_t u, int64_t cols) {
+    __device__ __forceinline__ void load(const void* row, int u, int cols) {
         if constexpr (V8) {
             if (u * 8 < cols) raw = ld8<DT>(row, u * 8);
             else
@@ -60,8 +64,30 @@ struct Unit {
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int64_t c = Map<V8>::col(u, e);
+                const int c = Map<V8>::col(u, e);
                 one[e] = c < cols ? ld1<DT>(row, c) : 0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ uint64_t pair(int q) const {
+        if constexpr (V8) return pair8<DT>(raw, q);
+        else return pack2(one[2 * q], one[2 * q + 1]);
+    }
+    // values that the type holds exactly
+    __device__ __forceinline__ void hold(const float (&v)[Map<V8>::E]) {
+        if constexpr (V8) raw = narrow8<DT>(v);
+        else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) one[e] = v[e];
+    }
+    __device__ __forceinline__ void store(void* row, int u, int cols) const {
+        if constexpr (V8) {
+            if (u * 8 < cols) st8<DT>(row, u * 8, raw);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = Map<V8>::col(u, e);
+                if (c < cols) st1<DT>(row, c, one[e]);
             }
         }
     }
@@ -73,21 +99,64 @@ struct Unit {
     }
 };
 
+// Rows on their way: a thread copies its own units of the next rows to its own
+// slots of shared memory (cp.async, 16 bytes each, past the registers and L1)
+// and waits for its own copies alone, so no barrier is involved.  Units that
+// are not whole 16-byte words are loaded when they are needed.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void copies_wait_all_but(int n) {     // n = stages - 1
+    if (n == 1) copies_wait<1>();
+    else if (n == 2) copies_wait<2>();
+    else copies_wait<3>();
+}
+
+// One matrix of a stage: NV units a thread, each of 1 or 2 words.
+template <int DT, int NV>
+struct Slots {
+    static constexpr int WORDS = DT == ZERO_F32 ? 2 : 1;
+    static constexpr int COUNT = NV * WORDS;          // words of a thread
+    uint4* at;                                        // this thread's first word; the next is blockDim.x further
+    __device__ __forceinline__ void copy(const void* row, int cols) const {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int u = Map<true>::unit(j);
+            if (u * 8 >= cols) continue;
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w)
+                copy16((uint32_t)__cvta_generic_to_shared(at + (j * WORDS + w) * blockDim.x),
+                       static_cast<const char*>(row) + (int64_t)u * 8 * Elem<DT>::SIZE + 16 * w);
+        }
+    }
+    __device__ __forceinline__ void read(Unit<DT, true> (&u)[NV], int cols) const {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w)
+                u[j].raw.w[w] = Map<true>::unit(j) * 8 < cols ? at[(j * WORDS + w) * blockDim.x] : make_uint4(0, 0, 0, 0);
+    }
+};
+
 template <int DT, bool V8>
-__device__ __forceinline__ void store_unit(void* row, int64_t u, int64_t cols, const float (&v)[Map<V8>::E]) {
+__device__ __forceinline__ void store_unit(void* row, int u, int cols, const float (&v)[Map<V8>::E]) {
     if constexpr (V8) {
         if (u * 8 < cols) st8<DT>(row, u * 8, narrow8<DT>(v));
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int64_t c = Map<V8>::col(u, e);
+            const int c = Map<V8>::col(u, e);
             if (c < cols) st1<DT>(row, c, v[e]);
         }
     }
 }
 
 template <bool V8>
-__device__ __forceinline__ void store_e4m3(void* row, int64_t u, int64_t cols, const float (&v)[Map<V8>::E]) {
+__device__ __forceinline__ void store_e4m3(void* row, int u, int cols, const float (&v)[Map<V8>::E]) {
     uint8_t* p = static_cast<uint8_t*>(row);
     if constexpr (V8) {
         if (u * 8 >= cols) return;
@@ -99,14 +168,37 @@ __device__ __forceinline__ void store_e4m3(void* row, int64_t u, int64_t cols, c
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int64_t c = Map<V8>::col(u, e);
+            const int c = Map<V8>::col(u, e);
             if (c < cols) p[c] = __nv_cvt_float_to_fp8(v[e], __NV_SATFINITE, __NV_E4M3);
         }
     }
 }
 
+// |y|'s largest of a unit, NaN kept (its bits then order above infinity's).
+template <int E>
+__device__ __forceinline__ float top_of(const float (&y)[E]) {
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) t = max3_nan(t, fabsf(y[e]), fabsf(y[e + 1]));
+    return fabsf(t);
+}
+// A block's scale from its largest magnitude: at least the floor's, NaN kept.
+__device__ __forceinline__ float scale_of(float top) {
+    return (top != top ? top : fmaxf(top, SCALE_FLOOR)) * (1.f / E4M3_MAX);
+}
+// The reciprocal is approximate (1 ulp): it moves a value across a rounding
+// boundary of 4 bits about once in 2^20, to a neighbour as near.
 template <bool V8>
-__device__ __forceinline__ void weights(const NormArgs& a, int64_t u, float (&w)[Map<V8>::E]) {
+__device__ __forceinline__ void quantised_store(void* row, int u, int cols, float (&v)[Map<V8>::E], float scale) {
+    float inv;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+#pragma unroll
+    for (int e = 0; e < Map<V8>::E; ++e) v[e] *= inv;
+    store_e4m3<V8>(row, u, cols, v);
+}
+
+template <bool V8>
+__device__ __forceinline__ void weights(const NormArgs& a, int u, float (&w)[Map<V8>::E]) {
     if (!a.w) {
 #pragma unroll
         for (int e = 0; e < Map<V8>::E; ++e) w[e] = 1.f;
@@ -118,9 +210,21 @@ __device__ __forceinline__ void weights(const NormArgs& a, int64_t u, float (&w)
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int64_t c = Map<V8>::col(u, e);
+            const int c = Map<V8>::col(u, e);
             w[e] = c < a.cols ? ld1_any(a.w, c, a.wdt) : 0.f;
         }
+    }
+}
+
+// A thread's columns are the same in every row it walks: their weights stay in registers.
+template <bool V8, int NV>
+__device__ __forceinline__ void weight_pairs(const NormArgs& a, uint64_t (&w)[NV][Map<V8>::E / 2]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        float v[Map<V8>::E];
+        weights<V8>(a, Map<V8>::unit(j), v);
+#pragma unroll
+        for (int q = 0; q < Map<V8>::E / 2; ++q) w[j][q] = pack2(v[2 * q], v[2 * q + 1]);
     }
 }
 
@@ -156,69 +260,98 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_cons
     __shared__ uint32_t smax[2][32];
     pdl_wait();
     pdl_launch_next();
-    int turn = 0;
+    extern __shared__ __align__(16) uint4 ring[];
+    const int S = a.stages;
+    constexpr int XW = Slots<XT, NV>::COUNT, RW = Slots<RT, NV>::COUNT;
+    const Slots<XT, NV> xs = {ring + threadIdx.x};
+    const Slots<RT, NV> rs = {ring + threadIdx.x + XW * blockDim.x};
+    const int stage_words = (XW + RW) * blockDim.x;
+    auto copy = [&](int64_t row, int st) {
+        if (row < a.rows) {
+            Slots<XT, NV>{xs.at + st * stage_words}.copy(row_of<XT>(a.x, a.ldx, row), a.cols);
+            if (a.r) Slots<RT, NV>{rs.at + st * stage_words}.copy(row_of<RT>(a.r, a.ldr, row), a.cols);
+        }
+        copies_commit();
+    };
+    if constexpr (V8)
+        for (int st = 0; st < S - 1; ++st) copy(blockIdx.x + (int64_t)st * gridDim.x, st);
+    uint64_t w[NV][E / 2];
+    weight_pairs<V8, NV>(a, w);
+    int turn = 0, st = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const void* X = row_of<XT>(a.x, a.ldx, row);
-        const void* R = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
         Unit<XT, V8> x[NV];
         Unit<RT, V8> r[NV];
+        if constexpr (V8) {
+            copy(row + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
+            copies_wait_all_but(S - 1);
+            Slots<XT, NV>{xs.at + st * stage_words}.read(x, a.cols);
+            if (a.r) Slots<RT, NV>{rs.at + st * stage_words}.read(r, a.cols);
+            st = st == S - 1 ? 0 : st + 1;
+        } else {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) x[j].load(X, Map<V8>::unit(j), a.cols);
-        if (R)
+            for (int j = 0; j < NV; ++j) x[j].load(row_of<XT>(a.x, a.ldx, row), Map<V8>::unit(j), a.cols);
+            if (a.r)
 #pragma unroll
-            for (int j = 0; j < NV; ++j) r[j].load(R, Map<V8>::unit(j), a.cols);
-        float h[NV][E];
-        float ss = 0.f;
+                for (int j = 0; j < NV; ++j) r[j].load(row_of<RT>(a.r, a.ldr, row), Map<V8>::unit(j), a.cols);
+        }
+        // h as it is stored: half the registers of its fp32 values
+        uint64_t s2 = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            add_unit<XT, RT, V8>(x[j], r[j], R != nullptr, h[j]);
+            float h[E];
+            add_unit<XT, RT, V8>(x[j], r[j], a.r != nullptr, h);
+            r[j].hold(h);
 #pragma unroll
-            for (int e = 0; e < E; ++e) ss = fmaf(h[j][e], h[j][e], ss);
-            if (a.h) store_unit<RT, V8>(row_of<RT>(a.h, a.ldh, row), Map<V8>::unit(j), a.cols, h[j]);
+            for (int q = 0; q < E / 2; ++q) s2 = fma2(pack2(h[2 * q], h[2 * q + 1]), pack2(h[2 * q], h[2 * q + 1]), s2);
+            if (a.h) r[j].store(row_of<RT>(a.h, a.ldh, row), Map<V8>::unit(j), a.cols);
         }
-        ss = block_sum(ss, ssum[turn]);
+        const float2 sp = unpack2(s2);
+        const float ss = block_sum(sp.x + sp.y, ssum[turn]);
         const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
         if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-        uint32_t top = 0;
+        const uint64_t rr = pack2(rstd, rstd);
+        auto normed = [&](int j, float (&y)[E]) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float w[E];
-            weights<V8>(a, Map<V8>::unit(j), w);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                h[j][e] = h[j][e] * rstd * w[e];
-                if (a.y8) top = max(top, abs_bits(h[j][e]));
+            for (int q = 0; q < E / 2; ++q) {
+                const float2 v = unpack2(mul2(mul2(r[j].pair(q), rr), w[j][q]));
+                y[2 * q] = v.x;
+                y[2 * q + 1] = v.y;
             }
-            if (!a.y8) {
-                store_unit<XT, V8>(row_of<XT>(a.y, a.ldy, row), Map<V8>::unit(j), a.cols, h[j]);
-            } else if (a.block128) {
-                const uint32_t t = lanes_max<Map<V8>::LANES>(top);
-                top = 0;
-                const float m = fmaxf(__uint_as_float(t), SCALE_FLOOR);
-                const float mm = __uint_as_float(t) != __uint_as_float(t) ? __uint_as_float(t) : m;
-                const float inv = E4M3_MAX / mm;
-                float q[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) q[e] = h[j][e] * inv;
-                const int64_t u = Map<V8>::unit(j);
-                store_e4m3<V8>(static_cast<uint8_t*>(a.y) + row * a.ldy, u, a.cols, q);
-                if ((u & (Map<V8>::LANES - 1)) == 0 && Map<V8>::any(u, a.cols))
-                    a.scale[row * a.n_scale + u / Map<V8>::LANES] = mm / E4M3_MAX;
-            }
-        }
-        if (a.y8 && !a.block128) {
-            const uint32_t t = block_max(top, smax[turn]);
-            const float m = fmaxf(__uint_as_float(t), SCALE_FLOOR);
-            const float mm = __uint_as_float(t) != __uint_as_float(t) ? __uint_as_float(t) : m;
-            const float inv = E4M3_MAX / mm;
+        };
+        if (!a.y8) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                float q[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) q[e] = h[j][e] * inv;
-                store_e4m3<V8>(static_cast<uint8_t*>(a.y) + row * a.ldy, Map<V8>::unit(j), a.cols, q);
+                float y[E];
+                normed(j, y);
+                store_unit<XT, V8>(row_of<XT>(a.y, a.ldy, row), Map<V8>::unit(j), a.cols, y);
             }
-            if (threadIdx.x == 0) a.scale[row * a.n_scale] = mm / E4M3_MAX;
+            continue;
+        }
+        uint8_t* Y = static_cast<uint8_t*>(a.y) + row * a.ldy;
+        float whole = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float y[E];
+            normed(j, y);
+            const float t = top_of<E>(y);
+            if (a.block128) {
+                const int u = Map<V8>::unit(j);
+                const float sc = scale_of(__uint_as_float(lanes_max<Map<V8>::LANES>(__float_as_uint(t))));
+                if ((u & (Map<V8>::LANES - 1)) == 0 && Map<V8>::any(u, a.cols))
+                    a.scale[row * a.n_scale + u / Map<V8>::LANES] = sc;
+                quantised_store<V8>(Y, u, a.cols, y, sc);
+            }
+            whole = max3_nan(whole, t, t);
+        }
+        if (!a.block128) {
+            const float sc = scale_of(__uint_as_float(block_max(__float_as_uint(whole), smax[turn])));
+            if (threadIdx.x == 0) a.scale[row * a.n_scale] = sc;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float y[E];
+                normed(j, y);
+                quantised_store<V8>(Y, Map<V8>::unit(j), a.cols, y, sc);
+            }
         }
     }
 }
@@ -233,14 +366,14 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
     __shared__ uint32_t smax[2][32];
     pdl_wait();
     pdl_launch_next();
-    const int64_t units = V8 ? a.cols / 8 : (a.cols + 127) / 128 * 32;
-    const int64_t steps = (units + blockDim.x - 1) / blockDim.x;
+    const int units = V8 ? a.cols / 8 : (a.cols + 127) / 128 * 32;
+    const int steps = (units + (int)blockDim.x - 1) / (int)blockDim.x;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const void* X = row_of<XT>(a.x, a.ldx, row);
         const void* R = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
         void* H = a.h ? row_of<RT>(a.h, a.ldh, row) : nullptr;
-        auto value = [&](int64_t u, float (&h)[E]) {      // h again, after it was stored over x or r
+        auto value = [&](int u, float (&h)[E]) {      // h again, after it was stored over x or r
             if (H) {
                 Unit<RT, V8> s;
                 s.load(H, u, a.cols);
@@ -254,8 +387,8 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
             }
         };
         float ss = 0.f;
-        for (int64_t j = 0; j < steps; ++j) {
-            const int64_t u = threadIdx.x + j * blockDim.x;
+        for (int j = 0; j < steps; ++j) {
+            const int u = threadIdx.x + j * blockDim.x;
             Unit<XT, V8> x;
             Unit<RT, V8> r;
             x.load(X, u, a.cols);
@@ -272,21 +405,19 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
         float whole = 0.f;
         if (a.y8 && !a.block128) {
             uint32_t top = 0;
-            for (int64_t j = 0; j < steps; ++j) {
-                const int64_t u = threadIdx.x + j * blockDim.x;
+            for (int j = 0; j < steps; ++j) {
+                const int u = threadIdx.x + j * blockDim.x;
                 float h[E], w[E];
                 value(u, h);
                 weights<V8>(a, u, w);
 #pragma unroll
                 for (int e = 0; e < E; ++e) top = max(top, abs_bits(h[e] * rstd * w[e]));
             }
-            const uint32_t t = block_max(top, smax[turn]);
-            const float m = fmaxf(__uint_as_float(t), SCALE_FLOOR);
-            whole = __uint_as_float(t) != __uint_as_float(t) ? __uint_as_float(t) : m;
-            if (threadIdx.x == 0) a.scale[row * a.n_scale] = whole / E4M3_MAX;
+            whole = scale_of(__uint_as_float(block_max(top, smax[turn])));
+            if (threadIdx.x == 0) a.scale[row * a.n_scale] = whole;
         }
-        for (int64_t j = 0; j < steps; ++j) {
-            const int64_t u = threadIdx.x + j * blockDim.x;
+        for (int j = 0; j < steps; ++j) {
+            const int u = threadIdx.x + j * blockDim.x;
             float h[E], w[E];
             value(u, h);
             weights<V8>(a, u, w);
@@ -302,16 +433,11 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
             }
             float mm = whole;
             if (a.block128) {
-                const uint32_t t = lanes_max<Map<V8>::LANES>(top);
-                const float m = fmaxf(__uint_as_float(t), SCALE_FLOOR);
-                mm = __uint_as_float(t) != __uint_as_float(t) ? __uint_as_float(t) : m;
+                mm = scale_of(__uint_as_float(lanes_max<Map<V8>::LANES>(top)));
                 if ((u & (Map<V8>::LANES - 1)) == 0 && Map<V8>::any(u, a.cols))
-                    a.scale[row * a.n_scale + u / Map<V8>::LANES] = mm / E4M3_MAX;
+                    a.scale[row * a.n_scale + u / Map<V8>::LANES] = mm;
             }
-            const float inv = E4M3_MAX / mm;
-#pragma unroll
-            for (int e = 0; e < E; ++e) h[e] *= inv;
-            store_e4m3<V8>(static_cast<uint8_t*>(a.y) + row * a.ldy, u, a.cols, h);
+            quantised_store<V8>(static_cast<uint8_t*>(a.y) + row * a.ldy, u, a.cols, h, mm);
         }
     }
 }
@@ -325,57 +451,72 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_con
     __shared__ float ssum[2][32];
     pdl_wait();
     pdl_launch_next();
-    float dw[NV][E];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < E; ++e) dw[j][e] = 0.f;
+    uint64_t dw[NV][E / 2] = {};
     const float inv_n = 1.f / (float)a.cols;
-    int turn = 0;
+    extern __shared__ __align__(16) uint4 ring[];
+    const int S = a.stages;
+    constexpr int XW = Slots<XT, NV>::COUNT, RW = Slots<RT, NV>::COUNT;
+    const int stage_words = (XW + 2 * RW) * blockDim.x;
+    const bool DH = a.r != nullptr;
+    auto copy = [&](int64_t row, int st) {
+        if (row < a.rows) {
+            uint4* at = ring + threadIdx.x + st * stage_words;
+            Slots<XT, NV>{at}.copy(row_of<XT>(a.x, a.ldx, row), a.cols);
+            Slots<RT, NV>{at + XW * blockDim.x}.copy(row_of<RT>(a.hin, a.ldhin, row), a.cols);
+            if (DH) Slots<RT, NV>{at + (XW + RW) * blockDim.x}.copy(row_of<RT>(a.r, a.ldr, row), a.cols);
+        }
+        copies_commit();
+    };
+    if constexpr (V8)
+        for (int st = 0; st < S - 1; ++st) copy(blockIdx.x + (int64_t)st * gridDim.x, st);
+    uint64_t w[NV][E / 2];
+    weight_pairs<V8, NV>(a, w);
+    int turn = 0, st = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const void* DY = row_of<XT>(a.x, a.ldx, row);
-        const void* H = row_of<RT>(a.hin, a.ldhin, row);
-        const void* DH = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
+        const float rstd = a.rstd[row];
         Unit<XT, V8> dy[NV];
         Unit<RT, V8> h[NV], dh[NV];
+        if constexpr (V8) {
+            copy(row + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
+            copies_wait_all_but(S - 1);
+            uint4* at = ring + threadIdx.x + st * stage_words;
+            Slots<XT, NV>{at}.read(dy, a.cols);
+            Slots<RT, NV>{at + XW * blockDim.x}.read(h, a.cols);
+            if (DH) Slots<RT, NV>{at + (XW + RW) * blockDim.x}.read(dh, a.cols);
+            st = st == S - 1 ? 0 : st + 1;
+        } else {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            dy[j].load(DY, Map<V8>::unit(j), a.cols);
-            h[j].load(H, Map<V8>::unit(j), a.cols);
-        }
-        if (DH)
-#pragma unroll
-            for (int j = 0; j < NV; ++j) dh[j].load(DH, Map<V8>::unit(j), a.cols);
-        const float rstd = a.rstd[row];
-        float dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float g[E], v[E], w[E];
-            dy[j].values(g);
-            h[j].values(v);
-            weights<V8>(a, Map<V8>::unit(j), w);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float xh = v[e] * rstd;
-                dw[j][e] = fmaf(g[e], xh, dw[j][e]);
-                dot = fmaf(g[e] * w[e], xh, dot);
+            for (int j = 0; j < NV; ++j) {
+                dy[j].load(row_of<XT>(a.x, a.ldx, row), Map<V8>::unit(j), a.cols);
+                h[j].load(row_of<RT>(a.hin, a.ldhin, row), Map<V8>::unit(j), a.cols);
+                if (DH) dh[j].load(row_of<RT>(a.r, a.ldr, row), Map<V8>::unit(j), a.cols);
             }
         }
-        const float c = block_sum(dot, ssum[turn]) * inv_n;
+        const uint64_t rr = pack2(rstd, rstd);
+        uint64_t d2 = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int q = 0; q < E / 2; ++q) {
+                const uint64_t xh = mul2(h[j].pair(q), rr), g = dy[j].pair(q);
+                dw[j][q] = fma2(g, xh, dw[j][q]);
+                d2 = fma2(mul2(g, w[j][q]), xh, d2);
+            }
+        const float2 dp = unpack2(d2);
+        const float c = block_sum(dp.x + dp.y, ssum[turn]) * inv_n;
+        // dx = rstd g w + (dh - xh rstd c), the sum in the brackets first
+        const uint64_t rc = pack2(-rstd * c, -rstd * c);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float g[E], v[E], w[E], up[E];
-            dy[j].values(g);
-            h[j].values(v);
-            weights<V8>(a, Map<V8>::unit(j), w);
-            if (DH) dh[j].values(up);
+            float v[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float xh = v[e] * rstd;
-                g[e] = rstd * (g[e] * w[e] - xh * c);
-                if (DH) g[e] += up[e];
+            for (int q = 0; q < E / 2; ++q) {
+                const uint64_t t = fma2(mul2(h[j].pair(q), rr), rc, DH ? dh[j].pair(q) : 0ull);
+                const float2 p = unpack2(fma2(mul2(dy[j].pair(q), w[j][q]), rr, t));
+                v[2 * q] = p.x;
+                v[2 * q + 1] = p.y;
             }
-            store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), Map<V8>::unit(j), a.cols, g);
+            store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), Map<V8>::unit(j), a.cols, v);
         }
     }
     if (!a.part) return;
@@ -383,8 +524,9 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_con
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int64_t c = Map<V8>::col(Map<V8>::unit(j), e);
-            if (c < a.cols) a.part[(int64_t)blockIdx.x * a.cols + c] = dw[j][e];
+            const int c = Map<V8>::col(Map<V8>::unit(j), e);
+            const float2 p = unpack2(dw[j][e / 2]);
+            if (c < a.cols) a.part[(int64_t)blockIdx.x * a.cols + c] = e % 2 ? p.y : p.x;
         }
 }
 
@@ -396,7 +538,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward_long(const __gri
     __shared__ float ssum[2][32];
     pdl_wait();
     pdl_launch_next();
-    const int64_t units = V8 ? a.cols / 8 : (a.cols + 127) / 128 * 32;
+    const int units = V8 ? a.cols / 8 : (a.cols + 127) / 128 * 32;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const void* DY = row_of<XT>(a.x, a.ldx, row);
@@ -404,7 +546,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward_long(const __gri
         const void* DH = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
         const float rstd = a.rstd[row];
         float dot = 0.f;
-        for (int64_t u = threadIdx.x; u < units; u += blockDim.x) {
+        for (int u = threadIdx.x; u < units; u += blockDim.x) {
             Unit<XT, V8> dy;
             Unit<RT, V8> h;
             dy.load(DY, u, a.cols);
@@ -417,7 +559,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward_long(const __gri
             for (int e = 0; e < E; ++e) dot = fmaf(g[e] * w[e], v[e] * rstd, dot);
         }
         const float c = block_sum(dot, ssum[turn]) / (float)a.cols;
-        for (int64_t u = threadIdx.x; u < units; u += blockDim.x) {
+        for (int u = threadIdx.x; u < units; u += blockDim.x) {
             Unit<XT, V8> dy;
             Unit<RT, V8> h, dh;
             dy.load(DY, u, a.cols);
@@ -451,25 +593,30 @@ __global__ void __launch_bounds__(128) k_norm_dw_long(const __grid_constant__ No
     a.part[(int64_t)blockIdx.y * a.cols + c] = s;
 }
 
-// dw[c] = sum of the n partial rows, in order in each of the block's 8 rows of
-// threads and then over those; added to what dw holds if accumulate.
-__global__ void __launch_bounds__(256) k_norm_dw(const float* part, int n, int64_t cols, void* dw, int dt,
-                                                 int accumulate) {
-    __shared__ float s[8][32];
+// dw[c] = sum of the n partial rows: each of the block's 32 warps adds every
+// 32nd of them, a butterfly adds the warps' sums; added to what dw holds if
+// accumulate.
+__global__ void __launch_bounds__(1024) k_norm_dw(const float* part, int n, int64_t cols, void* dw, int dt,
+                                                  int accumulate) {
+    __shared__ float s[32][33];
     pdl_wait();
     pdl_launch_next();
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float t = 0.f;
-    if (c < cols)
-        for (int i = k; i < n; i += 8) t += part[(int64_t)i * cols + c];
+    if (c < cols) {
+        const float* p = part + c;
+#pragma unroll 8
+        for (int i = k; i < n; i += 32) t += p[(int64_t)i * cols];
+    }
     s[k][lane] = t;
     __syncthreads();
-    if (k || c >= cols) return;
-#pragma unroll
-    for (int i = 1; i < 8; ++i) t += s[i][lane];
-    if (accumulate) t += ld1_any(dw, c, dt);
-    st1_any(dw, c, t, dt);
+    // the transpose: warp k has column k of the block's 32
+    t = warp_sum(s[lane][k]);
+    const int64_t cc = (int64_t)blockIdx.x * 32 + k;
+    if (lane || cc >= cols) return;
+    if (accumulate) t += ld1_any(dw, cc, dt);
+    st1_any(dw, cc, t, dt);
 }
 
 // ---------------------------------------------------------------- choice of the launch
@@ -501,14 +648,35 @@ static const void* norm_fn(bool fwd, int xt, int rt, bool v8, int nv) {
     return rt == ZERO_F32 ? pick<ZERO_F16, ZERO_F32>(fwd, v8, nv) : pick<ZERO_F16, ZERO_F16>(fwd, v8, nv);
 }
 
-// Units per thread (0 = the row does not fit the registers) and threads per row.
-static void shape_of(int64_t cols, bool v8, int* nv, int* threads) {
-    const int64_t per = v8 ? 8 : 4;
+static int words_of(int dt) { return dt == ZERO_F32 ? 2 : 1; }
+
+// How a row is shared out: units per thread (0: the row does not fit the
+// registers, or two stages of it shared memory), threads per row, blocks per
+// multiprocessor, stages and their bytes.  words: 16-byte words of a unit of
+// all matrices read.
+struct NormShape {
+    int nv, threads, per_sm, stages;
+    size_t smem;
+};
+static NormShape shape_of(int64_t cols, bool v8, int words, int sm_threads) {
+    NormShape s;
     const int64_t units = v8 ? (cols + 7) / 8 : (cols + 127) / 128 * 32;
-    (void)per;
-    *nv = units <= 2 * NORM_THREADS ? 2 : units <= 4 * NORM_THREADS ? 4 : 0;
-    const int64_t t = *nv ? (units + *nv - 1) / *nv : NORM_THREADS;
-    *threads = (int)((t + 31) / 32 * 32);
+    s.nv = units <= 2 * NORM_THREADS ? 2 : units <= 4 * NORM_THREADS ? 4 : 0;
+    const int64_t t = s.nv ? (units + s.nv - 1) / s.nv : NORM_THREADS;
+    s.threads = (int)((t + 31) / 32 * 32);
+    s.per_sm = sm_threads / s.threads < 1 ? 1 : sm_threads / s.threads;
+    s.stages = 2;
+    s.smem = 0;
+    if (!v8 || !s.nv) return s;
+    const size_t stage = (size_t)words * s.nv * s.threads * 16;
+    while (s.stages < NORM_MAX_STAGES && (s.stages + 1) * stage * s.per_sm <= NORM_SM_SMEM) ++s.stages;
+    s.smem = s.stages * stage;
+    if (s.smem <= NORM_SM_SMEM) return s;
+    return NormShape{0, NORM_THREADS, sm_threads / NORM_THREADS, 2, 0};
+}
+static int raise_smem(const void* f, size_t smem, const char* who) {
+    if (smem <= 40 * 1024) return ZERO_OK;
+    return cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), who);
 }
 
 static int check_weight(const zero_mat* w, int64_t cols, NormArgs& a) {
@@ -534,10 +702,10 @@ int zero_norm_forward(const zero_mat* x, const zero_mat* residual, const zero_ma
     if (rows < 0 || cols < 0) return fail(ZERO_EINVAL, "zero_norm_forward: negative rows or cols");
     if (cols > NORM_MAX_COLS) return fail(ZERO_ELIMIT, "zero_norm_forward: more than 1048576 columns");
     if (!(eps >= 0.f) || !(eps < INFINITY)) return fail(ZERO_EINVAL, "zero_norm_forward: eps must be finite and >= 0");
-    int rc = check_mat(x, rows, cols, FLOAT_TYPES, "zero_norm_forward: x");
-    if (rc == ZERO_OK) rc = check_mat(y, rows, cols, FLOAT_TYPES | 1u << ZERO_E4M3, "zero_norm_forward: y");
-    if (rc == ZERO_OK && residual) rc = check_mat(residual, rows, cols, FLOAT_TYPES, "zero_norm_forward: residual");
-    if (rc == ZERO_OK && h_out) rc = check_mat(h_out, rows, cols, FLOAT_TYPES, "zero_norm_forward: h_out");
+    int rc = check_mat(x, rows, cols, FLOAT_TYPES, "zero_norm_forward", "x");
+    if (rc == ZERO_OK) rc = check_mat(y, rows, cols, FLOAT_TYPES | 1u << ZERO_E4M3, "zero_norm_forward", "y");
+    if (rc == ZERO_OK && residual) rc = check_mat(residual, rows, cols, FLOAT_TYPES, "zero_norm_forward", "residual");
+    if (rc == ZERO_OK && h_out) rc = check_mat(h_out, rows, cols, FLOAT_TYPES, "zero_norm_forward", "h_out");
     if (rc != ZERO_OK) return rc;
     const int rt = residual ? residual->dtype : x->dtype;
     if (rt != x->dtype && rt != ZERO_F32)
@@ -562,7 +730,7 @@ int zero_norm_forward(const zero_mat* x, const zero_mat* residual, const zero_ma
     a.y = y->data;
     a.ldy = y->ld;
     a.rows = rows;
-    a.cols = cols;
+    a.cols = (int)cols;
     a.eps = eps;
     a.y8 = y8;
     a.block128 = y8 && scale_block == 128;
@@ -572,11 +740,17 @@ int zero_norm_forward(const zero_mat* x, const zero_mat* residual, const zero_ma
     const bool y_ok = y8 ? aligned(y->data, 8) && (rows == 1 || y->ld % 8 == 0) : rows_aligned(*y, rows);
     const bool v8 = cols % 8 == 0 && rows_aligned(*x, rows) && y_ok && (!residual || rows_aligned(*residual, rows)) &&
                     (!h_out || rows_aligned(*h_out, rows));
-    int nv, threads;
-    shape_of(cols, v8, &nv, &threads);
+    const NormShape p = shape_of(cols, v8, words_of(x->dtype) + words_of(rt), NORM_FORWARD_THREADS);
+    a.stages = p.stages;
+    const int sms = sm_count();
+    if (!sms) return ZERO_ECUDA;
+    const void* f = norm_fn(true, x->dtype, rt, v8, p.nv);
+    rc = raise_smem(f, p.smem, "zero_norm_forward shared-memory size");
+    if (rc != ZERO_OK) return rc;
+    const int64_t most = (int64_t)sms * p.per_sm;
     void* args[] = {&a};
-    return cuda_fail(launch_after_previous(norm_fn(true, x->dtype, rt, v8, nv), (int)(rows < 1 << 30 ? rows : 1 << 30),
-                                           threads, args, 0, static_cast<cudaStream_t>(stream)),
+    return cuda_fail(launch_after_previous(f, (int)(rows < most ? rows : most), p.threads, args, p.smem,
+                                           static_cast<cudaStream_t>(stream)),
                      "zero_norm_forward launch");
 }
 
@@ -589,11 +763,11 @@ int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* we
                        void* workspace, size_t workspace_bytes, void* stream) {
     if (rows < 0 || cols < 0) return fail(ZERO_EINVAL, "zero_norm_backward: negative rows or cols");
     if (cols > NORM_MAX_COLS) return fail(ZERO_ELIMIT, "zero_norm_backward: more than 1048576 columns");
-    int rc = check_mat(dy, rows, cols, FLOAT_TYPES, "zero_norm_backward: dy");
-    if (rc == ZERO_OK) rc = check_mat(h, rows, cols, FLOAT_TYPES, "zero_norm_backward: h");
-    if (rc == ZERO_OK) rc = check_mat(dx, rows, cols, FLOAT_TYPES, "zero_norm_backward: dx");
-    if (rc == ZERO_OK && dh) rc = check_mat(dh, rows, cols, FLOAT_TYPES, "zero_norm_backward: dh");
-    if (rc == ZERO_OK && dw) rc = check_mat(dw, 1, cols, FLOAT_TYPES, "zero_norm_backward: dw");
+    int rc = check_mat(dy, rows, cols, FLOAT_TYPES, "zero_norm_backward", "dy");
+    if (rc == ZERO_OK) rc = check_mat(h, rows, cols, FLOAT_TYPES, "zero_norm_backward", "h");
+    if (rc == ZERO_OK) rc = check_mat(dx, rows, cols, FLOAT_TYPES, "zero_norm_backward", "dx");
+    if (rc == ZERO_OK && dh) rc = check_mat(dh, rows, cols, FLOAT_TYPES, "zero_norm_backward", "dh");
+    if (rc == ZERO_OK && dw) rc = check_mat(dw, 1, cols, FLOAT_TYPES, "zero_norm_backward", "dw");
     if (rc != ZERO_OK) return rc;
     const int rt = h->dtype;
     if (rt != dy->dtype && rt != ZERO_F32) return fail(ZERO_EINVAL, "zero_norm_backward: h is in dy's type or fp32");
@@ -616,21 +790,23 @@ int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* we
     a.y = dx->data;
     a.ldy = dx->ld;
     a.rows = rows;
-    a.cols = cols;
+    a.cols = (int)cols;
     a.rstd = const_cast<float*>(rstd);
     a.part = dw ? static_cast<float*>(workspace) : nullptr;
     const bool v8 = cols % 8 == 0 && rows_aligned(*dy, rows) && rows_aligned(*h, rows) && rows_aligned(*dx, rows) &&
                     (!dh || rows_aligned(*dh, rows));
-    int nv, threads;
-    shape_of(cols, v8, &nv, &threads);
+    const NormShape p = shape_of(cols, v8, words_of(dy->dtype) + 2 * words_of(rt), NORM_BACKWARD_THREADS);
+    a.stages = p.stages;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* args[] = {&a};
-    int64_t g = 2 * (int64_t)sms;
+    int64_t g = (int64_t)p.per_sm * sms;
     if (g > NORM_MAX_GRID) g = NORM_MAX_GRID;
     if (g > rows) g = rows;
-    const void* f = norm_fn(false, dy->dtype, rt, v8, nv);
+    const void* f = norm_fn(false, dy->dtype, rt, v8, p.nv);
+    rc = raise_smem(f, p.smem, "zero_norm_backward shared-memory size");
+    if (rc != ZERO_OK) return rc;
     int parts = (int)g;
-    if (nv == 0 && dw && rows > 0) {
+    if (p.nv == 0 && dw && rows > 0) {
         // dw first: dx may be written over dy or dh
         const int64_t chunks = (cols + 127) / 128;
         int64_t shares = (8 * (int64_t)sms + chunks - 1) / chunks;
@@ -647,8 +823,8 @@ int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* we
         if (rc != ZERO_OK) return rc;
     }
     if (rows > 0) {
-        if (nv == 0) g = rows < 1 << 30 ? rows : 1 << 30;
-        rc = cuda_fail(launch_after_previous(f, (int)g, threads, args, 0, s), "zero_norm_backward launch");
+        if (p.nv == 0) g = rows < 1 << 30 ? rows : 1 << 30;
+        rc = cuda_fail(launch_after_previous(f, (int)g, p.threads, args, p.smem, s), "zero_norm_backward launch");
         if (rc != ZERO_OK) return rc;
     }
     if (!dw) return ZERO_OK;
@@ -657,7 +833,7 @@ int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* we
     int64_t nc = cols;
     void* out = dw->data;
     void* wargs[] = {&part, &n, &nc, &out, &dt, &accumulate};
-    return cuda_fail(launch_after_previous((const void*)k_norm_dw, (int)((cols + 31) / 32), 256, wargs, 0, s),
+    return cuda_fail(launch_after_previous((const void*)k_norm_dw, (int)((cols + 31) / 32), 1024, wargs, 0, s),
                      "zero_norm_backward dw reduction launch");
 }
 
