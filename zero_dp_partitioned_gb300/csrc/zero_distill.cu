@@ -144,11 +144,6 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
 // Store a pair at the same shared-memory address of block `rank` of the cluster.
 __device__ __forceinline__ void store_remote(float2* local, int rank, float2 v) {
     const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local));

@@ -203,6 +203,12 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s) {
     return t;
 }
 
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // ---------------------------------------------------------------- host
 // A matrix argument: not NULL, one of the types in `types` (a bit per code),
 // rows at least `cols` apart, aligned to its element.

@@ -64,143 +64,256 @@ __device__ __forceinline__ float2 from_e2m1(uint32_t byte) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// 8 elements of a row from column c; columns past the end are 0.
-template <int DT>
-__device__ __forceinline__ void read8(const void* row, int64_t c, int64_t cols, bool vec, float (&v)[8]) {
-    if (vec && c + 8 <= cols) {
-        widen8<DT>(ld8_stream<DT>(row, c), v);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? ld1<DT>(row, c + e) : 0.f;
+// A scale tile (128 rows by 4 blocks, as ZERO_MX4_TILES lays it out) from
+// shared memory to where q keeps it; i: which of the block's 128 threads.
+__device__ __forceinline__ void put_scales(const Mx4Dev& q, const uint8_t* tile, int64_t rows, int64_t tr, int64_t tb, int i) {
+    if (q.tiled) {
+        if (i < 32 && tr * 128 < rows && tb < q.tiles)
+            reinterpret_cast<uint4*>(q.scales + (tr * q.tiles + tb) * 512)[i] = reinterpret_cast<const uint4*>(tile)[i];
+    } else if (tr * 128 + i < rows) {
+        for (int b = 0; b < 4; ++b)
+            if (tb * 4 + b < q.blocks)
+                q.scales[(tr * 128 + i) * q.blocks + tb * 4 + b] = tile[(i & 31) * 16 + (i >> 5) * 4 + b];
     }
 }
 
-__device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
-    uint32_t t = 0;
+// 8 elements of a row from column c, as they lie; columns past the end are 0.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> read8(const void* row, int64_t c, int64_t cols, bool vec) {
+    if (vec && c + 8 <= cols) return ld8_stream<DT>(row, c);
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t = max(t, abs_bits(v[e]));
-    return t;
+    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? ld1<DT>(row, c + e) : 0.f;
+    return narrow8<DT>(v);
 }
 
-// Along the rows.  A warp takes 256 columns of a row (8 blocks, a step of the
-// product's tiles); rows and columns of the scales' padding are walked too.
+// The bits of the largest magnitude of 8 elements (ordered as unsigned
+// integers, NaN on top): of the fp32 value, or of a 16-bit one, two compared
+// at a time.
+template <int DT>
+__device__ __forceinline__ uint32_t top8(const Raw8<DT>& r) {
+    if constexpr (DT == ZERO_F32) {
+        uint32_t t = 0;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+            t = max(max(t, max(r.w[w].x & 0x7FFFFFFFu, r.w[w].y & 0x7FFFFFFFu)),
+                    max(r.w[w].z & 0x7FFFFFFFu, r.w[w].w & 0x7FFFFFFFu));
+        return t;
+    } else {
+        const uint32_t t = __vmaxu2(__vmaxu2(r.w[0].x & 0x7FFF7FFFu, r.w[0].y & 0x7FFF7FFFu),
+                                    __vmaxu2(r.w[0].z & 0x7FFF7FFFu, r.w[0].w & 0x7FFF7FFFu));
+        return max(t & 0xFFFFu, t >> 16);
+    }
+}
+// The scale byte from such bits.
+template <int DT>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+    if constexpr (DT == ZERO_F32) return mx4_scale(top);
+    else if constexpr (DT == ZERO_BF16) return mx4_scale(top << 16);
+    else return mx4_scale(__float_as_uint(Half16<DT>::widen(top)));
+}
+// The codes of 8 elements, scaled.
+template <int DT>
+__device__ __forceinline__ uint32_t codes8(const Raw8<DT>& r, uint64_t inv) {
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float2 p = unpack2(mul2(pair8<DT>(r, q), inv));
+        v[2 * q] = p.x;
+        v[2 * q + 1] = p.y;
+    }
+    return to_e2m1(v);
+}
+
+// Along the rows.  A warp takes up to MX4_SPAN pieces of 256 columns of a row
+// (8 blocks each, a step of the product's tiles), their loads issued together;
+// rows and columns of the scales' padding are walked too.
+constexpr int MX4_SPAN = 4;
 template <int DT>
 __global__ void __launch_bounds__(MX4_THREADS) k_mx4_rows(const __grid_constant__ QuantArgs a) {
     pdl_wait();
     pdl_launch_next();
     const int64_t rows = a.q.tiled ? (a.rows + 127) / 128 * 128 : a.rows;
-    const int64_t per = (a.cols + 255) / 256, n = rows * per;
+    const int64_t pieces = (a.cols + 255) / 256, per = (pieces + MX4_SPAN - 1) / MX4_SPAN, n = rows * per;
     const int lane = threadIdx.x & 31;
     const int64_t stride = (int64_t)gridDim.x * (MX4_THREADS / 32);
     for (int64_t i = (int64_t)blockIdx.x * (MX4_THREADS / 32) + (threadIdx.x >> 5); i < n; i += stride) {
-        const int64_t r = i / per, c = (i - r * per) * 256 + lane * 8, b = c >> 5;
-        float v[8];
-        if (r < a.rows) {
-            read8<DT>(static_cast<const char*>(a.src) + r * a.ld * Elem<DT>::SIZE, c, a.cols, a.aligned16, v);
-        } else {
+        const int64_t r = i / per, p0 = (i - r * per) * MX4_SPAN;
+        const int64_t c0 = p0 * 256 + lane * 8;
+        const char* row = static_cast<const char*>(a.src) + r * a.ld * Elem<DT>::SIZE;
+        Raw8<DT> v[MX4_SPAN];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        for (int k = 0; k < MX4_SPAN; ++k) {
+            if (r < a.rows && c0 + k * 256 < a.cols) {
+                v[k] = read8<DT>(row, c0 + k * 256, a.cols, a.aligned16);
+            } else {
+#pragma unroll
+                for (auto& w : v[k].w) w = make_uint4(0, 0, 0, 0);
+            }
         }
-        const uint32_t byte = mx4_scale(lanes_max<4>(top8(v)));
-        const float inv = mx4_inverse(byte);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= inv;
-        if (r < a.rows && b < a.q.blocks)
-            *reinterpret_cast<uint32_t*>(a.q.data + r * a.q.ld + c / 2) = to_e2m1(v);
-        // the 4 blocks of 16 lanes make one word of a tile
-        uint32_t word = byte << (8 * ((lane >> 2) & 3));
-        word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-        word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
-        if (a.q.tiled) {
-            if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(a.q.scales + mx4_tiled_at(r, b, a.q.tiles)) = word;
-        } else if ((lane & 3) == 0 && b < a.q.blocks) {
-            a.q.scales[r * a.q.blocks + b] = (uint8_t)byte;
+        for (int k = 0; k < MX4_SPAN; ++k) {
+            if (p0 + k >= pieces) break;
+            const int64_t c = c0 + k * 256, b = c >> 5;
+            const uint32_t byte = scale_byte<DT>(lanes_max<4>(top8<DT>(v[k])));
+            const float inv = mx4_inverse(byte);
+            const uint32_t code = codes8<DT>(v[k], pack2(inv, inv));
+            if (r < a.rows && b < a.q.blocks) *reinterpret_cast<uint32_t*>(a.q.data + r * a.q.ld + c / 2) = code;
+            // the 4 blocks of 16 lanes make one word of a tile
+            uint32_t word = byte << (8 * ((lane >> 2) & 3));
+            word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
+            word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
+            if (a.q.tiled) {
+                if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(a.q.scales + mx4_tiled_at(r, b, a.q.tiles)) = word;
+            } else if ((lane & 3) == 0 && b < a.q.blocks) {
+                a.q.scales[r * a.q.blocks + b] = (uint8_t)byte;
+            }
         }
     }
 }
 
-__device__ __forceinline__ void put_scale(const Mx4Dev& q, int64_t r, int64_t rows, int64_t b, uint32_t byte) {
-    if (q.tiled) {
-        if (r < (rows + 127) / 128 * 128 && b < q.tiles * 4) q.scales[mx4_tiled_at(r, b, q.tiles)] = (uint8_t)byte;
-    } else if (r < rows && b < q.blocks) {
-        q.scales[r * q.blocks + b] = (uint8_t)byte;
-    }
-}
+// Along the columns, and along the rows too if they are wanted.  A block takes
+// 128 by 128 elements -- one scale tile in each direction -- and a warp 32 of
+// its rows: it quantises the rows from its registers, leaves them in its own
+// piece of shared memory, and then quantises the columns, two to a lane.  The
+// columns' codes and both scale tiles are put together in shared memory, so
+// that they leave in pieces of 64 and 512 consecutive bytes.
+template <int DT>
+constexpr int mx4_both_smem() { return 128 * 128 * Elem<DT>::SIZE; }
 
-// Along the columns, and along the rows too if they are wanted.
 template <int DT>
 __global__ void __launch_bounds__(128) k_mx4_both(const __grid_constant__ QuantArgs a) {
-    __shared__ __align__(16) float tile[4][DT == ZERO_F32 ? 32 * 64 : 32 * 32];
+    extern __shared__ __align__(16) uint8_t tile_raw[];
+    __shared__ __align__(16) uint4 codes[128][4];
+    __shared__ __align__(16) uint8_t scale_q[512], scale_t[512];
     pdl_wait();
     pdl_launch_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // a block's 4 warps take 128 rows; both directions are padded to 256 for the scales
-    const int64_t nr = (a.rows + 255) / 256 * 2, nc = (a.cols + 255) / 256 * 4;
+    uint8_t* s = tile_raw + warp * 32 * 128 * Elem<DT>::SIZE;
+    // both directions are padded to 256 for the scales
+    const int64_t nr = (a.rows + 255) / 256 * 2, nc = (a.cols + 255) / 256 * 2;
     for (int64_t i = blockIdx.x; i < nr * nc; i += gridDim.x) {
-        const int64_t r0 = (i / nc) * 128 + warp * 32, c0 = (i % nc) * 64;
-        float* s = tile[warp];
-        const int64_t c = c0 + (lane & 7) * 8;
+        const int64_t tr = i / nc, tc = i - tr * nc, r0 = tr * 128 + warp * 32, c0 = tc * 128;
+        const int64_t c = c0 + (lane & 15) * 8;
+        const char* src = static_cast<const char*>(a.src) + c * Elem<DT>::SIZE;
+        const bool inside = a.aligned16 && r0 + 32 <= a.rows && c0 + 128 <= a.cols;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int rr = k * 4 + (lane >> 3);
-            const int64_t r = r0 + rr;
-            float v[8];
-            if (r < a.rows && c < a.cols) {
-                read8<DT>(static_cast<const char*>(a.src) + r * a.ld * Elem<DT>::SIZE, c, a.cols, a.aligned16, v);
-            } else {
+        for (int half = 0; half < 2; ++half) {
+            Raw8<DT> v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 0.f;
+            for (int k = 0; k < 8; ++k) {
+                const int64_t r = r0 + half * 16 + k * 2 + (lane >> 4);
+                if (inside) {
+                    v[k] = ld8_stream<DT>(src + r * a.ld * Elem<DT>::SIZE, 0);
+                } else if (r < a.rows && c < a.cols) {
+                    v[k] = read8<DT>(static_cast<const char*>(a.src) + r * a.ld * Elem<DT>::SIZE, c, a.cols, a.aligned16);
+                } else {
+#pragma unroll
+                    for (auto& w : v[k].w) w = make_uint4(0, 0, 0, 0);
+                }
             }
-            if (a.t.data) st8<DT>(s, rr * 64 + (lane & 7) * 8, narrow8<DT>(v));
-            if (a.q.data) {
-                const uint32_t byte = mx4_scale(lanes_max<4>(top8(v)));
-                const float inv = mx4_inverse(byte);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= inv;
-                if (r < a.rows && c / 32 < a.q.blocks)
-                    *reinterpret_cast<uint32_t*>(a.q.data + r * a.q.ld + c / 2) = to_e2m1(v);
-                if ((lane & 3) == 0) put_scale(a.q, r, a.rows, c / 32, byte);
+            for (int k = 0; k < 8; ++k) {
+                const int rr = half * 16 + k * 2 + (lane >> 4);
+                const int64_t r = r0 + rr;
+                if (a.t.data) st8<DT>(s, rr * 128 + (lane & 15) * 8, v[k]);
+                if (a.q.data) {
+                    const uint32_t byte = scale_byte<DT>(lanes_max<4>(top8<DT>(v[k])));
+                    const float inv = mx4_inverse(byte);
+                    const uint32_t code = codes8<DT>(v[k], pack2(inv, inv));
+                    if (r < a.rows && c < a.q.blocks * 32)
+                        *reinterpret_cast<uint32_t*>(a.q.data + r * a.q.ld + c / 2) = code;
+                    if ((lane & 3) == 0) scale_q[rr * 16 + warp * 4 + ((lane & 15) >> 2)] = (uint8_t)byte;
+                }
             }
         }
         __syncwarp();
         if (a.t.data) {
-            // columns c0 + 2 lane and the next, 32 rows: one block of each
-            float v[2][32];
-            uint32_t top[2] = {0, 0};
 #pragma unroll
-            for (int rr = 0; rr < 32; ++rr) {
+            for (int half = 0; half < 2; ++half) {
+                // columns c0 + 64 half + 2 lane and the next, this warp's 32 rows: one block of each
+                uint32_t top0 = 0, top1 = 0;
                 if constexpr (DT == ZERO_F32) {
-                    const float2 p = reinterpret_cast<const float2*>(s)[rr * 32 + lane];
-                    v[0][rr] = p.x;
-                    v[1][rr] = p.y;
+                    const float2* p = reinterpret_cast<const float2*>(s) + half * 32 + lane;
+                    float2 v[32];
+#pragma unroll
+                    for (int rr = 0; rr < 32; ++rr) {
+                        v[rr] = p[rr * 64];
+                        top0 = max(top0, abs_bits(v[rr].x));
+                        top1 = max(top1, abs_bits(v[rr].y));
+                    }
+                    const uint32_t b0 = mx4_scale(top0), b1 = mx4_scale(top1);
+                    const uint64_t inv = pack2(mx4_inverse(b0), mx4_inverse(b1));
+                    uint32_t w0[4], w1[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float x[8], y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 t = unpack2(mul2(pack2(v[q * 8 + e].x, v[q * 8 + e].y), inv));
+                            x[e] = t.x;
+                            y[e] = t.y;
+                        }
+                        w0[q] = to_e2m1(x);
+                        w1[q] = to_e2m1(y);
+                    }
+                    top0 = b0;
+                    top1 = b1;
+                    const int cc = half * 64 + 2 * lane, at = warp ^ (lane & 3);
+                    codes[cc][at] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+                    codes[cc + 1][at] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
                 } else {
-                    const uint32_t p = reinterpret_cast<const uint32_t*>(s)[rr * 32 + lane];
-                    v[0][rr] = Half16<DT>::widen(p & 0xFFFFu);
-                    v[1][rr] = Half16<DT>::widen(p >> 16);
+                    const uint32_t* p = reinterpret_cast<const uint32_t*>(s) + half * 32 + lane;
+                    uint32_t v[32], t = 0;
+#pragma unroll
+                    for (int rr = 0; rr < 32; ++rr) {
+                        v[rr] = p[rr * 64];
+                        t = __vmaxu2(t, v[rr] & 0x7FFF7FFFu);
+                    }
+                    const uint32_t b0 = scale_byte<DT>(t & 0xFFFFu), b1 = scale_byte<DT>(t >> 16);
+                    const uint64_t inv = pack2(mx4_inverse(b0), mx4_inverse(b1));
+                    uint32_t w0[4], w1[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float x[8], y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t u = v[q * 8 + e];
+                            const uint64_t both = DT == ZERO_BF16
+                                                      ? pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u))
+                                                      : pack2(Half16<DT>::widen(u & 0xFFFFu), Half16<DT>::widen(u >> 16));
+                            const float2 f = unpack2(mul2(both, inv));
+                            x[e] = f.x;
+                            y[e] = f.y;
+                        }
+                        w0[q] = to_e2m1(x);
+                        w1[q] = to_e2m1(y);
+                    }
+                    top0 = b0;
+                    top1 = b1;
+                    const int cc = half * 64 + 2 * lane, at = warp ^ (lane & 3);
+                    codes[cc][at] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+                    codes[cc + 1][at] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
                 }
-                top[0] = max(top[0], abs_bits(v[0][rr]));
-                top[1] = max(top[1], abs_bits(v[1][rr]));
-            }
-            const int64_t b = r0 / 32;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t col = c0 + 2 * lane + h;
-                const uint32_t byte = mx4_scale(top[h]);
-                const float inv = mx4_inverse(byte);
-                uint32_t w[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = v[h][q * 8 + e] * inv;
-                    w[q] = to_e2m1(x);
-                }
-                if (col < a.cols && b < a.t.blocks)
-                    *reinterpret_cast<uint4*>(a.t.data + col * a.t.ld + b * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                put_scale(a.t, col, a.cols, b, byte);
+                // row cc of the transpose's tile, block `warp` of its 4
+                const int cc = half * 64 + 2 * lane;
+                scale_t[(cc & 31) * 16 + (cc >> 5) * 4 + warp] = (uint8_t)top0;
+                scale_t[((cc + 1) & 31) * 16 + (cc >> 5) * 4 + warp] = (uint8_t)top1;
             }
         }
-        __syncwarp();
+        __syncthreads();
+        if (a.t.data) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int id = k * 128 + threadIdx.x, cc = id >> 2, ch = id & 3;
+                const int64_t b = tr * 4 + ch;
+                if (c0 + cc < a.cols && b < a.t.blocks)
+                    *reinterpret_cast<uint4*>(a.t.data + (c0 + cc) * a.t.ld + b * 16) = codes[cc][ch ^ ((cc >> 1) & 3)];
+            }
+            put_scales(a.t, scale_t, a.cols, tc, tr, threadIdx.x);
+        }
+        if (a.q.data) put_scales(a.q, scale_q, a.rows, tr, tc, 127 - threadIdx.x);
+        __syncthreads();
     }
 }
 
@@ -211,29 +324,47 @@ struct DequantArgs {
     int aligned16;
 };
 
+// A warp takes up to MX4_SPAN pieces of 256 columns of a row, 8 columns to a
+// lane and piece.
 template <int DT>
 __global__ void __launch_bounds__(MX4_THREADS) k_mx4_values(const __grid_constant__ DequantArgs a) {
     pdl_wait();
     pdl_launch_next();
-    const int64_t per = (a.cols + 7) / 8, n = a.rows * per;
-    for (int64_t i = (int64_t)blockIdx.x * MX4_THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * MX4_THREADS) {
-        const int64_t r = i / per, c = (i - r * per) * 8, b = c >> 5;
-        const uint32_t w = __ldcs(reinterpret_cast<const uint32_t*>(a.q.data + r * a.q.ld + c / 2));
-        const float s = mx4_value(a.q.scales[a.q.tiled ? mx4_tiled_at(r, b, a.q.tiles) : r * a.q.blocks + b]);
-        float v[8];
+    const int64_t per = (a.cols + 256 * MX4_SPAN - 1) / (256 * MX4_SPAN), n = a.rows * per;
+    const int lane = threadIdx.x & 31;
+    const int64_t stride = (int64_t)gridDim.x * (MX4_THREADS / 32);
+    for (int64_t i = (int64_t)blockIdx.x * (MX4_THREADS / 32) + (threadIdx.x >> 5); i < n; i += stride) {
+        const int64_t r = i / per, c0 = (i - r * per) * 256 * MX4_SPAN + lane * 8;
+        const uint8_t* data = a.q.data + r * a.q.ld + c0 / 2;
+        uint32_t w[MX4_SPAN], byte[MX4_SPAN];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float2 p = from_e2m1(w >> (8 * q) & 0xFFu);
-            v[2 * q] = p.x * s;
-            v[2 * q + 1] = p.y * s;
-        }
+        for (int k = 0; k < MX4_SPAN; ++k)
+            if (c0 + k * 256 < a.cols) {
+                const int64_t b = (c0 >> 5) + k * 8;
+                w[k] = __ldcs(reinterpret_cast<const uint32_t*>(data + k * 128));
+                byte[k] = a.q.scales[a.q.tiled ? mx4_tiled_at(r, b, a.q.tiles) : r * a.q.blocks + b];
+            }
         char* row = static_cast<char*>(a.dst) + r * a.ld * Elem<DT>::SIZE;
-        if (a.aligned16 && c + 8 <= a.cols) {
-            st8<DT>(row, c, narrow8<DT>(v));
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < a.cols) st1<DT>(row, c + e, v[e]);
+        for (int k = 0; k < MX4_SPAN; ++k) {
+            const int64_t c = c0 + k * 256;
+            if (c >= a.cols) break;
+            const float s = mx4_value(byte[k]);
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 p = from_e2m1(w[k] >> (8 * q) & 0xFFu);
+                const float2 f = unpack2(mul2(pack2(p.x, p.y), pack2(s, s)));
+                v[2 * q] = f.x;
+                v[2 * q + 1] = f.y;
+            }
+            if (a.aligned16 && c + 8 <= a.cols) {
+                st8<DT>(row, c, narrow8<DT>(v));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < a.cols) st1<DT>(row, c + e, v[e]);
+            }
         }
     }
 }
@@ -318,20 +449,25 @@ int zero_mx4_quantize(const zero_mat* src, int64_t rows, int64_t cols, const zer
     const int dt = src->dtype;
     const void* f;
     int grid, threads;
+    size_t smem = 0;
     if (out_t) {
         f = dt == ZERO_F32 ? (const void*)k_mx4_both<ZERO_F32>
           : dt == ZERO_BF16 ? (const void*)k_mx4_both<ZERO_BF16> : (const void*)k_mx4_both<ZERO_F16>;
         threads = 128;
-        grid = blocks_for((rows + 255) / 256 * 2 * ((cols + 255) / 256 * 4), 16);
+        smem = dt == ZERO_F32 ? mx4_both_smem<ZERO_F32>() : mx4_both_smem<ZERO_BF16>();
+        rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
+                       "zero_mx4_quantize shared-memory size");
+        if (rc != ZERO_OK) return rc;
+        grid = blocks_for((rows + 255) / 256 * 2 * ((cols + 255) / 256 * 2), dt == ZERO_F32 ? 2 : 5);
     } else {
         f = dt == ZERO_F32 ? (const void*)k_mx4_rows<ZERO_F32>
           : dt == ZERO_BF16 ? (const void*)k_mx4_rows<ZERO_BF16> : (const void*)k_mx4_rows<ZERO_F16>;
         threads = MX4_THREADS;
         const int64_t r = a.q.tiled ? (rows + 127) / 128 * 128 : rows;
-        grid = blocks_for((r * ((cols + 255) / 256) + 7) / 8, 8);
+        grid = blocks_for((r * ((cols + 256 * MX4_SPAN - 1) / (256 * MX4_SPAN)) + 7) / 8, 8);
     }
     void* args[] = {&a};
-    return cuda_fail(launch_after_previous(f, grid, threads, args, 0, static_cast<cudaStream_t>(stream)),
+    return cuda_fail(launch_after_previous(f, grid, threads, args, smem, static_cast<cudaStream_t>(stream)),
                      "zero_mx4_quantize launch");
 }
 
@@ -351,7 +487,7 @@ int zero_mx4_dequantize(const zero_mx4* src, const zero_mat* dst, void* stream) 
     const void* f = dt == ZERO_F32 ? (const void*)k_mx4_values<ZERO_F32>
                   : dt == ZERO_BF16 ? (const void*)k_mx4_values<ZERO_BF16> : (const void*)k_mx4_values<ZERO_F16>;
     void* args[] = {&a};
-    return cuda_fail(launch_after_previous(f, blocks_for((a.rows * ((a.cols + 7) / 8) + MX4_THREADS - 1) / MX4_THREADS, 16),
+    return cuda_fail(launch_after_previous(f, blocks_for((a.rows * ((a.cols + 256 * MX4_SPAN - 1) / (256 * MX4_SPAN)) + 7) / 8, 8),
                                            MX4_THREADS, args, 0, static_cast<cudaStream_t>(stream)),
                      "zero_mx4_dequantize launch");
 }

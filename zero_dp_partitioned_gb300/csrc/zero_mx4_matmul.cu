@@ -4,13 +4,20 @@
 //
 // A persistent block per SM walks tiles of 128 rows of one operand (X) by BN
 // rows of the other (Y).  Warp 0's first lane copies stages of 256 elements
-// of k into shared memory (TMA tiles of 128-byte rows, 128-byte swizzle; the
-// scales' tiles as plain bulk copies), warp 1's first lane moves the scales
-// to tensor memory and issues the four products of a stage, and warps 2 to 5
-// read the fp32 accumulator back, scale it and store it.  With BN = 256 the
-// two accumulators of 256 columns and the scales do not fit the 512 columns
-// of tensor memory side by side, so the accumulators overlap by 32 columns:
-// a tile's epilogue reads those 32 first and then lets the next tile start.
+// of k into shared memory (TMA tiles of 128-byte rows, 128-byte swizzle), the
+// last four warps load the stage's scales ahead into registers and store them
+// to tensor memory, warp 1's first lane issues the four products of a stage,
+// and warps 2 to 5 read the fp32 accumulator back, scale it and store it.
+//
+// The scales go by registers because shared memory is what bounds the loop: a
+// stage's products read 48 KB of it, its loads write 48 KB, in the 512 cycles
+// the products need.  Copied by TMA and then by tcgen05.cp, in order with the
+// products, they took 250 cycles of a stage of 975.
+//
+// With BN = 256 the two accumulators of 256 columns and three sets of scales
+// do not fit the 512 columns of tensor memory side by side, so the accumulators
+// overlap by 80 columns: a tile's epilogue reads those first and then lets
+// the next tile start.
 //
 // X is A, and Y is B, unless A has few rows (tokens): then X is B, the
 // weights, so that the 128 rows of a tile are all used, and the accumulator
@@ -30,25 +37,27 @@
 
 namespace zdp {
 
-constexpr int MM_THREADS = 192;
+constexpr int MM_THREADS = 320;
 constexpr int MM_BX = 128;
 constexpr int MM_KB = 128;                    // bytes of k in a stage: 256 elements
 constexpr int MM_HEADER = 1024;
-constexpr int MM_SF_COL = 480;                // tensor-memory column of the scales
+constexpr int MM_SF_COL = 432;                // tensor-memory column of the scales: sets of 24 columns, used by turns
+constexpr int MM_SF_SET = 24, MM_SF_SETS = 3;
 constexpr int MM_MAX_STAGES = 8;
 
 template <int BN>
 struct MmShape {
     static constexpr int Y_TILES = (BN + 127) / 128;           // 128-row scale tiles of Y
     static constexpr int X_BYTES = MM_BX * MM_KB, Y_BYTES = BN * MM_KB;
-    static constexpr int XS_BYTES = 1024, YS_BYTES = 1024 * Y_TILES;
-    static constexpr int STAGE = X_BYTES + Y_BYTES + XS_BYTES + YS_BYTES;
     // a stage starts on 1024 bytes (the swizzle's period)
-    static constexpr int STRIDE = (STAGE + 1023) / 1024 * 1024;
-    static constexpr int STAGES = (232448 - 2048) / STRIDE < MM_MAX_STAGES ? (232448 - 2048) / STRIDE : MM_MAX_STAGES;
-    static constexpr int SMEM = STAGES * STRIDE + 2048;
+    static constexpr int STAGE = X_BYTES + Y_BYTES;
+    static constexpr int STAGES = (232448 - 2048) / STAGE < MM_MAX_STAGES ? (232448 - 2048) / STAGE : MM_MAX_STAGES;
+    static constexpr int SMEM = STAGES * STAGE + 2048;
     static constexpr bool OVERLAP = BN == 256;
-    static constexpr int ACC1 = OVERLAP ? 224 : BN;            // column of the second accumulator
+    static constexpr int ACC1 = OVERLAP ? 176 : BN;            // column of the second accumulator
+    static constexpr int EARLY = OVERLAP ? 80 : BN;            // columns read before the next tile may start
+    static constexpr int SF_WORDS = 8 + 8 * Y_TILES;           // columns of a stage's scales: X, then Y
+    static_assert(STAGE % 1024 == 0 && SF_WORDS <= MM_SF_SET, "layout");
 };
 
 struct MmArgs {
@@ -57,6 +66,7 @@ struct MmArgs {
     int64_t ldd;
     int x_rows, y_rows;                       // rows of X and Y
     int x_tiles, y_tiles, k_steps;            // tiles of 128 and BN rows, stages of 256 elements
+    int xs_tiles, ys_tiles;                   // 128-row tiles of scales
     int dt, swap, wide_store;
     float alpha;
     int32_t* status;
@@ -73,9 +83,6 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, i
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                        bool add) {
     asm volatile(
@@ -84,6 +91,13 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((int)add)
         : "memory");
 }
+// A thread's words to its lane's consecutive columns.
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint4& a, const uint4& b) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(a.x), "r"(a.y),
+                 "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -99,15 +113,17 @@ __device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&v)[16]) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// 32 bytes to global memory, 32-byte aligned: a whole sector a lane.
+__device__ __forceinline__ void st32(void* p, const uint4& lo, const uint4& hi) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
+                 "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                 : "memory");
+}
 
-// Shared-memory descriptors.  Operand tiles: rows of 128 bytes in the 128-byte
-// swizzle, 8 rows (1024 bytes) from one group to the next.  Scale tiles: 32
-// rows of 16 bytes as they lie, 8 rows (128 bytes) to a group.
+// Shared-memory descriptor of an operand tile: rows of 128 bytes in the
+// 128-byte swizzle, 8 rows (1024 bytes) from one group to the next.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3FFF) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
-}
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(128 >> 4) << 32 | 1ull << 46;
 }
 // Instruction descriptor: both operands e2m1, scales e8m0, the shape, and
 // which half of a 4-byte word of scales is used.
@@ -116,12 +132,29 @@ __device__ __forceinline__ constexpr uint32_t mma_desc(int bn, int half) {
            (uint32_t)(MM_BX >> 4) << 24 | (uint32_t)(half * 2) << 29;
 }
 
+__device__ __forceinline__ bool mm_poll(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done;
+}
 // A bounded wait that also ends when another role of the block has given up.
+// A try is 16 polls, so that SPIN_LIMIT tries end after about a second.  The
+// first poll stands apart: with data at hand it takes 25 cycles, where
+// mbarrier.try_wait, or a poll inside the loop, takes 260 (the loop that issues
+// the products waited 520 cycles a stage for data that were there; 217 against
+// 200 us for 8192 x 14336 x 4096 with its quantisation).
 __device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, unsigned limit, volatile int* stop) {
-    for (unsigned it = 0; it < limit; it += 256) {
-        const unsigned n = limit - it < 256 ? limit - it : 256;
-        if (mbar_wait(bar, parity, n)) return true;
-        if (*stop) return false;
+    if (limit && mm_poll(bar, parity)) return true;
+    for (unsigned it = 0; it < limit; ++it) {
+        for (int p = 0; p < 16; ++p)
+            if (mm_poll(bar, parity)) return true;
+        if (stop && *stop) return false;
     }
     return false;
 }
@@ -143,11 +176,13 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023) & ~1023u;
     uint8_t* head = smem_raw + (base - raw);
-    // header: full[8], empty[8], acc_full[2], acc_free[2], drained, then the tensor-memory address, stop flag and count
-    const uint32_t full = base, empty = base + 64, acc_full = base + 128, acc_free = base + 144, drained = base + 160;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 168);
-    volatile int* stop = reinterpret_cast<volatile int*>(head + 172);
-    volatile int* loaded = reinterpret_cast<volatile int*>(head + 176);   // stages whose loads were issued
+    // header: full[8], empty[8], acc_full[2], acc_free[2], drained, sf_full[4], then the tensor-memory address, stop
+    // flag and count
+    const uint32_t full = base, empty = base + 64, acc_full = base + 128, acc_free = base + 144, drained = base + 160,
+                   sf_full = base + 168;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 200);
+    volatile int* stop = reinterpret_cast<volatile int*>(head + 204);
+    volatile int* loaded = reinterpret_cast<volatile int*>(head + 208);   // stages whose loads were issued
     const uint32_t stages = base + MM_HEADER;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -156,17 +191,18 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
         }
-        mbar_init(acc_full, 1);
-        mbar_init(acc_full + 8, 1);
-        mbar_init(acc_free, 4);
-        mbar_init(acc_free + 8, 4);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(acc_full + 8 * s, 1);
+            mbar_init(acc_free + 8 * s, 4);
+        }
+        for (int s = 0; s < MM_SF_SETS; ++s) mbar_init(sf_full + 8 * s, 4);
         mbar_init(drained, 1);
         fence_mbar_init();
         *stop = 0;
         *loaded = 0;
     }
     if (warp == 1)
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + 168) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + 200) : "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -188,18 +224,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = full + 8 * st, at = stages + st * S::STRIDE;
+                    // rows past the end read as 0
+                    const uint32_t bar = full + 8 * st, at = stages + st * S::STAGE;
                     mbar_expect_tx(bar, S::STAGE);
                     tma_tile(at, &xmap, k * MM_KB, x * MM_BX, bar);
                     tma_tile(at + S::X_BYTES, &ymap, k * MM_KB, y * BN, bar);
-                    bulk_load(at + S::X_BYTES + S::Y_BYTES, a.xs + ((int64_t)x * K + k) * 1024, 1024, bar);
-#pragma unroll
-                    for (int q = 0; q < S::Y_TILES; ++q) {
-                        // the last tile of Y may have fewer than BN rows: its last scale tile again, for rows that are 0
-                        const int yt = min(BN >= 128 ? y * S::Y_TILES + q : y * BN / 128, (a.y_rows + 127) / 128 - 1);
-                        bulk_load(at + S::X_BYTES + S::Y_BYTES + 1024 + 1024 * q, a.ys + ((int64_t)yt * K + k) * 1024, 1024,
-                                  bar);
-                    }
                     *loaded = ++count;
                     if (++st == S::STAGES) {
                         st = 0;
@@ -210,8 +239,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            int st = 0, n = 0;
-            uint32_t phase = 0;
+            int st = 0, set = 0, n = 0;
+            uint32_t phase = 0, set_phase = 0;
             for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x, ++n) {
                 // the accumulator of tile n was last used by tile n - 2; overlapping ones wait for tile n - 1's first
                 // columns (its epilogue began after tile n - 2's ended)
@@ -223,33 +252,103 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 tc_fence_after();
                 const uint32_t d = tmem + (n & 1 ? S::ACC1 : 0);
                 for (int k = 0; k < K; ++k) {
-                    if (!mm_wait(full + 8 * st, phase, a.spin_limit, stop)) {
+                    if (!mm_wait(sf_full + 8 * set, set_phase, a.spin_limit, stop) ||
+                        !mm_wait(full + 8 * st, phase, a.spin_limit, stop)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t at = stages + st * S::STRIDE, sx = at + S::X_BYTES + S::Y_BYTES, sy = sx + 1024;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tc_copy_scales(tmem + MM_SF_COL + 4 * h, scale_desc(sx + 512 * h));
-#pragma unroll
-                        for (int q = 0; q < S::Y_TILES; ++q)
-                            tc_copy_scales(tmem + MM_SF_COL + 8 + 4 * (h * S::Y_TILES + q), scale_desc(sy + 1024 * q + 512 * h));
-                    }
+                    const uint32_t at = stages + st * S::STAGE, sf = tmem + MM_SF_COL + set * MM_SF_SET;
                     const uint64_t dx = operand_desc(at), dy = operand_desc(at + S::X_BYTES);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        tc_mma(d, dx + 2 * q, dy + 2 * q, mma_desc(BN, q & 1), tmem + MM_SF_COL + 4 * (q >> 1),
-                               tmem + MM_SF_COL + 8 + 4 * S::Y_TILES * (q >> 1), k > 0 || q > 0);
+                        tc_mma(d, dx + 2 * q, dy + 2 * q, mma_desc(BN, q & 1), sf + 4 * (q >> 1),
+                               sf + 8 + 4 * S::Y_TILES * (q >> 1), k > 0 || q > 0);
                     tc_commit(empty + 8 * st);
                     if (++st == S::STAGES) {
                         st = 0;
                         phase ^= 1;
                     }
+                    if (++set == MM_SF_SETS) {
+                        set = 0;
+                        set_phase ^= 1;
+                    }
                 }
                 if (ok) tc_commit(acc_full + 8 * (n & 1));
             }
             tc_commit(drained);
+        }
+    } else if (warp >= 6) {
+        // Stage i's scales: lane l of every quarter holds rows l, 32 + l, 64 + l and 96 + l of a tile, a word of 4 blocks
+        // each, 16 bytes as they lie in the tile.  Loaded two stages ahead; a set is free when the stage that used it last is done.
+        const uint32_t sf0 = tmem + MM_SF_COL + ((uint32_t)((warp & 3) * 32) << 16);
+        struct Words {
+            uint4 x[2], y[2][S::Y_TILES];
+        };
+        int lt = blockIdx.x, lk = 0, lx = 0, ly = 0;          // the next stage to load
+        if (lt < n_tiles) tile_at(a, lt, lx, ly);
+        auto load = [&](Words& w) {
+            if (lt >= n_tiles) return;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            const int yt = BN >= 128 ? ly * S::Y_TILES : 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                w.x[h] = lx < a.xs_tiles ? __ldg(reinterpret_cast<const uint4*>(a.xs + ((int64_t)lx * K + lk) * 1024 + h * 512) + lane)
+                                         : zero;
+#pragma unroll
+                for (int q = 0; q < S::Y_TILES; ++q)
+                    w.y[h][q] = yt + q < a.ys_tiles
+                                    ? __ldg(reinterpret_cast<const uint4*>(a.ys + ((int64_t)(yt + q) * K + lk) * 1024 + h * 512) + lane)
+                                    : zero;
+            }
+            if (++lk == K) {
+                lk = 0;
+                lt += gridDim.x;
+                if (lt < n_tiles) tile_at(a, lt, lx, ly);
+            }
+        };
+        const int total = blockIdx.x < n_tiles ? ((n_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * K : 0;
+        static_assert(S::STAGES > MM_SF_SETS, "a barrier of the ring is waited for within its turn");
+        int set = 0, old = 0;                                 // the set of stage i, and the ring's place of stage i - sets
+        uint32_t old_phase = 0;
+        auto put = [&](int i, const Words& w) {
+            if (i >= MM_SF_SETS) {
+                ok = mm_wait(empty + 8 * old, old_phase, a.spin_limit, stop);
+                if (++old == S::STAGES) {
+                    old = 0;
+                    old_phase ^= 1;
+                }
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    return false;
+                }
+                tc_fence_after();
+            }
+            const uint32_t sf = sf0 + set * MM_SF_SET;
+            tc_st8(sf, w.x[0], w.x[1]);
+            if constexpr (S::Y_TILES == 2) {
+                tc_st8(sf + 8, w.y[0][0], w.y[0][1]);
+                tc_st8(sf + 16, w.y[1][0], w.y[1][1]);
+            } else {
+                tc_st8(sf + 8, w.y[0][0], w.y[1][0]);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sf_full + 8 * set);
+            if (++set == MM_SF_SETS) set = 0;
+            return true;
+        };
+        Words w0, w1;
+        load(w0);
+        load(w1);
+        for (int i = 0; i < total; i += 2) {
+            if (!put(i, w0)) break;
+            load(w0);
+            if (i + 1 < total) {
+                if (!put(i + 1, w1)) break;
+                load(w1);
+            }
         }
     } else {
         const int quarter = warp & 3;                        // the 32 lanes of tensor memory this warp can read
@@ -267,50 +366,65 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             const uint32_t d = tmem + (acc ? S::ACC1 : 0) + ((uint32_t)(quarter * 32) << 16);
             const int64_t xr = (int64_t)x * MM_BX + quarter * 32 + lane;
             const int64_t y0 = (int64_t)y * BN;
-            // 16 columns at a time; the overlapping 32 first: the last of accumulator 0, the first of accumulator 1
-            for (int c = 0; c < BN / 16; ++c) {
-                const int col = S::OVERLAP && !acc ? ((c + 14) & 15) * 16 : c * 16;
-                uint32_t v[16];
-                __syncwarp();
-                tc_ld16(d + col, v);
-                tc_wait_ld();
-                if (c == (S::OVERLAP ? 1 : BN / 16 - 1)) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(acc_free + 8 * acc);
-                }
-                if (xr >= a.x_rows) continue;
+            auto put = [&](int col, const uint32_t (&v)[16]) {
+                if (xr >= a.x_rows) return;
                 if (a.swap) {
                     // a lane holds one column of D: the warp stores 32 consecutive ones of each row
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         if (y0 + col + e < a.y_rows)
                             st1_any(a.d, (y0 + col + e) * a.ldd + xr, __uint_as_float(v[e]) * a.alpha, a.dt);
-                } else {
-                    const int64_t at = xr * a.ldd + y0 + col;
-                    if (a.wide_store && y0 + col + 16 <= a.y_rows) {
-                        float lo[8], hi[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            lo[e] = __uint_as_float(v[e]) * a.alpha;
-                            hi[e] = __uint_as_float(v[8 + e]) * a.alpha;
-                        }
-                        if (a.dt == ZERO_F32) {
-                            st8<ZERO_F32>(a.d, at, narrow8<ZERO_F32>(lo));
-                            st8<ZERO_F32>(a.d, at + 8, narrow8<ZERO_F32>(hi));
-                        } else if (a.dt == ZERO_BF16) {
-                            st8<ZERO_BF16>(a.d, at, narrow8<ZERO_BF16>(lo));
-                            st8<ZERO_BF16>(a.d, at + 8, narrow8<ZERO_BF16>(hi));
-                        } else {
-                            st8<ZERO_F16>(a.d, at, narrow8<ZERO_F16>(lo));
-                            st8<ZERO_F16>(a.d, at + 8, narrow8<ZERO_F16>(hi));
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (y0 + col + e < a.y_rows) st1_any(a.d, at + e, __uint_as_float(v[e]) * a.alpha, a.dt);
-                    }
+                    return;
                 }
+                const int64_t at = xr * a.ldd + y0 + col;
+                if (a.wide_store && y0 + col + 16 <= a.y_rows) {
+                    float lo[8], hi[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        lo[e] = __uint_as_float(v[e]) * a.alpha;
+                        hi[e] = __uint_as_float(v[8 + e]) * a.alpha;
+                    }
+                    if (a.dt == ZERO_F32) {
+                        const Raw8<ZERO_F32> l = narrow8<ZERO_F32>(lo), h = narrow8<ZERO_F32>(hi);
+                        st32(static_cast<float*>(a.d) + at, l.w[0], l.w[1]);
+                        st32(static_cast<float*>(a.d) + at + 8, h.w[0], h.w[1]);
+                    } else if (a.dt == ZERO_BF16) {
+                        st32(static_cast<uint16_t*>(a.d) + at, narrow8<ZERO_BF16>(lo).w[0], narrow8<ZERO_BF16>(hi).w[0]);
+                    } else {
+                        st32(static_cast<uint16_t*>(a.d) + at, narrow8<ZERO_F16>(lo).w[0], narrow8<ZERO_F16>(hi).w[0]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (y0 + col + e < a.y_rows) st1_any(a.d, at + e, __uint_as_float(v[e]) * a.alpha, a.dt);
+                }
+            };
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_free + 8 * acc);
+            };
+            int col = 0, end = BN;
+            if constexpr (S::OVERLAP) {
+                // the columns that the other accumulator shares first, all at once: the next tile waits for them
+                uint32_t v[S::EARLY / 16][16];
+                const int at = acc ? 0 : BN - S::EARLY;
+#pragma unroll
+                for (int c = 0; c < S::EARLY / 16; ++c) tc_ld16(d + at + 16 * c, v[c]);
+                tc_wait_ld();
+                release();
+#pragma unroll
+                for (int c = 0; c < S::EARLY / 16; ++c) put(at + 16 * c, v[c]);
+                if (acc) col = S::EARLY;
+                else end = BN - S::EARLY;
+            }
+            for (; col < end; col += 16) {
+                uint32_t v[16];
+                __syncwarp();
+                tc_ld16(d + col, v);
+                tc_wait_ld();
+                if (!S::OVERLAP && col + 16 == end) release();
+                put(col, v);
             }
         }
     }
@@ -321,12 +435,12 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // what was issued and not waited for: the products (their shared and tensor memory), and after a stop the loads
+    // what was issued and not waited for: the products, and after a stop the loads
     if (threadIdx.x == 32) {
-        mbar_wait(drained, 0, a.drain_limit);
+        mm_wait(drained, 0, a.drain_limit, nullptr);
         if (*stop)
             for (int c = max(0, *loaded - S::STAGES); c < *loaded; ++c)
-                mbar_wait(full + 8 * (c % S::STAGES), (uint32_t)(c / S::STAGES) & 1, a.drain_limit);
+                mm_wait(full + 8 * (c % S::STAGES), (uint32_t)(c / S::STAGES) & 1, a.drain_limit, nullptr);
     }
     tc_fence_before();
     __syncthreads();
@@ -363,8 +477,7 @@ static EncodeFn encode_fn() {
 static int make_map(CUtensorMap* map, const zero_mx4& m, int box_rows) {
     EncodeFn fn = encode_fn();
     if (!fn) return fail(ZERO_ECUDA, "zero_mx4_matmul: the driver has no cuTensorMapEncodeTiled");
-    const cuuint64_t dims[2] = {(cuuint64_t)(mx4_blocks(m.cols) * 16), (cuuint64_t)m.rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)m.ld};
+    const cuuint64_t dims[2] = {(cuuint64_t)(mx4_blocks(m.cols) * 16), (cuuint64_t)m.rows}, strides[1] = {(cuuint64_t)m.ld};
     const cuuint32_t box[2] = {MM_KB, (cuuint32_t)box_rows}, step[2] = {1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m.data, dims, strides, box, step,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -373,13 +486,24 @@ static int make_map(CUtensorMap* map, const zero_mx4& m, int box_rows) {
 }
 
 template <int BN>
-static int launch_matmul(const CUtensorMap& xm, const CUtensorMap& ym, const MmArgs& a, int grid, cudaStream_t s) {
-    const void* f = (const void*)k_mx4_matmul<BN>;
-    int rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, MmShape<BN>::SMEM),
-                       "zero_mx4_matmul shared-memory size");
+static int launch_matmul(const zero_mx4& x, const zero_mx4& y, MmArgs& a, int sms, cudaStream_t s) {
+    using S = MmShape<BN>;
+    const int64_t x_tiles = (x.rows + MM_BX - 1) / MM_BX, y_tiles = (y.rows + BN - 1) / BN;
+    if (x_tiles * y_tiles > INT32_MAX / 2) return fail(ZERO_ELIMIT, "zero_mx4_matmul: too many tiles");
+    a.x_tiles = (int)x_tiles;
+    a.y_tiles = (int)y_tiles;
+    CUtensorMap xm, ym;
+    int rc = make_map(&xm, x, MM_BX);
+    if (rc == ZERO_OK) rc = make_map(&ym, y, BN);
     if (rc != ZERO_OK) return rc;
-    void* args[] = {const_cast<CUtensorMap*>(&xm), const_cast<CUtensorMap*>(&ym), const_cast<MmArgs*>(&a)};
-    return cuda_fail(launch_after_previous(f, grid, MM_THREADS, args, MmShape<BN>::SMEM, s), "zero_mx4_matmul launch");
+    const void* f = (const void*)k_mx4_matmul<BN>;
+    rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM),
+                   "zero_mx4_matmul shared-memory size");
+    if (rc != ZERO_OK) return rc;
+    const int tiles = a.x_tiles * a.y_tiles;
+    void* args[] = {&xm, &ym, &a};
+    return cuda_fail(launch_after_previous(f, tiles < sms ? tiles : sms, MM_THREADS, args, S::SMEM, s),
+                     "zero_mx4_matmul launch");
 }
 
 __global__ void k_fill_zero(void* d, int64_t ld, int64_t rows, int64_t cols, int dt) {
@@ -424,33 +548,24 @@ int zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, float alpha, const zer
     const zero_mx4 &x = m.swap ? *b : *a, &y = m.swap ? *a : *b;
     m.xs = static_cast<const uint8_t*>(x.scales);
     m.ys = static_cast<const uint8_t*>(y.scales);
+    m.xs_tiles = (int)((x.rows + 127) / 128);
+    m.ys_tiles = (int)((y.rows + 127) / 128);
     m.d = d->data;
     m.ldd = d->ld;
     m.x_rows = (int)x.rows;
     m.y_rows = (int)y.rows;
-    m.x_tiles = (int)((x.rows + MM_BX - 1) / MM_BX);
     m.k_steps = (int)((a->cols + 255) / 256);
     m.dt = d->dtype;
-    m.wide_store = rows_aligned(*d, a->rows);
+    m.wide_store = aligned(d->data, 32) && (a->rows == 1 || d->ld * elem_size(d->dtype) % 32 == 0);
     m.alpha = alpha;
     m.status = status;
     const char* e = std::getenv("ZERO_GB300_SPIN_LIMIT");
     m.spin_limit = e ? (unsigned)std::strtoul(e, nullptr, 10) : SPIN_LIMIT;
     m.drain_limit = SPIN_LIMIT;
-    const int bn = m.swap ? (y.rows <= 16 ? 16 : y.rows <= 64 ? 64 : 128) : 256;
-    m.y_tiles = (int)((y.rows + bn - 1) / bn);
-    if ((int64_t)m.x_tiles * m.y_tiles > INT32_MAX) return fail(ZERO_ELIMIT, "zero_mx4_matmul: too many tiles");
-    const int tiles = m.x_tiles * m.y_tiles, grid = tiles < sms ? tiles : sms;
-    CUtensorMap xm, ym;
-    rc = make_map(&xm, x, MM_BX);
-    if (rc == ZERO_OK) rc = make_map(&ym, y, bn);
-    if (rc != ZERO_OK) return rc;
-    switch (bn) {
-        case 16: return launch_matmul<16>(xm, ym, m, grid, s);
-        case 64: return launch_matmul<64>(xm, ym, m, grid, s);
-        case 128: return launch_matmul<128>(xm, ym, m, grid, s);
-        default: return launch_matmul<256>(xm, ym, m, grid, s);
-    }
+    if (!m.swap) return launch_matmul<256>(x, y, m, sms, s);
+    if (y.rows <= 16) return launch_matmul<16>(x, y, m, sms, s);
+    if (y.rows <= 64) return launch_matmul<64>(x, y, m, sms, s);
+    return launch_matmul<128>(x, y, m, sms, s);
 }
 
 }  // extern "C"
