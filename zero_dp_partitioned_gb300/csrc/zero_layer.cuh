@@ -102,6 +102,13 @@ __device__ __forceinline__ void st8(void* p, int64_t i, const Raw8<DT>& r) {
     q[0] = r.w[0];
     if constexpr (DT == ZERO_F32) q[1] = r.w[1];
 }
+// 32 bytes to global memory, 32-byte aligned: a whole sector a lane.
+__device__ __forceinline__ void st32(void* p, const uint4& lo, const uint4& hi) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
+                 "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                 : "memory");
+}
+
 // Eight elements of a vector that other rows read too (a weight), whatever its alignment.
 __device__ __forceinline__ void ld8_any(const void* p, int64_t i, int dt, bool aligned16, float (&v)[8]) {
     if (!aligned16) {

@@ -141,6 +141,8 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_rows(const __grid_constant_
         const int64_t r = i / per, p0 = (i - r * per) * MX4_SPAN;
         const int64_t c0 = p0 * 256 + lane * 8;
         const char* row = static_cast<const char*>(a.src) + r * a.ld * Elem<DT>::SIZE;
+        uint8_t* data = a.q.data + r * a.q.ld + c0 / 2;
+        uint8_t* scales = a.q.tiled ? a.q.scales + mx4_tiled_at(r, c0 >> 5, a.q.tiles) : a.q.scales + r * a.q.blocks + (c0 >> 5);
         Raw8<DT> v[MX4_SPAN];
 #pragma unroll
         for (int k = 0; k < MX4_SPAN; ++k) {
@@ -154,166 +156,186 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_rows(const __grid_constant_
 #pragma unroll
         for (int k = 0; k < MX4_SPAN; ++k) {
             if (p0 + k >= pieces) break;
-            const int64_t c = c0 + k * 256, b = c >> 5;
+            const int64_t b = (c0 >> 5) + k * 8;
             const uint32_t byte = scale_byte<DT>(lanes_max<4>(top8<DT>(v[k])));
             const float inv = mx4_inverse(byte);
             const uint32_t code = codes8<DT>(v[k], pack2(inv, inv));
-            if (r < a.rows && b < a.q.blocks) *reinterpret_cast<uint32_t*>(a.q.data + r * a.q.ld + c / 2) = code;
+            if (r < a.rows && b < a.q.blocks) *reinterpret_cast<uint32_t*>(data + k * 128) = code;
             // the 4 blocks of 16 lanes make one word of a tile
             uint32_t word = byte << (8 * ((lane >> 2) & 3));
             word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
             word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
             if (a.q.tiled) {
-                if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(a.q.scales + mx4_tiled_at(r, b, a.q.tiles)) = word;
+                if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + k * 1024) = word;      // two tiles a piece
             } else if ((lane & 3) == 0 && b < a.q.blocks) {
-                a.q.scales[r * a.q.blocks + b] = (uint8_t)byte;
+                scales[k * 8] = (uint8_t)byte;
             }
         }
     }
 }
 
 // Along the columns, and along the rows too if they are wanted.  A block takes
-// 128 by 128 elements -- one scale tile in each direction -- and a warp 32 of
-// its rows: it quantises the rows from its registers, leaves them in its own
-// piece of shared memory, and then quantises the columns, two to a lane.  The
-// columns' codes and both scale tiles are put together in shared memory, so
-// that they leave in pieces of 64 and 512 consecutive bytes.
+// 128 by 128 elements -- one scale tile in each direction.  A warp copies 16
+// of its rows to shared memory and quantises those, and then 32 rows by 64
+// columns along the columns, two to a lane.  The columns' codes and both scale
+// tiles are put together in shared memory, so that they leave in pieces of 64
+// and 512 consecutive bytes.
+//
+// The next tile is on its way to shared memory (cp.async, each lane its own 16
+// bytes) while one is worked on; fp32 has room for one tile a block, and three
+// blocks cover for one another.
 template <int DT>
-constexpr int mx4_both_smem() { return 128 * 128 * Elem<DT>::SIZE; }
+struct Mx4Both {
+    static constexpr int TILE = 128 * 128 * Elem<DT>::SIZE, STAGES = DT == ZERO_F32 ? 1 : 2, SMEM = STAGES * TILE;
+    static constexpr int BLOCKS = 3;                 // of a multiprocessor
+};
 
+constexpr int MX4_BOTH_THREADS = 256;
 template <int DT>
-__global__ void __launch_bounds__(128) k_mx4_both(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(MX4_BOTH_THREADS) k_mx4_both(const __grid_constant__ QuantArgs a) {
+    using B = Mx4Both<DT>;
     extern __shared__ __align__(16) uint8_t tile_raw[];
     __shared__ __align__(16) uint4 codes[128][4];
     __shared__ __align__(16) uint8_t scale_q[512], scale_t[512];
     pdl_wait();
     pdl_launch_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint8_t* s = tile_raw + warp * 32 * 128 * Elem<DT>::SIZE;
     // both directions are padded to 256 for the scales
-    const int64_t nr = (a.rows + 255) / 256 * 2, nc = (a.cols + 255) / 256 * 2;
-    for (int64_t i = blockIdx.x; i < nr * nc; i += gridDim.x) {
-        const int64_t tr = i / nc, tc = i - tr * nc, r0 = tr * 128 + warp * 32, c0 = tc * 128;
-        const int64_t c = c0 + (lane & 15) * 8;
-        const char* src = static_cast<const char*>(a.src) + c * Elem<DT>::SIZE;
-        const bool inside = a.aligned16 && r0 + 32 <= a.rows && c0 + 128 <= a.cols;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            Raw8<DT> v[8];
+    const int64_t nr = (a.rows + 255) / 256 * 2, nc = (a.cols + 255) / 256 * 2, n = nr * nc;
+    const int lr = lane >> 4, lc = (lane & 15) * 8;  // this lane's rows lr, lr + 2, ... and columns lc .. lc + 7 of the warp's
+    auto fetch = [&](int64_t i, int st) {
+        if (i < n) {
+            const int64_t r0 = (i / nc) * 128 + warp * 16 + lr, c = (i % nc) * 128 + lc;
+            uint8_t* s = tile_raw + st * B::TILE + ((warp * 16 + lr) * 128 + lc) * Elem<DT>::SIZE;
+            const char* src = static_cast<const char*>(a.src) + (r0 * a.ld + c) * Elem<DT>::SIZE;
+            const bool inside = a.aligned16 && c + 8 <= a.cols;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const int64_t r = r0 + half * 16 + k * 2 + (lane >> 4);
-                if (inside) {
-                    v[k] = ld8_stream<DT>(src + r * a.ld * Elem<DT>::SIZE, 0);
-                } else if (r < a.rows && c < a.cols) {
-                    v[k] = read8<DT>(static_cast<const char*>(a.src) + r * a.ld * Elem<DT>::SIZE, c, a.cols, a.aligned16);
+                const int64_t r = r0 + 2 * k;
+                uint8_t* to = s + k * 2 * 128 * Elem<DT>::SIZE;
+                if (inside && r < a.rows) {
+                    const char* from = src + 2 * k * a.ld * Elem<DT>::SIZE;
+#pragma unroll
+                    for (int w = 0; w < Elem<DT>::SIZE / 2; ++w)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         (uint32_t)__cvta_generic_to_shared(to) + 16 * w),
+                                     "l"(from + 16 * w)
+                                     : "memory");
                 } else {
+                    Raw8<DT> v;
+                    if (r < a.rows && c < a.cols) {
+                        v = read8<DT>(static_cast<const char*>(a.src) + r * a.ld * Elem<DT>::SIZE, c, a.cols, a.aligned16);
+                    } else {
 #pragma unroll
-                    for (auto& w : v[k].w) w = make_uint4(0, 0, 0, 0);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int rr = half * 16 + k * 2 + (lane >> 4);
-                const int64_t r = r0 + rr;
-                if (a.t.data) st8<DT>(s, rr * 128 + (lane & 15) * 8, v[k]);
-                if (a.q.data) {
-                    const uint32_t byte = scale_byte<DT>(lanes_max<4>(top8<DT>(v[k])));
-                    const float inv = mx4_inverse(byte);
-                    const uint32_t code = codes8<DT>(v[k], pack2(inv, inv));
-                    if (r < a.rows && c < a.q.blocks * 32)
-                        *reinterpret_cast<uint32_t*>(a.q.data + r * a.q.ld + c / 2) = code;
-                    if ((lane & 3) == 0) scale_q[rr * 16 + warp * 4 + ((lane & 15) >> 2)] = (uint8_t)byte;
+                        for (auto& w : v.w) w = make_uint4(0, 0, 0, 0);
+                    }
+                    st8<DT>(to, 0, v);
                 }
             }
         }
-        __syncwarp();
-        if (a.t.data) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                // columns c0 + 64 half + 2 lane and the next, this warp's 32 rows: one block of each
-                uint32_t top0 = 0, top1 = 0;
-                if constexpr (DT == ZERO_F32) {
-                    const float2* p = reinterpret_cast<const float2*>(s) + half * 32 + lane;
-                    float2 v[32];
-#pragma unroll
-                    for (int rr = 0; rr < 32; ++rr) {
-                        v[rr] = p[rr * 64];
-                        top0 = max(top0, abs_bits(v[rr].x));
-                        top1 = max(top1, abs_bits(v[rr].y));
-                    }
-                    const uint32_t b0 = mx4_scale(top0), b1 = mx4_scale(top1);
-                    const uint64_t inv = pack2(mx4_inverse(b0), mx4_inverse(b1));
-                    uint32_t w0[4], w1[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float x[8], y[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 t = unpack2(mul2(pack2(v[q * 8 + e].x, v[q * 8 + e].y), inv));
-                            x[e] = t.x;
-                            y[e] = t.y;
-                        }
-                        w0[q] = to_e2m1(x);
-                        w1[q] = to_e2m1(y);
-                    }
-                    top0 = b0;
-                    top1 = b1;
-                    const int cc = half * 64 + 2 * lane, at = warp ^ (lane & 3);
-                    codes[cc][at] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-                    codes[cc + 1][at] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-                } else {
-                    const uint32_t* p = reinterpret_cast<const uint32_t*>(s) + half * 32 + lane;
-                    uint32_t v[32], t = 0;
-#pragma unroll
-                    for (int rr = 0; rr < 32; ++rr) {
-                        v[rr] = p[rr * 64];
-                        t = __vmaxu2(t, v[rr] & 0x7FFF7FFFu);
-                    }
-                    const uint32_t b0 = scale_byte<DT>(t & 0xFFFFu), b1 = scale_byte<DT>(t >> 16);
-                    const uint64_t inv = pack2(mx4_inverse(b0), mx4_inverse(b1));
-                    uint32_t w0[4], w1[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float x[8], y[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t u = v[q * 8 + e];
-                            const uint64_t both = DT == ZERO_BF16
-                                                      ? pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u))
-                                                      : pack2(Half16<DT>::widen(u & 0xFFFFu), Half16<DT>::widen(u >> 16));
-                            const float2 f = unpack2(mul2(both, inv));
-                            x[e] = f.x;
-                            y[e] = f.y;
-                        }
-                        w0[q] = to_e2m1(x);
-                        w1[q] = to_e2m1(y);
-                    }
-                    top0 = b0;
-                    top1 = b1;
-                    const int cc = half * 64 + 2 * lane, at = warp ^ (lane & 3);
-                    codes[cc][at] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-                    codes[cc + 1][at] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-                }
-                // row cc of the transpose's tile, block `warp` of its 4
-                const int cc = half * 64 + 2 * lane;
-                scale_t[(cc & 31) * 16 + (cc >> 5) * 4 + warp] = (uint8_t)top0;
-                scale_t[((cc + 1) & 31) * 16 + (cc >> 5) * 4 + warp] = (uint8_t)top1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int st = 0;
+    if (B::STAGES == 2) fetch(blockIdx.x, 0);
+    for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
+        if (B::STAGES == 2) fetch(i + gridDim.x, st ^ 1);
+        else fetch(i, 0);
+        asm volatile("cp.async.wait_group %0;" ::"n"(B::STAGES - 1) : "memory");
+        const int64_t tr = i / nc, tc = i - tr * nc, c0 = tc * 128;
+        const uint8_t* s = tile_raw + st * B::TILE;
+        if (a.q.data) {
+            const int64_t r0 = tr * 128, c = c0 + lc;
+            uint8_t* data = a.q.data + (r0 + warp * 16 + lr) * a.q.ld + c / 2;
+#pragma unroll 4
+            for (int k = 0; k < 8; ++k) {
+                const int rr = warp * 16 + lr + 2 * k;
+                const Raw8<DT> v = ld8<DT>(s, rr * 128 + lc);
+                const uint32_t byte = scale_byte<DT>(lanes_max<4>(top8<DT>(v)));
+                const float inv = mx4_inverse(byte);
+                const uint32_t code = codes8<DT>(v, pack2(inv, inv));
+                if (r0 + rr < a.rows && c < a.q.blocks * 32) *reinterpret_cast<uint32_t*>(data + 2 * k * a.q.ld) = code;
+                if ((lane & 3) == 0) scale_q[(rr & 31) * 16 + (rr >> 5) * 4 + ((lane & 15) >> 2)] = (uint8_t)byte;
             }
         }
         __syncthreads();
         if (a.t.data) {
+            // columns cc and the next, rows 32 rb .. + 31: one block of each
+            const int rb = warp >> 1, cc = (warp & 1) * 64 + 2 * lane;
+            uint32_t byte0, byte1, w0[4], w1[4];
+            if constexpr (DT == ZERO_F32) {
+                const float2* p = reinterpret_cast<const float2*>(s) + rb * 32 * 64 + cc / 2;
+                float2 v[32];
+                uint32_t top0 = 0, top1 = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int id = k * 128 + threadIdx.x, cc = id >> 2, ch = id & 3;
+                for (int rr = 0; rr < 32; ++rr) {
+                    v[rr] = p[rr * 64];
+                    top0 = max(top0, abs_bits(v[rr].x));
+                    top1 = max(top1, abs_bits(v[rr].y));
+                }
+                byte0 = mx4_scale(top0);
+                byte1 = mx4_scale(top1);
+                const uint64_t inv = pack2(mx4_inverse(byte0), mx4_inverse(byte1));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float x[8], y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 t = unpack2(mul2(pack2(v[q * 8 + e].x, v[q * 8 + e].y), inv));
+                        x[e] = t.x;
+                        y[e] = t.y;
+                    }
+                    w0[q] = to_e2m1(x);
+                    w1[q] = to_e2m1(y);
+                }
+            } else {
+                const uint32_t* p = reinterpret_cast<const uint32_t*>(s) + rb * 32 * 64 + cc / 2;
+                uint32_t v[32], t = 0;
+#pragma unroll
+                for (int rr = 0; rr < 32; ++rr) {
+                    v[rr] = p[rr * 64];
+                    t = __vmaxu2(t, v[rr] & 0x7FFF7FFFu);
+                }
+                byte0 = scale_byte<DT>(t & 0xFFFFu);
+                byte1 = scale_byte<DT>(t >> 16);
+                const uint64_t inv = pack2(mx4_inverse(byte0), mx4_inverse(byte1));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float x[8], y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t u = v[q * 8 + e];
+                        const uint64_t both = DT == ZERO_BF16
+                                                  ? pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u))
+                                                  : pack2(Half16<DT>::widen(u & 0xFFFFu), Half16<DT>::widen(u >> 16));
+                        const float2 f = unpack2(mul2(both, inv));
+                        x[e] = f.x;
+                        y[e] = f.y;
+                    }
+                    w0[q] = to_e2m1(x);
+                    w1[q] = to_e2m1(y);
+                }
+            }
+            const int at = rb ^ (lane & 3);
+            codes[cc][at] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+            codes[cc + 1][at] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+            // rows cc and cc + 1 of the transpose's tile, block rb of its 4
+            scale_t[(cc & 31) * 16 + (cc >> 5) * 4 + rb] = (uint8_t)byte0;
+            scale_t[((cc + 1) & 31) * 16 + (cc >> 5) * 4 + rb] = (uint8_t)byte1;
+        }
+        __syncthreads();
+        if (a.t.data) {
+#pragma unroll
+            for (int k = 0; k < 512 / MX4_BOTH_THREADS; ++k) {
+                const int id = k * MX4_BOTH_THREADS + threadIdx.x, cc = id >> 2, ch = id & 3;
                 const int64_t b = tr * 4 + ch;
                 if (c0 + cc < a.cols && b < a.t.blocks)
                     *reinterpret_cast<uint4*>(a.t.data + (c0 + cc) * a.t.ld + b * 16) = codes[cc][ch ^ ((cc >> 1) & 3)];
             }
-            put_scales(a.t, scale_t, a.cols, tc, tr, threadIdx.x);
+            if (threadIdx.x < 128) put_scales(a.t, scale_t, a.cols, tc, tr, threadIdx.x);
         }
-        if (a.q.data) put_scales(a.q, scale_q, a.rows, tr, tc, 127 - threadIdx.x);
+        if (a.q.data && threadIdx.x >= 128) put_scales(a.q, scale_q, a.rows, tr, tc, threadIdx.x - 128);
         __syncthreads();
+        if (B::STAGES == 2) st ^= 1;
     }
 }
 
@@ -321,7 +343,7 @@ struct DequantArgs {
     Mx4Dev q;
     void* dst;
     int64_t ld, rows, cols;
-    int aligned16;
+    int aligned16, aligned32;
 };
 
 // A warp takes up to MX4_SPAN pieces of 256 columns of a row, 8 columns to a
@@ -336,7 +358,7 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_values(const __grid_constan
     for (int64_t i = (int64_t)blockIdx.x * (MX4_THREADS / 32) + (threadIdx.x >> 5); i < n; i += stride) {
         const int64_t r = i / per, c0 = (i - r * per) * 256 * MX4_SPAN + lane * 8;
         const uint8_t* data = a.q.data + r * a.q.ld + c0 / 2;
-        uint32_t w[MX4_SPAN], byte[MX4_SPAN];
+        uint32_t w[MX4_SPAN] = {}, byte[MX4_SPAN] = {};
 #pragma unroll
         for (int k = 0; k < MX4_SPAN; ++k)
             if (c0 + k * 256 < a.cols) {
@@ -345,6 +367,20 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_values(const __grid_constan
                 byte[k] = a.q.scales[a.q.tiled ? mx4_tiled_at(r, b, a.q.tiles) : r * a.q.blocks + b];
             }
         char* row = static_cast<char*>(a.dst) + r * a.ld * Elem<DT>::SIZE;
+        if (!a.aligned16) {
+            // rows that start anywhere: 32 neighbouring elements a store, a lane's own picked from the lane that has them
+#pragma unroll
+            for (int k = 0; k < MX4_SPAN; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int from = e * 4 + (lane >> 3);
+                    const uint32_t code = __shfl_sync(0xFFFFFFFFu, w[k], from) >> (4 * (lane & 7)) & 0xFu;
+                    const float s = mx4_value(__shfl_sync(0xFFFFFFFFu, byte[k], from));
+                    const int64_t c = c0 - lane * 8 + k * 256 + e * 32 + lane;
+                    if (c < a.cols) st1<DT>(row, c, from_e2m1(code).x * s);
+                }
+            continue;
+        }
 #pragma unroll
         for (int k = 0; k < MX4_SPAN; ++k) {
             const int64_t c = c0 + k * 256;
@@ -358,8 +394,14 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_values(const __grid_constan
                 v[2 * q] = f.x;
                 v[2 * q + 1] = f.y;
             }
-            if (a.aligned16 && c + 8 <= a.cols) {
-                st8<DT>(row, c, narrow8<DT>(v));
+            if (c + 8 <= a.cols) {
+                const Raw8<DT> o = narrow8<DT>(v);
+                if constexpr (DT == ZERO_F32) {
+                    if (a.aligned32) st32(row + c * 4, o.w[0], o.w[1]);
+                    else st8<DT>(row, c, o);
+                } else {
+                    st8<DT>(row, c, o);
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -453,12 +495,12 @@ int zero_mx4_quantize(const zero_mat* src, int64_t rows, int64_t cols, const zer
     if (out_t) {
         f = dt == ZERO_F32 ? (const void*)k_mx4_both<ZERO_F32>
           : dt == ZERO_BF16 ? (const void*)k_mx4_both<ZERO_BF16> : (const void*)k_mx4_both<ZERO_F16>;
-        threads = 128;
-        smem = dt == ZERO_F32 ? mx4_both_smem<ZERO_F32>() : mx4_both_smem<ZERO_BF16>();
+        threads = MX4_BOTH_THREADS;
+        smem = dt == ZERO_F32 ? Mx4Both<ZERO_F32>::SMEM : Mx4Both<ZERO_BF16>::SMEM;
         rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
                        "zero_mx4_quantize shared-memory size");
         if (rc != ZERO_OK) return rc;
-        grid = blocks_for((rows + 255) / 256 * 2 * ((cols + 255) / 256 * 2), dt == ZERO_F32 ? 2 : 5);
+        grid = blocks_for((rows + 255) / 256 * 2 * ((cols + 255) / 256 * 2), Mx4Both<ZERO_BF16>::BLOCKS);
     } else {
         f = dt == ZERO_F32 ? (const void*)k_mx4_rows<ZERO_F32>
           : dt == ZERO_BF16 ? (const void*)k_mx4_rows<ZERO_BF16> : (const void*)k_mx4_rows<ZERO_F16>;
@@ -483,6 +525,7 @@ int zero_mx4_dequantize(const zero_mx4* src, const zero_mat* dst, void* stream) 
     a.rows = src->rows;
     a.cols = src->cols;
     a.aligned16 = rows_aligned(*dst, a.rows);
+    a.aligned32 = aligned(dst->data, 32) && (a.rows <= 1 || dst->ld * elem_size(dst->dtype) % 32 == 0);
     const int dt = dst->dtype;
     const void* f = dt == ZERO_F32 ? (const void*)k_mx4_values<ZERO_F32>
                   : dt == ZERO_BF16 ? (const void*)k_mx4_values<ZERO_BF16> : (const void*)k_mx4_values<ZERO_F16>;

@@ -113,13 +113,6 @@ __device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&v)[16]) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// 32 bytes to global memory, 32-byte aligned: a whole sector a lane.
-__device__ __forceinline__ void st32(void* p, const uint4& lo, const uint4& hi) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
-                 "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
-                 : "memory");
-}
-
 // Shared-memory descriptor of an operand tile: rows of 128 bytes in the
 // 128-byte swizzle, 8 rows (1024 bytes) from one group to the next.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
