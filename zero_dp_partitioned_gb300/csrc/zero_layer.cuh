@@ -2,13 +2,13 @@
 // matrices) share: element types, row access of any alignment, block
 // reductions, and the host checks of a zero_mat.
 //
-// A row is walked in units of E elements per thread.  V8: 8 consecutive
-// elements, one 16-byte access (two for fp32), taken when every row of every
-// matrix starts on a 16-byte boundary and the columns are a multiple of 8.
-// Otherwise 4 elements 32 apart, one per warp-wide coalesced access: rows
-// that start anywhere still read whole sectors.  Either way 128 consecutive
-// columns belong to 16 (V8) or 32 consecutive lanes of one warp, so a scale
-// per 128 columns needs no shared memory.
+// A row is walked in units of 8 consecutive elements, the units of a warp's
+// lanes one after another: 128 consecutive columns belong to 16 lanes.  Where
+// every row of every matrix starts on a 16-byte boundary a unit is one 16-byte
+// access (two for fp32).  Rows that start anywhere are still read and written
+// in aligned 16-byte words: a load takes the two words that a unit touches and
+// shifts them, a store takes the unit before it from the neighbouring lane;
+// only the ends of a row, and of a warp, go element by element.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -121,6 +121,136 @@ __device__ __forceinline__ void ld8_any(const void* p, int64_t i, int dt, bool a
     } else {
         widen8<ZERO_F16>(ld8<ZERO_F16>(p, i), v);
     }
+}
+
+// ---------------------------------------------------------------- rows that start anywhere
+// N words from byte `by` (below 16) of the words w[0 .. N + 3].  `by` is the
+// same for a whole row, so the branches do not diverge.
+template <int N>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[N + 4], int by) {
+    if (by & 8)
+#pragma unroll
+        for (int i = 0; i < N + 2; ++i) w[i] = w[i + 2];
+    if (by & 4)
+#pragma unroll
+        for (int i = 0; i < N + 1; ++i) w[i] = w[i + 1];
+    if (by & 3)
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (by & 3));
+}
+
+// The bytes a matrix occupies, first row to last element: no access leaves them.
+struct Extent {
+    const char *lo, *hi;
+};
+template <int DT>
+__device__ __forceinline__ Extent extent_of(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+    return Extent{static_cast<const char*>(p), static_cast<const char*>(p) + ((rows - 1) * ld + cols) * Elem<DT>::SIZE};
+}
+
+// 8 elements of a row from column c (a multiple of 8); columns past the end are 0.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> ld8_shifted(const void* row, int64_t c, int64_t cols, const Extent& x) {
+    constexpr int N = DT == ZERO_F32 ? 8 : 4;
+    const char* p = static_cast<const char*>(row) + c * Elem<DT>::SIZE;
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+    const char* q = p - off;
+    Raw8<DT> r;
+    if (c + 8 <= cols && q >= x.lo && q + 4 * N + 16 <= x.hi) {
+        uint32_t w[N + 4];
+#pragma unroll
+        for (int k = 0; k < N / 4 + 1; ++k) {
+            const uint4 u = reinterpret_cast<const uint4*>(q)[k];
+            w[4 * k] = u.x;
+            w[4 * k + 1] = u.y;
+            w[4 * k + 2] = u.z;
+            w[4 * k + 3] = u.w;
+        }
+        shift_words<N>(w, off);
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) r.w[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    } else {
+        uint32_t w[N] = {};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < cols) {
+                if constexpr (DT == ZERO_F32) w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+                else w[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
+            }
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) r.w[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+    return r;
+}
+
+// A unit of 8 elements of SIZE bytes (N words) to column c of a row that starts
+// anywhere.  The whole warp calls it, its lanes with consecutive units; `here`:
+// this lane's unit is to be written (its columns below cols).  A lane writes
+// the aligned words that end in its unit, with what the lane before has of
+// them, and what no lane after it will write.
+template <int SIZE, int N>
+__device__ __forceinline__ void st_shifted(void* row, int64_t c, int64_t cols, bool here, const uint32_t (&v)[N]) {
+    constexpr int G = N < 4 ? N : 4;                           // words of an aligned store
+    char* p = static_cast<char*>(row) + c * SIZE;
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & (4 * G - 1));
+    const int lane = threadIdx.x & 31;
+    const bool whole = here && c + 8 <= cols;
+    uint32_t w[N + 4];
+    if constexpr (G == 2) w[0] = w[1] = 0;
+#pragma unroll
+    for (int i = 0; i < G; ++i) w[4 - G + i] = __shfl_up_sync(0xFFFFFFFFu, v[N - G + i], 1);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[4 + i] = v[i];
+    const bool before = __shfl_up_sync(0xFFFFFFFFu, (int)whole, 1) && lane > 0;
+    const bool after = __shfl_down_sync(0xFFFFFFFFu, (int)whole, 1) && lane < 31;
+    if (!here) return;
+    int from = 0, to = (int)(cols - c < 8 ? cols - c : 8);     // elements still to be written one by one
+    if (whole && (before || off == 0)) {
+        if (off) {
+            // words from byte 16 - off of (the lane before's last G words at 4 - G, own words at 4)
+            if constexpr (G == 4) {
+                shift_words<N>(w, 16 - off);
+            } else {
+                // 8-byte words: from byte 16 - off, off below 8, so past w[2]
+                uint32_t t[N + 4] = {w[2], w[3], w[4], w[5]};
+                shift_words<N>(t, 8 - off);
+                w[0] = t[0];
+                w[1] = t[1];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = v[i];
+        }
+        if constexpr (G == 4) {
+#pragma unroll
+            for (int k = 0; k < N / 4; ++k)
+                reinterpret_cast<uint4*>(p - off)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        } else {
+            *reinterpret_cast<uint2*>(p - off) = make_uint2(w[0], w[1]);
+        }
+        from = 8 - off / SIZE;
+    }
+    if (whole && after) to = 8 - off / SIZE;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e >= from && e < to) {
+            if constexpr (SIZE == 4) reinterpret_cast<uint32_t*>(p)[e] = v[e];
+            else if constexpr (SIZE == 2) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+            else reinterpret_cast<uint8_t*>(p)[e] = (uint8_t)(v[e / 4] >> (8 * (e & 3)));
+        }
+}
+template <int DT>
+__device__ __forceinline__ void st8_shifted(void* row, int64_t c, int64_t cols, bool here, const Raw8<DT>& r) {
+    constexpr int N = DT == ZERO_F32 ? 8 : 4;
+    uint32_t v[N];
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+        v[4 * k] = r.w[k].x;
+        v[4 * k + 1] = r.w[k].y;
+        v[4 * k + 2] = r.w[k].z;
+        v[4 * k + 3] = r.w[k].w;
+    }
+    st_shifted<Elem<DT>::SIZE, N>(row, c, cols, here, v);
 }
 
 // ---------------------------------------------------------------- pairs

@@ -79,12 +79,9 @@ __device__ __forceinline__ void put_scales(const Mx4Dev& q, const uint8_t* tile,
 
 // 8 elements of a row from column c, as they lie; columns past the end are 0.
 template <int DT>
-__device__ __forceinline__ Raw8<DT> read8(const void* row, int64_t c, int64_t cols, bool vec) {
+__device__ __forceinline__ Raw8<DT> read8(const void* row, int64_t c, int64_t cols, bool vec, const Extent& x) {
     if (vec && c + 8 <= cols) return ld8_stream<DT>(row, c);
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? ld1<DT>(row, c + e) : 0.f;
-    return narrow8<DT>(v);
+    return ld8_shifted<DT>(row, c, cols, x);
 }
 
 // The bits of the largest magnitude of 8 elements (ordered as unsigned
@@ -133,6 +130,7 @@ template <int DT>
 __global__ void __launch_bounds__(MX4_THREADS) k_mx4_rows(const __grid_constant__ QuantArgs a) {
     pdl_wait();
     pdl_launch_next();
+    const Extent x = extent_of<DT>(a.src, a.ld, a.rows, a.cols);
     const int64_t rows = a.q.tiled ? (a.rows + 127) / 128 * 128 : a.rows;
     const int64_t pieces = (a.cols + 255) / 256, per = (pieces + MX4_SPAN - 1) / MX4_SPAN, n = rows * per;
     const int lane = threadIdx.x & 31;
@@ -147,7 +145,7 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_rows(const __grid_constant_
 #pragma unroll
         for (int k = 0; k < MX4_SPAN; ++k) {
             if (r < a.rows && c0 + k * 256 < a.cols) {
-                v[k] = read8<DT>(row, c0 + k * 256, a.cols, a.aligned16);
+                v[k] = read8<DT>(row, c0 + k * 256, a.cols, a.aligned16, x);
             } else {
 #pragma unroll
                 for (auto& w : v[k].w) w = make_uint4(0, 0, 0, 0);
@@ -199,6 +197,7 @@ __global__ void __launch_bounds__(MX4_BOTH_THREADS) k_mx4_both(const __grid_cons
     __shared__ __align__(16) uint8_t scale_q[512], scale_t[512];
     pdl_wait();
     pdl_launch_next();
+    const Extent x = extent_of<DT>(a.src, a.ld, a.rows, a.cols);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // both directions are padded to 256 for the scales
     const int64_t nr = (a.rows + 255) / 256 * 2, nc = (a.cols + 255) / 256 * 2, n = nr * nc;
@@ -224,7 +223,7 @@ __global__ void __launch_bounds__(MX4_BOTH_THREADS) k_mx4_both(const __grid_cons
                 } else {
                     Raw8<DT> v;
                     if (r < a.rows && c < a.cols) {
-                        v = read8<DT>(static_cast<const char*>(a.src) + r * a.ld * Elem<DT>::SIZE, c, a.cols, a.aligned16);
+                        v = read8<DT>(static_cast<const char*>(a.src) + r * a.ld * Elem<DT>::SIZE, c, a.cols, a.aligned16, x);
                     } else {
 #pragma unroll
                         for (auto& w : v.w) w = make_uint4(0, 0, 0, 0);
@@ -367,24 +366,10 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_values(const __grid_constan
                 byte[k] = a.q.scales[a.q.tiled ? mx4_tiled_at(r, b, a.q.tiles) : r * a.q.blocks + b];
             }
         char* row = static_cast<char*>(a.dst) + r * a.ld * Elem<DT>::SIZE;
-        if (!a.aligned16) {
-            // rows that start anywhere: 32 neighbouring elements a store, a lane's own picked from the lane that has them
-#pragma unroll
-            for (int k = 0; k < MX4_SPAN; ++k)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int from = e * 4 + (lane >> 3);
-                    const uint32_t code = __shfl_sync(0xFFFFFFFFu, w[k], from) >> (4 * (lane & 7)) & 0xFu;
-                    const float s = mx4_value(__shfl_sync(0xFFFFFFFFu, byte[k], from));
-                    const int64_t c = c0 - lane * 8 + k * 256 + e * 32 + lane;
-                    if (c < a.cols) st1<DT>(row, c, from_e2m1(code).x * s);
-                }
-            continue;
-        }
 #pragma unroll
         for (int k = 0; k < MX4_SPAN; ++k) {
             const int64_t c = c0 + k * 256;
-            if (c >= a.cols) break;
+            if (c - lane * 8 >= a.cols) break;             // the whole warp together
             const float s = mx4_value(byte[k]);
             float v[8];
 #pragma unroll
@@ -394,8 +379,10 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_values(const __grid_constan
                 v[2 * q] = f.x;
                 v[2 * q + 1] = f.y;
             }
-            if (c + 8 <= a.cols) {
-                const Raw8<DT> o = narrow8<DT>(v);
+            const Raw8<DT> o = narrow8<DT>(v);
+            if (!a.aligned16) {
+                st8_shifted<DT>(row, c, a.cols, c < a.cols, o);
+            } else if (c + 8 <= a.cols) {
                 if constexpr (DT == ZERO_F32) {
                     if (a.aligned32) st32(row + c * 4, o.w[0], o.w[1]);
                     else st8<DT>(row, c, o);

@@ -44,6 +44,8 @@ constexpr int MM_HEADER = 1024;
 constexpr int MM_SF_COL = 432;                // tensor-memory column of the scales: sets of 24 columns, used by turns
 constexpr int MM_SF_SET = 24, MM_SF_SETS = 3;
 constexpr int MM_MAX_STAGES = 8;
+constexpr int MM_EPI = 4 * 32 * 17 * 4;       // a 32 x 16 piece of D for each epilogue warp, padded
+constexpr int MM_SPLIT = 8;                   // most blocks that share a tile's sum over k (the portable cluster size)
 
 template <int BN>
 struct MmShape {
@@ -51,8 +53,11 @@ struct MmShape {
     static constexpr int X_BYTES = MM_BX * MM_KB, Y_BYTES = BN * MM_KB;
     // a stage starts on 1024 bytes (the swizzle's period)
     static constexpr int STAGE = X_BYTES + Y_BYTES;
-    static constexpr int STAGES = (232448 - 2048) / STAGE < MM_MAX_STAGES ? (232448 - 2048) / STAGE : MM_MAX_STAGES;
-    static constexpr int SMEM = STAGES * STAGE + 2048;
+    static constexpr int FIT = (232448 - 2048 - MM_EPI) / STAGE;
+    static constexpr int STAGES = FIT < MM_MAX_STAGES ? FIT : MM_MAX_STAGES;
+    static constexpr int SMEM = STAGES * STAGE + 2048 + MM_EPI;
+    // with the sum over k shared out, the other blocks' parts of this block's columns lie where the stages were
+    static_assert((MM_SPLIT - 1) * MM_BX * (BN / MM_SPLIT) * 4 <= STAGES * STAGE, "parts fit");
     static constexpr bool OVERLAP = BN == 256;
     static constexpr int ACC1 = OVERLAP ? 176 : BN;            // column of the second accumulator
     static constexpr int EARLY = OVERLAP ? 80 : BN;            // columns read before the next tile may start
@@ -67,7 +72,8 @@ struct MmArgs {
     int x_rows, y_rows;                       // rows of X and Y
     int x_tiles, y_tiles, k_steps;            // tiles of 128 and BN rows, stages of 256 elements
     int xs_tiles, ys_tiles;                   // 128-row tiles of scales
-    int dt, swap, wide_store;
+    int dt, swap, store;                      // store: bytes of an aligned store of D's rows (32, 16, or 0: unaligned)
+    int split;                                // blocks that share a tile's sum over k
     float alpha;
     int32_t* status;
     unsigned spin_limit, drain_limit;
@@ -137,17 +143,25 @@ __device__ __forceinline__ bool mm_poll(uint32_t bar, uint32_t parity) {
     return done;
 }
 // A bounded wait that also ends when another role of the block has given up.
-// A try is 16 polls, so that SPIN_LIMIT tries end after about a second.  The
-// first poll stands apart: with data at hand it takes 25 cycles, where
-// mbarrier.try_wait, or a poll inside the loop, takes 260 (the loop that issues
-// the products waited 520 cycles a stage for data that were there; 217 against
-// 200 us for 8192 x 14336 x 4096 with its quantisation).
+// A try suspends the thread for 1 us at most, so that SPIN_LIMIT tries end
+// after a few seconds.  The lane that issues the products polls first (POLL):
+// with data at hand a poll takes 25 cycles and mbarrier.try_wait 260, twice a
+// stage (8192 x 14336 x 4096: 170 us, 198 without the poll).
+template <bool POLL = false>
 __device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, unsigned limit, volatile int* stop) {
-    if (limit && mm_poll(bar, parity)) return true;
+    if (POLL && limit && mm_poll(bar, parity)) return true;
+#pragma unroll 1
     for (unsigned it = 0; it < limit; ++it) {
-        for (int p = 0; p < 16; ++p)
-            if (mm_poll(bar, parity)) return true;
-        if (stop && *stop) return false;
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((it & 255) == 255 && stop && *stop) return false;
     }
     return false;
 }
@@ -161,7 +175,77 @@ __device__ __forceinline__ void tile_at(const MmArgs& a, int t, int& x, int& y) 
     y = y0 + r % w;
 }
 
-template <int BN>
+// 16 columns of D from column y0 + col, of this lane's row xr of X: scaled,
+// rounded and stored.  buf: this warp's piece of shared memory.  The whole warp
+// calls it.
+__device__ __forceinline__ void put16(const MmArgs& a, int64_t xr, int64_t y0, int col, int n, const uint32_t (&v)[16],
+                                      float* buf) {
+    const int lane = threadIdx.x & 31;
+    if (a.swap) {
+        // a lane holds one column of D: the warp stores 32 consecutive ones of each row
+        if (xr < a.x_rows)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (e < n && y0 + col + e < a.y_rows)
+                    st1_any(a.d, (y0 + col + e) * a.ldd + xr, __uint_as_float(v[e]) * a.alpha, a.dt);
+        return;
+    }
+    if (a.store && n == 16 && y0 + col + 16 <= a.y_rows) {
+        if (xr >= a.x_rows) return;
+        const int64_t at = xr * a.ldd + y0 + col;
+        float lo[8], hi[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            lo[e] = __uint_as_float(v[e]) * a.alpha;
+            hi[e] = __uint_as_float(v[8 + e]) * a.alpha;
+        }
+        if (a.dt == ZERO_F32) {
+            const Raw8<ZERO_F32> l = narrow8<ZERO_F32>(lo), h = narrow8<ZERO_F32>(hi);
+            if (a.store == 32) {
+                st32(static_cast<float*>(a.d) + at, l.w[0], l.w[1]);
+                st32(static_cast<float*>(a.d) + at + 8, h.w[0], h.w[1]);
+            } else {
+                st8<ZERO_F32>(a.d, at, l);
+                st8<ZERO_F32>(a.d, at + 8, h);
+            }
+        } else {
+            const uint4 l = a.dt == ZERO_BF16 ? narrow8<ZERO_BF16>(lo).w[0] : narrow8<ZERO_F16>(lo).w[0];
+            const uint4 h = a.dt == ZERO_BF16 ? narrow8<ZERO_BF16>(hi).w[0] : narrow8<ZERO_F16>(hi).w[0];
+            uint16_t* p = static_cast<uint16_t*>(a.d) + at;
+            if (a.store == 32) {
+                st32(p, l, h);
+            } else {
+                reinterpret_cast<uint4*>(p)[0] = l;
+                reinterpret_cast<uint4*>(p)[1] = h;
+            }
+        }
+        return;
+    }
+    // rows that start anywhere, and the last columns: by shared memory, 16 neighbouring columns of two rows a store
+#pragma unroll
+    for (int e = 0; e < 16; ++e) buf[lane * 17 + e] = __uint_as_float(v[e]) * a.alpha;
+    __syncwarp();
+    const int64_t c = y0 + col + (lane & 15), r0 = xr - lane;
+    if ((lane & 15) < n && c < a.y_rows)
+#pragma unroll 4
+        for (int r = lane >> 4; r < 32; r += 2)
+            if (r0 + r < a.x_rows) st1_any(a.d, (r0 + r) * a.ldd + c, buf[r * 17 + (lane & 15)], a.dt);
+    __syncwarp();
+}
+
+__device__ __forceinline__ void st_remote4(uint32_t addr, const uint32_t* v) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t remote_addr(uint32_t local, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+
+// SPLIT: a cluster of a.split blocks shares one tile, each a stretch of k; see
+// the end of the kernel.
+template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(MM_THREADS, 1)
     k_mx4_matmul(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap ymap,
                  const __grid_constant__ MmArgs a) {
@@ -178,6 +262,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     volatile int* loaded = reinterpret_cast<volatile int*>(head + 208);   // stages whose loads were issued
     const uint32_t stages = base + MM_HEADER;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quarter = warp & 3;                            // the 32 lanes of tensor memory this warp can reach
+    float* epi = reinterpret_cast<float*>(head + MM_HEADER + S::STAGES * S::STAGE) + quarter * 32 * 17;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::STAGES; ++s) {
@@ -203,16 +289,20 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     pdl_wait();
     pdl_launch_next();
 
+    // this block's tiles and its stretch of k
+    const int rank = SPLIT ? (int)(blockIdx.x % (unsigned)a.split) : 0;
+    const int first = SPLIT ? blockIdx.x / (unsigned)a.split : blockIdx.x, step = SPLIT ? a.x_tiles * a.y_tiles : gridDim.x;
     const int n_tiles = a.x_tiles * a.y_tiles, K = a.k_steps;
+    const int k0 = SPLIT ? (int)((int64_t)K * rank / a.split) : 0, k1 = SPLIT ? (int)((int64_t)K * (rank + 1) / a.split) : K;
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) {
             int st = 0, count = 0;
             uint32_t phase = 0;
-            for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+            for (int t = first; t < n_tiles && ok; t += step) {
                 int x, y;
                 tile_at(a, t, x, y);
-                for (int k = 0; k < K; ++k) {
+                for (int k = k0; k < k1; ++k) {
                     if (count >= S::STAGES && !mm_wait(empty + 8 * st, phase ^ 1, a.spin_limit, stop)) {
                         ok = false;
                         break;
@@ -234,19 +324,19 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         if (lane == 0) {
             int st = 0, set = 0, n = 0;
             uint32_t phase = 0, set_phase = 0;
-            for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x, ++n) {
+            for (int t = first; t < n_tiles && ok; t += step, ++n) {
                 // the accumulator of tile n was last used by tile n - 2; overlapping ones wait for tile n - 1's first
                 // columns (its epilogue began after tile n - 2's ended)
                 const int need = S::OVERLAP ? n - 1 : n - 2;
-                if (need >= 0 && !mm_wait(acc_free + 8 * (need & 1), (need >> 1) & 1, a.spin_limit, stop)) {
+                if (need >= 0 && !mm_wait<true>(acc_free + 8 * (need & 1), (need >> 1) & 1, a.spin_limit, stop)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (n & 1 ? S::ACC1 : 0);
-                for (int k = 0; k < K; ++k) {
-                    if (!mm_wait(sf_full + 8 * set, set_phase, a.spin_limit, stop) ||
-                        !mm_wait(full + 8 * st, phase, a.spin_limit, stop)) {
+                for (int k = k0; k < k1; ++k) {
+                    if (!mm_wait<true>(sf_full + 8 * set, set_phase, a.spin_limit, stop) ||
+                        !mm_wait<true>(full + 8 * st, phase, a.spin_limit, stop)) {
                         ok = false;
                         break;
                     }
@@ -256,7 +346,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         tc_mma(d, dx + 2 * q, dy + 2 * q, mma_desc(BN, q & 1), sf + 4 * (q >> 1),
-                               sf + 8 + 4 * S::Y_TILES * (q >> 1), k > 0 || q > 0);
+                               sf + 8 + 4 * S::Y_TILES * (q >> 1), k > k0 || q > 0);
                     tc_commit(empty + 8 * st);
                     if (++st == S::STAGES) {
                         st = 0;
@@ -274,11 +364,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     } else if (warp >= 6) {
         // Stage i's scales: lane l of every quarter holds rows l, 32 + l, 64 + l and 96 + l of a tile, a word of 4 blocks
         // each, 16 bytes as they lie in the tile.  Loaded two stages ahead; a set is free when the stage that used it last is done.
-        const uint32_t sf0 = tmem + MM_SF_COL + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t sf0 = tmem + MM_SF_COL + ((uint32_t)(quarter * 32) << 16);
         struct Words {
             uint4 x[2], y[2][S::Y_TILES];
         };
-        int lt = blockIdx.x, lk = 0, lx = 0, ly = 0;          // the next stage to load
+        int lt = first, lk = k0, lx = 0, ly = 0;              // the next stage to load
         if (lt < n_tiles) tile_at(a, lt, lx, ly);
         auto load = [&](Words& w) {
             if (lt >= n_tiles) return;
@@ -294,13 +384,13 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                                     ? __ldg(reinterpret_cast<const uint4*>(a.ys + ((int64_t)(yt + q) * K + lk) * 1024 + h * 512) + lane)
                                     : zero;
             }
-            if (++lk == K) {
-                lk = 0;
-                lt += gridDim.x;
+            if (++lk == k1) {
+                lk = k0;
+                lt += step;
                 if (lt < n_tiles) tile_at(a, lt, lx, ly);
             }
         };
-        const int total = blockIdx.x < n_tiles ? ((n_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * K : 0;
+        const int total = first < n_tiles ? ((n_tiles - 1 - first) / step + 1) * (k1 - k0) : 0;
         static_assert(S::STAGES > MM_SF_SETS, "a barrier of the ring is waited for within its turn");
         int set = 0, old = 0;                                 // the set of stage i, and the ring's place of stage i - sets
         uint32_t old_phase = 0;
@@ -338,15 +428,15 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         for (int i = 0; i < total; i += 2) {
             if (!put(i, w0)) break;
             load(w0);
-            if (i + 1 < total) {
-                if (!put(i + 1, w1)) break;
-                load(w1);
-            }
+            if (i + 1 == total || !put(i + 1, w1)) break;
+            load(w1);
         }
+    } else if (SPLIT) {
+        ok = mm_wait(acc_full, 0, a.spin_limit, stop);
+        ok = __all_sync(0xFFFFFFFFu, ok);
     } else {
-        const int quarter = warp & 3;                        // the 32 lanes of tensor memory this warp can read
         int n = 0;
-        for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, ++n) {
+        for (int t = first; t < n_tiles; t += step, ++n) {
             int x, y;
             tile_at(a, t, x, y);
             const int acc = n & 1;
@@ -359,39 +449,6 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             const uint32_t d = tmem + (acc ? S::ACC1 : 0) + ((uint32_t)(quarter * 32) << 16);
             const int64_t xr = (int64_t)x * MM_BX + quarter * 32 + lane;
             const int64_t y0 = (int64_t)y * BN;
-            auto put = [&](int col, const uint32_t (&v)[16]) {
-                if (xr >= a.x_rows) return;
-                if (a.swap) {
-                    // a lane holds one column of D: the warp stores 32 consecutive ones of each row
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (y0 + col + e < a.y_rows)
-                            st1_any(a.d, (y0 + col + e) * a.ldd + xr, __uint_as_float(v[e]) * a.alpha, a.dt);
-                    return;
-                }
-                const int64_t at = xr * a.ldd + y0 + col;
-                if (a.wide_store && y0 + col + 16 <= a.y_rows) {
-                    float lo[8], hi[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        lo[e] = __uint_as_float(v[e]) * a.alpha;
-                        hi[e] = __uint_as_float(v[8 + e]) * a.alpha;
-                    }
-                    if (a.dt == ZERO_F32) {
-                        const Raw8<ZERO_F32> l = narrow8<ZERO_F32>(lo), h = narrow8<ZERO_F32>(hi);
-                        st32(static_cast<float*>(a.d) + at, l.w[0], l.w[1]);
-                        st32(static_cast<float*>(a.d) + at + 8, h.w[0], h.w[1]);
-                    } else if (a.dt == ZERO_BF16) {
-                        st32(static_cast<uint16_t*>(a.d) + at, narrow8<ZERO_BF16>(lo).w[0], narrow8<ZERO_BF16>(hi).w[0]);
-                    } else {
-                        st32(static_cast<uint16_t*>(a.d) + at, narrow8<ZERO_F16>(lo).w[0], narrow8<ZERO_F16>(hi).w[0]);
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (y0 + col + e < a.y_rows) st1_any(a.d, at + e, __uint_as_float(v[e]) * a.alpha, a.dt);
-                }
-            };
             auto release = [&] {
                 tc_fence_before();
                 __syncwarp();
@@ -407,17 +464,18 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
                 tc_wait_ld();
                 release();
 #pragma unroll
-                for (int c = 0; c < S::EARLY / 16; ++c) put(at + 16 * c, v[c]);
+                for (int c = 0; c < S::EARLY / 16; ++c) put16(a, xr, y0, at + 16 * c, 16, v[c], epi);
                 if (acc) col = S::EARLY;
                 else end = BN - S::EARLY;
             }
+#pragma unroll 1
             for (; col < end; col += 16) {
                 uint32_t v[16];
                 __syncwarp();
                 tc_ld16(d + col, v);
                 tc_wait_ld();
                 if (!S::OVERLAP && col + 16 == end) release();
-                put(col, v);
+                put16(a, xr, y0, col, 16, v, epi);
             }
         }
     }
@@ -437,6 +495,73 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (SPLIT) {
+        // Every block of the cluster finishes BN / split of the tile's columns: it gets the others' parts of them where
+        // its stages were, and adds all in the order of k, so that the sum does not depend on who comes first.
+        cluster_arrive();
+        cluster_wait();                        // all products and loads of the cluster are done
+        tc_fence_after();
+        const int own = BN / a.split;          // a multiple of 4
+        const uint32_t d = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int row = quarter * 32 + lane;
+        const bool epilogue = warp >= 2 && warp < 6;
+        if (epilogue)
+            for (int col = 0; col < BN; col += 16) {
+                uint32_t v[16];
+                __syncwarp();
+                tc_ld16(d + col, v);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const int to = (col + e) / own;
+                    if (to == rank) continue;
+                    // this block's place among the other blocks' parts there; four columns of a row together
+                    const int slot = rank < to ? rank : rank - 1, c = (col + e) - to * own;
+                    st_remote4(remote_addr(stages, to) + (((slot * own + c) >> 2) * MM_BX + row) * 16, v + e);
+                }
+            }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();                        // all parts are there; no block leaves before its last one has been sent
+        if (epilogue) {
+            int x, y;
+            tile_at(a, first, x, y);
+            const float4* parts = reinterpret_cast<const float4*>(head + MM_HEADER);
+            for (int col = 0; col < own; col += 16) {
+                // columns c0 .. c0 + n - 1 are this block's; they lie in the 16 from base16 on, at `at`
+                const int n = min(16, own - col), c0 = rank * own + col, at = c0 & 15;
+                uint32_t t[16], v[16];
+                __syncwarp();
+                tc_ld16(d + c0 - at, t);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    float4 mine = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int f = 0; f < 16; f += 4)
+                        if (f == at + e)
+                            mine = make_float4(__uint_as_float(t[f]), __uint_as_float(t[f + 1]), __uint_as_float(t[f + 2]),
+                                               __uint_as_float(t[f + 3]));
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (e < n)
+                        for (int r = 0; r < a.split; ++r) {
+                            const float4 p = r == rank ? mine : parts[(((r < rank ? r : r - 1) * own + col + e) >> 2) * MM_BX + row];
+                            sum.x += p.x;
+                            sum.y += p.y;
+                            sum.z += p.z;
+                            sum.w += p.w;
+                        }
+                    v[e] = __float_as_uint(sum.x);
+                    v[e + 1] = __float_as_uint(sum.y);
+                    v[e + 2] = __float_as_uint(sum.z);
+                    v[e + 3] = __float_as_uint(sum.w);
+                }
+                put16(a, (int64_t)x * MM_BX + row, (int64_t)y * BN, c0, n, v, epi);
+            }
+        }
+        tc_fence_before();
+        __syncthreads();
+    }
     tc_fence_after();
     if (warp == 1) {
         __syncwarp();
@@ -478,25 +603,48 @@ static int make_map(CUtensorMap* map, const zero_mx4& m, int box_rows) {
     return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_ECUDA, "zero_mx4_matmul: cuTensorMapEncodeTiled failed");
 }
 
-template <int BN>
-static int launch_matmul(const zero_mx4& x, const zero_mx4& y, MmArgs& a, int sms, cudaStream_t s) {
+template <int BN, bool SPLIT>
+static int launch_matmul(const CUtensorMap& xm, const CUtensorMap& ym, const MmArgs& a, int grid, cudaStream_t s) {
     using S = MmShape<BN>;
-    const int64_t x_tiles = (x.rows + MM_BX - 1) / MM_BX, y_tiles = (y.rows + BN - 1) / BN;
-    if (x_tiles * y_tiles > INT32_MAX / 2) return fail(ZERO_ELIMIT, "zero_mx4_matmul: too many tiles");
+    const void* f = (const void*)k_mx4_matmul<BN, SPLIT>;
+    int rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM),
+                       "zero_mx4_matmul shared-memory size");
+    if (rc != ZERO_OK) return rc;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(MM_THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = SPLIT ? 2 : 1;
+    void* args[] = {const_cast<CUtensorMap*>(&xm), const_cast<CUtensorMap*>(&ym), const_cast<MmArgs*>(&a)};
+    return cuda_fail(cudaLaunchKernelExC(&cfg, f, args), "zero_mx4_matmul launch");
+}
+
+template <int BN>
+static int matmul(const zero_mx4& x, const zero_mx4& y, MmArgs& a, int sms, cudaStream_t s) {
+    const int64_t x_tiles = (x.rows + MM_BX - 1) / MM_BX, y_tiles = (y.rows + BN - 1) / BN, tiles = x_tiles * y_tiles;
+    if (tiles > INT32_MAX / 2) return fail(ZERO_ELIMIT, "zero_mx4_matmul: too many tiles");
     a.x_tiles = (int)x_tiles;
     a.y_tiles = (int)y_tiles;
     CUtensorMap xm, ym;
     int rc = make_map(&xm, x, MM_BX);
     if (rc == ZERO_OK) rc = make_map(&ym, y, BN);
     if (rc != ZERO_OK) return rc;
-    const void* f = (const void*)k_mx4_matmul<BN>;
-    rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM),
-                   "zero_mx4_matmul shared-memory size");
-    if (rc != ZERO_OK) return rc;
-    const int tiles = a.x_tiles * a.y_tiles;
-    void* args[] = {&xm, &ym, &a};
-    return cuda_fail(launch_after_previous(f, tiles < sms ? tiles : sms, MM_THREADS, args, S::SMEM, s),
-                     "zero_mx4_matmul launch");
+    // Few tiles and a long sum: blocks share it while the GPU has room for all
+    // of them at once and each keeps 7 stages (clusters of 4 and 8 do not fill
+    // every SM of a GPC).
+    a.split = 1;
+    while (a.split < MM_SPLIT && BN / (2 * a.split) >= 4 && tiles * 2 * a.split <= (a.split == 1 ? sms : sms * 5 / 6) && a.k_steps / (2 * a.split) >= 7)
+        a.split *= 2;
+    if (a.split > 1) return launch_matmul<BN, true>(xm, ym, a, (int)tiles * a.split, s);
+    return launch_matmul<BN, false>(xm, ym, a, tiles < sms ? (int)tiles : sms, s);
 }
 
 __global__ void k_fill_zero(void* d, int64_t ld, int64_t rows, int64_t cols, int dt) {
@@ -549,16 +697,23 @@ int zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, float alpha, const zer
     m.y_rows = (int)y.rows;
     m.k_steps = (int)((a->cols + 255) / 256);
     m.dt = d->dtype;
-    m.wide_store = aligned(d->data, 32) && (a->rows == 1 || d->ld * elem_size(d->dtype) % 32 == 0);
+    const auto rows_on = [&](int n) { return aligned(d->data, n) && (a->rows == 1 || d->ld * elem_size(d->dtype) % n == 0); };
+    m.store = rows_on(32) ? 32 : rows_on(16) ? 16 : 0;
     m.alpha = alpha;
     m.status = status;
     const char* e = std::getenv("ZERO_GB300_SPIN_LIMIT");
     m.spin_limit = e ? (unsigned)std::strtoul(e, nullptr, 10) : SPIN_LIMIT;
     m.drain_limit = SPIN_LIMIT;
-    if (!m.swap) return launch_matmul<256>(x, y, m, sms, s);
-    if (y.rows <= 16) return launch_matmul<16>(x, y, m, sms, s);
-    if (y.rows <= 64) return launch_matmul<64>(x, y, m, sms, s);
-    return launch_matmul<128>(x, y, m, sms, s);
+    if (!m.swap) {
+        // 256 columns a tile, or 128 where that gives more tiles in as many rounds: a tile of 128 columns takes 0.9 of the
+        // time (4001 x 1600 x 6400: three rounds of them 33.6 us, two of 256 columns 24.9)
+        const int64_t xt = (x.rows + MM_BX - 1) / MM_BX;
+        const auto rounds = [&](int bn) { return (xt * ((y.rows + bn - 1) / bn) + sms - 1) / sms; };
+        return rounds(256) * 10 <= rounds(128) * 9 ? matmul<256>(x, y, m, sms, s) : matmul<128>(x, y, m, sms, s);
+    }
+    if (y.rows <= 16) return matmul<16>(x, y, m, sms, s);
+    if (y.rows <= 64) return matmul<64>(x, y, m, sms, s);
+    return matmul<128>(x, y, m, sms, s);
 }
 
 }  // extern "C"

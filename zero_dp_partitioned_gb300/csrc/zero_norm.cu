@@ -35,74 +35,41 @@ struct NormArgs {
     float* part;                        // backward: [grid][cols] partial dw
 };
 
-// Columns of element e of unit u: V8 units are 8 consecutive columns, the
-// others 4 columns 32 apart inside a warp's 128.
-template <bool V8>
+// Units of 8 columns (zero_layer.cuh).  V8: every row of every matrix starts on
+// a 16-byte boundary and the columns are a multiple of 8.
 struct Map {
-    static constexpr int E = V8 ? 8 : 4;
-    static constexpr int LANES = V8 ? 16 : 32;      // lanes that share 128 columns
+    static constexpr int E = 8, LANES = 16;         // elements of a unit, lanes that share 128 columns
     // this thread's j-th unit
     static __device__ __forceinline__ int unit(int j) { return threadIdx.x + j * blockDim.x; }
-    static __device__ __forceinline__ int col(int u, int e) {
-        return V8 ? u * 8 + e : (u >> 5) * 128 + e * 32 + (u & 31);
-    }
-    static __device__ __forceinline__ bool any(int u, int cols) { return col(u, 0) < cols; }
+    static __device__ __forceinline__ int col(int u, int e) { return u * 8 + e; }
+    static __device__ __forceinline__ bool any(int u, int cols) { return u * 8 < cols; }
 };
 
-// Loads of one unit of a row, kept as they lie until they are used, so that
-// every load of a row is in flight before the first is waited for.
+// One unit of a row, as it lies in memory.  A warp's lanes hold consecutive
+// units, and call store() together.
 template <int DT, bool V8>
 struct Unit {
-    Raw8<DT> raw;                        // V8
-    float one[V8 ? 1 : 4];
-    __device__ __forceinline__ void load(const void* row, int u, int cols) {
-        if constexpr (V8) {
-            if (u * 8 < cols) raw = ld8<DT>(row, u * 8);
-            else
-#pragma unroll
-                for (auto& w : raw.w) w = make_uint4(0, 0, 0, 0);
+    Raw8<DT> raw;
+    __device__ __forceinline__ void load(const void* row, int u, int cols, const Extent& x) {
+        if (u * 8 < cols) {
+            raw = V8 ? ld8<DT>(row, u * 8) : ld8_shifted<DT>(row, u * 8, cols, x);
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = Map<V8>::col(u, e);
-                one[e] = c < cols ? ld1<DT>(row, c) : 0.f;
-            }
+            for (auto& w : raw.w) w = make_uint4(0, 0, 0, 0);
         }
     }
-    __device__ __forceinline__ uint64_t pair(int q) const {
-        if constexpr (V8) return pair8<DT>(raw, q);
-        else return pack2(one[2 * q], one[2 * q + 1]);
-    }
-    // values that the type holds exactly
-    __device__ __forceinline__ void hold(const float (&v)[Map<V8>::E]) {
-        if constexpr (V8) raw = narrow8<DT>(v);
-        else
-#pragma unroll
-            for (int e = 0; e < 4; ++e) one[e] = v[e];
-    }
+    __device__ __forceinline__ uint64_t pair(int q) const { return pair8<DT>(raw, q); }
+    __device__ __forceinline__ void hold(const float (&v)[8]) { raw = narrow8<DT>(v); }
     __device__ __forceinline__ void store(void* row, int u, int cols) const {
-        if constexpr (V8) {
-            if (u * 8 < cols) st8<DT>(row, u * 8, raw);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = Map<V8>::col(u, e);
-                if (c < cols) st1<DT>(row, c, one[e]);
-            }
-        }
+        if constexpr (!V8) st8_shifted<DT>(row, u * 8, cols, u * 8 < cols, raw);
+        else if (u * 8 < cols) st8<DT>(row, u * 8, raw);
     }
-    __device__ __forceinline__ void values(float (&v)[Map<V8>::E]) const {
-        if constexpr (V8) widen8<DT>(raw, v);
-        else
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = one[e];
-    }
+    __device__ __forceinline__ void values(float (&v)[8]) const { widen8<DT>(raw, v); }
 };
 
 // Rows on their way: a thread copies its own units of the next rows to its own
 // slots of shared memory (cp.async, 16 bytes each, past the registers and L1)
-// and waits for its own copies alone, so no barrier is involved.  Units that
-// are not whole 16-byte words are loaded when they are needed.
+// and waits for its own copies alone, so no barrier is involved.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -116,62 +83,91 @@ __device__ __forceinline__ void copies_wait_all_but(int n) {     // n = stages -
     else copies_wait<3>();
 }
 
-// One matrix of a stage: NV units a thread, each of 1 or 2 words.
-template <int DT, int NV>
+// One matrix of a stage: NV units a thread.  A unit is 1 word (fp32: 2) of
+// shared memory, and one more where rows start anywhere: the aligned words that
+// it touches, each lane for itself (the word that two lanes share is read from
+// L2 twice, and no lane waits for another).
+template <int DT, int NV, bool V8>
 struct Slots {
-    static constexpr int WORDS = DT == ZERO_F32 ? 2 : 1;
+    static constexpr int N = DT == ZERO_F32 ? 8 : 4, WORDS = N / 4 + (V8 ? 0 : 1);
     static constexpr int COUNT = NV * WORDS;          // words of a thread
     uint4* at;                                        // this thread's first word; the next is blockDim.x further
-    __device__ __forceinline__ void copy(const void* row, int cols) const {
+    __device__ __forceinline__ void copy(const void* row, int cols, const Extent& x) const {
+        const char* p = static_cast<const char*>(row);
+        const int off = V8 ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int u = Map<true>::unit(j);
+            const int u = Map::unit(j);
             if (u * 8 >= cols) continue;
+            const char* q = p + (int64_t)u * 8 * Elem<DT>::SIZE - off;
+            uint4* slot = at + j * WORDS * blockDim.x;
+            if (V8 || (q >= x.lo && q + 16 * WORDS <= x.hi)) {
 #pragma unroll
-            for (int w = 0; w < WORDS; ++w)
-                copy16((uint32_t)__cvta_generic_to_shared(at + (j * WORDS + w) * blockDim.x),
-                       static_cast<const char*>(row) + (int64_t)u * 8 * Elem<DT>::SIZE + 16 * w);
+                for (int w = 0; w < WORDS; ++w)
+                    copy16((uint32_t)__cvta_generic_to_shared(slot + w * blockDim.x), q + 16 * w);
+            } else {
+                // the matrix's first or last words, not whole: element by element, to where the shift will look for them
+#pragma unroll 1
+                for (int e = 0; e < 8; ++e) {
+                    const int by = off + e * Elem<DT>::SIZE;
+                    char* to = reinterpret_cast<char*>(slot + (by >> 4) * blockDim.x) + (by & 15);
+                    const char* from = q + by;
+                    if constexpr (DT == ZERO_F32)
+                        *reinterpret_cast<uint32_t*>(to) = u * 8 + e < cols ? *reinterpret_cast<const uint32_t*>(from) : 0u;
+                    else
+                        *reinterpret_cast<uint16_t*>(to) =
+                            u * 8 + e < cols ? *reinterpret_cast<const uint16_t*>(from) : (uint16_t)0;
+                }
+            }
         }
     }
-    __device__ __forceinline__ void read(Unit<DT, true> (&u)[NV], int cols) const {
+    __device__ __forceinline__ void read(Unit<DT, V8> (&u)[NV], const void* row, int cols) const {
+        const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const uint4* slot = at + j * WORDS * blockDim.x;
+            const int left = cols - Map::unit(j) * 8;       // columns from this unit's first
+            uint32_t w[N + 4];
 #pragma unroll
-            for (int w = 0; w < WORDS; ++w)
-                u[j].raw.w[w] = Map<true>::unit(j) * 8 < cols ? at[(j * WORDS + w) * blockDim.x] : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < WORDS; ++k) {
+                const uint4 v = left > 0 ? slot[k * blockDim.x] : make_uint4(0, 0, 0, 0);
+                w[4 * k] = v.x;
+                w[4 * k + 1] = v.y;
+                w[4 * k + 2] = v.z;
+                w[4 * k + 3] = v.w;
+            }
+            if constexpr (!V8) {
+                shift_words<N>(w, off);
+                if (left < 8)                               // what follows the row's last column is not the row's
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e >= left) {
+                            if constexpr (DT == ZERO_F32) w[e] = 0;
+                            else w[e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                        }
+            }
+#pragma unroll
+            for (int k = 0; k < N / 4; ++k) u[j].raw.w[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        }
     }
 };
 
 template <int DT, bool V8>
-__device__ __forceinline__ void store_unit(void* row, int u, int cols, const float (&v)[Map<V8>::E]) {
-    if constexpr (V8) {
-        if (u * 8 < cols) st8<DT>(row, u * 8, narrow8<DT>(v));
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = Map<V8>::col(u, e);
-            if (c < cols) st1<DT>(row, c, v[e]);
-        }
-    }
+__device__ __forceinline__ void store_unit(void* row, int u, int cols, const float (&v)[8]) {
+    Unit<DT, V8> o;
+    o.hold(v);
+    o.store(row, u, cols);
 }
 
 template <bool V8>
-__device__ __forceinline__ void store_e4m3(void* row, int u, int cols, const float (&v)[Map<V8>::E]) {
-    uint8_t* p = static_cast<uint8_t*>(row);
-    if constexpr (V8) {
-        if (u * 8 >= cols) return;
-        uint32_t h[4];
+__device__ __forceinline__ void store_e4m3(void* row, int u, int cols, const float (&v)[8]) {
+    uint32_t h[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            h[q] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * q], v[2 * q + 1]), __NV_SATFINITE, __NV_E4M3);
-        *reinterpret_cast<uint2*>(p + u * 8) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = Map<V8>::col(u, e);
-            if (c < cols) p[c] = __nv_cvt_float_to_fp8(v[e], __NV_SATFINITE, __NV_E4M3);
-        }
-    }
+    for (int q = 0; q < 4; ++q)
+        h[q] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * q], v[2 * q + 1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t w[2] = {h[0] | h[1] << 16, h[2] | h[3] << 16};
+    if constexpr (!V8) st_shifted<1, 2>(row, u * 8, cols, u * 8 < cols, w);
+    else if (u * 8 < cols) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(row) + u * 8) = make_uint2(w[0], w[1]);
 }
 
 // |y|'s largest of a unit, NaN kept (its bits then order above infinity's).
@@ -189,42 +185,35 @@ __device__ __forceinline__ float scale_of(float top) {
 // The reciprocal is approximate (1 ulp): it moves a value across a rounding
 // boundary of 4 bits about once in 2^20, to a neighbour as near.
 template <bool V8>
-__device__ __forceinline__ void quantised_store(void* row, int u, int cols, float (&v)[Map<V8>::E], float scale) {
+__device__ __forceinline__ void quantised_store(void* row, int u, int cols, float (&v)[Map::E], float scale) {
     float inv;
     asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(scale));
 #pragma unroll
-    for (int e = 0; e < Map<V8>::E; ++e) v[e] *= inv;
+    for (int e = 0; e < Map::E; ++e) v[e] *= inv;
     store_e4m3<V8>(row, u, cols, v);
 }
 
-template <bool V8>
-__device__ __forceinline__ void weights(const NormArgs& a, int u, float (&w)[Map<V8>::E]) {
+__device__ __forceinline__ void weights(const NormArgs& a, int u, float (&w)[8]) {
     if (!a.w) {
 #pragma unroll
-        for (int e = 0; e < Map<V8>::E; ++e) w[e] = 1.f;
-    } else if constexpr (V8) {
-        if (u * 8 < a.cols) ld8_any(a.w, u * 8, a.wdt, a.w_aligned, w);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 0.f;
+        for (int e = 0; e < 8; ++e) w[e] = 1.f;
+    } else if (u * 8 + 8 <= a.cols) {
+        ld8_any(a.w, u * 8, a.wdt, a.w_aligned, w);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = Map<V8>::col(u, e);
-            w[e] = c < a.cols ? ld1_any(a.w, c, a.wdt) : 0.f;
-        }
+        for (int e = 0; e < 8; ++e) w[e] = u * 8 + e < a.cols ? ld1_any(a.w, u * 8 + e, a.wdt) : 0.f;
     }
 }
 
 // A thread's columns are the same in every row it walks: their weights stay in registers.
-template <bool V8, int NV>
-__device__ __forceinline__ void weight_pairs(const NormArgs& a, uint64_t (&w)[NV][Map<V8>::E / 2]) {
+template <int NV>
+__device__ __forceinline__ void weight_pairs(const NormArgs& a, uint64_t (&w)[NV][Map::E / 2]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        float v[Map<V8>::E];
-        weights<V8>(a, Map<V8>::unit(j), v);
+        float v[Map::E];
+        weights(a, Map::unit(j), v);
 #pragma unroll
-        for (int q = 0; q < Map<V8>::E / 2; ++q) w[j][q] = pack2(v[2 * q], v[2 * q + 1]);
+        for (int q = 0; q < Map::E / 2; ++q) w[j][q] = pack2(v[2 * q], v[2 * q + 1]);
     }
 }
 
@@ -240,13 +229,13 @@ __device__ __forceinline__ void* row_of(void* p, int64_t ld, int64_t r) {
 // x + r of one unit, rounded to the type h is stored in.
 template <int XT, int RT, bool V8>
 __device__ __forceinline__ void add_unit(const Unit<XT, V8>& x, const Unit<RT, V8>& r, bool has_r,
-                                         float (&h)[Map<V8>::E]) {
+                                         float (&h)[Map::E]) {
     x.values(h);
     if (!has_r) return;
-    float b[Map<V8>::E];
+    float b[Map::E];
     r.values(b);
 #pragma unroll
-    for (int e = 0; e < Map<V8>::E; ++e) {
+    for (int e = 0; e < Map::E; ++e) {
         h[e] = __fadd_rn(h[e], b[e]);
         if constexpr (RT != ZERO_F32) h[e] = Half16<RT>::widen(Half16<RT>::narrow(h[e]));
     }
@@ -255,45 +244,37 @@ __device__ __forceinline__ void add_unit(const Unit<XT, V8>& x, const Unit<RT, V
 // A row in NV units per thread, in registers.
 template <int XT, int RT, bool V8, int NV>
 __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_constant__ NormArgs a) {
-    constexpr int E = Map<V8>::E;
+    constexpr int E = Map::E;
     __shared__ float ssum[2][32];
     __shared__ uint32_t smax[2][32];
     pdl_wait();
     pdl_launch_next();
+    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols);
     extern __shared__ __align__(16) uint4 ring[];
-    const int S = a.stages;
-    constexpr int XW = Slots<XT, NV>::COUNT, RW = Slots<RT, NV>::COUNT;
-    const Slots<XT, NV> xs = {ring + threadIdx.x};
-    const Slots<RT, NV> rs = {ring + threadIdx.x + XW * blockDim.x};
-    const int stage_words = (XW + RW) * blockDim.x;
+    using X = Slots<XT, NV, V8>;
+    using R = Slots<RT, NV, V8>;
+    const int S = a.stages, stage_words = (X::COUNT + R::COUNT) * blockDim.x;
     auto copy = [&](int64_t row, int st) {
         if (row < a.rows) {
-            Slots<XT, NV>{xs.at + st * stage_words}.copy(row_of<XT>(a.x, a.ldx, row), a.cols);
-            if (a.r) Slots<RT, NV>{rs.at + st * stage_words}.copy(row_of<RT>(a.r, a.ldr, row), a.cols);
+            uint4* at = ring + threadIdx.x + st * stage_words;
+            X{at}.copy(row_of<XT>(a.x, a.ldx, row), a.cols, ex);
+            if (a.r) R{at + X::COUNT * blockDim.x}.copy(row_of<RT>(a.r, a.ldr, row), a.cols, er);
         }
         copies_commit();
     };
-    if constexpr (V8)
-        for (int st = 0; st < S - 1; ++st) copy(blockIdx.x + (int64_t)st * gridDim.x, st);
+    for (int st = 0; st < S - 1; ++st) copy(blockIdx.x + (int64_t)st * gridDim.x, st);
     uint64_t w[NV][E / 2];
-    weight_pairs<V8, NV>(a, w);
+    weight_pairs<NV>(a, w);
     int turn = 0, st = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         Unit<XT, V8> x[NV];
         Unit<RT, V8> r[NV];
-        if constexpr (V8) {
-            copy(row + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
-            copies_wait_all_but(S - 1);
-            Slots<XT, NV>{xs.at + st * stage_words}.read(x, a.cols);
-            if (a.r) Slots<RT, NV>{rs.at + st * stage_words}.read(r, a.cols);
-            st = st == S - 1 ? 0 : st + 1;
-        } else {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) x[j].load(row_of<XT>(a.x, a.ldx, row), Map<V8>::unit(j), a.cols);
-            if (a.r)
-#pragma unroll
-                for (int j = 0; j < NV; ++j) r[j].load(row_of<RT>(a.r, a.ldr, row), Map<V8>::unit(j), a.cols);
-        }
+        copy(row + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
+        copies_wait_all_but(S - 1);
+        uint4* at = ring + threadIdx.x + st * stage_words;
+        X{at}.read(x, row_of<XT>(a.x, a.ldx, row), a.cols);
+        if (a.r) R{at + X::COUNT * blockDim.x}.read(r, row_of<RT>(a.r, a.ldr, row), a.cols);
+        st = st == S - 1 ? 0 : st + 1;
         // h as it is stored: half the registers of its fp32 values
         uint64_t s2 = 0;
 #pragma unroll
@@ -303,7 +284,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_cons
             r[j].hold(h);
 #pragma unroll
             for (int q = 0; q < E / 2; ++q) s2 = fma2(pack2(h[2 * q], h[2 * q + 1]), pack2(h[2 * q], h[2 * q + 1]), s2);
-            if (a.h) r[j].store(row_of<RT>(a.h, a.ldh, row), Map<V8>::unit(j), a.cols);
+            if (a.h) r[j].store(row_of<RT>(a.h, a.ldh, row), Map::unit(j), a.cols);
         }
         const float2 sp = unpack2(s2);
         const float ss = block_sum(sp.x + sp.y, ssum[turn]);
@@ -323,7 +304,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_cons
             for (int j = 0; j < NV; ++j) {
                 float y[E];
                 normed(j, y);
-                store_unit<XT, V8>(row_of<XT>(a.y, a.ldy, row), Map<V8>::unit(j), a.cols, y);
+                store_unit<XT, V8>(row_of<XT>(a.y, a.ldy, row), Map::unit(j), a.cols, y);
             }
             continue;
         }
@@ -335,10 +316,10 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_cons
             normed(j, y);
             const float t = top_of<E>(y);
             if (a.block128) {
-                const int u = Map<V8>::unit(j);
-                const float sc = scale_of(__uint_as_float(lanes_max<Map<V8>::LANES>(__float_as_uint(t))));
-                if ((u & (Map<V8>::LANES - 1)) == 0 && Map<V8>::any(u, a.cols))
-                    a.scale[row * a.n_scale + u / Map<V8>::LANES] = sc;
+                const int u = Map::unit(j);
+                const float sc = scale_of(__uint_as_float(lanes_max<Map::LANES>(__float_as_uint(t))));
+                if ((u & (Map::LANES - 1)) == 0 && Map::any(u, a.cols))
+                    a.scale[row * a.n_scale + u / Map::LANES] = sc;
                 quantised_store<V8>(Y, u, a.cols, y, sc);
             }
             whole = max3_nan(whole, t, t);
@@ -350,7 +331,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_cons
             for (int j = 0; j < NV; ++j) {
                 float y[E];
                 normed(j, y);
-                quantised_store<V8>(Y, Map<V8>::unit(j), a.cols, y, sc);
+                quantised_store<V8>(Y, Map::unit(j), a.cols, y, sc);
             }
         }
     }
@@ -361,13 +342,13 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_cons
 // time from L2.
 template <int XT, int RT, bool V8>
 __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid_constant__ NormArgs a) {
-    constexpr int E = Map<V8>::E;
+    constexpr int E = Map::E;
     __shared__ float ssum[2][32];
     __shared__ uint32_t smax[2][32];
     pdl_wait();
     pdl_launch_next();
-    const int units = V8 ? a.cols / 8 : (a.cols + 127) / 128 * 32;
-    const int steps = (units + (int)blockDim.x - 1) / (int)blockDim.x;
+    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols), eh = extent_of<RT>(a.h, a.ldh, a.rows, a.cols);
+    const int steps = ((a.cols + 7) / 8 + (int)blockDim.x - 1) / (int)blockDim.x;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const void* X = row_of<XT>(a.x, a.ldx, row);
@@ -376,13 +357,13 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
         auto value = [&](int u, float (&h)[E]) {      // h again, after it was stored over x or r
             if (H) {
                 Unit<RT, V8> s;
-                s.load(H, u, a.cols);
+                s.load(H, u, a.cols, eh);
                 s.values(h);
             } else {
                 Unit<XT, V8> x;
                 Unit<RT, V8> r;
-                x.load(X, u, a.cols);
-                if (R) r.load(R, u, a.cols);
+                x.load(X, u, a.cols, ex);
+                if (R) r.load(R, u, a.cols, er);
                 add_unit<XT, RT, V8>(x, r, R != nullptr, h);
             }
         };
@@ -391,8 +372,8 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
             const int u = threadIdx.x + j * blockDim.x;
             Unit<XT, V8> x;
             Unit<RT, V8> r;
-            x.load(X, u, a.cols);
-            if (R) r.load(R, u, a.cols);
+            x.load(X, u, a.cols, ex);
+            if (R) r.load(R, u, a.cols, er);
             float h[E];
             add_unit<XT, RT, V8>(x, r, R != nullptr, h);
 #pragma unroll
@@ -409,7 +390,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
                 const int u = threadIdx.x + j * blockDim.x;
                 float h[E], w[E];
                 value(u, h);
-                weights<V8>(a, u, w);
+                weights(a, u, w);
 #pragma unroll
                 for (int e = 0; e < E; ++e) top = max(top, abs_bits(h[e] * rstd * w[e]));
             }
@@ -420,7 +401,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
             const int u = threadIdx.x + j * blockDim.x;
             float h[E], w[E];
             value(u, h);
-            weights<V8>(a, u, w);
+            weights(a, u, w);
             uint32_t top = 0;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -433,9 +414,9 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
             }
             float mm = whole;
             if (a.block128) {
-                mm = scale_of(__uint_as_float(lanes_max<Map<V8>::LANES>(top)));
-                if ((u & (Map<V8>::LANES - 1)) == 0 && Map<V8>::any(u, a.cols))
-                    a.scale[row * a.n_scale + u / Map<V8>::LANES] = mm;
+                mm = scale_of(__uint_as_float(lanes_max<Map::LANES>(top)));
+                if ((u & (Map::LANES - 1)) == 0 && Map::any(u, a.cols))
+                    a.scale[row * a.n_scale + u / Map::LANES] = mm;
             }
             quantised_store<V8>(static_cast<uint8_t*>(a.y) + row * a.ldy, u, a.cols, h, mm);
         }
@@ -447,51 +428,42 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
 // written once, as one row of `part`.
 template <int XT, int RT, bool V8, int NV>
 __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_constant__ NormArgs a) {
-    constexpr int E = Map<V8>::E;
+    constexpr int E = Map::E;
     __shared__ float ssum[2][32];
     pdl_wait();
     pdl_launch_next();
+    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols), eh = extent_of<RT>(a.hin, a.ldhin, a.rows, a.cols);
     uint64_t dw[NV][E / 2] = {};
     const float inv_n = 1.f / (float)a.cols;
     extern __shared__ __align__(16) uint4 ring[];
-    const int S = a.stages;
-    constexpr int XW = Slots<XT, NV>::COUNT, RW = Slots<RT, NV>::COUNT;
-    const int stage_words = (XW + 2 * RW) * blockDim.x;
+    using X = Slots<XT, NV, V8>;
+    using R = Slots<RT, NV, V8>;
+    const int S = a.stages, stage_words = (X::COUNT + 2 * R::COUNT) * blockDim.x;
     const bool DH = a.r != nullptr;
     auto copy = [&](int64_t row, int st) {
         if (row < a.rows) {
             uint4* at = ring + threadIdx.x + st * stage_words;
-            Slots<XT, NV>{at}.copy(row_of<XT>(a.x, a.ldx, row), a.cols);
-            Slots<RT, NV>{at + XW * blockDim.x}.copy(row_of<RT>(a.hin, a.ldhin, row), a.cols);
-            if (DH) Slots<RT, NV>{at + (XW + RW) * blockDim.x}.copy(row_of<RT>(a.r, a.ldr, row), a.cols);
+            X{at}.copy(row_of<XT>(a.x, a.ldx, row), a.cols, ex);
+            R{at + X::COUNT * blockDim.x}.copy(row_of<RT>(a.hin, a.ldhin, row), a.cols, eh);
+            if (DH) R{at + (X::COUNT + R::COUNT) * blockDim.x}.copy(row_of<RT>(a.r, a.ldr, row), a.cols, er);
         }
         copies_commit();
     };
-    if constexpr (V8)
-        for (int st = 0; st < S - 1; ++st) copy(blockIdx.x + (int64_t)st * gridDim.x, st);
+    for (int st = 0; st < S - 1; ++st) copy(blockIdx.x + (int64_t)st * gridDim.x, st);
     uint64_t w[NV][E / 2];
-    weight_pairs<V8, NV>(a, w);
+    weight_pairs<NV>(a, w);
     int turn = 0, st = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const float rstd = a.rstd[row];
         Unit<XT, V8> dy[NV];
         Unit<RT, V8> h[NV], dh[NV];
-        if constexpr (V8) {
-            copy(row + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
-            copies_wait_all_but(S - 1);
-            uint4* at = ring + threadIdx.x + st * stage_words;
-            Slots<XT, NV>{at}.read(dy, a.cols);
-            Slots<RT, NV>{at + XW * blockDim.x}.read(h, a.cols);
-            if (DH) Slots<RT, NV>{at + (XW + RW) * blockDim.x}.read(dh, a.cols);
-            st = st == S - 1 ? 0 : st + 1;
-        } else {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                dy[j].load(row_of<XT>(a.x, a.ldx, row), Map<V8>::unit(j), a.cols);
-                h[j].load(row_of<RT>(a.hin, a.ldhin, row), Map<V8>::unit(j), a.cols);
-                if (DH) dh[j].load(row_of<RT>(a.r, a.ldr, row), Map<V8>::unit(j), a.cols);
-            }
-        }
+        copy(row + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
+        copies_wait_all_but(S - 1);
+        uint4* at = ring + threadIdx.x + st * stage_words;
+        X{at}.read(dy, row_of<XT>(a.x, a.ldx, row), a.cols);
+        R{at + X::COUNT * blockDim.x}.read(h, row_of<RT>(a.hin, a.ldhin, row), a.cols);
+        if (DH) R{at + (X::COUNT + R::COUNT) * blockDim.x}.read(dh, row_of<RT>(a.r, a.ldr, row), a.cols);
+        st = st == S - 1 ? 0 : st + 1;
         const uint64_t rr = pack2(rstd, rstd);
         uint64_t d2 = 0;
 #pragma unroll
@@ -516,7 +488,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_con
                 v[2 * q] = p.x;
                 v[2 * q + 1] = p.y;
             }
-            store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), Map<V8>::unit(j), a.cols, v);
+            store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), Map::unit(j), a.cols, v);
         }
     }
     if (!a.part) return;
@@ -524,7 +496,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_con
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int c = Map<V8>::col(Map<V8>::unit(j), e);
+            const int c = Map::col(Map::unit(j), e);
             const float2 p = unpack2(dw[j][e / 2]);
             if (c < a.cols) a.part[(int64_t)blockIdx.x * a.cols + c] = e % 2 ? p.y : p.x;
         }
@@ -534,11 +506,12 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_con
 // blocks that own 128 columns and a share of the rows (gridDim.y shares).
 template <int XT, int RT, bool V8>
 __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward_long(const __grid_constant__ NormArgs a) {
-    constexpr int E = Map<V8>::E;
+    constexpr int E = Map::E;
     __shared__ float ssum[2][32];
     pdl_wait();
     pdl_launch_next();
-    const int units = V8 ? a.cols / 8 : (a.cols + 127) / 128 * 32;
+    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols), eh = extent_of<RT>(a.hin, a.ldhin, a.rows, a.cols);
+    const int steps = ((a.cols + 7) / 8 + (int)blockDim.x - 1) / (int)blockDim.x;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const void* DY = row_of<XT>(a.x, a.ldx, row);
@@ -546,29 +519,31 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward_long(const __gri
         const void* DH = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
         const float rstd = a.rstd[row];
         float dot = 0.f;
-        for (int u = threadIdx.x; u < units; u += blockDim.x) {
+        for (int j = 0; j < steps; ++j) {
+            const int u = threadIdx.x + j * blockDim.x;
             Unit<XT, V8> dy;
             Unit<RT, V8> h;
-            dy.load(DY, u, a.cols);
-            h.load(H, u, a.cols);
+            dy.load(DY, u, a.cols, ex);
+            h.load(H, u, a.cols, eh);
             float g[E], v[E], w[E];
             dy.values(g);
             h.values(v);
-            weights<V8>(a, u, w);
+            weights(a, u, w);
 #pragma unroll
             for (int e = 0; e < E; ++e) dot = fmaf(g[e] * w[e], v[e] * rstd, dot);
         }
         const float c = block_sum(dot, ssum[turn]) / (float)a.cols;
-        for (int u = threadIdx.x; u < units; u += blockDim.x) {
+        for (int j = 0; j < steps; ++j) {
+            const int u = threadIdx.x + j * blockDim.x;
             Unit<XT, V8> dy;
             Unit<RT, V8> h, dh;
-            dy.load(DY, u, a.cols);
-            h.load(H, u, a.cols);
-            if (DH) dh.load(DH, u, a.cols);
+            dy.load(DY, u, a.cols, ex);
+            h.load(H, u, a.cols, eh);
+            if (DH) dh.load(DH, u, a.cols, er);
             float g[E], v[E], w[E], up[E];
             dy.values(g);
             h.values(v);
-            weights<V8>(a, u, w);
+            weights(a, u, w);
             if (DH) dh.values(up);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -648,7 +623,7 @@ static const void* norm_fn(bool fwd, int xt, int rt, bool v8, int nv) {
     return rt == ZERO_F32 ? pick<ZERO_F16, ZERO_F32>(fwd, v8, nv) : pick<ZERO_F16, ZERO_F16>(fwd, v8, nv);
 }
 
-static int words_of(int dt) { return dt == ZERO_F32 ? 2 : 1; }
+static int words_of(int dt, bool v8) { return (dt == ZERO_F32 ? 2 : 1) + (v8 ? 0 : 1); }
 
 // How a row is shared out: units per thread (0: the row does not fit the
 // registers, or two stages of it shared memory), threads per row, blocks per
@@ -658,16 +633,16 @@ struct NormShape {
     int nv, threads, per_sm, stages;
     size_t smem;
 };
-static NormShape shape_of(int64_t cols, bool v8, int words, int sm_threads) {
+static NormShape shape_of(int64_t cols, int words, int sm_threads) {
     NormShape s;
-    const int64_t units = v8 ? (cols + 7) / 8 : (cols + 127) / 128 * 32;
+    const int64_t units = (cols + 7) / 8;
     s.nv = units <= 2 * NORM_THREADS ? 2 : units <= 4 * NORM_THREADS ? 4 : 0;
     const int64_t t = s.nv ? (units + s.nv - 1) / s.nv : NORM_THREADS;
     s.threads = (int)((t + 31) / 32 * 32);
     s.per_sm = sm_threads / s.threads < 1 ? 1 : sm_threads / s.threads;
     s.stages = 2;
     s.smem = 0;
-    if (!v8 || !s.nv) return s;
+    if (!s.nv) return s;
     const size_t stage = (size_t)words * s.nv * s.threads * 16;
     while (s.stages < NORM_MAX_STAGES && (s.stages + 1) * stage * s.per_sm <= NORM_SM_SMEM) ++s.stages;
     s.smem = s.stages * stage;
@@ -740,7 +715,7 @@ int zero_norm_forward(const zero_mat* x, const zero_mat* residual, const zero_ma
     const bool y_ok = y8 ? aligned(y->data, 8) && (rows == 1 || y->ld % 8 == 0) : rows_aligned(*y, rows);
     const bool v8 = cols % 8 == 0 && rows_aligned(*x, rows) && y_ok && (!residual || rows_aligned(*residual, rows)) &&
                     (!h_out || rows_aligned(*h_out, rows));
-    const NormShape p = shape_of(cols, v8, words_of(x->dtype) + words_of(rt), NORM_FORWARD_THREADS);
+    const NormShape p = shape_of(cols, words_of(x->dtype, v8) + words_of(rt, v8), NORM_FORWARD_THREADS);
     a.stages = p.stages;
     const int sms = sm_count();
     if (!sms) return ZERO_ECUDA;
@@ -795,7 +770,7 @@ int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* we
     a.part = dw ? static_cast<float*>(workspace) : nullptr;
     const bool v8 = cols % 8 == 0 && rows_aligned(*dy, rows) && rows_aligned(*h, rows) && rows_aligned(*dx, rows) &&
                     (!dh || rows_aligned(*dh, rows));
-    const NormShape p = shape_of(cols, v8, words_of(dy->dtype) + 2 * words_of(rt), NORM_BACKWARD_THREADS);
+    const NormShape p = shape_of(cols, words_of(dy->dtype, v8) + 2 * words_of(rt, v8), NORM_BACKWARD_THREADS);
     a.stages = p.stages;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* args[] = {&a};
