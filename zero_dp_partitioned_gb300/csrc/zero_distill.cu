@@ -411,12 +411,12 @@ static int distill(const char* who, const zero_mat* logits, int64_t rows, int64_
     a.grad_scale = grad_scale;
 
     // Threads so that a short row leaves none idle; a block to a row, and a
-    // cluster of more while the rows alone do not fill the GPU.
+    // cluster of more while all of them run at once.
     const int W = 16 / elem_size(logits->dtype);
     const int64_t n = cols / W + 1;          // whole vectors of a row, at most
     const int threads = n <= 1024 ? 128 : DISTILL_THREADS;
     int split = 1;
-    while (split < DISTILL_CLUSTER && rows * split < 2 * (int64_t)sms && split * threads < n) split *= 2;
+    while (split < DISTILL_CLUSTER && rows * split <= DISTILL_BLOCKS / 2 * (int64_t)sms && split * threads < n) split *= 2;
     a.split = split;
     // what a thread keeps: all its vectors if they are few, in whole batches
     const int64_t own = (n + (int64_t)split * threads - 1) / ((int64_t)split * threads);
@@ -437,10 +437,8 @@ static int distill(const char* who, const zero_mat* logits, int64_t rows, int64_
     cfg.numAttrs = bwd ? 1 : 2;
     const void* f = logits->dtype == ZERO_F32 ? distill_fn<ZERO_F32>(bwd)
                   : logits->dtype == ZERO_BF16 ? distill_fn<ZERO_BF16>(bwd) : distill_fn<ZERO_F16>(bwd);
-    if (cfg.dynamicSmemBytes > 40 * 1024) {
-        rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes), who);
-        if (rc != ZERO_OK) return rc;
-    }
+    rc = raise_smem(f, cfg.dynamicSmemBytes, who);
+    if (rc != ZERO_OK) return rc;
     void* args[] = {&a};
     return cuda_fail(cudaLaunchKernelExC(&cfg, f, args), who);
 }

@@ -1,6 +1,7 @@
 // zero_layer.cu -- host checks shared by the layer operators.
 #include <map>
 #include <mutex>
+#include <utility>
 
 #include "zero_layer.cuh"
 
@@ -21,6 +22,20 @@ int check_mat(const zero_mat* m, int64_t rows, int64_t cols, unsigned types, con
     if (!aligned(m->data, (size_t)elem_size(m->dtype)))
         return refuse(ZERO_EALIGN, call, what, ": not aligned to its element");
     return ZERO_OK;
+}
+
+int raise_smem(const void* f, size_t smem, const char* who) {
+    static std::mutex mu;
+    static std::map<std::pair<int, const void*>, size_t> raised;     // (device, kernel) -> its limit
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    std::lock_guard<std::mutex> g(mu);
+    size_t& had = raised[{dev, f}];
+    if (smem <= (had ? had : 40 * 1024)) return ZERO_OK;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) had = smem;
+    return cuda_fail(e, who);
 }
 
 int sm_count() {

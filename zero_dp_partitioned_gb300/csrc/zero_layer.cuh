@@ -357,6 +357,9 @@ constexpr unsigned FLOAT_TYPES = 1u << ZERO_F16 | 1u << ZERO_BF16 | 1u << ZERO_F
 inline bool rows_aligned(const zero_mat& m, int64_t rows) {
     return aligned(m.data, 16) && (rows <= 1 || (m.ld * elem_size(m.dtype)) % 16 == 0);
 }
+// Raises a kernel's limit of dynamic shared memory on the current device to
+// `smem` where it is lower (asked of the driver once).
+int raise_smem(const void* f, size_t smem, const char* who);
 // SM count of the current device (0 and an error message if it cannot be had).
 int sm_count();
 

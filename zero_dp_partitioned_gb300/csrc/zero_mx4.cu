@@ -484,8 +484,7 @@ int zero_mx4_quantize(const zero_mat* src, int64_t rows, int64_t cols, const zer
           : dt == ZERO_BF16 ? (const void*)k_mx4_both<ZERO_BF16> : (const void*)k_mx4_both<ZERO_F16>;
         threads = MX4_BOTH_THREADS;
         smem = dt == ZERO_F32 ? Mx4Both<ZERO_F32>::SMEM : Mx4Both<ZERO_BF16>::SMEM;
-        rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                       "zero_mx4_quantize shared-memory size");
+        rc = raise_smem(f, smem, "zero_mx4_quantize shared-memory size");
         if (rc != ZERO_OK) return rc;
         grid = blocks_for((rows + 255) / 256 * 2 * ((cols + 255) / 256 * 2), Mx4Both<ZERO_BF16>::BLOCKS);
     } else {

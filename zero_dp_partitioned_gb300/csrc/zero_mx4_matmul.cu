@@ -607,8 +607,7 @@ template <int BN, bool SPLIT>
 static int launch_matmul(const CUtensorMap& xm, const CUtensorMap& ym, const MmArgs& a, int grid, cudaStream_t s) {
     using S = MmShape<BN>;
     const void* f = (const void*)k_mx4_matmul<BN, SPLIT>;
-    int rc = cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM),
-                       "zero_mx4_matmul shared-memory size");
+    int rc = raise_smem(f, S::SMEM, "zero_mx4_matmul shared-memory size");
     if (rc != ZERO_OK) return rc;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

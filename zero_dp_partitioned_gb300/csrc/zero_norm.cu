@@ -33,6 +33,7 @@ struct NormArgs {
     int wdt, w_aligned, y8, block128, stages;
     float *scale, *rstd;
     float* part;                        // backward: [grid][cols] partial dw
+    int part16;                         // its rows start on 16-byte boundaries
 };
 
 // Units of 8 columns (zero_layer.cuh).  V8: every row of every matrix starts on
@@ -492,14 +493,24 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_con
         }
     }
     if (!a.part) return;
+    float* part = a.part + (int64_t)blockIdx.x * a.cols;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+        const int c = Map::unit(j) * 8;
+        if (a.part16 && c + 8 <= a.cols) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int c = Map::col(Map::unit(j), e);
-            const float2 p = unpack2(dw[j][e / 2]);
-            if (c < a.cols) a.part[(int64_t)blockIdx.x * a.cols + c] = e % 2 ? p.y : p.x;
+            for (int q = 0; q < 4; q += 2) {
+                const float2 x = unpack2(dw[j][q]), y = unpack2(dw[j][q + 1]);
+                *reinterpret_cast<float4*>(part + c + 2 * q) = make_float4(x.x, x.y, y.x, y.y);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 p = unpack2(dw[j][e / 2]);
+                if (c + e < a.cols) part[c + e] = e % 2 ? p.y : p.x;
+            }
         }
+    }
 }
 
 // Rows too long for the registers: dx by walking the row twice, and dw by
@@ -649,11 +660,6 @@ static NormShape shape_of(int64_t cols, int words, int sm_threads) {
     if (s.smem <= NORM_SM_SMEM) return s;
     return NormShape{0, NORM_THREADS, sm_threads / NORM_THREADS, 2, 0};
 }
-static int raise_smem(const void* f, size_t smem, const char* who) {
-    if (smem <= 40 * 1024) return ZERO_OK;
-    return cuda_fail(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), who);
-}
-
 static int check_weight(const zero_mat* w, int64_t cols, NormArgs& a) {
     if (!w || !w->data) return ZERO_OK;
     if (w->dtype != ZERO_F16 && w->dtype != ZERO_BF16 && w->dtype != ZERO_F32)
@@ -768,6 +774,7 @@ int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* we
     a.cols = (int)cols;
     a.rstd = const_cast<float*>(rstd);
     a.part = dw ? static_cast<float*>(workspace) : nullptr;
+    a.part16 = cols % 4 == 0 && aligned(workspace, 16);
     const bool v8 = cols % 8 == 0 && rows_aligned(*dy, rows) && rows_aligned(*h, rows) && rows_aligned(*dx, rows) &&
                     (!dh || rows_aligned(*dh, rows));
     const NormShape p = shape_of(cols, words_of(dy->dtype, v8) + 2 * words_of(rt, v8), NORM_BACKWARD_THREADS);
