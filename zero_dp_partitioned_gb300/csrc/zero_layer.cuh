@@ -317,16 +317,20 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // The block's sum, the same in every thread and every run (a butterfly in
-// each warp, then the warps in order).  s: 32 floats of shared memory that no
-// call in flight uses; the caller alternates two of them between calls.
+// each warp, then the warps in order).  s: 32 floats of shared memory, 16-byte
+// aligned, that no call in flight uses, zero beyond the block's warps; the
+// caller alternates two of them between calls.
 __device__ __forceinline__ float block_sum(float v, float* s) {
     v = warp_sum(v);
     if (blockDim.x <= 32) return v;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
-    const int nw = blockDim.x >> 5;
+    const int n4 = (blockDim.x + 127) >> 7;
     float t = 0.f;
-    for (int w = 0; w < nw; ++w) t += s[w];
+    for (int w = 0; w < n4; ++w) {
+        const float4 p = reinterpret_cast<const float4*>(s)[w];
+        t += (p.x + p.y) + (p.z + p.w);
+    }
     return t;
 }
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s) {

@@ -18,7 +18,7 @@ constexpr int NORM_THREADS = 512;       // most threads that share a row
 constexpr int64_t NORM_MAX_COLS = 1 << 20;
 constexpr int NORM_MAX_STAGES = 4;      // rows a thread has on their way or at hand
 constexpr int NORM_SM_SMEM = 216 * 1024;
-constexpr int NORM_FORWARD_THREADS = 1024, NORM_BACKWARD_THREADS = 512;   // of a multiprocessor, walking rows
+constexpr int NORM_FORWARD_THREADS = 1536, NORM_BACKWARD_THREADS = 512;   // of a multiprocessor, walking rows
 constexpr int NORM_MAX_GRID = 608;      // blocks of the backward pass, each with a partial dw
 constexpr float E4M3_MAX = 448.f;
 constexpr float SCALE_FLOOR = 7.888609052210118e-31f;   // 2^-100: a zero row still has a usable scale
@@ -229,27 +229,35 @@ __device__ __forceinline__ void* row_of(void* p, int64_t ld, int64_t r) {
 
 // x + r of one unit, rounded to the type h is stored in.
 template <int XT, int RT, bool V8>
-__device__ __forceinline__ void add_unit(const Unit<XT, V8>& x, const Unit<RT, V8>& r, bool has_r,
-                                         float (&h)[Map::E]) {
-    x.values(h);
-    if (!has_r) return;
-    float b[Map::E];
-    r.values(b);
+__device__ __forceinline__ Unit<RT, V8> add_unit(const Unit<XT, V8>& x, const Unit<RT, V8>& r, bool has_r) {
+    Unit<RT, V8> h;
+    uint32_t w[8];
 #pragma unroll
-    for (int e = 0; e < Map::E; ++e) {
-        h[e] = __fadd_rn(h[e], b[e]);
-        if constexpr (RT != ZERO_F32) h[e] = Half16<RT>::widen(Half16<RT>::narrow(h[e]));
+    for (int q = 0; q < 4; ++q) {
+        const float2 p = unpack2(has_r ? add2(x.pair(q), r.pair(q)) : x.pair(q));
+        if constexpr (RT == ZERO_F32) {
+            w[2 * q] = __float_as_uint(p.x);
+            w[2 * q + 1] = __float_as_uint(p.y);
+        } else {
+            w[q] = Half16<RT>::narrow2(p.x, p.y);
+        }
     }
+    h.raw.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (RT == ZERO_F32) h.raw.w[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    return h;
 }
 
 // A row in NV units per thread, in registers.
 template <int XT, int RT, bool V8, int NV>
 __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_constant__ NormArgs a) {
     constexpr int E = Map::E;
-    __shared__ float ssum[2][32];
+    __shared__ __align__(16) float ssum[2][32];
+    if (threadIdx.x < 64) ssum[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
+    __syncthreads();
     __shared__ uint32_t smax[2][32];
     pdl_wait();
     pdl_launch_next();
+    const float inv_n = 1.f / (float)a.cols;
     const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols);
     extern __shared__ __align__(16) uint4 ring[];
     using X = Slots<XT, NV, V8>;
@@ -280,16 +288,14 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_cons
         uint64_t s2 = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float h[E];
-            add_unit<XT, RT, V8>(x[j], r[j], a.r != nullptr, h);
-            r[j].hold(h);
+            r[j] = add_unit<XT, RT, V8>(x[j], r[j], a.r != nullptr);
 #pragma unroll
-            for (int q = 0; q < E / 2; ++q) s2 = fma2(pack2(h[2 * q], h[2 * q + 1]), pack2(h[2 * q], h[2 * q + 1]), s2);
+            for (int q = 0; q < E / 2; ++q) s2 = fma2(r[j].pair(q), r[j].pair(q), s2);
             if (a.h) r[j].store(row_of<RT>(a.h, a.ldh, row), Map::unit(j), a.cols);
         }
         const float2 sp = unpack2(s2);
         const float ss = block_sum(sp.x + sp.y, ssum[turn]);
-        const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
+        const float rstd = rsqrtf(fmaf(ss, inv_n, a.eps));
         if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
         const uint64_t rr = pack2(rstd, rstd);
         auto normed = [&](int j, float (&y)[E]) {
@@ -344,10 +350,13 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_cons
 template <int XT, int RT, bool V8>
 __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid_constant__ NormArgs a) {
     constexpr int E = Map::E;
-    __shared__ float ssum[2][32];
+    __shared__ __align__(16) float ssum[2][32];
+    if (threadIdx.x < 64) ssum[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
+    __syncthreads();
     __shared__ uint32_t smax[2][32];
     pdl_wait();
     pdl_launch_next();
+    const float inv_n = 1.f / (float)a.cols;
     const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols), eh = extent_of<RT>(a.h, a.ldh, a.rows, a.cols);
     const int steps = ((a.cols + 7) / 8 + (int)blockDim.x - 1) / (int)blockDim.x;
     int turn = 0;
@@ -365,7 +374,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
                 Unit<RT, V8> r;
                 x.load(X, u, a.cols, ex);
                 if (R) r.load(R, u, a.cols, er);
-                add_unit<XT, RT, V8>(x, r, R != nullptr, h);
+                add_unit<XT, RT, V8>(x, r, R != nullptr).values(h);
             }
         };
         float ss = 0.f;
@@ -375,14 +384,15 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
             Unit<RT, V8> r;
             x.load(X, u, a.cols, ex);
             if (R) r.load(R, u, a.cols, er);
+            const Unit<RT, V8> s = add_unit<XT, RT, V8>(x, r, R != nullptr);
             float h[E];
-            add_unit<XT, RT, V8>(x, r, R != nullptr, h);
+            s.values(h);
 #pragma unroll
             for (int e = 0; e < E; ++e) ss = fmaf(h[e], h[e], ss);
-            if (H) store_unit<RT, V8>(H, u, a.cols, h);
+            if (H) s.store(H, u, a.cols);
         }
         ss = block_sum(ss, ssum[turn]);
-        const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
+        const float rstd = rsqrtf(fmaf(ss, inv_n, a.eps));
         if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
         float whole = 0.f;
         if (a.y8 && !a.block128) {
@@ -430,7 +440,9 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward_long(const __grid
 template <int XT, int RT, bool V8, int NV>
 __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_constant__ NormArgs a) {
     constexpr int E = Map::E;
-    __shared__ float ssum[2][32];
+    __shared__ __align__(16) float ssum[2][32];
+    if (threadIdx.x < 64) ssum[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
+    __syncthreads();
     pdl_wait();
     pdl_launch_next();
     const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols), eh = extent_of<RT>(a.hin, a.ldhin, a.rows, a.cols);
@@ -518,7 +530,9 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_con
 template <int XT, int RT, bool V8>
 __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward_long(const __grid_constant__ NormArgs a) {
     constexpr int E = Map::E;
-    __shared__ float ssum[2][32];
+    __shared__ __align__(16) float ssum[2][32];
+    if (threadIdx.x < 64) ssum[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
+    __syncthreads();
     pdl_wait();
     pdl_launch_next();
     const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols), eh = extent_of<RT>(a.hin, a.ldhin, a.rows, a.cols);
