@@ -122,6 +122,23 @@ __device__ __forceinline__ uint32_t codes8(const Raw8<DT>& r, uint64_t inv) {
     return to_e2m1(v);
 }
 
+// i = first, first + step, ... as (row, place) of rows of `per` places: two
+// divisions at the start, none on the way (a 64-bit one costs as much as the
+// work on 8 elements).
+struct Walk {
+    int64_t row, at, d_row, d_at, per;
+    __device__ __forceinline__ Walk(int64_t first, int64_t step, int64_t per_)
+        : row(first / per_), at(first % per_), d_row(step / per_), d_at(step % per_), per(per_) {}
+    __device__ __forceinline__ void next() {
+        row += d_row;
+        at += d_at;
+        if (at >= per) {
+            at -= per;
+            ++row;
+        }
+    }
+};
+
 // Along the rows.  A warp takes up to MX4_SPAN pieces of 256 columns of a row
 // (8 blocks each, a step of the product's tiles), their loads issued together;
 // rows and columns of the scales' padding are walked too.
@@ -132,11 +149,12 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_rows(const __grid_constant_
     pdl_launch_next();
     const Extent x = extent_of<DT>(a.src, a.ld, a.rows, a.cols);
     const int64_t rows = a.q.tiled ? (a.rows + 127) / 128 * 128 : a.rows;
-    const int64_t pieces = (a.cols + 255) / 256, per = (pieces + MX4_SPAN - 1) / MX4_SPAN, n = rows * per;
+    const int64_t pieces = (a.cols + 255) / 256;
     const int lane = threadIdx.x & 31;
-    const int64_t stride = (int64_t)gridDim.x * (MX4_THREADS / 32);
-    for (int64_t i = (int64_t)blockIdx.x * (MX4_THREADS / 32) + (threadIdx.x >> 5); i < n; i += stride) {
-        const int64_t r = i / per, p0 = (i - r * per) * MX4_SPAN;
+    for (Walk i((int64_t)blockIdx.x * (MX4_THREADS / 32) + (threadIdx.x >> 5), (int64_t)gridDim.x * (MX4_THREADS / 32),
+                (pieces + MX4_SPAN - 1) / MX4_SPAN);
+         i.row < rows; i.next()) {
+        const int64_t r = i.row, p0 = i.at * MX4_SPAN;
         const int64_t c0 = p0 * 256 + lane * 8;
         const char* row = static_cast<const char*>(a.src) + r * a.ld * Elem<DT>::SIZE;
         uint8_t* data = a.q.data + r * a.q.ld + c0 / 2;
@@ -180,12 +198,12 @@ __global__ void __launch_bounds__(MX4_THREADS) k_mx4_rows(const __grid_constant_
 // and 512 consecutive bytes.
 //
 // The next tile is on its way to shared memory (cp.async, each lane its own 16
-// bytes) while one is worked on; fp32 has room for one tile a block, and three
-// blocks cover for one another.
+// bytes) while one is worked on; fp32 has room for one tile a block, and two
+// blocks cover for each other.
 template <int DT>
 struct Mx4Both {
     static constexpr int TILE = 128 * 128 * Elem<DT>::SIZE, STAGES = DT == ZERO_F32 ? 1 : 2, SMEM = STAGES * TILE;
-    static constexpr int BLOCKS = 3;                 // of a multiprocessor
+    static constexpr int BLOCKS = DT == ZERO_F32 ? 2 : 3;                 // of a multiprocessor
 };
 
 constexpr int MX4_BOTH_THREADS = 256;
@@ -200,20 +218,22 @@ __global__ void __launch_bounds__(MX4_BOTH_THREADS) k_mx4_both(const __grid_cons
     const Extent x = extent_of<DT>(a.src, a.ld, a.rows, a.cols);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // both directions are padded to 256 for the scales
-    const int64_t nr = (a.rows + 255) / 256 * 2, nc = (a.cols + 255) / 256 * 2, n = nr * nc;
+    const int64_t nr = (a.rows + 255) / 256 * 2, nc = (a.cols + 255) / 256 * 2;
     const int lr = lane >> 4, lc = (lane & 15) * 8;  // this lane's rows lr, lr + 2, ... and columns lc .. lc + 7 of the warp's
-    auto fetch = [&](int64_t i, int st) {
-        if (i < n) {
-            const int64_t r0 = (i / nc) * 128 + warp * 16 + lr, c = (i % nc) * 128 + lc;
+    auto fetch = [&](const Walk& i, int st) {
+        if (i.row < nr) {
+            const int64_t r0 = i.row * 128 + warp * 16 + lr, c = i.at * 128 + lc;
             uint8_t* s = tile_raw + st * B::TILE + ((warp * 16 + lr) * 128 + lc) * Elem<DT>::SIZE;
             const char* src = static_cast<const char*>(a.src) + (r0 * a.ld + c) * Elem<DT>::SIZE;
             const bool inside = a.aligned16 && c + 8 <= a.cols;
+            const int left = (int)(a.rows - r0 < 16 ? a.rows - r0 : 16);        // rows of the matrix from r0 on
+            const int64_t down = 2 * a.ld * Elem<DT>::SIZE;
+            const char* from = src;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 8; ++k, from += down) {
                 const int64_t r = r0 + 2 * k;
                 uint8_t* to = s + k * 2 * 128 * Elem<DT>::SIZE;
-                if (inside && r < a.rows) {
-                    const char* from = src + 2 * k * a.ld * Elem<DT>::SIZE;
+                if (inside && 2 * k < left) {
 #pragma unroll
                     for (int w = 0; w < Elem<DT>::SIZE / 2; ++w)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
@@ -235,24 +255,27 @@ __global__ void __launch_bounds__(MX4_BOTH_THREADS) k_mx4_both(const __grid_cons
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int st = 0;
-    if (B::STAGES == 2) fetch(blockIdx.x, 0);
-    for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
-        if (B::STAGES == 2) fetch(i + gridDim.x, st ^ 1);
+    Walk i(blockIdx.x, gridDim.x, nc), ahead = i;
+    if (B::STAGES == 2) fetch(i, 0);
+    for (; i.row < nr; i.next()) {
+        ahead.next();
+        if (B::STAGES == 2) fetch(ahead, st ^ 1);
         else fetch(i, 0);
         asm volatile("cp.async.wait_group %0;" ::"n"(B::STAGES - 1) : "memory");
-        const int64_t tr = i / nc, tc = i - tr * nc, c0 = tc * 128;
+        const int64_t tr = i.row, tc = i.at, c0 = tc * 128;
         const uint8_t* s = tile_raw + st * B::TILE;
         if (a.q.data) {
             const int64_t r0 = tr * 128, c = c0 + lc;
             uint8_t* data = a.q.data + (r0 + warp * 16 + lr) * a.q.ld + c / 2;
+            const int left = c < a.q.blocks * 32 ? (int)(a.rows - r0 < 128 ? a.rows - r0 : 128) : 0;    // rows to write
 #pragma unroll 4
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 8; ++k, data += 2 * a.q.ld) {
                 const int rr = warp * 16 + lr + 2 * k;
                 const Raw8<DT> v = ld8<DT>(s, rr * 128 + lc);
                 const uint32_t byte = scale_byte<DT>(lanes_max<4>(top8<DT>(v)));
                 const float inv = mx4_inverse(byte);
                 const uint32_t code = codes8<DT>(v, pack2(inv, inv));
-                if (r0 + rr < a.rows && c < a.q.blocks * 32) *reinterpret_cast<uint32_t*>(data + 2 * k * a.q.ld) = code;
+                if (rr < left) *reinterpret_cast<uint32_t*>(data) = code;
                 if ((lane & 3) == 0) scale_q[(rr & 31) * 16 + (rr >> 5) * 4 + ((lane & 15) >> 2)] = (uint8_t)byte;
             }
         }
@@ -351,19 +374,22 @@ template <int DT>
 __global__ void __launch_bounds__(MX4_THREADS) k_mx4_values(const __grid_constant__ DequantArgs a) {
     pdl_wait();
     pdl_launch_next();
-    const int64_t per = (a.cols + 256 * MX4_SPAN - 1) / (256 * MX4_SPAN), n = a.rows * per;
     const int lane = threadIdx.x & 31;
-    const int64_t stride = (int64_t)gridDim.x * (MX4_THREADS / 32);
-    for (int64_t i = (int64_t)blockIdx.x * (MX4_THREADS / 32) + (threadIdx.x >> 5); i < n; i += stride) {
-        const int64_t r = i / per, c0 = (i - r * per) * 256 * MX4_SPAN + lane * 8;
+    for (Walk i((int64_t)blockIdx.x * (MX4_THREADS / 32) + (threadIdx.x >> 5), (int64_t)gridDim.x * (MX4_THREADS / 32),
+                (a.cols + 256 * MX4_SPAN - 1) / (256 * MX4_SPAN));
+         i.row < a.rows; i.next()) {
+        const int64_t r = i.row, c0 = i.at * 256 * MX4_SPAN + lane * 8;
         const uint8_t* data = a.q.data + r * a.q.ld + c0 / 2;
+        // a piece is two tiles, or 8 blocks of a row
+        const uint8_t* scales =
+            a.q.tiled ? a.q.scales + mx4_tiled_at(r, c0 >> 5, a.q.tiles) : a.q.scales + r * a.q.blocks + (c0 >> 5);
+        const int piece = a.q.tiled ? 1024 : 8;
         uint32_t w[MX4_SPAN] = {}, byte[MX4_SPAN] = {};
 #pragma unroll
         for (int k = 0; k < MX4_SPAN; ++k)
             if (c0 + k * 256 < a.cols) {
-                const int64_t b = (c0 >> 5) + k * 8;
                 w[k] = __ldcs(reinterpret_cast<const uint32_t*>(data + k * 128));
-                byte[k] = a.q.scales[a.q.tiled ? mx4_tiled_at(r, b, a.q.tiles) : r * a.q.blocks + b];
+                byte[k] = scales[k * piece];
             }
         char* row = static_cast<char*>(a.dst) + r * a.ld * Elem<DT>::SIZE;
 #pragma unroll
@@ -486,7 +512,7 @@ int zero_mx4_quantize(const zero_mat* src, int64_t rows, int64_t cols, const zer
         smem = dt == ZERO_F32 ? Mx4Both<ZERO_F32>::SMEM : Mx4Both<ZERO_BF16>::SMEM;
         rc = raise_smem(f, smem, "zero_mx4_quantize shared-memory size");
         if (rc != ZERO_OK) return rc;
-        grid = blocks_for((rows + 255) / 256 * 2 * ((cols + 255) / 256 * 2), Mx4Both<ZERO_BF16>::BLOCKS);
+        grid = blocks_for((rows + 255) / 256 * 2 * ((cols + 255) / 256 * 2), dt == ZERO_F32 ? Mx4Both<ZERO_F32>::BLOCKS : Mx4Both<ZERO_BF16>::BLOCKS);
     } else {
         f = dt == ZERO_F32 ? (const void*)k_mx4_rows<ZERO_F32>
           : dt == ZERO_BF16 ? (const void*)k_mx4_rows<ZERO_BF16> : (const void*)k_mx4_rows<ZERO_F16>;
