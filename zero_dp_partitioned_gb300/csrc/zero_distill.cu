@@ -7,10 +7,19 @@
 //   dz_v = w S c T (P q_v - sum of p_i with id_i = v)
 //
 // Bound: HBM, 4 bytes a logit in 16 bits (read once, gradient written once).
-// A row is split over a cluster of up to 8 blocks so that each block's share
-// stays in registers (8 16-byte vectors a thread) from the load to the
-// gradient: the row's maximum and sum cross the cluster through distributed
-// shared memory, and no logit is read twice.
+// A block walks its row twice: once for the maximum and the sum together
+// (batches of 8 vectors a thread, the sum brought to a new maximum when there
+// is one), once for the gradient.  The second walk finds 8 vectors a thread in
+// shared memory and the rest in L2.  Few rows are split over a cluster of up to
+// 8 blocks, whose pairs of maximum and sum cross through distributed shared
+// memory.
+//
+// Measured (GB300): 4096 x 128256 bf16 in 360 us, 5.8 TB/s (0.86 of the
+// measured copy bandwidth); 1999 x 50257 fp32 in 149 us, 5.4 TB/s (0.79).
+// Without the vectors in shared memory 385 us (a fifth of the second walk
+// missed L2); with 12 of them 431 (too little L1 left for the loads in flight);
+// with every row in the registers of a cluster of 8 blocks 580 (the work that
+// is done once a block came 8 times, and blocks waited for one another).
 //
 // Exponentials are taken in base 2 with one fused multiply-add, 2^(z k - m k)
 // with k = log2(e) / T; m k is rounded once and used for the sum, the

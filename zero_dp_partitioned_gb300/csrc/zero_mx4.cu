@@ -10,9 +10,12 @@
 //
 // Bound: HBM.  Along the rows 8 consecutive elements go to a thread and 4
 // lanes share a block.  Along the columns (the operand of a product that sums
-// over rows) a warp takes 32 rows by 64 columns, quantises the rows from its
-// registers, and the columns from its own piece of shared memory, two to a
-// lane: both forms from one read of the matrix.
+// over rows) a block takes 128 x 128 elements through shared memory; both forms
+// come from one read of the matrix.
+//
+// Measured (GB300, 14336 x 4096 bf16; the floor is the bytes at the measured
+// copy bandwidth): rows 28.7 us (floor 21.9), columns 25.6 (21.9), both 40.9
+// (26.5: the two passes' instructions bound it), values back 26.6 (21.9).
 #include "zero_layer.cuh"
 #include "zero_mx4.cuh"
 
