@@ -339,3 +339,38 @@ def test_a_wait_that_runs_out_is_reported(Z, monkeypatch, m):
     monkeypatch.delenv("ZERO_GB300_SPIN_LIMIT")
     status.zero_()
     product(Z, a, b, F32)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 500, 14000), (5, 2001, 12001), (40, 130, 9001), (100, 300, 8000),
+                                   (129, 700, 9000), (300, 600, 14336), (16, 4096, 7168)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_product_whose_sum_is_shared(Z, m, n, k, dtype):
+    """Few tiles and a long sum: clusters of 2, 4 or 8 blocks share it, and add in the order of k."""
+    g = gen(m + n + k)
+    a, b = torch.randn(m, k, generator=g, device=DEV).to(BF16), torch.randn(n, k, generator=g, device=DEV).to(BF16)
+    one = product(Z, a, b, dtype)
+    assert torch.equal(one, product(Z, a, b, dtype))
+    product(Z, a, b, dtype, off=1)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3, 4, 5, 8])
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_rows_that_start_anywhere(Z, off, dtype):
+    """Every shift of a row against 16 bytes, in and out, and nothing written beside it."""
+    g = gen(off)
+    for rows, cols in ((3, 700), (70, 33), (2, 2049)):
+        wide = torch.randn(rows, cols + 9, generator=g, device=DEV).to(dtype)
+        x = wide[:, off:off + cols]
+        q, t = Z.mx4(rows, cols, device=DEV), Z.mx4(cols, rows, device=DEV)
+        Z.zero_mx4_quantize(x, rows, cols, q, t)
+        for m, src in ((q, x), (t, x.t())):
+            code, byte = unpacked(m, *src.shape)
+            rc, rb = reference(src)
+            assert torch.equal(code, rc) and torch.equal(byte, rb)
+        r = Z.mx4(rows, cols, device=DEV)
+        Z.zero_mx4_quantize(x, rows, cols, r, None)
+        assert torch.equal(r.buffers[0], q.buffers[0])
+        out = torch.full((rows, cols + 9), 5.0, dtype=dtype, device=DEV)
+        Z.zero_mx4_dequantize(q, out[:, off:off + cols])
+        assert torch.equal(out[:, off:off + cols], values(*reference(x), cols).to(dtype))
+        assert bool((out[:, :off] == 5).all()) and bool((out[:, off + cols:] == 5).all())

@@ -243,3 +243,42 @@ def test_empty_matrices(Z):
     Z.zero_norm_forward(e, e, None, 0, 64, 1e-5, e, e, None, 0, None)
     e = torch.empty(5, 0, dtype=BF16, device=DEV)
     Z.zero_norm_forward(e, None, None, 5, 0, 1e-5, None, e, None, 0, None)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3, 4, 6, 7])
+@pytest.mark.parametrize("xt,rt", [(F16, F16), (F32, F32), (BF16, F32)])
+def test_rows_that_start_anywhere(Z, off, xt, rt):
+    """Every shift of a row against 16 bytes, each matrix at its own, results inside wider rows; the
+    values are those of aligned rows, bit for bit, and nothing beside them is written."""
+    g = gen(off)
+    for rows, cols in ((3, 40), (5, 1000), (2, 2057)):
+        def inside(dtype, o):
+            wide = torch.full((rows, cols + 11), 3.0, dtype=dtype, device=DEV)
+            return wide, wide[:, o:o + cols]
+        x, r, dy, dh = (torch.randn(rows, cols, generator=g, device=DEV).to(t) for t in (xt, rt, xt, rt))
+        w = torch.randn(cols, generator=g, device=DEV).to(xt)
+        res = []
+        for o in (None, off):
+            ins, outs = [], []
+            for t, v, k in ((xt, x, 0), (rt, r, 1), (xt, dy, 2), (rt, dh, 0)):
+                wide, m = inside(t, 0 if o is None else (o + k) % 8)
+                m.copy_(v)
+                ins.append(m if o is not None else v.clone())
+            shapes = ((rt, 1), (xt, 0), (rt, 2), (torch.float8_e4m3fn, 3))
+            for t, k in shapes:
+                if o is None:
+                    outs.append((None, torch.empty(rows, cols, dtype=t, device=DEV), 0))
+                else:
+                    at = (o + k) % 8
+                    outs.append((*inside(t, at), at))
+            h, y, dx, y8 = (m for _, m, _ in outs)
+            rstd, scale = torch.empty(rows, device=DEV), torch.empty(rows, -(-cols // 128), device=DEV)
+            Z.zero_norm_forward(ins[0], ins[1], w, rows, cols, 1e-5, h, y, None, 0, rstd)
+            Z.zero_norm_forward(ins[0], ins[1], w, rows, cols, 1e-5, None, y8, scale, 128, None)
+            Z.zero_norm_backward(ins[2], h, w, rows, cols, rstd, ins[3], dx, None, 0, None, 0)
+            for wide, m, at in outs:
+                if wide is not None:
+                    assert bool((wide[:, :at].float() == 3).all()) and bool((wide[:, at + cols:].float() == 3).all())
+            res.append([m.float().clone() for _, m, _ in outs] + [rstd, scale])
+        for a, b in zip(*res):
+            assert torch.equal(a, b)
