@@ -19,7 +19,9 @@
 // Without the vectors in shared memory 385 us (a fifth of the second walk
 // missed L2); with 12 of them 431 (too little L1 left for the loads in flight);
 // with every row in the registers of a cluster of 8 blocks 580 (the work that
-// is done once a block came 8 times, and blocks waited for one another).
+// is done once a block came 8 times, and blocks waited for one another); with
+// blocks that stay and fetch the next row's vectors into shared memory as they
+// write the gradient 400 to 455.
 //
 // Exponentials are taken in base 2 with one fused multiply-add, 2^(z k - m k)
 // with k = log2(e) / T; m k is rounded once and used for the sum, the

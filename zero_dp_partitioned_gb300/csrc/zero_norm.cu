@@ -29,7 +29,11 @@ constexpr int NORM_THREADS = 512;       // most threads that share a row
 constexpr int64_t NORM_MAX_COLS = 1 << 20;
 constexpr int NORM_MAX_STAGES = 4;      // rows a thread has on their way or at hand
 constexpr int NORM_SM_SMEM = 216 * 1024;
-constexpr int NORM_FORWARD_THREADS = 1536, NORM_BACKWARD_THREADS = 512;   // of a multiprocessor, walking rows
+constexpr int NORM_FORWARD_THREADS = 1024, NORM_BACKWARD_THREADS = 512;   // of a multiprocessor, walking rows
+// Blocks launched for each that runs at once: in the forward pass SMs that are
+// done early take the rows of others (8192 x 4096 bf16 44.9 against 48.8 us; the
+// backward pass, whose blocks each leave a partial dw, gains nothing).
+constexpr int NORM_FORWARD_OVER = 2, NORM_BACKWARD_OVER = 1;
 constexpr int NORM_MAX_GRID = 608;      // blocks of the backward pass, each with a partial dw
 constexpr float E4M3_MAX = 448.f;
 constexpr float SCALE_FLOOR = 7.888609052210118e-31f;   // 2^-100: a zero row still has a usable scale
@@ -81,7 +85,7 @@ struct Unit {
 
 // Rows on their way: a thread copies its own units of the next rows to its own
 // slots of shared memory (cp.async, 16 bytes each, past the registers and L1)
-// and waits for its own copies alone, so no barrier is involved.
+// and, where rows are aligned, waits for its own copies alone.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -95,15 +99,19 @@ __device__ __forceinline__ void copies_wait_all_but(int n) {     // n = stages -
     else copies_wait<3>();
 }
 
-// One matrix of a stage: NV units a thread.  A unit is 1 word (fp32: 2) of
-// shared memory, and one more where rows start anywhere: the aligned words that
-// it touches, each lane for itself (the word that two lanes share is read from
-// L2 twice, and no lane waits for another).
+// One matrix of a stage: NV units a thread, each of 1 word (fp32: 2) of shared
+// memory.  Where rows start anywhere, the words are the aligned ones that the
+// row lies in, and one more at its end; a unit then begins in its thread's own
+// words and ends in the next one's, so a barrier stands between copy and read.
 template <int DT, int NV, bool V8>
 struct Slots {
-    static constexpr int N = DT == ZERO_F32 ? 8 : 4, WORDS = N / 4 + (V8 ? 0 : 1);
-    static constexpr int COUNT = NV * WORDS;          // words of a thread
-    uint4* at;                                        // this thread's first word; the next is blockDim.x further
+    static constexpr int N = DT == ZERO_F32 ? 8 : 4, W = N / 4, PER_WORD = 16 / Elem<DT>::SIZE;
+    static __device__ __forceinline__ int words() { return NV * W * blockDim.x + (V8 ? 0 : 1); }
+    uint4* at;                                        // the matrix's part of the stage
+    // word w of this thread's j-th unit: a thread's words blockDim.x apart, or in the row's order
+    static __device__ __forceinline__ int word(int j, int w) {
+        return V8 ? (j * W + w) * blockDim.x + threadIdx.x : Map::unit(j) * W + w;
+    }
     __device__ __forceinline__ void copy(const void* row, int cols, const Extent& x) const {
         const char* p = static_cast<const char*>(row);
         const int off = V8 ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u);
@@ -112,23 +120,24 @@ struct Slots {
             const int u = Map::unit(j);
             if (u * 8 >= cols) continue;
             const char* q = p + (int64_t)u * 8 * Elem<DT>::SIZE - off;
-            uint4* slot = at + j * WORDS * blockDim.x;
-            if (V8 || (q >= x.lo && q + 16 * WORDS <= x.hi)) {
+            const int n = V8 || (u + 1) * 8 < cols ? W : W + 1;       // the row's last unit takes the word after it too
 #pragma unroll
-                for (int w = 0; w < WORDS; ++w)
-                    copy16((uint32_t)__cvta_generic_to_shared(slot + w * blockDim.x), q + 16 * w);
-            } else {
-                // the matrix's first or last words, not whole: element by element, to where the shift will look for them
+            for (int w = 0; w < W + 1; ++w) {
+                if (w >= n) break;
+                uint4* to = at + word(j, w);
+                if (V8 || (q + 16 * w >= x.lo && q + 16 * w + 16 <= x.hi)) {
+                    copy16((uint32_t)__cvta_generic_to_shared(to), q + 16 * w);
+                } else {
+                    // partly outside the matrix: element by element
 #pragma unroll 1
-                for (int e = 0; e < 8; ++e) {
-                    const int by = off + e * Elem<DT>::SIZE;
-                    char* to = reinterpret_cast<char*>(slot + (by >> 4) * blockDim.x) + (by & 15);
-                    const char* from = q + by;
-                    if constexpr (DT == ZERO_F32)
-                        *reinterpret_cast<uint32_t*>(to) = u * 8 + e < cols ? *reinterpret_cast<const uint32_t*>(from) : 0u;
-                    else
-                        *reinterpret_cast<uint16_t*>(to) =
-                            u * 8 + e < cols ? *reinterpret_cast<const uint16_t*>(from) : (uint16_t)0;
+                    for (int e = 0; e < PER_WORD; ++e) {
+                        const char* from = q + 16 * w + e * Elem<DT>::SIZE;
+                        const bool in = from >= x.lo && from + Elem<DT>::SIZE <= x.hi;
+                        if constexpr (DT == ZERO_F32)
+                            reinterpret_cast<uint32_t*>(to)[e] = in ? *reinterpret_cast<const uint32_t*>(from) : 0u;
+                        else
+                            reinterpret_cast<uint16_t*>(to)[e] = in ? *reinterpret_cast<const uint16_t*>(from) : (uint16_t)0;
+                    }
                 }
             }
         }
@@ -137,12 +146,11 @@ struct Slots {
         const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const uint4* slot = at + j * WORDS * blockDim.x;
             const int left = cols - Map::unit(j) * 8;       // columns from this unit's first
             uint32_t w[N + 4];
 #pragma unroll
-            for (int k = 0; k < WORDS; ++k) {
-                const uint4 v = left > 0 ? slot[k * blockDim.x] : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < W + (V8 ? 0 : 1); ++k) {
+                const uint4 v = left > 0 ? at[word(j, k)] : make_uint4(0, 0, 0, 0);
                 w[4 * k] = v.x;
                 w[4 * k + 1] = v.y;
                 w[4 * k + 2] = v.z;
@@ -260,7 +268,7 @@ __device__ __forceinline__ Unit<RT, V8> add_unit(const Unit<XT, V8>& x, const Un
 
 // A row in NV units per thread, in registers.
 template <int XT, int RT, bool V8, int NV>
-__global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(NORM_THREADS, NV == 2 && RT != ZERO_F32 ? 2 : 1) k_norm_forward(const __grid_constant__ NormArgs a) {
     constexpr int E = Map::E;
     __shared__ __align__(16) float ssum[2][32];
     if (threadIdx.x < 64) ssum[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
@@ -273,12 +281,12 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_cons
     extern __shared__ __align__(16) uint4 ring[];
     using X = Slots<XT, NV, V8>;
     using R = Slots<RT, NV, V8>;
-    const int S = a.stages, stage_words = (X::COUNT + R::COUNT) * blockDim.x;
+    const int S = a.stages, stage_words = X::words() + R::words();
     auto copy = [&](int64_t row, int st) {
         if (row < a.rows) {
-            uint4* at = ring + threadIdx.x + st * stage_words;
+            uint4* at = ring + st * stage_words;
             X{at}.copy(row_of<XT>(a.x, a.ldx, row), a.cols, ex);
-            if (a.r) R{at + X::COUNT * blockDim.x}.copy(row_of<RT>(a.r, a.ldr, row), a.cols, er);
+            if (a.r) R{at + X::words()}.copy(row_of<RT>(a.r, a.ldr, row), a.cols, er);
         }
         copies_commit();
     };
@@ -291,9 +299,10 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_forward(const __grid_cons
         Unit<RT, V8> r[NV];
         copy(row + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
         copies_wait_all_but(S - 1);
-        uint4* at = ring + threadIdx.x + st * stage_words;
+        if (!V8) __syncthreads();
+        uint4* at = ring + st * stage_words;
         X{at}.read(x, row_of<XT>(a.x, a.ldx, row), a.cols);
-        if (a.r) R{at + X::COUNT * blockDim.x}.read(r, row_of<RT>(a.r, a.ldr, row), a.cols);
+        if (a.r) R{at + X::words()}.read(r, row_of<RT>(a.r, a.ldr, row), a.cols);
         st = st == S - 1 ? 0 : st + 1;
         // h as it is stored: half the registers of its fp32 values
         uint64_t s2 = 0;
@@ -462,14 +471,14 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_con
     extern __shared__ __align__(16) uint4 ring[];
     using X = Slots<XT, NV, V8>;
     using R = Slots<RT, NV, V8>;
-    const int S = a.stages, stage_words = (X::COUNT + 2 * R::COUNT) * blockDim.x;
+    const int S = a.stages, stage_words = X::words() + 2 * R::words();
     const bool DH = a.r != nullptr;
     auto copy = [&](int64_t row, int st) {
         if (row < a.rows) {
-            uint4* at = ring + threadIdx.x + st * stage_words;
+            uint4* at = ring + st * stage_words;
             X{at}.copy(row_of<XT>(a.x, a.ldx, row), a.cols, ex);
-            R{at + X::COUNT * blockDim.x}.copy(row_of<RT>(a.hin, a.ldhin, row), a.cols, eh);
-            if (DH) R{at + (X::COUNT + R::COUNT) * blockDim.x}.copy(row_of<RT>(a.r, a.ldr, row), a.cols, er);
+            R{at + X::words()}.copy(row_of<RT>(a.hin, a.ldhin, row), a.cols, eh);
+            if (DH) R{at + X::words() + R::words()}.copy(row_of<RT>(a.r, a.ldr, row), a.cols, er);
         }
         copies_commit();
     };
@@ -483,10 +492,11 @@ __global__ void __launch_bounds__(NORM_THREADS) k_norm_backward(const __grid_con
         Unit<RT, V8> h[NV], dh[NV];
         copy(row + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
         copies_wait_all_but(S - 1);
-        uint4* at = ring + threadIdx.x + st * stage_words;
+        if (!V8) __syncthreads();
+        uint4* at = ring + st * stage_words;
         X{at}.read(dy, row_of<XT>(a.x, a.ldx, row), a.cols);
-        R{at + X::COUNT * blockDim.x}.read(h, row_of<RT>(a.hin, a.ldhin, row), a.cols);
-        if (DH) R{at + (X::COUNT + R::COUNT) * blockDim.x}.read(dh, row_of<RT>(a.r, a.ldr, row), a.cols);
+        R{at + X::words()}.read(h, row_of<RT>(a.hin, a.ldhin, row), a.cols);
+        if (DH) R{at + X::words() + R::words()}.read(dh, row_of<RT>(a.r, a.ldr, row), a.cols);
         st = st == S - 1 ? 0 : st + 1;
         const uint64_t rr = pack2(rstd, rstd);
         uint64_t d2 = 0;
@@ -659,7 +669,7 @@ static const void* norm_fn(bool fwd, int xt, int rt, bool v8, int nv) {
     return rt == ZERO_F32 ? pick<ZERO_F16, ZERO_F32>(fwd, v8, nv) : pick<ZERO_F16, ZERO_F16>(fwd, v8, nv);
 }
 
-static int words_of(int dt, bool v8) { return (dt == ZERO_F32 ? 2 : 1) + (v8 ? 0 : 1); }
+static int words_of(int dt) { return dt == ZERO_F32 ? 2 : 1; }
 
 // How a row is shared out: units per thread (0: the row does not fit the
 // registers, or two stages of it shared memory), threads per row, blocks per
@@ -679,7 +689,7 @@ static NormShape shape_of(int64_t cols, int words, int sm_threads) {
     s.stages = 2;
     s.smem = 0;
     if (!s.nv) return s;
-    const size_t stage = (size_t)words * s.nv * s.threads * 16;
+    const size_t stage = ((size_t)words * s.nv * s.threads + 3) * 16;      // and a word after each of up to three rows
     const int fit = (int)(NORM_SM_SMEM / (2 * stage));         // blocks with two stages each
     if (s.per_sm > fit) s.per_sm = fit < 1 ? 1 : fit;
     while (s.stages < NORM_MAX_STAGES && (s.stages + 1) * stage * s.per_sm <= NORM_SM_SMEM) ++s.stages;
@@ -748,14 +758,14 @@ int zero_norm_forward(const zero_mat* x, const zero_mat* residual, const zero_ma
     const bool y_ok = y8 ? aligned(y->data, 8) && (rows == 1 || y->ld % 8 == 0) : rows_aligned(*y, rows);
     const bool v8 = cols % 8 == 0 && rows_aligned(*x, rows) && y_ok && (!residual || rows_aligned(*residual, rows)) &&
                     (!h_out || rows_aligned(*h_out, rows));
-    const NormShape p = shape_of(cols, words_of(x->dtype, v8) + words_of(rt, v8), NORM_FORWARD_THREADS);
+    const NormShape p = shape_of(cols, words_of(x->dtype) + words_of(rt), NORM_FORWARD_THREADS);
     a.stages = p.stages;
     const int sms = sm_count();
     if (!sms) return ZERO_ECUDA;
     const void* f = norm_fn(true, x->dtype, rt, v8, p.nv);
     rc = raise_smem(f, p.smem, "zero_norm_forward shared-memory size");
     if (rc != ZERO_OK) return rc;
-    const int64_t most = (int64_t)sms * p.per_sm;
+    const int64_t most = (int64_t)sms * p.per_sm * NORM_FORWARD_OVER;
     void* args[] = {&a};
     return cuda_fail(launch_after_previous(f, (int)(rows < most ? rows : most), p.threads, args, p.smem,
                                            static_cast<cudaStream_t>(stream)),
@@ -804,11 +814,11 @@ int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* we
     a.part16 = cols % 4 == 0 && aligned(workspace, 16);
     const bool v8 = cols % 8 == 0 && rows_aligned(*dy, rows) && rows_aligned(*h, rows) && rows_aligned(*dx, rows) &&
                     (!dh || rows_aligned(*dh, rows));
-    const NormShape p = shape_of(cols, words_of(dy->dtype, v8) + 2 * words_of(rt, v8), NORM_BACKWARD_THREADS);
+    const NormShape p = shape_of(cols, words_of(dy->dtype) + 2 * words_of(rt), NORM_BACKWARD_THREADS);
     a.stages = p.stages;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* args[] = {&a};
-    int64_t g = (int64_t)p.per_sm * sms;
+    int64_t g = (int64_t)p.per_sm * sms * NORM_BACKWARD_OVER;
     if (g > NORM_MAX_GRID) g = NORM_MAX_GRID;
     if (g > rows) g = rows;
     const void* f = norm_fn(false, dy->dtype, rt, v8, p.nv);
