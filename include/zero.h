@@ -658,6 +658,10 @@ int zero_shard_step_host(const void* const* host_grad_slices, int n_slices, int 
  *    and results do not depend on timing: no sum uses atomics.
  *  - "may be X" means: the very same data pointer and ld as X.  No other
  *    output may overlap an input or another output.
+ *  - The kernels' shared-memory limits are raised once a device and kept for
+ *    the life of the process; like the streams of zero_shard_step_host they do
+ *    not survive cudaDeviceReset, after which these calls must not be made on
+ *    that device again in the same process.
  * ------------------------------------------------------------------------ */
 typedef struct {
     void* data;
