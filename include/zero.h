@@ -681,8 +681,9 @@ typedef struct {
  * h_out      in the residual's type (x's without one); NULL: not stored; may
  *            be residual or x
  * y          in x's type, or ZERO_E4M3: y is then divided by a scale, s = the
- *            largest |y| of its block (at least 2^-100) / 448, and rounded to
- *            nearest; a NaN or an infinity in a block makes the scale so
+ *            largest |y| of its block (at least 2^-100) times 1 / 448 in fp32,
+ *            and the quotient rounded to nearest, ties to even; a NaN or an
+ *            infinity in a block makes the scale so
  * y_scale    ZERO_E4M3 only: the scales, rows x 1 (scale_block 0: a block is a
  *            row) or rows x ceil(cols / 128) (scale_block 128)
  * rstd       rows values, NULL: not stored

@@ -282,3 +282,30 @@ def test_rows_that_start_anywhere(Z, off, xt, rt):
             res.append([m.float().clone() for _, m, _ in outs] + [rstd, scale])
         for a, b in zip(*res):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 7), (300, 1337), (2000, 4096), (40, 8200), (3, 20001)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("block", [0, 128])
+def test_eight_bit_output_is_the_quotient_rounded(Z, rows, cols, dtype, block):
+    """Bit for bit: y in fp32 by the stored rstd, the scale its block's largest magnitude times 1 / 448, and the
+    stored value the correctly rounded quotient of the two, rounded to nearest (16-bit weights make many a quotient
+    an exact tie).  An infinite weight makes its blocks' scales infinite and their other values 0."""
+    g = gen(rows + cols + block)
+    x, r, w = rnd(g, rows, cols, dtype=dtype), rnd(g, rows, cols, dtype=dtype, std=2.0), rnd(g, cols, dtype=dtype) + 1
+    x[rows // 2], r[rows // 2] = 0, 0
+    width = block or cols
+    n = -(-cols // width)
+    h, rstd = torch.empty_like(x), torch.empty(rows, device=DEV)
+    y8, scale = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=DEV), torch.empty(rows, n, device=DEV)
+    for _ in range(2):
+        Z.zero_norm_forward(x, r, w, rows, cols, 1e-5, h, y8, scale, block, rstd)
+        y = h.float() * rstd[:, None] * w.float()
+        b = torch.nn.functional.pad(y, (0, -cols % width)).view(rows, n, width)
+        top = b.abs().amax(2).clamp(min=2.0 ** -100)
+        q = (b / scale[:, :, None]).view(rows, -1)[:, :cols].to(torch.float8_e4m3fn)
+        for got, ref in ((scale, top * torch.full_like(top, 1 / 448)), (y8.float(), q.float())):
+            assert torch.equal(torch.isnan(got), torch.isnan(ref))
+            assert torch.equal(torch.where(torch.isnan(got), 0.0, got), torch.where(torch.isnan(ref), 0.0, ref))
+        w[cols // 2] = float("inf")
+        h[rows // 2], x[rows // 2] = 1, 1                 # 0 times infinity is not a number
