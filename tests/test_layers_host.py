@@ -170,3 +170,46 @@ def test_mx4_refusals(Z):
     refused(Z, Z.ZERO_EINVAL, mm, q(), q(), float("nan"), m(Z), FAKE)
     refused(Z, Z.ZERO_ELIMIT, mm, q(rows=1 << 31), q(), 1.0, m(Z), FAKE)
     Z.zero_mx4_matmul(q(rows=0), q(), 1.0, m(Z), FAKE, stream=0)          # nothing to do: no launch
+
+
+def test_buffers_that_are_not_on_a_gpu_are_refused(Z):
+    """Matrices, workspace, chain and status given as CPU tensors: an error before any launch."""
+    host, n = torch.zeros(4, 64, dtype=torch.bfloat16), Z.zero_norm_workspace_bytes(64)
+    u8 = torch.zeros(4096, dtype=torch.uint8)
+    q = Z.mx4(4, 64, device="cpu")
+    over = Z.mx4(4, 64, u8, FAKE)                                         # one buffer on the host is enough
+    gpu = Z.zero_mx4(FAKE, FAKE, 4, 64, 32, 1, 0)
+    rows = Z.zero_mx4(FAKE, FAKE, 4, 64, 32, 0, 0)
+    e = Z.ZERO_EINVAL
+    for bad in (q, over):
+        refused(Z, e, Z.zero_mx4_quantize, m(Z), 4, 64, bad, None)
+        refused(Z, e, Z.zero_mx4_dequantize, bad, m(Z))
+        refused(Z, e, Z.zero_mx4_tile_scales, rows, bad)
+        refused(Z, e, Z.zero_mx4_matmul, bad, gpu, 1.0, m(Z), FAKE)
+        refused(Z, e, Z.zero_mx4_matmul, gpu, bad, 1.0, m(Z), FAKE)
+    refused(Z, e, Z.zero_mx4_quantize, m(Z), 64, 4, None, Z.mx4(4, 64, device="cpu"))
+    refused(Z, e, Z.zero_mx4_quantize, Z.mat(host), 4, 64, gpu, None)
+    refused(Z, e, Z.zero_mx4_matmul, gpu, gpu, 1.0, m(Z), torch.zeros(1, dtype=torch.int32))
+    refused(Z, e, Z.zero_norm_backward, m(Z), m(Z), None, 4, 64, FAKE, None, m(Z), m(Z), 0,
+            torch.zeros(n, dtype=torch.uint8), n)
+    args = (m(Z), 4, 64, m(Z, 8, 6), m(Z, 8), 8, None, 1.0, None, 1.0, torch.zeros(56, dtype=torch.uint8))
+    refused(Z, e, Z.zero_distill_loss, *args, FAKE, FAKE, None)
+    refused(Z, e, Z.zero_distill_backward, *args, FAKE, m(Z))
+
+
+def test_buffers_that_are_too_small_are_refused(Z):
+    n = Z.zero_norm_workspace_bytes(64)
+    refused(Z, Z.ZERO_EWORKSPACE, Z.zero_norm_backward, m(Z), m(Z), None, 4, 64, FAKE, None, m(Z), m(Z), 0,
+            torch.zeros(n - 1, dtype=torch.uint8), n)
+    gpu = Z.zero_mx4(FAKE, FAKE, 4, 64, 32, 1, 0)
+    refused(Z, Z.ZERO_EINVAL, Z.zero_mx4_matmul, gpu, gpu, 1.0, m(Z), torch.zeros(2, dtype=torch.uint8))
+    refused(Z, Z.ZERO_EINVAL, Z.zero_distill_loss, m(Z), 4, 64, m(Z, 8, 6), m(Z, 8), 8, None, 1.0, None, 1.0,
+            torch.zeros(55, dtype=torch.uint8), FAKE, FAKE, None)
+
+
+def test_a_4_bit_matrix_is_made_on_the_current_gpu(Z, monkeypatch):
+    where = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: where.append(str(device)) or empty(*a, **k))
+    Z.mx4(4, 64)
+    assert where == ["cuda"]

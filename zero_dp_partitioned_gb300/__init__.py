@@ -71,12 +71,14 @@ class zero_result(ctypes.Structure):
 class zero_mat(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+    on_host = False                        # whether mat() was given a tensor that is not on a GPU
 
 
 class zero_mx4(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("layout", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+    on_host = False                        # whether mx4() was given or made a buffer that is not on a GPU
 
     @property
     def tensors(self):
@@ -450,6 +452,7 @@ def mat(data, ld=None, dtype=None) -> zero_mat:
         raise ZeroError(ZERO_EINVAL, "a zero_mat has one or two dimensions and adjacent columns")
     m = zero_mat(data.data_ptr(), data.stride(0) if data.dim() == 2 else data.shape[0], code, 0)
     m.tensor = data                        # kept alive with the argument
+    m.on_host = not data.is_cuda
     return m
 
 
@@ -459,6 +462,8 @@ def _mat(x, rows, cols, what):
     if x is None:
         return None
     if isinstance(x, zero_mat):
+        if x.on_host:
+            raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU")
         return ctypes.byref(x)
     code = _codes.get(x.dtype) or _code(x.dtype)
     shape, step = x.shape, x.stride()
@@ -487,6 +492,20 @@ def _vec(x, n, what):
     return int(x)
 
 
+def _buf(x, n, what, code=ZERO_EINVAL):
+    """A buffer argument: None, an address, or a tensor of at least n contiguous
+    bytes."""
+    if x is None or isinstance(x, int):
+        return x
+    if hasattr(x, "data_ptr"):
+        if x.numel() * x.element_size() < n or not x.is_contiguous():
+            raise ZeroError(code, f"{what} must be at least {n} contiguous bytes")
+        if not x.is_cuda:
+            raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU")
+        return x.data_ptr()
+    return int(x)
+
+
 def zero_norm_forward(x, residual, weight, rows, cols, eps, h_out, y, y_scale, scale_block, rstd, stream=None):
     """h = x + residual, y = RMSnorm(h) * weight per row; y in x's type, or
     float8_e4m3fn with a scale per row (scale_block 0) or per 128 columns."""
@@ -507,7 +526,8 @@ def zero_norm_backward(dy, h, weight, rows, cols, rstd, dh, dx, dw, accumulate, 
     _check(lib.zero_norm_backward(_mat(dy, rows, cols, "dy"), _mat(h, rows, cols, "h"),
                                   _mat(weight, 1, cols, "weight"), rows, cols, _vec(rstd, rows, "rstd"),
                                   _mat(dh, rows, cols, "dh"), _mat(dx, rows, cols, "dx"), _mat(dw, 1, cols, "dw"),
-                                  int(accumulate), _ptr(workspace), workspace_bytes, _stream(stream)))
+                                  int(accumulate), _buf(workspace, workspace_bytes, "workspace", ZERO_EWORKSPACE),
+                                  workspace_bytes, _stream(stream)))
 
 
 def zero_distill_loss(logits, rows, cols, ids, teacher, k, teacher_lse, temperature, row_weight, grad_scale, chain_dev,
@@ -516,7 +536,8 @@ def zero_distill_loss(logits, rows, cols, ids, teacher, k, teacher_lse, temperat
     gradient, scaled by grad_scale and by the loss scale of the device chain."""
     _check(lib.zero_distill_loss(_mat(logits, rows, cols, "logits"), rows, cols, _mat(ids, rows, k, "ids"),
                                  _mat(teacher, rows, k, "teacher"), k, _vec(teacher_lse, rows, "teacher_lse"),
-                                 temperature, _vec(row_weight, rows, "row_weight"), grad_scale, _ptr(chain_dev),
+                                 temperature, _vec(row_weight, rows, "row_weight"), grad_scale,
+                                 _buf(chain_dev, ctypes.sizeof(zero_chain), "chain_dev"),
                                  _vec(loss, rows, "loss"), _vec(lse, rows, "lse"),
                                  _mat(dlogits, rows, cols, "dlogits"), _stream(stream)))
 
@@ -526,7 +547,8 @@ def zero_distill_backward(logits, rows, cols, ids, teacher, k, teacher_lse, temp
     """The gradient alone, from the lse that zero_distill_loss stored."""
     _check(lib.zero_distill_backward(_mat(logits, rows, cols, "logits"), rows, cols, _mat(ids, rows, k, "ids"),
                                      _mat(teacher, rows, k, "teacher"), k, _vec(teacher_lse, rows, "teacher_lse"),
-                                     temperature, _vec(row_weight, rows, "row_weight"), grad_scale, _ptr(chain_dev),
+                                     temperature, _vec(row_weight, rows, "row_weight"), grad_scale,
+                                     _buf(chain_dev, ctypes.sizeof(zero_chain), "chain_dev"),
                                      _vec(lse, rows, "lse"), _mat(dlogits, rows, cols, "dlogits"), _stream(stream)))
 
 
@@ -540,14 +562,16 @@ def zero_mx4_bytes(rows, cols, layout=ZERO_MX4_TILES):
 
 def mx4(rows, cols, data=None, scales=None, layout=ZERO_MX4_TILES, device=None) -> zero_mx4:
     """A zero_mx4 over given buffers (torch uint8 tensors or addresses), or over
-    new ones on `device`; rows follow one another without gaps."""
+    new ones on `device` (None: the current GPU); rows follow one another
+    without gaps."""
     ld, n_data, n_scales = zero_mx4_bytes(rows, cols, layout)
     if data is None and scales is None:
         import torch
-        buf = torch.empty(n_data + n_scales, dtype=torch.uint8, device=device)
+        buf = torch.empty(n_data + n_scales, dtype=torch.uint8, device="cuda" if device is None else device)
         at = buf.data_ptr()
         m = zero_mx4(at, at + n_data, rows, cols, ld, layout, 0)
         m.buffers = (buf, None, n_data)    # kept alive with the argument
+        m.on_host = not buf.is_cuda
         return m
     if data is None or scales is None:
         raise ZeroError(ZERO_EINVAL, "data and scales: both or neither")
@@ -556,32 +580,38 @@ def mx4(rows, cols, data=None, scales=None, layout=ZERO_MX4_TILES, device=None) 
             raise ZeroError(ZERO_EINVAL, f"{what} must be at least {n} contiguous bytes")
     m = zero_mx4(_ptr(data), _ptr(scales), rows, cols, ld, layout, 0)
     m.buffers = (data, scales, None)
+    m.on_host = any(hasattr(t, "data_ptr") and not t.is_cuda for t in (data, scales))
     return m
 
 
-def _mx4(x):
-    return None if x is None else ctypes.byref(x)
+def _mx4(x, what):
+    if x is None:
+        return None
+    if x.on_host:
+        raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU")
+    return ctypes.byref(x)
 
 
 def zero_mx4_quantize(src, rows, cols, out, out_t, stream=None):
     """src to 4 bits along its rows (out) and along its columns (out_t: cols x
     rows); either may be None."""
-    _check(lib.zero_mx4_quantize(_mat(src, rows, cols, "src"), rows, cols, _mx4(out), _mx4(out_t), _stream(stream)))
+    _check(lib.zero_mx4_quantize(_mat(src, rows, cols, "src"), rows, cols, _mx4(out, "out"), _mx4(out_t, "out_t"),
+                                 _stream(stream)))
 
 
 def zero_mx4_dequantize(src, dst, stream=None):
     """The values of a 4-bit matrix in dst's type."""
     d = None if src is None else _mat(dst, src.rows, src.cols, "dst")
-    _check(lib.zero_mx4_dequantize(_mx4(src), d, _stream(stream)))
+    _check(lib.zero_mx4_dequantize(_mx4(src, "src"), d, _stream(stream)))
 
 
 def zero_mx4_tile_scales(src, dst, stream=None):
     """Scales gathered row by row (ZERO_MX4_ROWS) to the product's tiles."""
-    _check(lib.zero_mx4_tile_scales(_mx4(src), _mx4(dst), _stream(stream)))
+    _check(lib.zero_mx4_tile_scales(_mx4(src, "src"), _mx4(dst, "dst"), _stream(stream)))
 
 
 def zero_mx4_matmul(a, b, alpha, d, status, stream=None):
     """d = alpha a b^T of two 4-bit matrices; status: device int32 (zero-filled by
     the caller), bit 0 set if a wait ran out."""
     m = None if a is None or b is None else _mat(d, a.rows, b.rows, "d")
-    _check(lib.zero_mx4_matmul(_mx4(a), _mx4(b), alpha, m, _ptr(status), _stream(stream)))
+    _check(lib.zero_mx4_matmul(_mx4(a, "a"), _mx4(b, "b"), alpha, m, _buf(status, 4, "status"), _stream(stream)))
