@@ -213,3 +213,15 @@ def test_a_4_bit_matrix_is_made_on_the_current_gpu(Z, monkeypatch):
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: where.append(str(device)) or empty(*a, **k))
     Z.mx4(4, 64)
     assert where == ["cuda"]
+
+
+def test_the_current_stream_without_torchs_private_calls(Z, monkeypatch):
+    """A torch that has renamed them gives the stream by its public calls."""
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(Z, "_raw_stream", None)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "init", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: type("S", (), {"cuda_stream": 0x1000 + d}))
+    assert Z._stream(None) == 0x1003

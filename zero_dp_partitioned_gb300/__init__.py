@@ -173,14 +173,18 @@ _raw_stream = None
 def _current_stream():
     """torch's current stream on the current device (None without a GPU), by the
     calls under torch.cuda.current_stream(): its Stream object alone costs as
-    much as a small kernel (2.8 us on the host that drives a GB300)."""
+    much as a small kernel (2.8 us on the host that drives a GB300).  They are
+    not public; a torch without them is asked by the public calls."""
     global _raw_stream
     if _raw_stream is None:
         import torch
         if not torch.cuda.is_available():
             return None
         torch.cuda.init()
-        _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+        calls = tuple(getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if None in calls:
+            calls = (lambda d: torch.cuda.current_stream(d).cuda_stream, torch.cuda.current_device)
+        _raw_stream = calls
     return _raw_stream[0](_raw_stream[1]())
 
 
