@@ -225,3 +225,41 @@ def test_the_current_stream_without_torchs_private_calls(Z, monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: type("S", (), {"cuda_stream": 0x1000 + d}))
     assert Z._stream(None) == 0x1003
+
+
+class OnGpu:
+    """What the calls ask of a tensor, on the GPU of the given number."""
+
+    def __init__(self, gpu, *shape, dtype=torch.bfloat16):
+        self.like, self.gpu = torch.empty(*shape, dtype=dtype), gpu
+        self.dtype, self.shape, self.is_cuda = dtype, self.like.shape, True
+
+    def get_device(self):
+        return self.gpu
+
+    def data_ptr(self):
+        return FAKE
+
+    def __getattr__(self, name):
+        return getattr(self.like, name)
+
+
+def test_tensors_of_another_gpu_are_refused(Z, monkeypatch):
+    """Their addresses mean nothing, or something else, to a kernel on the current one."""
+    monkeypatch.setattr(Z, "_raw_stream", (lambda d: 0, lambda: 1))
+    e, f32, u8 = Z.ZERO_EINVAL, torch.float32, torch.uint8
+    there = OnGpu(0, 4, 64)
+    n = Z.zero_norm_workspace_bytes(64)
+    gpu = Z.zero_mx4(FAKE, FAKE, 4, 64, 32, 1, 0)
+    refused(Z, e, Z.zero_norm_forward, there, None, None, 4, 64, 1e-5, None, m(Z), None, 0, None)
+    refused(Z, e, Z.zero_norm_forward, Z.mat(there), None, None, 4, 64, 1e-5, None, m(Z), None, 0, None)
+    refused(Z, e, Z.zero_norm_forward, m(Z), None, None, 4, 64, 1e-5, None, m(Z), None, 0, OnGpu(0, 4, dtype=f32))
+    refused(Z, e, Z.zero_norm_backward, m(Z), m(Z), None, 4, 64, FAKE, None, m(Z), m(Z), 0, OnGpu(0, n, dtype=u8), n)
+    refused(Z, e, Z.zero_mx4_quantize, m(Z), 4, 64, Z.mx4(4, 64, OnGpu(0, 4096, dtype=u8), FAKE), None)
+    refused(Z, e, Z.zero_mx4_matmul, gpu, gpu, 1.0, m(Z), OnGpu(0, 1, dtype=torch.int32))
+    with pytest.raises(Z.ZeroError):
+        Z.mx4(4, 64, OnGpu(0, 4096, dtype=u8), OnGpu(1, 4096, dtype=u8))
+    # on the current one they pass: nothing to do, so nothing is launched
+    here = OnGpu(1, 0, 64)
+    Z.zero_norm_forward(here, None, None, 0, 64, 1e-5, None, here, None, 0, OnGpu(1, 0, dtype=f32), stream=0)
+    Z.zero_mx4_quantize(here, 0, 64, Z.mx4(0, 64, OnGpu(1, 0, dtype=u8), OnGpu(1, 0, dtype=u8)), None, stream=0)

@@ -71,14 +71,14 @@ class zero_result(ctypes.Structure):
 class zero_mat(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
-    on_host = False                        # whether mat() was given a tensor that is not on a GPU
+    device = None                          # of the tensor that mat() was given, -1: not a GPU
 
 
 class zero_mx4(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("layout", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
-    on_host = False                        # whether mx4() was given or made a buffer that is not on a GPU
+    device = None                          # of the tensors that mx4() was given or made, -1: not a GPU
 
     @property
     def tensors(self):
@@ -175,6 +175,15 @@ def _current_stream():
     calls under torch.cuda.current_stream(): its Stream object alone costs as
     much as a small kernel (2.8 us on the host that drives a GB300).  They are
     not public; a torch without them is asked by the public calls."""
+    return _raw_stream[0](_raw_stream[1]()) if _raw_stream or _find_raw_stream() else None
+
+
+def _current_device():
+    """torch's current device (-1 without a GPU)."""
+    return _raw_stream[1]() if _raw_stream or _find_raw_stream() else -1
+
+
+def _find_raw_stream():
     global _raw_stream
     if _raw_stream is None:
         import torch
@@ -185,7 +194,7 @@ def _current_stream():
         if None in calls:
             calls = (lambda d: torch.cuda.current_stream(d).cuda_stream, torch.cuda.current_device)
         _raw_stream = calls
-    return _raw_stream[0](_raw_stream[1]())
+    return _raw_stream
 
 
 def _check(rc):
@@ -456,8 +465,13 @@ def mat(data, ld=None, dtype=None) -> zero_mat:
         raise ZeroError(ZERO_EINVAL, "a zero_mat has one or two dimensions and adjacent columns")
     m = zero_mat(data.data_ptr(), data.stride(0) if data.dim() == 2 else data.shape[0], code, 0)
     m.tensor = data                        # kept alive with the argument
-    m.on_host = not data.is_cuda
+    m.device = data.get_device()
     return m
+
+
+def _elsewhere(device, what):
+    raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU" if device < 0 else
+                    f"{what} is on GPU {device}, not on the current one")
 
 
 def _mat(x, rows, cols, what):
@@ -466,8 +480,8 @@ def _mat(x, rows, cols, what):
     if x is None:
         return None
     if isinstance(x, zero_mat):
-        if x.on_host:
-            raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU")
+        if x.device is not None and (x.device < 0 or x.device != _current_device()):
+            _elsewhere(x.device, what)
         return ctypes.byref(x)
     code = _codes.get(x.dtype) or _code(x.dtype)
     shape, step = x.shape, x.stride()
@@ -477,8 +491,9 @@ def _mat(x, rows, cols, what):
         raise ZeroError(ZERO_EINVAL, f"{what} is {tuple(x.shape)}, not {rows} x {cols}")
     if step[1] != 1 and cols > 1:
         raise ZeroError(ZERO_EINVAL, f"{what}: its columns are not adjacent")
-    if not x.is_cuda:
-        raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU")
+    device = x.get_device()
+    if device < 0 or device != _current_device():
+        _elsewhere(device, what)
     return _pack_mat(x.data_ptr(), step[0], code, 0)
 
 
@@ -490,8 +505,9 @@ def _vec(x, n, what):
     if hasattr(x, "data_ptr"):
         if x.numel() < n or (_codes.get(x.dtype) or _code(x.dtype)) != ZERO_F32 or not x.is_contiguous():
             raise ZeroError(ZERO_EINVAL, f"{what} must be {n} contiguous float32 values")
-        if not x.is_cuda:
-            raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU")
+        device = x.get_device()
+        if device < 0 or device != _current_device():
+            _elsewhere(device, what)
         return x.data_ptr()
     return int(x)
 
@@ -504,8 +520,9 @@ def _buf(x, n, what, code=ZERO_EINVAL):
     if hasattr(x, "data_ptr"):
         if x.numel() * x.element_size() < n or not x.is_contiguous():
             raise ZeroError(code, f"{what} must be at least {n} contiguous bytes")
-        if not x.is_cuda:
-            raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU")
+        device = x.get_device()
+        if device < 0 or device != _current_device():
+            _elsewhere(device, what)
         return x.data_ptr()
     return int(x)
 
@@ -575,7 +592,7 @@ def mx4(rows, cols, data=None, scales=None, layout=ZERO_MX4_TILES, device=None) 
         at = buf.data_ptr()
         m = zero_mx4(at, at + n_data, rows, cols, ld, layout, 0)
         m.buffers = (buf, None, n_data)    # kept alive with the argument
-        m.on_host = not buf.is_cuda
+        m.device = buf.get_device()
         return m
     if data is None or scales is None:
         raise ZeroError(ZERO_EINVAL, "data and scales: both or neither")
@@ -584,15 +601,18 @@ def mx4(rows, cols, data=None, scales=None, layout=ZERO_MX4_TILES, device=None) 
             raise ZeroError(ZERO_EINVAL, f"{what} must be at least {n} contiguous bytes")
     m = zero_mx4(_ptr(data), _ptr(scales), rows, cols, ld, layout, 0)
     m.buffers = (data, scales, None)
-    m.on_host = any(hasattr(t, "data_ptr") and not t.is_cuda for t in (data, scales))
+    on = {t.get_device() for t in (data, scales) if hasattr(t, "data_ptr")}
+    if len(on) == 2 and min(on) >= 0:
+        raise ZeroError(ZERO_EINVAL, "data and scales are on two GPUs")
+    m.device = min(on) if on else None
     return m
 
 
 def _mx4(x, what):
     if x is None:
         return None
-    if x.on_host:
-        raise ZeroError(ZERO_EINVAL, f"{what} is not on a GPU")
+    if x.device is not None and (x.device < 0 or x.device != _current_device()):
+        _elsewhere(x.device, what)
     return ctypes.byref(x)
 
 
