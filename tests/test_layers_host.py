@@ -263,3 +263,17 @@ def test_tensors_of_another_gpu_are_refused(Z, monkeypatch):
     here = OnGpu(1, 0, 64)
     Z.zero_norm_forward(here, None, None, 0, 64, 1e-5, None, here, None, 0, OnGpu(1, 0, dtype=f32), stream=0)
     Z.zero_mx4_quantize(here, 0, 64, Z.mx4(0, 64, OnGpu(1, 0, dtype=u8), OnGpu(1, 0, dtype=u8)), None, stream=0)
+
+
+def test_a_weight_without_data_is_refused(Z):
+    """An address of 0 (a unit that is not gathered) is not a weight of 1."""
+    ws = Z.zero_norm_workspace_bytes(64)
+    for dtype in (1, 2, 3):
+        w = m(Z, dtype=dtype, data=0)
+        for call, f, args in (("zero_norm_forward", Z.zero_norm_forward,
+                               (m(Z), None, w, 4, 64, 1e-5, None, m(Z), None, 0, None)),
+                              ("zero_norm_backward", Z.zero_norm_backward,
+                               (m(Z), m(Z), w, 4, 64, FAKE, None, m(Z), m(Z), 0, FAKE, ws))):
+            with pytest.raises(Z.ZeroError, match=f"{call}: weight") as e:
+                f(*args, stream=0)
+            assert e.value.code == Z.ZERO_EINVAL

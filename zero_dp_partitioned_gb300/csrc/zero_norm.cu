@@ -711,11 +711,10 @@ static NormShape shape_of(int64_t cols, int words, int sm_threads) {
     if (s.smem <= NORM_SM_SMEM) return s;
     return NormShape{0, NORM_THREADS, sm_threads / NORM_THREADS, 2, 0};
 }
-static int check_weight(const zero_mat* w, int64_t cols, NormArgs& a) {
-    if (!w || !w->data) return ZERO_OK;
-    if (w->dtype != ZERO_F16 && w->dtype != ZERO_BF16 && w->dtype != ZERO_F32)
-        return fail(ZERO_EINVAL, "norm: unknown weight dtype");
-    if (!aligned(w->data, elem_size(w->dtype))) return fail(ZERO_EALIGN, "norm: weight not aligned to its element");
+static int check_weight(const zero_mat* w, int64_t cols, NormArgs& a, const char* call) {
+    if (!w) return ZERO_OK;
+    const int rc = check_mat(w, 1, cols, FLOAT_TYPES, call, "weight");
+    if (rc != ZERO_OK || cols == 0) return rc;
     a.w = w->data;
     a.wdt = w->dtype;
     a.w_aligned = aligned(w->data, 16);
@@ -751,7 +750,7 @@ int zero_norm_forward(const zero_mat* x, const zero_mat* residual, const zero_ma
     if (y8 && rows > 0 && cols > 0 && !y_scale) return fail(ZERO_EINVAL, "zero_norm_forward: e4m3 output needs y_scale");
     if (!aligned(y_scale, 4) || !aligned(rstd, 4)) return fail(ZERO_EALIGN, "zero_norm_forward: y_scale or rstd not 4-byte aligned");
     NormArgs a = {};
-    rc = check_weight(weight, cols, a);
+    rc = check_weight(weight, cols, a, "zero_norm_forward");
     if (rc != ZERO_OK || rows == 0 || cols == 0) return rc;
     a.x = x->data;
     a.ldx = x->ld;
@@ -809,7 +808,7 @@ int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* we
     if (dw && cols > 0 && (!workspace || !aligned(workspace, 4) || workspace_bytes < zero_norm_workspace_bytes(cols)))
         return fail(ZERO_EWORKSPACE, "zero_norm_backward: workspace smaller than zero_norm_workspace_bytes(cols)");
     NormArgs a = {};
-    rc = check_weight(weight, cols, a);
+    rc = check_weight(weight, cols, a, "zero_norm_backward");
     if (rc != ZERO_OK || cols == 0) return rc;
     const int sms = sm_count();
     if (!sms) return ZERO_ECUDA;
