@@ -653,7 +653,9 @@ int zero_shard_step_host(const void* const* host_grad_slices, int n_slices, int 
  *    Any row distance and any alignment to the element is taken; rows that all
  *    start on 16-byte boundaries run with 16-byte accesses.  ld may be
  *    anything (0 included) when there is at most one row.
- *  - A matrix of no rows or no columns is allowed and gives an empty result.
+ *  - A matrix of no rows or no columns is allowed and gives an empty result:
+ *    what has a value for each row (rstd, a row's scale) is not written for
+ *    rows of no columns, except the losses and lse of zero_distill_loss.
  *  - Sums are held in fp32 or more, each output is rounded once to its type,
  *    and results do not depend on timing: no sum uses atomics.
  *  - "may be X" means: the very same data pointer and ld as X.  No other
@@ -732,7 +734,7 @@ size_t zero_norm_workspace_bytes(int64_t cols);
  *            not NULL, S = chain->loss_scale read on the device when the kernel
  *            runs (1 otherwise): the scale that the chained step divides by
  * loss, lse  rows values each (lse of logits / T, for the backward call);
- *            NULL: not wanted
+ *            NULL: not wanted; rows of no columns have loss 0 and lse -inf
  * dlogits    in the logits' type; may be logits; NULL: not wanted
  * k <= 1024.  Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ELIMIT, ZERO_ECUDA. */
 int zero_distill_loss(const zero_mat* logits, int64_t rows, int64_t cols, const zero_mat* ids, const zero_mat* teacher,

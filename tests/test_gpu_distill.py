@@ -228,3 +228,19 @@ def test_another_stream_and_the_same_bits(Z):
         outs.append((loss, lse, dz))
     for o in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(outs[0], o))
+
+
+@pytest.mark.parametrize("rows", [1, 5, 50000])
+def test_rows_of_no_columns(Z, rows):
+    """No id is a column: every row is without entries, and its log-sum-exp is that of nothing."""
+    z, k = torch.empty(rows, 0, dtype=BF16, device=DEV), 3
+    ids, t = torch.zeros(rows, k, dtype=torch.int64, device=DEV), torch.ones(rows, k, device=DEV)
+    loss, lse = (torch.full((rows + 1,), 7.0, device=DEV) for _ in range(2))
+    Z.zero_distill_loss(z, rows, 0, ids, t, k, None, 1.0, None, 1.0, None, loss, None, z)
+    assert not loss[:rows].any() and loss[rows] == 7 and bool((lse == 7).all())
+    loss.fill_(7.0)
+    Z.zero_distill_loss(z, rows, 0, ids, t, k, None, 1.0, None, 1.0, None, loss, lse, None)
+    assert not loss[:rows].any() and loss[rows] == 7
+    assert bool((lse[:rows] == -math.inf).all()) and lse[rows] == 7
+    Z.zero_distill_backward(z, rows, 0, ids, t, k, None, 1.0, None, 1.0, None, lse, z)
+    Z.zero_distill_loss(z[:0], 0, 0, ids[:0], t[:0], k, None, 1.0, None, 1.0, None, loss[:0], lse[:0], None)

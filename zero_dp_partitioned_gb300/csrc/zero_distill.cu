@@ -365,6 +365,16 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
     }
 }
 
+// Rows of no columns: no entries, and a sum of nothing.
+__global__ void __launch_bounds__(256) k_distill_empty(float* loss, float* lse, int64_t rows) {
+    pdl_wait();
+    pdl_launch_next();
+    for (int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < rows; r += (int64_t)gridDim.x * blockDim.x) {
+        if (loss) loss[r] = 0.f;
+        if (lse) lse[r] = -INFINITY;
+    }
+}
+
 template <int DT>
 static const void* distill_fn(bool bwd) {
     return bwd ? (const void*)k_distill<DT, true> : (const void*)k_distill<DT, false>;
@@ -393,9 +403,16 @@ static int distill(const char* who, const zero_mat* logits, int64_t rows, int64_
     if (!aligned(teacher_lse, 4) || !aligned(row_weight, 4) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(lse_in, 4))
         return bad(ZERO_EALIGN, "a row array is not 4-byte aligned");
     if (!aligned(chain, 8)) return bad(ZERO_EALIGN, "chain not 8-byte aligned");
-    if (rows == 0 || cols == 0) return ZERO_OK;
+    if (rows == 0 || (cols == 0 && !loss && !lse)) return ZERO_OK;
     const int sms = sm_count();
     if (!sms) return ZERO_ECUDA;
+    if (cols == 0) {
+        int64_t n = rows;
+        void* args[] = {&loss, &lse, &n};
+        return cuda_fail(launch_after_previous((const void*)k_distill_empty, (int)(rows < sms * 256 ? (rows + 255) / 256 : sms),
+                                               256, args, 0, static_cast<cudaStream_t>(stream)),
+                         who);
+    }
 
     DistillArgs a = {};
     a.z = logits->data;
