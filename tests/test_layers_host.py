@@ -247,6 +247,7 @@ class OnGpu:
 def test_tensors_of_another_gpu_are_refused(Z, monkeypatch):
     """Their addresses mean nothing, or something else, to a kernel on the current one."""
     monkeypatch.setattr(Z, "_raw_stream", (lambda d: 0, lambda: 1))
+    monkeypatch.setattr(Z, "_gpus", 2)
     e, f32, u8 = Z.ZERO_EINVAL, torch.float32, torch.uint8
     there = OnGpu(0, 4, 64)
     n = Z.zero_norm_workspace_bytes(64)

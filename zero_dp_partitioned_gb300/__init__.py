@@ -168,6 +168,7 @@ def _stream(stream):
 
 
 _raw_stream = None
+_gpus = 0                                  # of this process; 0: not known yet
 
 
 def _current_stream():
@@ -184,7 +185,7 @@ def _current_device():
 
 
 def _find_raw_stream():
-    global _raw_stream
+    global _raw_stream, _gpus
     if _raw_stream is None:
         import torch
         if not torch.cuda.is_available():
@@ -193,7 +194,7 @@ def _find_raw_stream():
         calls = tuple(getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
         if None in calls:
             calls = (lambda d: torch.cuda.current_stream(d).cuda_stream, torch.cuda.current_device)
-        _raw_stream = calls
+        _raw_stream, _gpus = calls, torch.cuda.device_count()
     return _raw_stream
 
 
@@ -491,9 +492,8 @@ def _mat(x, rows, cols, what):
         raise ZeroError(ZERO_EINVAL, f"{what} is {tuple(x.shape)}, not {rows} x {cols}")
     if step[1] != 1 and cols > 1:
         raise ZeroError(ZERO_EINVAL, f"{what}: its columns are not adjacent")
-    device = x.get_device()
-    if device < 0 or device != _current_device():
-        _elsewhere(device, what)
+    if not x.is_cuda or (_gpus != 1 and x.get_device() != _current_device()):
+        _elsewhere(x.get_device(), what)
     return _pack_mat(x.data_ptr(), step[0], code, 0)
 
 
@@ -505,9 +505,8 @@ def _vec(x, n, what):
     if hasattr(x, "data_ptr"):
         if x.numel() < n or (_codes.get(x.dtype) or _code(x.dtype)) != ZERO_F32 or not x.is_contiguous():
             raise ZeroError(ZERO_EINVAL, f"{what} must be {n} contiguous float32 values")
-        device = x.get_device()
-        if device < 0 or device != _current_device():
-            _elsewhere(device, what)
+        if not x.is_cuda or (_gpus != 1 and x.get_device() != _current_device()):
+            _elsewhere(x.get_device(), what)
         return x.data_ptr()
     return int(x)
 
@@ -520,9 +519,8 @@ def _buf(x, n, what, code=ZERO_EINVAL):
     if hasattr(x, "data_ptr"):
         if x.numel() * x.element_size() < n or not x.is_contiguous():
             raise ZeroError(code, f"{what} must be at least {n} contiguous bytes")
-        device = x.get_device()
-        if device < 0 or device != _current_device():
-            _elsewhere(device, what)
+        if not x.is_cuda or (_gpus != 1 and x.get_device() != _current_device()):
+            _elsewhere(x.get_device(), what)
         return x.data_ptr()
     return int(x)
 
@@ -611,7 +609,7 @@ def mx4(rows, cols, data=None, scales=None, layout=ZERO_MX4_TILES, device=None) 
 def _mx4(x, what):
     if x is None:
         return None
-    if x.device is not None and (x.device < 0 or x.device != _current_device()):
+    if x.device is not None and (x.device < 0 or (_gpus != 1 and x.device != _current_device())):
         _elsewhere(x.device, what)
     return ctypes.byref(x)
 
