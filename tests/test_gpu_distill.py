@@ -244,3 +244,40 @@ def test_rows_of_no_columns(Z, rows):
     assert bool((lse[:rows] == -math.inf).all()) and lse[rows] == 7
     Z.zero_distill_backward(z, rows, 0, ids, t, k, None, 1.0, None, 1.0, None, lse, z)
     Z.zero_distill_loss(z[:0], 0, 0, ids[:0], t[:0], k, None, 1.0, None, 1.0, None, loss[:0], lse[:0], None)
+
+
+@pytest.mark.parametrize("off", [1e4, -1e4, 1e6])
+@pytest.mark.parametrize("tau", [1.0, 3.0])
+def test_a_teacher_far_from_zero(Z, off, tau):
+    """Only differences of the teacher's logits count: p is as near as that of logits about 0."""
+    g, z, ids, t = problem(16, 9, 3000, 70, F32)
+    t += off
+    loss, lse, dz = torch.empty(9, device=DEV), torch.empty(9, device=DEV), torch.empty_like(z)
+    Z.zero_distill_loss(z, 9, 3000, ids, t, 70, None, tau, None, 1.0, None, loss, lse, dz)
+    check(z, ids, t, tau, None, 1.0, loss, lse, dz)
+    Z.zero_distill_backward(z, 9, 3000, ids, t, 70, None, tau, None, 1.0, None, lse, dz)
+    check(z, ids, t, tau, None, 1.0, None, None, dz)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("tau", [0.25, 1.0, 2.0])
+def test_a_teacher_of_the_lowest_values(Z, dtype, tau):
+    """Entries masked with the type's lowest value count for nothing beside others, and alike among themselves; the
+    same of its largest value.  The reference is given the teacher's logits less their largest: 64 bits do not hold
+    3e38 + log 600."""
+    low, k = torch.finfo(dtype).min, 600
+    _, z, ids, t = problem(17, 6, 3000, k, dtype)
+    t[0, 1:], t[1], t[2, 300:] = low, low, low
+    t[3, 7], t[3, 500], t[4] = -low, -low, low / 1.5
+    near = t.double() - t.double().amax(1, keepdim=True)
+    loss, dz = torch.empty(6, device=DEV), torch.empty_like(z)
+    Z.zero_distill_loss(z, 6, 3000, ids, t, k, None, tau, None, 1.0, None, loss, None, dz)
+    check(z, ids, near, tau, None, 1.0, loss, None, dz)
+    lse = torch.logsumexp(z.double() / tau, 1).float()
+    Z.zero_distill_backward(z, 6, 3000, ids, t, k, None, tau, None, 1.0, None, lse, dz)
+    check(z, ids, near, tau, None, 1.0, None, None, dz)
+    t[3, 7], t[3, 500] = 1.0, 1.0
+    t_lse = torch.logsumexp(t.double() / tau, 1).float()
+    t_lse = torch.where(t_lse > -1e4, t_lse + 0.3, 0.0)            # beside the rest of the teacher's vocabulary
+    Z.zero_distill_loss(z, 6, 3000, ids, t, k, t_lse, tau, None, 1.0, None, loss, None, dz)
+    check(z, ids, t, tau, None, 1.0, loss, None, dz, t_lse)

@@ -49,10 +49,10 @@ struct DistillArgs {
 };
 
 // One entry of the row's teacher list, in shared memory: the column (-1: no
-// entry), the teacher's logit times k2, and the student's logit.
+// entry), the teacher's logit, the student's logit, and p before it is divided.
 struct Entry {
     int id;
-    float t, z;
+    float t, z, p;
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -179,6 +179,15 @@ __device__ __forceinline__ float2 merge(const float2* part, int n) {
     return make_float2(m, warp_sum(s));
 }
 
+// The teacher's parts, one a lane -- a largest logit and the sum of 2^((t - it) k)
+// -- to those of the row; plain sums where the base is given (no softmax of its own).
+__device__ __forceinline__ float2 merge_teacher(const float2* part, int n, float k2, bool own) {
+    const int lane = threadIdx.x & 31;
+    const float2 p = lane < n ? part[lane] : make_float2(-INFINITY, 0.f);
+    const float top = warp_max(p.x);
+    return make_float2(top, warp_sum(own && p.x != top ? p.y * exp2f((p.x - top) * k2) : p.y));
+}
+
 // BWD: the row's log-sum-exp is given (lse_in), so that only the gradient is
 // walked and nothing crosses the cluster.
 //
@@ -217,14 +226,19 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
         const int64_t id = a.id64 ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
         const float t = ld1_any(a.t, row * a.ldt + i, a.t_dt);
         const bool have = id >= 0 && id < a.cols && t != -INFINITY;
-        Entry en = {have ? (int)id : -1, have ? t * a.k2 : -INFINITY, 0.f};
+        Entry en = {have ? (int)id : -1, t, 0.f, 0.f};
         // the backward pass alone has no barrier between its blocks: it reads what it itself will write
         if (have && (!BWD || mine(en.id))) en.z = ld1<DT>(rv.base, en.id);
         entry[i] = en;
-        if (have) tmax = fmaxf(tmax, t != t ? 0.f : en.t);      // a NaN entry makes the sum NaN, not the row empty
+        if (have) tmax = fmaxf(tmax, t != t ? 0.f : t);         // a NaN entry makes the sum NaN, not the row empty
     }
     const float k2 = a.k2;
     const uint64_t kk = pack2(k2, k2);
+    // log2 of the teacher's p: with its log-sum-exp, or (own) of the difference to the row's largest logit and not yet
+    // divided by the sum, so that a common offset of the logits does not matter
+    const bool own = !a.t_lse;
+    const float tl = own ? 0.f : a.t_lse[row] * 1.4426950408889634f;
+    auto log_term = [&](float t, float top) { return fmaf(t - top, k2, -tl); };      // top: 0 with a log-sum-exp
     float m = -INFINITY, s = 0.f;                 // this thread's m k and sum
     if constexpr (!BWD) {
         uint64_t s2 = 0;
@@ -274,10 +288,11 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
     }
     {
         const float tm = warp_max(tmax);
+        const float top = own ? tm : 0.f;
         float ts = 0.f;
         if (warp * 32 < a.k)
             for (int i = threadIdx.x; i < a.k; i += T)
-                if (entry[i].id >= 0) ts += exp2f(entry[i].t - tm);
+                if (entry[i].id >= 0) ts += exp2f(log_term(entry[i].t, top));
         ts = warp_sum(ts);
         if (lane == 0) tpart[warp] = make_float2(tm, ts);
     }
@@ -302,24 +317,23 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
         mk = whole.x == -INFINITY ? 0.f : whole.x;
         total = whole.y;
     }
-    const float2 tw = merge(tpart, T >> 5);
+    const float2 tw = merge_teacher(tpart, T >> 5, k2, own);
     const bool none = tw.x == -INFINITY;          // no teacher entry in the row
-    // p_i = 2^(t_i - tm) pscale
-    const float tl = a.t_lse ? a.t_lse[row] * 1.4426950408889634f : 0.f;
-    const float tm = tw.x, pscale = a.t_lse ? exp2f(tm - tl) : 1.f / tw.y, P = none ? 0.f : tw.y * pscale;
+    // p_i = 2^(log_term(t_i, tm)) pscale
+    const float tm = own ? tw.x : 0.f, pscale = own ? 1.f / tw.y : 1.f, P = none ? 0.f : tw.y * pscale;
     const float w = a.w ? a.w[row] : 1.f;
     const bool dead = none || w == 0.f;
     if constexpr (!BWD) {
         const float lg = log2f(total);
         if (a.lse && rank == 0 && threadIdx.x == 0) a.lse[row] = (mk + lg) * 0.6931471805599453f;
         if (a.loss && rank == 0 && warp == 0) {
-            const float lpoff = a.t_lse ? tl : tm + log2f(tw.y);
+            const float lt = own ? log2f(tw.y) : 0.f;
             float l = 0.f;
             if (!dead)
                 for (int i = lane; i < a.k; i += 32) {
                     const Entry en = entry[i];
-                    const float p = en.id >= 0 ? exp2f(en.t - tm) * pscale : 0.f;
-                    if (p != 0.f) l += p * ((en.t - lpoff) - (fmaf(en.z, k2, -mk) - lg));
+                    const float lp = log_term(en.t, tm), p = en.id >= 0 ? exp2f(lp) * pscale : 0.f;
+                    if (p != 0.f) l += p * ((lp - lt) - (fmaf(en.z, k2, -mk) - lg));
                 }
             l = warp_sum(l);
             if (lane == 0) a.loss[row] = dead ? 0.f : l * 0.6931471805599453f * a.temperature * a.temperature * w;
@@ -337,6 +351,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
         if (edge >= 0) st1<DT>(drow, edge, 0.f);
         return;
     }
+    for (int j = threadIdx.x; j < a.k; j += T) entry[j].p = exp2f(log_term(entry[j].t, tm));     // read after a barrier
     const float g = coef * P / total;
     const uint64_t gg = pack2(g, g), nm = pack2(-mk, -mk);
     int i = first;
@@ -360,7 +375,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
         if (en.id < 0 || !mine(en.id)) continue;
         float p = 0.f;
         for (int o = 0; o < a.k; ++o)
-            if (entry[o].id == en.id) p += exp2f(entry[o].t - tm);
+            if (entry[o].id == en.id) p += entry[o].p;
         st1<DT>(drow, en.id, fmaf(g, exp2_fast(fmaf(en.z, k2, -mk)), -coef * p * pscale));
     }
 }
