@@ -743,7 +743,10 @@ int zero_distill_loss(const zero_mat* logits, int64_t rows, int64_t cols, const 
 
 /* The gradient alone, when the rows' upstream gradients are known only after
  * the loss (row_weight carries them): dlogits from lse as zero_distill_loss
- * stored it, the rest as there. */
+ * stored it, the rest as there.  q = exp(logits / T - lse) has what precision
+ * lse, an fp32 value, leaves it: none for rows whose logits / T are beyond 10^7
+ * (a row masked with a type's lowest value), whose gradient zero_distill_loss
+ * still gives. */
 int zero_distill_backward(const zero_mat* logits, int64_t rows, int64_t cols, const zero_mat* ids,
                           const zero_mat* teacher, int k, const float* teacher_lse, float temperature,
                           const float* row_weight, float grad_scale, const zero_chain* chain, const float* lse,

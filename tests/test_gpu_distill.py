@@ -281,3 +281,37 @@ def test_a_teacher_of_the_lowest_values(Z, dtype, tau):
     t_lse = torch.where(t_lse > -1e4, t_lse + 0.3, 0.0)            # beside the rest of the teacher's vocabulary
     Z.zero_distill_loss(z, 6, 3000, ids, t, k, t_lse, tau, None, 1.0, None, loss, None, dz)
     check(z, ids, t, tau, None, 1.0, loss, None, dz, t_lse)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("tau", [0.25, 1.0, 2.0])
+@pytest.mark.parametrize("cols", [3000, 70001])
+@pytest.mark.parametrize("copies", [1, 50])
+def test_logits_of_the_lowest_values(Z, dtype, tau, cols, copies):
+    """A row masked with the type's lowest value throughout is a uniform one, and any row of finite logits has a
+    finite gradient.  The reference is given the logits less their largest (64 bits do not hold 3e38 + log cols);
+    losses are compared where fp32 holds log q of every entry."""
+    low, k, rows = torch.finfo(dtype).min, 40, 8 * copies
+    g, z, ids, t = problem(18, 8, cols, k, dtype)
+    z[0], z[1] = low, low
+    z[1, 77] = 2.0
+    z[2, :cols // 2], z[2, cols // 2:] = low, low / 1.5
+    z[3] = -low
+    z[4] = torch.where(torch.rand(cols, generator=g, device=DEV) < 0.5, low / 64, -low / 64)
+    if dtype != F16:
+        z[5], z[6] = (z[5].float() * 1e4 + 1e10).to(dtype), (z[6].float() * 100 - 5e8).to(dtype)
+    z[7, cols // 3:] = low                                         # a part of the vocabulary
+    z, ids, t = (x.repeat(copies, 1) for x in (z, ids, t))
+    loss, lse, dz = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV), z.clone()
+    Z.zero_distill_loss(dz, rows, cols, ids, t, k, None, tau, None, 1.0, None, loss, lse, dz)
+    top = z.double().amax(1, keepdim=True)
+    rl, rlse, rdz, mag, size = reference(z.double() - top, ids, t, tau, None, 1.0)
+    full = top[:, 0] / tau + rlse
+    # at a temperature below 1 the lowest value's lse is itself beyond fp32, and rounds to infinity
+    near = (lse.double() - full).abs() <= 2.0 ** -20 + full.abs() * 2.0 ** -23
+    assert bool((near | (lse == full.float())).all())
+    lim = rdz.abs() * U[dtype] + mag * 2.0 ** -17 + (2.0 ** -25 if dtype == F16 else 1e-37)
+    assert bool(((dz.double() - rdz).abs() <= lim).all())
+    holds = [r for r in range(rows) if r % 8 not in (1, 2, 7)] if dtype != F16 else range(rows)
+    lim = 2.0 ** -19 * tau * tau * (1 + size + full.abs())
+    assert bool(((loss.double() - rl).abs() <= lim)[list(holds)].all())

@@ -36,6 +36,7 @@ constexpr int DISTILL_BATCH = 8;         // vectors a thread has in flight
 constexpr int DISTILL_KEEP = 8;          // most vectors a thread keeps in shared memory (a multiple of the batch)
 constexpr int DISTILL_CLUSTER = 8;       // most blocks that share a row (the portable cluster size)
 constexpr int DISTILL_MAX_K = 1024;
+constexpr float DISTILL_EXTREME = 1073741824.f;   // 2^30, of a row's largest z k
 
 struct DistillArgs {
     const void *z, *t, *ids;
@@ -164,8 +165,7 @@ __device__ __forceinline__ void store_remote(float2* local, int rank, float2 v) 
 }
 
 // A maximum and the sum of 2^(x - it) of several parts, one a lane and step,
-// to those of the whole.  A part whose maximum is -inf has a sum of 0, or of
-// NaN, which is kept (a maximum drops it).
+// to those of the whole.  A NaN is kept in the sums (a maximum drops it).
 __device__ __forceinline__ float2 merge(const float2* part, int n) {
     const int lane = threadIdx.x & 31;
     float m = -INFINITY;
@@ -174,9 +174,43 @@ __device__ __forceinline__ float2 merge(const float2* part, int n) {
     float s = 0.f;
     for (int i = lane; i < n; i += 32) {
         const float2 p = part[i];
-        s += p.x == -INFINITY ? p.y : p.y * exp2f(p.x - m);
+        s += p.y * exp2f(p.x - m);
     }
     return make_float2(m, warp_sum(s));
+}
+
+// A row whose largest |z k| is DISTILL_EXTREME or more (masked with the type's
+// lowest value, say): fp32 does not hold its exponents, but different logits are
+// then at least 2^6 apart, so that a term is 1 where the logit is the largest
+// and below 2^-64 elsewhere.  The row's largest logit (a NaN is kept) and how
+// often it comes; the whole block calls it and walks the whole row, off the path
+// of every other row.
+template <int DT>
+__device__ __noinline__ float2 extreme_row(const void* row, int cols) {
+    __shared__ float part[DISTILL_THREADS / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    float m = -INFINITY;
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) m = max3_nan(m, m, ld1<DT>(row, c));
+    for (int o = 16; o > 0; o >>= 1) {
+        const float v = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+        m = max3_nan(m, m, v);
+    }
+    if (lane == 0) part[warp] = m;
+    __syncthreads();
+    for (int w = 0; w < nw; ++w) m = max3_nan(m, m, part[w]);
+    float n = 0.f;
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) n += ld1<DT>(row, c) == m ? 1.f : 0.f;
+    n = warp_sum(n);
+    __syncthreads();
+    if (lane == 0) part[warp] = n;
+    __syncthreads();
+    n = 0.f;
+    for (int w = 0; w < nw; ++w) n += part[w];
+    return make_float2(m, n);
+}
+// A power of two that brings such a logit to 2^125, so that its product is exact.
+__device__ __forceinline__ float extreme_scale(float top) {
+    return __uint_as_float(min(254u, 379u - (__float_as_uint(top) >> 23 & 255u)) << 23);
 }
 
 // The teacher's parts, one a lane -- a largest logit and the sum of 2^((t - it) k)
@@ -233,13 +267,15 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
         if (have) tmax = fmaxf(tmax, t != t ? 0.f : t);         // a NaN entry makes the sum NaN, not the row empty
     }
     const float k2 = a.k2;
-    const uint64_t kk = pack2(k2, k2);
+    uint64_t kk = pack2(k2, k2);
     // log2 of the teacher's p: with its log-sum-exp, or (own) of the difference to the row's largest logit and not yet
     // divided by the sum, so that a common offset of the logits does not matter
     const bool own = !a.t_lse;
     const float tl = own ? 0.f : a.t_lse[row] * 1.4426950408889634f;
     auto log_term = [&](float t, float top) { return fmaf(t - top, k2, -tl); };      // top: 0 with a log-sum-exp
-    float m = -INFINITY, s = 0.f;                 // this thread's m k and sum
+    // This thread's m k and sum.  m k is not below -DISTILL_EXTREME: far below, what it was rounded by would be an
+    // exponent of its own (a thread with nothing but the type's lowest value), so such logits count for 0 against it.
+    float m = -DISTILL_EXTREME, s = 0.f;
     if constexpr (!BWD) {
         uint64_t s2 = 0;
         auto take = [&](float t) {                // bring the sum to a larger maximum
@@ -249,7 +285,6 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
                 m = t;
             }
         };
-        auto neg = [&] { return m == -INFINITY ? 0.f : -m; };   // nothing but -inf so far: exponents from 0
         int i = first, j = 0;
         for (; i + (U - 1) * step < rv.n; i += U * step, j += U) {
             uint4 r[U];
@@ -266,7 +301,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
 #pragma unroll
             for (int u = 1; u < U; ++u) t = fmaxf(t, R::top(r[u]));
             take(t * k2);
-            const uint64_t nm = pack2(neg(), neg());
+            const uint64_t nm = pack2(-m, -m);
 #pragma unroll
             for (int u = 0; u < U; ++u) s2 = R::sum(r[u], kk, nm, s2);
         }
@@ -274,16 +309,16 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
             const uint4 r = rv.load(i);
             if (j < a.keep) kept[j * T + threadIdx.x] = r;
             take(R::top(r) * k2);
-            s2 = R::sum(r, kk, pack2(neg(), neg()), s2);
+            s2 = R::sum(r, kk, pack2(-m, -m), s2);
         }
         if (edge >= 0) {
             take(edge_z * k2);
-            s2 = add2(s2, pack2(exp2_fast(fmaf(edge_z, k2, neg())), 0.f));
+            s2 = add2(s2, pack2(exp2_fast(fmaf(edge_z, k2, -m)), 0.f));
         }
         const float2 p = unpack2(s2);
         s = p.x + p.y;
         const float wm = warp_max(m);
-        s = warp_sum(m == -INFINITY ? s : s * exp2f(m - wm));
+        s = warp_sum(s * exp2f(m - wm));
         m = wm;
     }
     {
@@ -297,6 +332,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
         if (lane == 0) tpart[warp] = make_float2(tm, ts);
     }
     float mk, total;                              // m k and the sum over the whole row
+    float kz = k2, ztop = 0.f;                    // an extreme row's k and largest logit
     if constexpr (BWD) {
         __syncthreads();
         mk = a.lse_in[row] * 1.4426950408889634f;
@@ -314,8 +350,22 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
             cluster_wait();                        // every pair is here; no block leaves before its last arrives
         }
         const float2 whole = merge(zpart, C * nw);
-        mk = whole.x == -INFINITY ? 0.f : whole.x;
+        mk = whole.x;
         total = whole.y;
+        if (fabsf(whole.x) >= DISTILL_EXTREME) {  // the same in every thread of the cluster
+            const float2 e = extreme_row<DT>(rv.base, rv.cols);
+            if (C > 1) {                          // no block writes a gradient where another still reads
+                cluster_arrive();
+                cluster_wait();
+            }
+            if (fabsf(e.x) < INFINITY) {          // infinities and NaN stay what they are
+                kz = extreme_scale(e.x);
+                kk = pack2(kz, kz);
+                ztop = e.x;
+                mk = ztop * kz;
+                total = e.y;
+            }
+        }
     }
     const float2 tw = merge_teacher(tpart, T >> 5, k2, own);
     const bool none = tw.x == -INFINITY;          // no teacher entry in the row
@@ -324,8 +374,8 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
     const float w = a.w ? a.w[row] : 1.f;
     const bool dead = none || w == 0.f;
     if constexpr (!BWD) {
-        const float lg = log2f(total);
-        if (a.lse && rank == 0 && threadIdx.x == 0) a.lse[row] = (mk + lg) * 0.6931471805599453f;
+        const float lg = log2f(total), zk = ztop == 0.f ? mk : 0.f;       // log2 of q: (z - ztop) k2 - zk - lg
+        if (a.lse && rank == 0 && threadIdx.x == 0) a.lse[row] = ztop / a.temperature + (zk + lg) * 0.6931471805599453f;
         if (a.loss && rank == 0 && warp == 0) {
             const float lt = own ? log2f(tw.y) : 0.f;
             float l = 0.f;
@@ -333,7 +383,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
                 for (int i = lane; i < a.k; i += 32) {
                     const Entry en = entry[i];
                     const float lp = log_term(en.t, tm), p = en.id >= 0 ? exp2f(lp) * pscale : 0.f;
-                    if (p != 0.f) l += p * ((lp - lt) - (fmaf(en.z, k2, -mk) - lg));
+                    if (p != 0.f) l += p * ((lp - lt) - (fmaf(en.z - ztop, k2, -zk) - lg));
                 }
             l = warp_sum(l);
             if (lane == 0) a.loss[row] = dead ? 0.f : l * 0.6931471805599453f * a.temperature * a.temperature * w;
@@ -366,7 +416,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
         for (int u = 0; u < U; ++u) R::grad(dvec + (int64_t)(i + u * step) * 16, al, r[u], kk, nm, gg);
     }
     for (; i < rv.n; i += step) R::grad(dvec + (int64_t)i * 16, al, rv.load_last(i), kk, nm, gg);
-    if (edge >= 0) st1<DT>(drow, edge, g * exp2_fast(fmaf(edge_z, k2, -mk)));
+    if (edge >= 0) st1<DT>(drow, edge, g * exp2_fast(fmaf(edge_z, kz, -mk)));
     // the entries that lie in this block's part, written over after it wrote
     // that: the same id twice gives the same value twice
     __syncthreads();
@@ -376,7 +426,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS, DISTILL_BLOCKS) k_distill(con
         float p = 0.f;
         for (int o = 0; o < a.k; ++o)
             if (entry[o].id == en.id) p += entry[o].p;
-        st1<DT>(drow, en.id, fmaf(g, exp2_fast(fmaf(en.z, k2, -mk)), -coef * p * pscale));
+        st1<DT>(drow, en.id, fmaf(g, exp2_fast(fmaf(en.z, kz, -mk)), -coef * p * pscale));
     }
 }
 
