@@ -309,3 +309,41 @@ def test_eight_bit_output_is_the_quotient_rounded(Z, rows, cols, dtype, block):
             assert torch.equal(torch.where(torch.isnan(got), 0.0, got), torch.where(torch.isnan(ref), 0.0, ref))
         w[cols // 2] = float("inf")
         h[rows // 2], x[rows // 2] = 1, 1                 # 0 times infinity is not a number
+
+
+@pytest.mark.parametrize("rows,cols", [(12000, 1030), (12000, 1032), (5000, 4096), (3000, 8200), (2000, 8199), (1000, 20001)])
+@pytest.mark.parametrize("xt,rt", [(F16, F16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("off", [0, 1])
+def test_blocks_that_walk_many_rows(Z, rows, cols, xt, rt, off):
+    """Several rows a block, none like another: shared memory and the threads' part of dw are used again and again.
+    h over the residual, dx over dh, and an e4m3 y beside the 16-bit one."""
+    g = gen(rows + cols + off)
+    x, r = rnd(g, rows, cols, dtype=xt, off=off), rnd(g, rows, cols, dtype=rt, std=2.0, off=off)
+    r *= torch.exp2(torch.randint(-3, 4, (rows, 1), generator=g, device=DEV).float()).to(rt)
+    w = rnd(g, cols, dtype=xt, off=off) + 1
+    hr, rr, yr = reference(x, r, w, 1e-5)
+    n = -(-cols // 128)
+    y8, scale = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=DEV), torch.empty(rows, n, device=DEV)
+    y, rstd = torch.empty(rows, cols, dtype=xt, device=DEV), torch.empty(rows, device=DEV)
+    Z.zero_norm_forward(x, r, w, rows, cols, 1e-5, None, y8, scale, 128, None)
+    Z.zero_norm_forward(x, r, w, rows, cols, 1e-5, r, y, None, 0, rstd)
+    assert torch.equal(r, hr)
+    near(rstd, rr, U[F32], 0)
+    near(y, yr, U[xt], TINY[xt])
+    q = hr.float() * rstd[:, None] * w.float()
+    b = torch.nn.functional.pad(q, (0, -cols % 128)).view(rows, n, 128)
+    assert torch.equal(scale, b.abs().amax(2).clamp(min=2.0 ** -100) * torch.full_like(scale, 1 / 448))
+    q = (b / scale[:, :, None]).view(rows, -1)[:, :cols].to(torch.float8_e4m3fn)
+    assert torch.equal(y8.view(torch.uint8), q.view(torch.uint8))
+    del y, y8, q, b, yr
+    dy, dh = rnd(g, rows, cols, dtype=xt, off=off), rnd(g, rows, cols, dtype=rt, off=off)
+    xh, gw = hr.double() * rr[:, None], dy.double() * w.double()
+    mean, mag = (gw * xh).mean(1, keepdim=True), (gw * xh).abs().mean(1, keepdim=True)
+    ref = rr[:, None] * (gw - xh * mean) + dh.double()
+    size = rr[:, None] * (gw.abs() + xh.abs() * mag) + dh.double().abs()
+    dw = torch.empty(cols, dtype=F32, device=DEV)
+    ws = torch.empty(Z.zero_norm_workspace_bytes(cols), dtype=torch.uint8, device=DEV)
+    Z.zero_norm_backward(dy, r, w, rows, cols, rstd, dh, dh, dw, 0, ws, ws.numel())
+    near(dh, ref, U[rt], TINY[rt], size * 128 * E)
+    terms = dy.double() * xh
+    near(dw, terms.sum(0), U[F32], TINY[F32], terms.abs().sum(0) * (rows + 96) * E)
