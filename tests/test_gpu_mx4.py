@@ -374,3 +374,43 @@ def test_rows_that_start_anywhere(Z, off, dtype):
         Z.zero_mx4_dequantize(q, out[:, off:off + cols])
         assert torch.equal(out[:, off:off + cols], values(*reference(x), cols).to(dtype))
         assert bool((out[:, :off] == 5).all()) and bool((out[:, off + cols:] == 5).all())
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("rows,cols", [(2000, 7000), (2001, 7001)])
+@pytest.mark.parametrize("off", [0, 1])
+def test_blocks_that_walk_many_tiles(Z, dtype, rows, cols, off):
+    """Several tiles a block and pieces a warp, both ways, along the rows alone, and back."""
+    x = matrix(gen(rows + off), rows, cols, dtype, off)
+    q, t, r = Z.mx4(rows, cols, device=DEV), Z.mx4(cols, rows, device=DEV), Z.mx4(rows, cols, device=DEV)
+    Z.zero_mx4_quantize(x, rows, cols, q, t)
+    Z.zero_mx4_quantize(x, rows, cols, r, None)
+    assert torch.equal(r.buffers[0], q.buffers[0])
+    for m, src in ((q, x), (t, x.t())):
+        code, byte = unpacked(m, *src.shape)
+        rc, rb = reference(src)
+        assert torch.equal(byte, rb) and torch.equal(code, rc)
+        y = torch.empty(src.shape, dtype=dtype, device=DEV)
+        Z.zero_mx4_dequantize(m, y)
+        assert torch.equal(y, values(rc, rb, src.shape[1]).to(dtype))
+
+
+def test_scales_tiled_by_threads_that_walk(Z):
+    rows, cols = 8100, 14400
+    x = torch.randn(rows, cols, generator=gen(20), device=DEV).to(BF16)
+    a, b, c = (Z.mx4(rows, cols, layout=l, device=DEV) for l in (0, 1, 1))
+    c.tensors[1].fill_(0xFF)
+    Z.zero_mx4_quantize(x, rows, cols, a, None)
+    Z.zero_mx4_quantize(x, rows, cols, b, None)
+    Z.zero_mx4_tile_scales(a, c)
+    assert torch.equal(b.tensors[1], c.tensors[1])
+
+
+@pytest.mark.parametrize("m,n,k", [(4096, 4096, 300), (5000, 4100, 96), (3000, 6000, 2500), (10, 70000, 300),
+                                   (40, 70000, 700), (100, 70000, 2100)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_product_of_many_tiles_a_block(Z, m, n, k, dtype):
+    """Four tiles a block and more: each accumulator is used again, overlapping ones too."""
+    g = gen(m + n + k)
+    a, b = torch.randn(m, k, generator=g, device=DEV).to(BF16), torch.randn(n, k, generator=g, device=DEV).to(BF16)
+    product(Z, a, b, dtype)
