@@ -651,7 +651,8 @@ int zero_shard_step_host(const void* const* host_grad_slices, int n_slices, int 
  * allocation, argument errors before any work) and these:
  *  - A matrix is a zero_mat: element (r, c) at data + (r * ld + c) elements.
  *    Any row distance and any alignment to the element is taken; rows that all
- *    start on 16-byte boundaries run with 16-byte accesses.  ld may be
+ *    start on 16-byte boundaries run with 16-byte accesses (in the norm, rows
+ *    of a multiple of 8 columns; others are shifted into place).  ld may be
  *    anything (0 included) when there is at most one row.
  *  - A matrix of no rows or no columns is allowed and gives an empty result:
  *    what has a value for each row (rstd, a row's scale) is not written for

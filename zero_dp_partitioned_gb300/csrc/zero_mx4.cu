@@ -14,8 +14,14 @@
 // come from one read of the matrix.
 //
 // Measured (GB300, 14336 x 4096 bf16; the floor is the bytes at the measured
-// copy bandwidth): rows 28.7 us (floor 21.9), columns 25.6 (21.9), both 40.9
-// (26.5: the two passes' instructions bound it), values back 26.6 (21.9).
+// copy bandwidth): rows 29.5 us (floor 21.9), columns 25.7 (21.9), both 41.0
+// (26.5), values back 26.9 (21.9).  Both ways nothing is near full (DRAM 0.42
+// of its peak, instruction issue 0.58, a third of the warps): the two passes
+// and the stores take turns behind three barriers a tile.  fp32 8192 x 4096:
+// rows 27.5 (22.4), both 36.5 (25.0), back 26.5 (22.4).  Rows that start
+// anywhere are 2.5 to 3.3 times their floor (8192 x 4097 bf16: 33.6, 49.6 and
+// 30.7 us), by the second word of each unit and the shifts.  The tiling of
+// gathered scales takes 4.8 us, about a launch (floor 0.5).
 #include "zero_layer.cuh"
 #include "zero_mx4.cuh"
 

@@ -9,8 +9,9 @@
 // to tensor memory, warp 1's first lane issues the four products of a stage,
 // and warps 2 to 5 read the fp32 accumulator back, scale it and store it.
 //
-// Measured (GB300): 8192 x 14336 x 4096 in 170 us, 5.7 PFLOP/s (2.9 times the
-// measured bf16 rate).  A stage takes 850 cycles: its four products need 512,
+// Measured (GB300): 8192 x 14336 x 4096 in 171 us, 5.6 PFLOP/s (2.9 times the
+// measured bf16 rate).  A stage takes 850 cycles at 1.94 GHz: its four products
+// need 512 (102 us if nothing else took time),
 // and shared memory, from which they read 48 KB and into which the loads write
 // 48 KB, 770 at 128 bytes a cycle.  So the scales go by registers: copied to
 // shared memory by TMA and on by tcgen05.cp, in order with the products, they
@@ -26,8 +27,12 @@
 // X is A, and Y is B, unless A has few rows (tokens, up to 128): then X is B,
 // the weights, so that the 128 rows of a tile are all used, and the accumulator
 // is stored transposed.  Few tiles share their sum over k: clusters of 2 to 8
-// blocks, each with a stretch of k (16 x 4096 x 14336 in 14 us, 22 without; one
-// token through 14336 x 4096 takes 8.3 us, its 31 MB 4.6).
+// blocks, each with a stretch of k (16 x 4096 x 14336 in 14 to 16 us, 22
+// without).  One token through 14336 x 4096 takes 8 to 9 us, its 31 MB 4.6; 128
+// take 16: 112 tiles of 128 rows leave a quarter of the SMs idle, and are too
+// many to share k.  Rows a multiple of 128 bytes apart are the fast ones: 4096 x
+// 4104 x 4104 takes 51 us where 4096 of each takes 34, and an n that is no
+// multiple of 8 costs the wide stores (4096 x 4097 x 4096: 82).
 //
 // Every wait is bounded.  A block whose wait runs out sets bit 0 of *status,
 // its roles stop, what they have in flight is waited for (bounded again), the

@@ -13,14 +13,24 @@
 // walk rows: the next rows are on their way to shared memory meanwhile, and a
 // thread's columns, weights and part of dw are the same in every row.
 //
-// Measured (GB300, bf16): forward 8192 x 4096 in 43 us, 6.2 TB/s (0.92 of the
+// Measured (GB300, bf16): forward 8192 x 4096 in 43 us, 6.3 TB/s (0.92 of the
 // measured copy bandwidth); with an e4m3 output and a scale per 128 columns
-// 16384 x 4096 in 74 us, 6.4 TB/s (0.94); backward 8192 x 4096 in 49 us
-// without dw, 5.5 TB/s (0.80; 512 threads a multiprocessor fill its registers,
-// and each row waits for the block's sum), 53 us with it.  Loading a row when
-// its turn comes took 46 and 80 us, rows ahead in registers no less (fewer
-// threads fit); one row in threads of 8 columns with fp32 arithmetic one
-// element at a time was bound by its instructions (29 an element).
+// 16384 x 4096 in 74 us, 6.4 TB/s (0.94), a scale per row 73; backward 8192 x
+// 4096 in 51 us without dw, 5.3 TB/s (0.78; 512 threads a multiprocessor fill
+// its registers, and each row waits for the block's sum), 55 us with it.
+// Loading a row when its turn comes took 46 and 80 us, rows ahead in registers
+// no less (fewer threads fit); one row in threads of 8 columns with fp32
+// arithmetic one element at a time was bound by its instructions (29 an element).
+//
+// Further from the copy bandwidth: fp32 rows (8192 x 4096 in 116 and 138 us,
+// 0.68 and 0.57: each lane's 32 bytes are moved as two accesses of 16, half of
+// every sector an access touches), widths that are not a multiple of 8 or rows
+// that start anywhere (8192 x 4097 bf16 in 109 and 121 us, 0.36 and 0.33: the
+// shifts and one more barrier a row), and backward rows of 8193 to 16384
+// columns, whose four units a thread do not fit its registers (320 to 568 bytes
+// a thread go to local memory; 4096 x 12288 bf16 in 115 us, 0.51).  fp32 rows of
+// that length, and all longer ones, are walked twice (4096 x 12288 fp32 in 214
+// us, 0.55; 2048 x 20480 bf16 in 163, 0.30).
 #include "zero_layer.cuh"
 
 namespace zdp {
@@ -29,11 +39,14 @@ constexpr int NORM_THREADS = 512;       // most threads that share a row
 constexpr int64_t NORM_MAX_COLS = 1 << 20;
 constexpr int NORM_MAX_STAGES = 4;      // rows a thread has on their way or at hand
 constexpr int NORM_SM_SMEM = 216 * 1024;
-constexpr int NORM_FORWARD_THREADS = 1536, NORM_BACKWARD_THREADS = 512;   // of a multiprocessor, walking rows
-// Blocks launched for each that runs at once: in the forward pass SMs that are
-// done early take the rows of others (16384 x 4096 e4m3 73 against 79 us; the
-// backward pass, whose blocks each leave a partial dw, gains nothing).
-constexpr int NORM_FORWARD_OVER = 2, NORM_BACKWARD_OVER = 1;
+// Threads a multiprocessor that the grid and the stages are made for.  Of the
+// forward pass registers let 1024 run at once (64 each, 16-bit rows of up to
+// 8192 columns) or 512 (101 to 128: fp32, wider rows); with half as many again,
+// and twice the blocks that gives, SMs that are done early take the rows of
+// others (16384 x 4096 e4m3 73 us, 79 with once as many).  The backward pass,
+// whose blocks each leave a partial dw, gains nothing from more than run.
+constexpr int NORM_FORWARD_THREADS = 1536, NORM_BACKWARD_THREADS = 512;
+constexpr int NORM_FORWARD_OVER = 2;
 constexpr int NORM_MAX_GRID = 608;      // blocks of the backward pass, each with a partial dw
 constexpr float E4M3_MAX = 448.f;
 constexpr float SCALE_FLOOR = 7.888609052210118e-31f;   // 2^-100: a zero row still has a usable scale
@@ -832,7 +845,7 @@ int zero_norm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* we
     a.stages = p.stages;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* args[] = {&a};
-    int64_t g = (int64_t)p.per_sm * sms * NORM_BACKWARD_OVER;
+    int64_t g = (int64_t)p.per_sm * sms;
     if (g > NORM_MAX_GRID) g = NORM_MAX_GRID;
     if (g > rows) g = rows;
     const void* f = norm_fn(false, dy->dtype, rt, v8, p.nv);
