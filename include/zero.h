@@ -808,6 +808,81 @@ int zero_mx4_tile_scales(const zero_mx4* src, const zero_mx4* dst, void* stream)
  * columns), ZERO_ECUDA. */
 int zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, float alpha, const zero_mat* d, int32_t* status, void* stream);
 
+/* Dropout whose mask is never stored.  Element (r, c) of a rows x cols matrix is
+ * kept if the 16-bit half c % 8 of Philox4x32-10's four words (word c % 8 / 2, the
+ * low half first) is at least p in units of 2^-16, rounded to nearest; what is
+ * kept is scaled by the inverse of the probability of that.  The key is the seed
+ * (its low word first), the counter (unit's low word, its high word, site, step),
+ * unit = r ceil(cols / 8) + c / 8.  The same zero_drop and sizes give the same
+ * mask in the forward and in the backward pass, whatever the row distances.
+ * seed     of the run (and rank: ranks with different data want different ones)
+ * site     which dropout of the model; two that share it drop the same elements
+ * p        0 .. 1; below 2^-17 nothing is dropped, from 1 - 2^-17 all is
+ * chain    not NULL: the low word of chain->step, read on the device when the
+ *          kernel runs, so that a captured step draws a new mask each time it is
+ *          replayed and a skipped one keeps its mask; `step` is then not used */
+typedef struct {
+    uint64_t seed;
+    uint32_t site;
+    float p;
+    int64_t step;
+    const zero_chain* chain;
+} zero_drop;
+
+/* y = dropout(x) + residual, rows x cols; the gradient of x is the same call on
+ * dy without a residual.
+ * x, y       ZERO_F16, ZERO_BF16 or ZERO_F32, all of one type; y may be x or
+ *            residual
+ * residual   NULL: none
+ * What is dropped counts for nothing, an infinity or NaN too.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ELIMIT (2^59 elements), ZERO_ECUDA. */
+int zero_dropout(const zero_mat* x, const zero_mat* residual, int64_t rows, int64_t cols, const zero_drop* drop,
+                 const zero_mat* y, void* stream);
+
+/* Layer norm of a residual stream, behind the dropout of what is added to it.
+ *   h = round(dropout(x) + residual);  m = mean(h);  rstd = 1 / sqrt(mean((h - m)^2) + eps)
+ *   y = (h - m) rstd weight + bias
+ * per row, the norm of h as it is stored.
+ * x          rows x cols, ZERO_F16, ZERO_BF16 or ZERO_F32
+ * residual   the same, or ZERO_F32; NULL: none
+ * drop       NULL: no dropout
+ * weight, bias   cols values each (fp16, bf16 or fp32); NULL: 1 and 0
+ * h_out      in the residual's type (x's without one); NULL: not stored; may be
+ *            residual or x
+ * y          in x's type
+ * mean, rstd rows values each; NULL: not stored
+ * The squares are taken about the mean, so a row far off zero keeps its
+ * variance.  Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ELIMIT (more than 1048576
+ * columns), ZERO_ECUDA. */
+int zero_layernorm_forward(const zero_mat* x, const zero_mat* residual, const zero_drop* drop, const zero_mat* weight,
+                           const zero_mat* bias, int64_t rows, int64_t cols, float eps, const zero_mat* h_out,
+                           const zero_mat* y, float* mean, float* rstd, void* stream);
+
+/* Its backward pass, with xh = (h - m) rstd and g = dy weight:
+ *   dr = rstd (g - mean(g) - xh mean(g xh)) + dh    the gradient of residual
+ *   dx = dropout(dr)                                the gradient of x
+ *   dw = sum over rows of dy xh,  db = sum over rows of dy
+ * dy         the gradient of y (ZERO_F16, ZERO_BF16, ZERO_F32)
+ * h, mean, rstd   from the forward pass; h in dy's type or ZERO_F32
+ * dh         the gradient that reaches h by the residual stream, in h's type;
+ *            NULL: none
+ * drop       as in the forward pass (NULL: dx is dr, in dy's type)
+ * dr         in h's type; may be dy (of the same type) or dh; NULL: not wanted
+ * dx         in dy's type; may be dy or dh (of the same type); NULL: not wanted;
+ *            one of dr and dx is
+ * dw, db     cols values each (fp16, bf16 or fp32, e.g. in a gradient bucket);
+ *            NULL: not wanted; accumulate nonzero: added to what is there, in
+ *            fp32, and rounded once
+ * workspace  zero_layernorm_workspace_bytes(cols) bytes, 4-byte aligned,
+ *            contents irrelevant (NULL if dw and db are)
+ * With no rows dw and db are 0 (or unchanged).  Errors as
+ * zero_layernorm_forward, and ZERO_EWORKSPACE. */
+int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* weight, int64_t rows, int64_t cols,
+                            const float* mean, const float* rstd, const zero_mat* dh, const zero_drop* drop,
+                            const zero_mat* dr, const zero_mat* dx, const zero_mat* dw, const zero_mat* db, int accumulate,
+                            void* workspace, size_t workspace_bytes, void* stream);
+size_t zero_layernorm_workspace_bytes(int64_t cols);
+
 /* Message of the last error on this thread ("" if none). */
 const char* zero_last_error(void);
 

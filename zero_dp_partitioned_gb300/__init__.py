@@ -87,6 +87,13 @@ class zero_mx4(ctypes.Structure):
         return (data, scales) if n is None else (data[:n], data[n:])
 
 
+class zero_drop(ctypes.Structure):
+    _fields_ = [("seed", ctypes.c_uint64), ("site", ctypes.c_uint32), ("p", ctypes.c_float), ("step", ctypes.c_int64),
+                ("chain", ctypes.c_void_p)]
+    device = None                          # of the chain's tensor, None: an address or none
+
+
+assert ctypes.sizeof(zero_drop) == 32
 assert ctypes.sizeof(zero_mat) == 24 and ctypes.sizeof(zero_mx4) == 48
 assert ctypes.sizeof(zero_hyper) == 32 and ctypes.sizeof(zero_shard) == 80
 assert ctypes.sizeof(zero_stats) == 16 and ctypes.sizeof(zero_result) == 48 and ctypes.sizeof(zero_chain) == 56
@@ -133,6 +140,11 @@ _SIGS = {
     "zero_mx4_dequantize": (_I, [_P, _P, _P]),
     "zero_mx4_tile_scales": (_I, [_P, _P, _P]),
     "zero_mx4_matmul": (_I, [_P, _P, ctypes.c_float, _P, _P, _P]),
+    "zero_dropout": (_I, [_P, _P, _I64, _I64, _P, _P, _P]),
+    "zero_layernorm_forward": (_I, [_P, _P, _P, _P, _P, _I64, _I64, ctypes.c_float, _P, _P, _P, _P, _P]),
+    "zero_layernorm_backward": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, ctypes.c_size_t,
+                                     _P]),
+    "zero_layernorm_workspace_bytes": (ctypes.c_size_t, [_I64]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
 # every symbol include/zero.h declares
@@ -637,3 +649,54 @@ def zero_mx4_matmul(a, b, alpha, d, status, stream=None):
     the caller), bit 0 set if a wait ran out."""
     m = None if a is None or b is None else _mat(d, a.rows, b.rows, "d")
     _check(lib.zero_mx4_matmul(_mx4(a, "a"), _mx4(b, "b"), alpha, m, _buf(status, 4, "status"), _stream(stream)))
+
+
+def drop(p, seed, site=0, step=0, chain_dev=None) -> zero_drop:
+    """A dropout: the probability of dropping, the run's 64-bit seed, the place in
+    the model, and the step, or the device zero_chain whose step is taken when
+    the kernel runs."""
+    d = zero_drop(int(seed) & 0xFFFFFFFFFFFFFFFF, int(site) & 0xFFFFFFFF, p, int(step),
+                  _buf(chain_dev, ctypes.sizeof(zero_chain), "chain_dev"))
+    if hasattr(chain_dev, "data_ptr"):
+        d.tensor = chain_dev               # kept alive with the argument
+        d.device = chain_dev.get_device()
+    return d
+
+
+def _drop(d):
+    if d is None:
+        return None
+    if d.device is not None and _gpus != 1 and d.device != _current_device():
+        _elsewhere(d.device, "drop's chain")
+    return ctypes.byref(d)
+
+
+def zero_dropout(x, residual, rows, cols, drop, y, stream=None):
+    """y = dropout(x) + residual; the gradient of x is the same call on dy."""
+    _check(lib.zero_dropout(_mat(x, rows, cols, "x"), _mat(residual, rows, cols, "residual"), rows, cols, _drop(drop),
+                            _mat(y, rows, cols, "y"), _stream(stream)))
+
+
+def zero_layernorm_forward(x, residual, drop, weight, bias, rows, cols, eps, h_out, y, mean, rstd, stream=None):
+    """h = dropout(x) + residual, y = layernorm(h) * weight + bias per row."""
+    _check(lib.zero_layernorm_forward(_mat(x, rows, cols, "x"), _mat(residual, rows, cols, "residual"), _drop(drop),
+                                      _mat(weight, 1, cols, "weight"), _mat(bias, 1, cols, "bias"), rows, cols, eps,
+                                      _mat(h_out, rows, cols, "h_out"), _mat(y, rows, cols, "y"),
+                                      _vec(mean, rows, "mean"), _vec(rstd, rows, "rstd"), _stream(stream)))
+
+
+def zero_layernorm_workspace_bytes(cols):
+    return lib.zero_layernorm_workspace_bytes(cols)
+
+
+def zero_layernorm_backward(dy, h, weight, rows, cols, mean, rstd, dh, drop, dr, dx, dw, db, accumulate, workspace,
+                            workspace_bytes, stream=None):
+    """dr (of the residual), dx (of x, behind the dropout), dw and db of
+    zero_layernorm_forward."""
+    _check(lib.zero_layernorm_backward(_mat(dy, rows, cols, "dy"), _mat(h, rows, cols, "h"),
+                                       _mat(weight, 1, cols, "weight"), rows, cols, _vec(mean, rows, "mean"),
+                                       _vec(rstd, rows, "rstd"), _mat(dh, rows, cols, "dh"), _drop(drop),
+                                       _mat(dr, rows, cols, "dr"), _mat(dx, rows, cols, "dx"), _mat(dw, 1, cols, "dw"),
+                                       _mat(db, 1, cols, "db"), int(accumulate),
+                                       _buf(workspace, workspace_bytes, "workspace", ZERO_EWORKSPACE),
+                                       workspace_bytes, _stream(stream)))

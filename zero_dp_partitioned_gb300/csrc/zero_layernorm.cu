@@ -1,0 +1,322 @@
+// zero_layernorm.cu -- the layer norm behind a residual's dropout, forward.
+//
+//   h = round(dropout(x) + r)      (r and h in x's type, or both in fp32)
+//   y = (h - m) rstd w + b,  m = mean(h),  rstd = 1 / sqrt(mean((h - m)^2) + eps)
+//
+// Bound: HBM (x and r read, h and y written: 8 bytes an element in 16 bits).  A
+// row is read once and kept in registers, as in the RMS norm (zero_norm.cu),
+// whose blocks that stay and rows on their way to shared memory it shares.
+//
+// The mean and the squares about it come with one barrier: a warp takes the
+// mean of its own columns, then the squares about that mean from its registers,
+// and the warps' (count, mean, squares) are joined by
+//   M2 = sum M2_w + sum n_w (m_w - m)^2
+// (T. Chan, G. Golub, R. LeVeque, Algorithms for computing the sample
+// variance, 1983), so that a row far off zero loses nothing to cancellation.
+#include "zero_layernorm.cuh"
+
+namespace zdp {
+
+constexpr int LN_FORWARD_THREADS = 1536;    // a multiprocessor, for the grid and the stages
+constexpr int LN_FORWARD_OVER = 2;
+
+// What a block keeps of its warps: the columns of each, and, in two sets used by
+// turns, mean and squares.
+struct WarpStats {
+    float n[32];
+    float2 s[2][32];
+};
+
+// valid columns of this warp's units
+__device__ __forceinline__ int warp_columns(int cols, int nv) {
+    int n = 0;
+    for (int j = 0; j < nv; ++j) {
+        const int c = ((int)(threadIdx.x & ~31u) + j * (int)blockDim.x) * 8;
+        n += max(0, min(256, cols - c));
+    }
+    return n;
+}
+
+// WT: the type in which weight and bias stay in registers, x's where they are of
+// it (half the registers, and with them twice the threads) or fp32.
+template <int XT, int RT, int WT, bool V8, int NV>
+__global__ void __launch_bounds__(NORM_THREADS, NV == 2 && RT != ZERO_F32 && WT != ZERO_F32 ? 2 : 1)
+    k_layernorm_forward(const __grid_constant__ LayerNormArgs a) {
+    constexpr int E = Map::E;
+    __shared__ __align__(16) WarpStats st;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int mine = warp_columns(a.cols, NV);
+    const float inv_mine = mine ? 1.f / (float)mine : 0.f;
+    if (lane == 0) st.n[warp] = (float)mine;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_next();
+    const uint32_t step = drop_step(a.drop);
+    const float inv_n = 1.f / (float)a.cols;
+    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols);
+    extern __shared__ __align__(16) uint4 ring[];
+    using X = Slots<XT, NV, V8>;
+    using R = Slots<RT, NV, V8>;
+    const int S = a.stages, stage_words = X::words() + R::words();
+    auto copy = [&](int64_t row, int at_stage) {
+        if (row < a.rows) {
+            uint4* at = ring + at_stage * stage_words;
+            X{at}.copy(row_of<XT>(a.x, a.ldx, row), a.cols, ex);
+            if (a.r) R{at + X::words()}.copy(row_of<RT>(a.r, a.ldr, row), a.cols, er);
+        }
+        copies_commit();
+    };
+    for (int s = 0; s < S - 1; ++s) copy(blockIdx.x + (int64_t)s * gridDim.x, s);
+    Raw8<WT> w[NV], b[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        float v[E];
+        vector8(a.w, a.wdt, a.w_aligned, a.cols, Map::unit(j), 1.f, v);
+        w[j] = narrow8<WT>(v);
+        vector8(a.b, a.bdt, a.b_aligned, a.cols, Map::unit(j), 0.f, v);
+        b[j] = narrow8<WT>(v);
+    }
+    int turn = 0, at_stage = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        Unit<XT, V8> x[NV];
+        Unit<RT, V8> r[NV];
+        copy(row + (int64_t)(S - 1) * gridDim.x, at_stage == 0 ? S - 1 : at_stage - 1);
+        copies_wait_all_but(S - 1);
+        if (!V8) __syncthreads();
+        uint4* at = ring + at_stage * stage_words;
+        X{at}.read(x, row_of<XT>(a.x, a.ldx, row), a.cols);
+        if (a.r) R{at + X::words()}.read(r, row_of<RT>(a.r, a.ldr, row), a.cols);
+        at_stage = at_stage == S - 1 ? 0 : at_stage + 1;
+        // h as it is stored
+        uint64_t s2 = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            r[j] = a.drop.on ? drop_add_unit<XT, RT, V8>(x[j], r[j], a.r != nullptr, a.drop, step, row * a.units + Map::unit(j))
+                             : add_unit<XT, RT, V8>(x[j], r[j], a.r != nullptr);
+#pragma unroll
+            for (int q = 0; q < E / 2; ++q) s2 = add2(s2, r[j].pair(q));
+            if (a.h) r[j].store(row_of<RT>(a.h, a.ldh, row), Map::unit(j), a.cols);
+        }
+        const float2 sp = unpack2(s2);
+        const float mw = warp_sum(sp.x + sp.y) * inv_mine;
+        const uint64_t mw2 = pack2(-mw, -mw);
+        uint64_t v2 = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int left = a.cols - Map::unit(j) * 8;
+#pragma unroll
+            for (int q = 0; q < E / 2; ++q) {
+                uint64_t d = add2(r[j].pair(q), mw2);
+                if (V8) {
+                    if (left <= 0) d = 0;
+                } else {
+                    const float2 p = unpack2(d);
+                    d = pack2(2 * q < left ? p.x : 0.f, 2 * q + 1 < left ? p.y : 0.f);
+                }
+                v2 = fma2(d, d, v2);
+            }
+        }
+        const float2 vp = unpack2(v2);
+        float m2 = warp_sum(vp.x + vp.y), mean = mw;
+        if (warps > 1) {
+            if (lane == 0) st.s[turn][warp] = make_float2(mw, m2);
+            __syncthreads();
+            float sum = 0.f;
+            for (int k = 0; k < warps; ++k) sum = fmaf(st.n[k], st.s[turn][k].x, sum);
+            mean = sum * inv_n;
+            m2 = 0.f;
+            for (int k = 0; k < warps; ++k) {
+                const float2 p = st.s[turn][k];
+                const float d = p.x - mean;
+                m2 += fmaf(st.n[k] * d, d, p.y);
+            }
+        }
+        const float rstd = rsqrtf(fmaf(m2, inv_n, a.eps));
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        const uint64_t mm = pack2(-mean, -mean), rr = pack2(rstd, rstd);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float y[E];
+#pragma unroll
+            for (int q = 0; q < E / 2; ++q) {
+                const float2 v = unpack2(fma2(mul2(add2(r[j].pair(q), mm), rr), pair8<WT>(w[j], q), pair8<WT>(b[j], q)));
+                y[2 * q] = v.x;
+                y[2 * q + 1] = v.y;
+            }
+            store_unit<XT, V8>(row_of<XT>(a.y, a.ldy, row), Map::unit(j), a.cols, y);
+        }
+    }
+}
+
+// A row too long for the registers: the block walks it for the sum (storing h,
+// if it is wanted), for the squares and for the output, after the first time
+// from L2.
+template <int XT, int RT, bool V8>
+__global__ void __launch_bounds__(NORM_THREADS) k_layernorm_forward_long(const __grid_constant__ LayerNormArgs a) {
+    constexpr int E = Map::E;
+    __shared__ __align__(16) float ssum[2][32];
+    if (threadIdx.x < 64) ssum[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_next();
+    const uint32_t step = drop_step(a.drop);
+    const float inv_n = 1.f / (float)a.cols;
+    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols),
+                 eh = extent_of<RT>(a.h, a.ldh, a.rows, a.cols);
+    const int steps = (a.units + (int)blockDim.x - 1) / (int)blockDim.x;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const void* X = row_of<XT>(a.x, a.ldx, row);
+        const void* R = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
+        void* H = a.h ? row_of<RT>(a.h, a.ldh, row) : nullptr;
+        auto first = [&](int u) {
+            Unit<XT, V8> x;
+            Unit<RT, V8> r;
+            x.load(X, u, a.cols, ex);
+            if (R) r.load(R, u, a.cols, er);
+            return a.drop.on ? drop_add_unit<XT, RT, V8>(x, r, R != nullptr, a.drop, step, row * a.units + u)
+                             : add_unit<XT, RT, V8>(x, r, R != nullptr);
+        };
+        auto again = [&](int u, float (&h)[E]) {      // after h was stored, over x or r perhaps
+            if (H) {
+                Unit<RT, V8> s;
+                s.load(H, u, a.cols, eh);
+                s.values(h);
+            } else {
+                first(u).values(h);
+            }
+        };
+        float sum = 0.f;
+        for (int j = 0; j < steps; ++j) {
+            const int u = threadIdx.x + j * blockDim.x;
+            const Unit<RT, V8> s = first(u);
+            float h[E];
+            s.values(h);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (u * 8 + e < a.cols) sum += h[e];
+            if (H) s.store(H, u, a.cols);
+        }
+        const float mean = block_sum(sum, ssum[0]) * inv_n;
+        float m2 = 0.f;
+        for (int j = 0; j < steps; ++j) {
+            const int u = threadIdx.x + j * blockDim.x;
+            float h[E];
+            again(u, h);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (u * 8 + e < a.cols) m2 = fmaf(h[e] - mean, h[e] - mean, m2);
+        }
+        const float rstd = rsqrtf(fmaf(block_sum(m2, ssum[1]), inv_n, a.eps));
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        for (int j = 0; j < steps; ++j) {
+            const int u = threadIdx.x + j * blockDim.x;
+            float h[E], w[E], b[E];
+            again(u, h);
+            vector8(a.w, a.wdt, a.w_aligned, a.cols, u, 1.f, w);
+            vector8(a.b, a.bdt, a.b_aligned, a.cols, u, 0.f, b);
+#pragma unroll
+            for (int e = 0; e < E; ++e) h[e] = fmaf((h[e] - mean) * rstd, w[e], b[e]);
+            store_unit<XT, V8>(row_of<XT>(a.y, a.ldy, row), u, a.cols, h);
+        }
+    }
+}
+
+// w16: V8, and weight and bias in x's type.
+template <int XT, int RT>
+static const void* pick(bool v8, bool w16, int nv) {
+    switch (nv) {
+        case 2:
+            if (w16) return (const void*)k_layernorm_forward<XT, RT, XT, true, 2>;
+            return v8 ? (const void*)k_layernorm_forward<XT, RT, ZERO_F32, true, 2>
+                      : (const void*)k_layernorm_forward<XT, RT, ZERO_F32, false, 2>;
+        case 4:
+            if (w16) return (const void*)k_layernorm_forward<XT, RT, XT, true, 4>;
+            return v8 ? (const void*)k_layernorm_forward<XT, RT, ZERO_F32, true, 4>
+                      : (const void*)k_layernorm_forward<XT, RT, ZERO_F32, false, 4>;
+        default:
+            return v8 ? (const void*)k_layernorm_forward_long<XT, RT, true>
+                      : (const void*)k_layernorm_forward_long<XT, RT, false>;
+    }
+}
+static const void* layernorm_forward_fn(int xt, int rt, bool v8, bool w16, int nv) {
+    if (xt == ZERO_F32) return pick<ZERO_F32, ZERO_F32>(v8, w16, nv);
+    if (xt == ZERO_BF16)
+        return rt == ZERO_F32 ? pick<ZERO_BF16, ZERO_F32>(v8, w16, nv) : pick<ZERO_BF16, ZERO_BF16>(v8, w16, nv);
+    return rt == ZERO_F32 ? pick<ZERO_F16, ZERO_F32>(v8, w16, nv) : pick<ZERO_F16, ZERO_F16>(v8, w16, nv);
+}
+
+}  // namespace zdp
+
+using namespace zdp;
+
+extern "C" int zero_layernorm_forward(const zero_mat* x, const zero_mat* residual, const zero_drop* drop,
+                                      const zero_mat* weight, const zero_mat* bias, int64_t rows, int64_t cols, float eps,
+                                      const zero_mat* h_out, const zero_mat* y, float* mean, float* rstd, void* stream) {
+    const char* me = "zero_layernorm_forward";
+    if (rows < 0 || cols < 0) return fail(ZERO_EINVAL, "zero_layernorm_forward: negative rows or cols");
+    if (cols > NORM_MAX_COLS) return fail(ZERO_ELIMIT, "zero_layernorm_forward: more than 1048576 columns");
+    if (!(eps >= 0.f) || !(eps < INFINITY)) return fail(ZERO_EINVAL, "zero_layernorm_forward: eps must be finite and >= 0");
+    int rc = check_mat(x, rows, cols, FLOAT_TYPES, me, "x");
+    if (rc == ZERO_OK) rc = check_mat(y, rows, cols, FLOAT_TYPES, me, "y");
+    if (rc == ZERO_OK && residual) rc = check_mat(residual, rows, cols, FLOAT_TYPES, me, "residual");
+    if (rc == ZERO_OK && h_out) rc = check_mat(h_out, rows, cols, FLOAT_TYPES, me, "h_out");
+    if (rc == ZERO_OK && weight) rc = check_mat(weight, 1, cols, FLOAT_TYPES, me, "weight");
+    if (rc == ZERO_OK && bias) rc = check_mat(bias, 1, cols, FLOAT_TYPES, me, "bias");
+    if (rc != ZERO_OK) return rc;
+    const int rt = residual ? residual->dtype : x->dtype;
+    if (rt != x->dtype && rt != ZERO_F32)
+        return fail(ZERO_EINVAL, "zero_layernorm_forward: the residual is in x's type or fp32");
+    if (h_out && h_out->dtype != rt)
+        return fail(ZERO_EINVAL, "zero_layernorm_forward: h_out is in the residual's type (x's without one)");
+    if (y->dtype != x->dtype) return fail(ZERO_EINVAL, "zero_layernorm_forward: y is in x's type");
+    if (!aligned(mean, 4) || !aligned(rstd, 4))
+        return fail(ZERO_EALIGN, "zero_layernorm_forward: mean or rstd not 4-byte aligned");
+    LayerNormArgs a = {};
+    rc = check_drop(drop, a.drop, me);
+    if (rc != ZERO_OK || rows == 0 || cols == 0) return rc;
+    a.x = x->data;
+    a.ldx = x->ld;
+    a.r = residual ? residual->data : nullptr;
+    a.ldr = residual ? residual->ld : 0;
+    a.h = h_out ? h_out->data : nullptr;
+    a.ldh = h_out ? h_out->ld : 0;
+    a.y = y->data;
+    a.ldy = y->ld;
+    if (weight) {
+        a.w = weight->data;
+        a.wdt = weight->dtype;
+        a.w_aligned = aligned(weight->data, 16);
+    }
+    if (bias) {
+        a.b = bias->data;
+        a.bdt = bias->dtype;
+        a.b_aligned = aligned(bias->data, 16);
+    }
+    a.rows = rows;
+    a.cols = (int)cols;
+    a.units = (int)((cols + 7) / 8);
+    a.eps = eps;
+    a.mean = mean;
+    a.rstd = rstd;
+    const bool v8 = cols % 8 == 0 && rows_aligned(*x, rows) && rows_aligned(*y, rows) &&
+                    (!residual || rows_aligned(*residual, rows)) && (!h_out || rows_aligned(*h_out, rows));
+    const NormShape p = shape_of(cols, words_of(x->dtype) + words_of(rt), LN_FORWARD_THREADS);
+    a.stages = p.stages;
+    const int sms = sm_count();
+    if (!sms) return ZERO_ECUDA;
+    const bool w16 = v8 && (!weight || weight->dtype == x->dtype) && (!bias || bias->dtype == x->dtype);
+    const void* f = layernorm_forward_fn(x->dtype, rt, v8, w16, p.nv);
+    rc = raise_smem(f, p.smem, "zero_layernorm_forward shared-memory size");
+    if (rc != ZERO_OK) return rc;
+    const int64_t most = (int64_t)sms * p.per_sm * LN_FORWARD_OVER;
+    void* args[] = {&a};
+    return cuda_fail(launch_after_previous(f, (int)(rows < most ? rows : most), p.threads, args, p.smem,
+                                           static_cast<cudaStream_t>(stream)),
+                     "zero_layernorm_forward launch");
+}

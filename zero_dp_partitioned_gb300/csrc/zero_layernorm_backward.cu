@@ -1,0 +1,410 @@
+// zero_layernorm_backward.cu -- the layer norm's gradients, with the sums over
+// the rows for its weight and bias, and the gradient behind the dropout.
+//
+// With xh = (h - m) rstd and g = dy w:
+//   dr = rstd (g - mean(g) - xh mean(g xh)) + dh     (of h, and so of r)
+//   dx = dropout(dr)                                 (of x, by the forward's mask)
+//   dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// Bound: HBM (dy, h and dh read, dr and dx written).  As in the RMS norm's
+// backward pass (zero_norm.cu) a block walks rows, a thread owns the same
+// columns of all of them, and its parts of dw and db stay in registers and are
+// written once a block; k_layernorm_sums adds the blocks' parts in order.
+#include "zero_layernorm.cuh"
+
+namespace zdp {
+
+constexpr int LN_BACKWARD_THREADS = 512;    // a multiprocessor: what the registers let run
+
+// Sums of two values over the block, the same in every thread and every run.
+// s: 32 pairs that no call in flight uses, zero beyond the block's warps.
+__device__ __forceinline__ float2 block_sum2(float x, float y, float2* s) {
+    x = warp_sum(x);
+    y = warp_sum(y);
+    if (blockDim.x <= 32) return make_float2(x, y);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(x, y);
+    __syncthreads();
+    const int n2 = (blockDim.x + 63) >> 6;
+    float tx = 0.f, ty = 0.f;
+    for (int w = 0; w < n2; ++w) {
+        const float4 p = reinterpret_cast<const float4*>(s)[w];
+        tx += p.x + p.z;
+        ty += p.y + p.w;
+    }
+    return make_float2(tx, ty);
+}
+
+// The gradient of one unit stored: of r as it is, of x by the forward's mask.
+template <int XT, int RT, bool V8>
+__device__ __forceinline__ void store_gradients(const LayerNormArgs& a, uint32_t step, int64_t row, int u, float (&v)[8]) {
+    if (a.y) store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), u, a.cols, v);
+    if (!a.h) return;
+    if (a.drop.on) {
+        const uint4 bits = drop_bits(a.drop, step, row * a.units + u);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t w = word_of(bits, q);
+            v[2 * q] = kept_low(w, a.drop.above) ? v[2 * q] * a.drop.scale : 0.f;
+            v[2 * q + 1] = kept_high(w, a.drop.above) ? v[2 * q + 1] * a.drop.scale : 0.f;
+        }
+    }
+    store_unit<XT, V8>(row_of<XT>(a.h, a.ldh, row), u, a.cols, v);
+}
+
+// WT: the type in which the weight stays in registers, dy's where it is of it, or fp32.
+template <int XT, int RT, int WT, bool V8, int NV>
+__global__ void __launch_bounds__(NORM_THREADS, 1) k_layernorm_backward(const __grid_constant__ LayerNormArgs a) {
+    constexpr int E = Map::E;
+    __shared__ __align__(16) float2 ssum[2][32];
+    if (threadIdx.x < 64) ssum[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.f, 0.f);
+    if (blockDim.x < 64 && threadIdx.x < 32) ssum[1][threadIdx.x] = make_float2(0.f, 0.f);
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_next();
+    const uint32_t step = drop_step(a.drop);
+    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols),
+                 eh = extent_of<RT>(a.hin, a.ldhin, a.rows, a.cols);
+    uint64_t dw[NV][E / 2] = {}, db[NV][E / 2] = {};
+    const float inv_n = 1.f / (float)a.cols;
+    extern __shared__ __align__(16) uint4 ring[];
+    using X = Slots<XT, NV, V8>;
+    using R = Slots<RT, NV, V8>;
+    const int S = a.stages, stage_words = X::words() + 2 * R::words();
+    const bool DH = a.r != nullptr;
+    auto copy = [&](int64_t row, int st) {
+        if (row < a.rows) {
+            uint4* at = ring + st * stage_words;
+            X{at}.copy(row_of<XT>(a.x, a.ldx, row), a.cols, ex);
+            R{at + X::words()}.copy(row_of<RT>(a.hin, a.ldhin, row), a.cols, eh);
+            if (DH) R{at + X::words() + R::words()}.copy(row_of<RT>(a.r, a.ldr, row), a.cols, er);
+        }
+        copies_commit();
+    };
+    for (int st = 0; st < S - 1; ++st) copy(blockIdx.x + (int64_t)st * gridDim.x, st);
+    Raw8<WT> w[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        float v[E];
+        vector8(a.w, a.wdt, a.w_aligned, a.cols, Map::unit(j), 1.f, v);
+        w[j] = narrow8<WT>(v);
+    }
+    int turn = 0, st = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const float rstd = a.rstd[row], mean = a.mean[row];
+        Unit<XT, V8> dy[NV];
+        Unit<RT, V8> h[NV], dh[NV];
+        copy(row + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
+        copies_wait_all_but(S - 1);
+        if (!V8) __syncthreads();
+        uint4* at = ring + st * stage_words;
+        X{at}.read(dy, row_of<XT>(a.x, a.ldx, row), a.cols);
+        R{at + X::words()}.read(h, row_of<RT>(a.hin, a.ldhin, row), a.cols);
+        if (DH) R{at + X::words() + R::words()}.read(dh, row_of<RT>(a.r, a.ldr, row), a.cols);
+        st = st == S - 1 ? 0 : st + 1;
+        const uint64_t rr = pack2(rstd, rstd), mm = pack2(-mean, -mean);
+        uint64_t g2 = 0, d2 = 0;
+        // past the row's end dy is 0, and with it every term
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int q = 0; q < E / 2; ++q) {
+                const uint64_t xh = mul2(add2(h[j].pair(q), mm), rr), g = dy[j].pair(q), gw = mul2(g, pair8<WT>(w[j], q));
+                dw[j][q] = fma2(g, xh, dw[j][q]);
+                db[j][q] = add2(g, db[j][q]);
+                g2 = add2(g2, gw);
+                d2 = fma2(gw, xh, d2);
+            }
+        const float2 gp = unpack2(g2), dp = unpack2(d2);
+        const float2 c = block_sum2(gp.x + gp.y, dp.x + dp.y, ssum[turn]);
+        // dr = rstd g w + (dh - rstd c1 - xh rstd c2), the sum in the brackets first
+        const float c1 = -rstd * (c.x * inv_n), c2 = -rstd * (c.y * inv_n);
+        const uint64_t p1 = pack2(c1, c1), p2 = pack2(c2, c2);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float v[E];
+#pragma unroll
+            for (int q = 0; q < E / 2; ++q) {
+                const uint64_t xh = mul2(add2(h[j].pair(q), mm), rr);
+                const uint64_t t = fma2(xh, p2, DH ? add2(dh[j].pair(q), p1) : p1);
+                const float2 p = unpack2(fma2(mul2(dy[j].pair(q), pair8<WT>(w[j], q)), rr, t));
+                v[2 * q] = p.x;
+                v[2 * q + 1] = p.y;
+            }
+            store_gradients<XT, RT, V8>(a, step, row, Map::unit(j), v);
+        }
+    }
+    if (!a.part) return;
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = Map::unit(j) * 8;
+        if (a.part16 && c + 8 <= a.cols) {
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+                const float2 x = unpack2(dw[j][q]), y = unpack2(dw[j][q + 1]);
+                *reinterpret_cast<float4*>(part + c + 2 * q) = make_float4(x.x, x.y, y.x, y.y);
+                const float2 s = unpack2(db[j][q]), t = unpack2(db[j][q + 1]);
+                *reinterpret_cast<float4*>(part + a.cols + c + 2 * q) = make_float4(s.x, s.y, t.x, t.y);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 p = unpack2(dw[j][e / 2]), q = unpack2(db[j][e / 2]);
+                if (c + e < a.cols) {
+                    part[c + e] = e % 2 ? p.y : p.x;
+                    part[a.cols + c + e] = e % 2 ? q.y : q.x;
+                }
+            }
+        }
+    }
+}
+
+// Rows too long for the registers: dr and dx by walking the row twice, dw and db
+// by blocks that own 128 columns and a share of the rows (gridDim.y shares).
+template <int XT, int RT, bool V8>
+__global__ void __launch_bounds__(NORM_THREADS) k_layernorm_backward_long(const __grid_constant__ LayerNormArgs a) {
+    constexpr int E = Map::E;
+    __shared__ __align__(16) float2 ssum[2][32];
+    if (threadIdx.x < 64) ssum[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.f, 0.f);
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_next();
+    const uint32_t step = drop_step(a.drop);
+    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols),
+                 eh = extent_of<RT>(a.hin, a.ldhin, a.rows, a.cols);
+    const int steps = (a.units + (int)blockDim.x - 1) / (int)blockDim.x;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const void* DY = row_of<XT>(a.x, a.ldx, row);
+        const void* H = row_of<RT>(a.hin, a.ldhin, row);
+        const void* DH = a.r ? row_of<RT>(a.r, a.ldr, row) : nullptr;
+        const float rstd = a.rstd[row], mean = a.mean[row];
+        float s1 = 0.f, s2 = 0.f;
+        for (int j = 0; j < steps; ++j) {
+            const int u = threadIdx.x + j * blockDim.x;
+            Unit<XT, V8> dy;
+            Unit<RT, V8> h;
+            dy.load(DY, u, a.cols, ex);
+            h.load(H, u, a.cols, eh);
+            float g[E], v[E], w[E];
+            dy.values(g);
+            h.values(v);
+            vector8(a.w, a.wdt, a.w_aligned, a.cols, u, 1.f, w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                s1 = fmaf(g[e], w[e], s1);
+                s2 = fmaf(g[e] * w[e], (v[e] - mean) * rstd, s2);
+            }
+        }
+        const float2 c = block_sum2(s1, s2, ssum[turn]);
+        const float c1 = c.x / (float)a.cols, c2 = c.y / (float)a.cols;
+        for (int j = 0; j < steps; ++j) {
+            const int u = threadIdx.x + j * blockDim.x;
+            Unit<XT, V8> dy;
+            Unit<RT, V8> h, dh;
+            dy.load(DY, u, a.cols, ex);
+            h.load(H, u, a.cols, eh);
+            if (DH) dh.load(DH, u, a.cols, er);
+            float g[E], v[E], w[E], up[E];
+            dy.values(g);
+            h.values(v);
+            vector8(a.w, a.wdt, a.w_aligned, a.cols, u, 1.f, w);
+            if (DH) dh.values(up);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                g[e] = rstd * (g[e] * w[e] - c1 - (v[e] - mean) * rstd * c2);
+                if (DH) g[e] += up[e];
+            }
+            store_gradients<XT, RT, V8>(a, step, row, u, g);
+        }
+    }
+}
+
+// Launched before k_layernorm_backward_long, whose outputs may overwrite dy or dh.
+template <int XT, int RT>
+__global__ void __launch_bounds__(128) k_layernorm_sums_long(const __grid_constant__ LayerNormArgs a) {
+    pdl_wait();
+    pdl_launch_next();
+    const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (c >= a.cols) return;
+    float s = 0.f, t = 0.f;
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        const float g = ld1<XT>(row_of<XT>(a.x, a.ldx, row), c);
+        s = fmaf(g, (ld1<RT>(row_of<RT>(a.hin, a.ldhin, row), c) - a.mean[row]) * a.rstd[row], s);
+        t += g;
+    }
+    float* part = a.part + (int64_t)blockIdx.y * 2 * a.cols;
+    part[c] = s;
+    part[a.cols + c] = t;
+}
+
+// dw (the first half of the blocks) and db from the n partial rows of each: every
+// one of the block's 32 warps adds every 32nd of them, a butterfly adds the warps' sums;
+// added to what is there if accumulate.
+struct SumsArgs {
+    const float* part;
+    int n, accumulate;
+    int64_t cols;
+    void* out[2];
+    int dt[2];
+};
+__global__ void __launch_bounds__(1024) k_layernorm_sums(const __grid_constant__ SumsArgs a) {
+    __shared__ float s[32][33];
+    pdl_wait();
+    pdl_launch_next();
+    const int chunks = gridDim.x / 2, which = blockIdx.x >= chunks, chunk = blockIdx.x - which * chunks;
+    void* out = a.out[which];
+    if (!out) return;
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, dt = a.dt[which];
+    const int64_t c = (int64_t)chunk * 32 + lane;
+    float t = 0.f;
+    if (c < a.cols) {
+        const float* p = a.part + which * a.cols + c;
+#pragma unroll 8
+        for (int i = k; i < a.n; i += 32) t += p[(int64_t)i * 2 * a.cols];
+    }
+    s[k][lane] = t;
+    __syncthreads();
+    // the transpose: warp k has column k of the block's 32
+    t = warp_sum(s[lane][k]);
+    const int64_t cc = (int64_t)chunk * 32 + k;
+    if (lane || cc >= a.cols) return;
+    if (a.accumulate) t += ld1_any(out, cc, dt);
+    st1_any(out, cc, t, dt);
+}
+
+// w16: V8, and the weight in dy's type.
+template <int XT, int RT>
+static const void* pick(bool v8, bool w16, int nv) {
+    switch (nv) {
+        case 2:
+            if (w16) return (const void*)k_layernorm_backward<XT, RT, XT, true, 2>;
+            return v8 ? (const void*)k_layernorm_backward<XT, RT, ZERO_F32, true, 2>
+                      : (const void*)k_layernorm_backward<XT, RT, ZERO_F32, false, 2>;
+        case 4:
+            if (w16) return (const void*)k_layernorm_backward<XT, RT, XT, true, 4>;
+            return v8 ? (const void*)k_layernorm_backward<XT, RT, ZERO_F32, true, 4>
+                      : (const void*)k_layernorm_backward<XT, RT, ZERO_F32, false, 4>;
+        default:
+            return v8 ? (const void*)k_layernorm_backward_long<XT, RT, true>
+                      : (const void*)k_layernorm_backward_long<XT, RT, false>;
+    }
+}
+static const void* layernorm_backward_fn(int xt, int rt, bool v8, bool w16, int nv) {
+    if (xt == ZERO_F32) return pick<ZERO_F32, ZERO_F32>(v8, w16, nv);
+    if (xt == ZERO_BF16)
+        return rt == ZERO_F32 ? pick<ZERO_BF16, ZERO_F32>(v8, w16, nv) : pick<ZERO_BF16, ZERO_BF16>(v8, w16, nv);
+    return rt == ZERO_F32 ? pick<ZERO_F16, ZERO_F32>(v8, w16, nv) : pick<ZERO_F16, ZERO_F16>(v8, w16, nv);
+}
+static const void* sums_long_fn(int xt, int rt) {
+    if (xt == ZERO_F32) return (const void*)k_layernorm_sums_long<ZERO_F32, ZERO_F32>;
+    if (xt == ZERO_BF16)
+        return rt == ZERO_F32 ? (const void*)k_layernorm_sums_long<ZERO_BF16, ZERO_F32>
+                              : (const void*)k_layernorm_sums_long<ZERO_BF16, ZERO_BF16>;
+    return rt == ZERO_F32 ? (const void*)k_layernorm_sums_long<ZERO_F16, ZERO_F32>
+                          : (const void*)k_layernorm_sums_long<ZERO_F16, ZERO_F16>;
+}
+
+}  // namespace zdp
+
+using namespace zdp;
+
+extern "C" {
+
+size_t zero_layernorm_workspace_bytes(int64_t cols) {
+    return cols > 0 && cols <= NORM_MAX_COLS ? (size_t)NORM_MAX_GRID * (size_t)cols * 8 : 0;
+}
+
+int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* weight, int64_t rows, int64_t cols,
+                            const float* mean, const float* rstd, const zero_mat* dh, const zero_drop* drop,
+                            const zero_mat* dr, const zero_mat* dx, const zero_mat* dw, const zero_mat* db, int accumulate,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    const char* me = "zero_layernorm_backward";
+    if (rows < 0 || cols < 0) return fail(ZERO_EINVAL, "zero_layernorm_backward: negative rows or cols");
+    if (cols > NORM_MAX_COLS) return fail(ZERO_ELIMIT, "zero_layernorm_backward: more than 1048576 columns");
+    int rc = check_mat(dy, rows, cols, FLOAT_TYPES, me, "dy");
+    if (rc == ZERO_OK) rc = check_mat(h, rows, cols, FLOAT_TYPES, me, "h");
+    if (rc == ZERO_OK && weight) rc = check_mat(weight, 1, cols, FLOAT_TYPES, me, "weight");
+    if (rc == ZERO_OK && dh) rc = check_mat(dh, rows, cols, FLOAT_TYPES, me, "dh");
+    if (rc == ZERO_OK && dr) rc = check_mat(dr, rows, cols, FLOAT_TYPES, me, "dr");
+    if (rc == ZERO_OK && dx) rc = check_mat(dx, rows, cols, FLOAT_TYPES, me, "dx");
+    if (rc == ZERO_OK && dw) rc = check_mat(dw, 1, cols, FLOAT_TYPES, me, "dw");
+    if (rc == ZERO_OK && db) rc = check_mat(db, 1, cols, FLOAT_TYPES, me, "db");
+    if (rc != ZERO_OK) return rc;
+    if (!dr && !dx) return fail(ZERO_EINVAL, "zero_layernorm_backward: neither dr nor dx");
+    const int rt = h->dtype;
+    if (rt != dy->dtype && rt != ZERO_F32) return fail(ZERO_EINVAL, "zero_layernorm_backward: h is in dy's type or fp32");
+    if ((dr && dr->dtype != rt) || (dh && dh->dtype != rt))
+        return fail(ZERO_EINVAL, "zero_layernorm_backward: dr and dh are in h's type");
+    if (dx && dx->dtype != dy->dtype) return fail(ZERO_EINVAL, "zero_layernorm_backward: dx is in dy's type");
+    if (rows > 0 && cols > 0 && (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4)))
+        return fail(ZERO_EINVAL, "zero_layernorm_backward: mean or rstd NULL or not 4-byte aligned");
+    if ((dw || db) && cols > 0 &&
+        (!workspace || !aligned(workspace, 4) || workspace_bytes < zero_layernorm_workspace_bytes(cols)))
+        return fail(ZERO_EWORKSPACE, "zero_layernorm_backward: workspace smaller than zero_layernorm_workspace_bytes(cols)");
+    LayerNormArgs a = {};
+    rc = check_drop(drop, a.drop, me);
+    if (rc != ZERO_OK || cols == 0) return rc;
+    const int sms = sm_count();
+    if (!sms) return ZERO_ECUDA;
+    a.x = dy->data;
+    a.ldx = dy->ld;
+    a.hin = h->data;
+    a.ldhin = h->ld;
+    a.r = dh ? dh->data : nullptr;
+    a.ldr = dh ? dh->ld : 0;
+    a.y = dr ? dr->data : nullptr;
+    a.ldy = dr ? dr->ld : 0;
+    a.h = dx ? dx->data : nullptr;
+    a.ldh = dx ? dx->ld : 0;
+    if (weight) {
+        a.w = weight->data;
+        a.wdt = weight->dtype;
+        a.w_aligned = aligned(weight->data, 16);
+    }
+    a.rows = rows;
+    a.cols = (int)cols;
+    a.units = (int)((cols + 7) / 8);
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.part = dw || db ? static_cast<float*>(workspace) : nullptr;
+    a.part16 = cols % 4 == 0 && aligned(workspace, 16);
+    const bool v8 = cols % 8 == 0 && rows_aligned(*dy, rows) && rows_aligned(*h, rows) && (!dr || rows_aligned(*dr, rows)) &&
+                    (!dx || rows_aligned(*dx, rows)) && (!dh || rows_aligned(*dh, rows));
+    const NormShape p = shape_of(cols, words_of(dy->dtype) + 2 * words_of(rt), LN_BACKWARD_THREADS);
+    a.stages = p.stages;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void* args[] = {&a};
+    int64_t g = (int64_t)p.per_sm * sms;
+    if (g > NORM_MAX_GRID) g = NORM_MAX_GRID;
+    if (g > rows) g = rows;
+    const void* f = layernorm_backward_fn(dy->dtype, rt, v8, v8 && (!weight || weight->dtype == dy->dtype), p.nv);
+    rc = raise_smem(f, p.smem, "zero_layernorm_backward shared-memory size");
+    if (rc != ZERO_OK) return rc;
+    int parts = (int)g;
+    if (p.nv == 0 && a.part && rows > 0) {
+        // dw and db first: dr and dx may be written over dy or dh
+        const int64_t chunks = (cols + 127) / 128;
+        int64_t shares = (8 * (int64_t)sms + chunks - 1) / chunks;
+        if (shares > NORM_MAX_GRID) shares = NORM_MAX_GRID;
+        if (shares > rows) shares = rows;
+        parts = (int)shares;
+        const dim3 grid((unsigned)chunks, (unsigned)shares);
+        rc = cuda_fail(cudaLaunchKernel(sums_long_fn(dy->dtype, rt), grid, dim3(128), args, 0, s),
+                       "zero_layernorm_backward sums launch");
+        if (rc != ZERO_OK) return rc;
+    }
+    if (rows > 0) {
+        if (p.nv == 0) g = rows < 1 << 30 ? rows : 1 << 30;
+        rc = cuda_fail(launch_after_previous(f, (int)g, p.threads, args, p.smem, s), "zero_layernorm_backward launch");
+        if (rc != ZERO_OK) return rc;
+    }
+    if (!a.part) return ZERO_OK;
+    SumsArgs sums = {a.part, rows > 0 ? parts : 0, accumulate, cols, {dw ? dw->data : nullptr, db ? db->data : nullptr},
+                     {dw ? dw->dtype : 0, db ? db->dtype : 0}};
+    void* sargs[] = {&sums};
+    return cuda_fail(launch_after_previous((const void*)k_layernorm_sums, (int)((cols + 31) / 32) * 2, 1024, sargs, 0, s),
+                     "zero_layernorm_backward sums launch");
+}
+
+}  // extern "C"
