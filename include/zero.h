@@ -883,6 +883,57 @@ int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_ma
                             void* workspace, size_t workspace_bytes, void* stream);
 size_t zero_layernorm_workspace_bytes(int64_t cols);
 
+/* The gated feed-forward block of a unit, up to its second matrix:
+ *   G = x gate_w^T;  U = x up_w^T;  h = act(G) U
+ * both projections, the activation and the product in one kernel, G and U held
+ * in fp32 there.
+ * x          rows x cols; gate_w, up_w: ff x cols (rows of a gathered unit, say);
+ *            h: rows x ff; all ZERO_F16 or all ZERO_BF16
+ * act        ZERO_SILU: g / (1 + exp(-g)); ZERO_GELU_TANH: GELU's tanh form
+ * gate, up   rows x ff, G and U rounded, for the backward pass; both or neither
+ * workspace  zero_gated_forward_workspace_bytes of the same arguments, 16-byte
+ *            aligned, contents irrelevant: 0 where the rows of x and of the
+ *            weights start on 16-byte boundaries, else copies of those whose
+ *            rows do not (NULL if 0)
+ * status     device int32 the caller zero-fills; a block whose bounded wait runs
+ *            out sets bit 0, and the outputs are then incomplete
+ *            (ZERO_GB300_SPIN_LIMIT as for zero3_gather_bulk)
+ * With no columns h, G and U are 0.  A NaN or infinity in a row of x or of a
+ * weight stays in that row or column of h.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EWORKSPACE, ZERO_ELIMIT (2^30 rows or
+ * columns, or tiles of 256 x 256, and more), ZERO_ECUDA. */
+typedef enum { ZERO_SILU = 0, ZERO_GELU_TANH = 1 } zero_act;
+int zero_gated_forward(const zero_mat* x, const zero_mat* gate_w, const zero_mat* up_w, int64_t rows, int64_t cols,
+                       int64_t ff, int act, const zero_mat* h, const zero_mat* gate, const zero_mat* up, void* workspace,
+                       size_t workspace_bytes, int32_t* status, void* stream);
+size_t zero_gated_forward_workspace_bytes(const zero_mat* x, const zero_mat* gate_w, const zero_mat* up_w, int64_t rows,
+                                          int64_t cols, int64_t ff);
+
+/* Its backward pass, from gate and up as the forward pass stored them:
+ *   dgate = round(dh up act'(gate));  dup = round(dh act(gate))
+ *   dx = dgate gate_w + dup up_w;  dgate_w = dgate^T x;  dup_w = dup^T x
+ * the products of dgate and dup as they are stored, with fp32 sums.
+ * dh         rows x ff; all matrices of dh's type, but see dgate_w
+ * dgate, dup rows x ff; may be gate and up (in either order) or dh
+ * dx         rows x cols; NULL: not wanted (gate_w and up_w are then not read)
+ * dgate_w, dup_w   ff x cols, both in dh's type or both ZERO_F32, e.g. in a
+ *            gradient bucket; both NULL: not wanted (x is then not read);
+ *            accumulate nonzero: added to what is there, in fp32, and rounded
+ *            once
+ * workspace  zero_gated_backward_workspace_bytes of the same arguments (NULL for
+ *            what is not read), as for the forward pass: copies of what the
+ *            products read and whose rows do not start on 16-byte boundaries
+ * With no rows dgate_w and dup_w are 0 (or unchanged), with ff = 0 dx is.
+ * Errors as zero_gated_forward. */
+int zero_gated_backward(const zero_mat* dh, const zero_mat* gate, const zero_mat* up, const zero_mat* x,
+                        const zero_mat* gate_w, const zero_mat* up_w, int64_t rows, int64_t cols, int64_t ff, int act,
+                        const zero_mat* dgate, const zero_mat* dup, const zero_mat* dx, const zero_mat* dgate_w,
+                        const zero_mat* dup_w, int accumulate, void* workspace, size_t workspace_bytes, int32_t* status,
+                        void* stream);
+size_t zero_gated_backward_workspace_bytes(const zero_mat* x, const zero_mat* gate_w, const zero_mat* up_w,
+                                           const zero_mat* dgate, const zero_mat* dup, int64_t rows, int64_t cols,
+                                           int64_t ff);
+
 /* Message of the last error on this thread ("" if none). */
 const char* zero_last_error(void);
 

@@ -142,3 +142,63 @@ def test_layernorm_backward_refusals(Z):
     call(Z.ZERO_EWORKSPACE, workspace=torch.zeros(ws - 1, dtype=torch.uint8))
     call(Z.ZERO_ELIMIT, cols=(1 << 20) + 1)
     call(Z.ZERO_EINVAL, drop=Z.drop(-1.0, 1))
+
+
+def test_gated_forward_refusals(Z):
+    def call(code, **kw):
+        a = dict(x=m(Z), gate_w=m(Z), up_w=m(Z), rows=4, cols=64, ff=64, act=0, h=m(Z), gate=m(Z), up=m(Z),
+                 workspace=None, workspace_bytes=0, status=FAKE)
+        a.update(kw)
+        refused(Z, code, Z.zero_gated_forward, *a.values())
+
+    for size in ("rows", "cols", "ff"):
+        call(Z.ZERO_EINVAL, **{size: -1})
+        call(Z.ZERO_ELIMIT, **{size: 1 << 31})
+    call(Z.ZERO_ELIMIT, rows=1 << 29, ff=1 << 29)                # too many tiles
+    call(Z.ZERO_EINVAL, act=2)
+    call(Z.ZERO_EINVAL, act=-1)
+    for what in ("x", "gate_w", "up_w", "h"):
+        call(Z.ZERO_EINVAL, **{what: None})
+    for what in ("x", "gate_w", "up_w", "h", "gate", "up"):
+        call(Z.ZERO_EINVAL, **{what: m(Z, data=0)})
+        call(Z.ZERO_EINVAL, **{what: m(Z, dtype=3)})
+        call(Z.ZERO_EINVAL, **{what: m(Z, dtype=1)})             # fp16 beside bf16
+        call(Z.ZERO_EINVAL, **{what: m(Z, ld=63)})
+        call(Z.ZERO_EALIGN, **{what: m(Z, data=FAKE + 1)})
+    call(Z.ZERO_EINVAL, gate=None)
+    call(Z.ZERO_EINVAL, up=None)
+    call(Z.ZERO_EINVAL, status=None)
+    call(Z.ZERO_EINVAL, status=FAKE + 2)
+    call(Z.ZERO_EWORKSPACE, x=m(Z, data=FAKE + 2))               # rows off 16 bytes need a copy
+    need = Z.zero_gated_forward_workspace_bytes(m(Z), m(Z, ld=65), m(Z), 4, 64, 64)
+    assert need == 64 * 64 * 2
+    call(Z.ZERO_EWORKSPACE, gate_w=m(Z, ld=65), workspace=FAKE, workspace_bytes=need - 1)
+    call(Z.ZERO_EWORKSPACE, gate_w=m(Z, ld=65), workspace=FAKE + 8, workspace_bytes=need)
+    call(Z.ZERO_EINVAL, x=torch.zeros(4, 63, dtype=torch.bfloat16))
+
+
+def test_gated_backward_refusals(Z):
+    def call(code, **kw):
+        a = dict(dh=m(Z), gate=m(Z), up=m(Z), x=m(Z), gate_w=m(Z), up_w=m(Z), rows=4, cols=64, ff=64, act=1, dgate=m(Z),
+                 dup=m(Z), dx=m(Z), dgate_w=m(Z), dup_w=m(Z), accumulate=0, workspace=None, workspace_bytes=0, status=FAKE)
+        a.update(kw)
+        refused(Z, code, Z.zero_gated_backward, *a.values())
+
+    for size in ("rows", "cols", "ff"):
+        call(Z.ZERO_EINVAL, **{size: -1})
+        call(Z.ZERO_ELIMIT, **{size: 1 << 31})
+    call(Z.ZERO_EINVAL, act=7)
+    for what in ("dh", "gate", "up", "x", "gate_w", "up_w", "dgate", "dup"):
+        call(Z.ZERO_EINVAL, **{what: None})
+    for what in ("dh", "gate", "up", "x", "gate_w", "up_w", "dgate", "dup", "dx"):
+        call(Z.ZERO_EINVAL, **{what: m(Z, dtype=3)})
+        call(Z.ZERO_EINVAL, **{what: m(Z, dtype=1)})
+        call(Z.ZERO_EALIGN, **{what: m(Z, data=FAKE + 1)})
+    call(Z.ZERO_EINVAL, dgate_w=None)
+    call(Z.ZERO_EINVAL, dup_w=None)
+    call(Z.ZERO_EINVAL, dup_w=m(Z, dtype=3))
+    call(Z.ZERO_EINVAL, dgate_w=m(Z, dtype=1), dup_w=m(Z, dtype=1))
+    call(Z.ZERO_EINVAL, status=None)
+    call(Z.ZERO_EWORKSPACE, dgate=m(Z, ld=65))
+    assert Z.zero_gated_backward_workspace_bytes(None, None, None, m(Z), m(Z, ld=70), 4, 64, 100) == 4 * 128 * 2
+    assert Z.zero_gated_backward_workspace_bytes(m(Z), m(Z), m(Z), m(Z), m(Z), 4, 64, 64) == 0

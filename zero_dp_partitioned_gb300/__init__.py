@@ -23,6 +23,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libzero_gb300.so")
 ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_EWORKSPACE, ZERO_ECUDA, ZERO_ELIMIT = 0, -1, -2, -3, -4, -5
 ZERO_F16, ZERO_BF16, ZERO_F32, ZERO_E4M3, ZERO_I32, ZERO_I64 = 1, 2, 3, 4, 5, 6
 ZERO_MX4_ROWS, ZERO_MX4_TILES = 0, 1
+ZERO_SILU, ZERO_GELU_TANH = 0, 1
 ZERO_PLAN_PADDED, ZERO_PLAN_UNPADDED = 0, 1
 ZERO_MAX_SLICES = ZERO_MAX_SHARDS = 64
 
@@ -145,6 +146,11 @@ _SIGS = {
     "zero_layernorm_backward": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, ctypes.c_size_t,
                                      _P]),
     "zero_layernorm_workspace_bytes": (ctypes.c_size_t, [_I64]),
+    "zero_gated_forward": (_I, [_P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "zero_gated_forward_workspace_bytes": (ctypes.c_size_t, [_P, _P, _P, _I64, _I64, _I64]),
+    "zero_gated_backward": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _I, _P,
+                                 ctypes.c_size_t, _P, _P]),
+    "zero_gated_backward_workspace_bytes": (ctypes.c_size_t, [_P, _P, _P, _P, _P, _I64, _I64, _I64]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
 # every symbol include/zero.h declares
@@ -700,3 +706,41 @@ def zero_layernorm_backward(dy, h, weight, rows, cols, mean, rstd, dh, drop, dr,
                                        _mat(db, 1, cols, "db"), int(accumulate),
                                        _buf(workspace, workspace_bytes, "workspace", ZERO_EWORKSPACE),
                                        workspace_bytes, _stream(stream)))
+
+
+def zero_gated_forward_workspace_bytes(x, gate_w, up_w, rows, cols, ff):
+    """0 where the rows of x and of the weights start on 16-byte boundaries."""
+    return lib.zero_gated_forward_workspace_bytes(_mat(x, rows, cols, "x"), _mat(gate_w, ff, cols, "gate_w"),
+                                                  _mat(up_w, ff, cols, "up_w"), rows, cols, ff)
+
+
+def zero_gated_forward(x, gate_w, up_w, rows, cols, ff, act, h, gate, up, workspace, workspace_bytes, status,
+                       stream=None):
+    """h = act(x gate_w^T) * (x up_w^T), and, with gate and up, both projections;
+    status: device int32 (zero-filled by the caller), bit 0 set if a wait ran
+    out."""
+    _check(lib.zero_gated_forward(_mat(x, rows, cols, "x"), _mat(gate_w, ff, cols, "gate_w"),
+                                  _mat(up_w, ff, cols, "up_w"), rows, cols, ff, act, _mat(h, rows, ff, "h"),
+                                  _mat(gate, rows, ff, "gate"), _mat(up, rows, ff, "up"),
+                                  _buf(workspace, workspace_bytes, "workspace", ZERO_EWORKSPACE), workspace_bytes,
+                                  _buf(status, 4, "status"), _stream(stream)))
+
+
+def zero_gated_backward_workspace_bytes(x, gate_w, up_w, dgate, dup, rows, cols, ff):
+    """0 where the rows of all of them start on 16-byte boundaries."""
+    return lib.zero_gated_backward_workspace_bytes(_mat(x, rows, cols, "x"), _mat(gate_w, ff, cols, "gate_w"),
+                                                   _mat(up_w, ff, cols, "up_w"), _mat(dgate, rows, ff, "dgate"),
+                                                   _mat(dup, rows, ff, "dup"), rows, cols, ff)
+
+
+def zero_gated_backward(dh, gate, up, x, gate_w, up_w, rows, cols, ff, act, dgate, dup, dx, dgate_w, dup_w, accumulate,
+                        workspace, workspace_bytes, status, stream=None):
+    """dgate and dup (the projections' gradients, stored), and of them dx and the
+    weights' gradients."""
+    _check(lib.zero_gated_backward(_mat(dh, rows, ff, "dh"), _mat(gate, rows, ff, "gate"), _mat(up, rows, ff, "up"),
+                                   _mat(x, rows, cols, "x"), _mat(gate_w, ff, cols, "gate_w"),
+                                   _mat(up_w, ff, cols, "up_w"), rows, cols, ff, act, _mat(dgate, rows, ff, "dgate"),
+                                   _mat(dup, rows, ff, "dup"), _mat(dx, rows, cols, "dx"),
+                                   _mat(dgate_w, ff, cols, "dgate_w"), _mat(dup_w, ff, cols, "dup_w"), int(accumulate),
+                                   _buf(workspace, workspace_bytes, "workspace", ZERO_EWORKSPACE), workspace_bytes,
+                                   _buf(status, 4, "status"), _stream(stream)))
