@@ -323,3 +323,23 @@ def test_a_wait_that_runs_out_is_reported(Z, monkeypatch):
         monkeypatch.delenv("ZERO_GB300_SPIN_LIMIT")
         b.status.zero_()
         b.check_forward(b.forward())
+
+
+def test_many_passes_one_behind_the_other(Z):
+    """Passes that nothing waits between: the products of one start beside the
+    slopes' last blocks, one block of a pair well before the other, and pairs of
+    the next product on SMs that this one leaves idle."""
+    g = gen(9)
+    rows, cols, ff = 2001, 512, 1352
+    b = Block(Z, rnd(g, rows, cols), rnd(g, ff, cols, std=0.04), rnd(g, ff, cols, std=0.04), 0)
+    dh, out = rnd(g, rows, ff), []
+    for i in range(2):
+        o = [b.new(rows, ff) for _ in range(5)] + [b.new(rows, cols), b.new(ff, cols), b.new(ff, cols)]
+        h, gate, up, dg, du, dx, dwg, dwu = o
+        for _ in range(1 if i == 0 else 500):
+            Z.zero_gated_forward(b.x, b.wg, b.wu, rows, cols, ff, 0, h, gate, up, None, 0, b.status)
+            Z.zero_gated_backward(dh, gate, up, b.x, b.wg, b.wu, rows, cols, ff, 0, dg, du, dx, dwg, dwu, 0, None, 0, b.status)
+        torch.cuda.synchronize()
+        out.append(o)
+    assert int(b.status) == 0
+    assert all(torch.equal(p, q) for p, q in zip(*out))

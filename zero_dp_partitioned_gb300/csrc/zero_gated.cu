@@ -293,8 +293,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
         *stop = 0;
         *loaded = 0;
     }
-    if (warp == 1)
+    // Both blocks run before either allocates, and neither leaves before both have freed: the allocation is the pair's.
+    // Without the first barrier, a block that had started well before its partner (beside a kernel whose blocks were still
+    // on the partner's SM) was through, and the partner's allocation never returned.
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + 200) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
     tc_fence_before();
     __syncthreads();
     cluster_arrive();
@@ -458,9 +465,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     tc_fence_after();
     if (warp == 1) {
         __syncwarp();
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
 }
 
 // ---------------------------------------------------------------- the slopes
