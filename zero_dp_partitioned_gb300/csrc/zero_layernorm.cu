@@ -17,7 +17,7 @@
 
 namespace zdp {
 
-constexpr int LN_FORWARD_THREADS = 1536;    // a multiprocessor, for the grid and the stages
+constexpr int LN_FORWARD_THREADS = 1536;    // a multiprocessor, for the grid and the stages of the general form
 constexpr int LN_FORWARD_OVER = 2;
 
 // What a block keeps of its warps: the columns of each, and, in two sets used by
@@ -37,12 +37,13 @@ __device__ __forceinline__ int warp_columns(int cols, int nv) {
     return n;
 }
 
-// WT: the type in which weight and bias stay in registers, x's where they are of
-// it (half the registers, and with them twice the threads) or fp32.
-template <int XT, int RT, int WT, bool V8, int NV>
-__global__ void __launch_bounds__(NORM_THREADS, NV == 2 && RT != ZERO_F32 && WT != ZERO_F32 ? 2 : 1)
+// The general form, for rows that start anywhere and widths that are no multiple of 8.
+template <int XT, int RT, int NV>
+__global__ void __launch_bounds__(NORM_THREADS, 1)
     k_layernorm_forward(const __grid_constant__ LayerNormArgs a) {
     constexpr int E = Map::E;
+    constexpr bool V8 = false;
+    constexpr int WT = ZERO_F32;
     __shared__ __align__(16) WarpStats st;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int mine = warp_columns(a.cols, NV);
@@ -107,12 +108,8 @@ __global__ void __launch_bounds__(NORM_THREADS, NV == 2 && RT != ZERO_F32 && WT 
 #pragma unroll
             for (int q = 0; q < E / 2; ++q) {
                 uint64_t d = add2(r[j].pair(q), mw2);
-                if (V8) {
-                    if (left <= 0) d = 0;
-                } else {
-                    const float2 p = unpack2(d);
-                    d = pack2(2 * q < left ? p.x : 0.f, 2 * q + 1 < left ? p.y : 0.f);
-                }
+                const float2 p = unpack2(d);
+                d = pack2(2 * q < left ? p.x : 0.f, 2 * q + 1 < left ? p.y : 0.f);
                 v2 = fma2(d, d, v2);
             }
         }
@@ -147,6 +144,122 @@ __global__ void __launch_bounds__(NORM_THREADS, NV == 2 && RT != ZERO_F32 && WT 
                 y[2 * q + 1] = v.y;
             }
             store_unit<XT, V8>(row_of<XT>(a.y, a.ldy, row), Map::unit(j), a.cols, y);
+        }
+    }
+}
+
+// Rows on 16-byte boundaries.  WT: the type in which weight and bias stay in
+// registers, x's where they are of it (half the registers) or fp32.
+template <int XT, int RT, int WT, int NV>
+__global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const __grid_constant__ LayerNormArgs a) {
+    __shared__ __align__(16) WarpStats st;
+    const int T = a.T, G = blockDim.x / T, group = threadIdx.x / T, u0 = threadIdx.x - group * T, units = a.units;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = T >> 5, w0 = group * warps;
+    int mine = 0;                                            // columns of this warp
+#pragma unroll
+    for (int j = 0; j < NV; ++j) mine += max(0, min(256, a.cols - ((u0 & ~31) + j * T) * 8));
+    const float inv_mine = mine ? 1.f / (float)mine : 0.f, inv_n = 1.f / (float)a.cols;
+    if (lane == 0) st.n[warp] = (float)mine;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_next();
+    const uint32_t step = drop_step(a.drop);
+    extern __shared__ __align__(16) uint4 ring[];
+    using X = Lane<XT, NV>;
+    using R = Lane<RT, NV>;
+    const int S = a.stages, stage_words = X::words() + R::words();
+    const int64_t first = group * (int64_t)gridDim.x + blockIdx.x, every = (int64_t)G * gridDim.x;
+    auto copy = [&](int64_t row, int at_stage) {
+        if (row < a.rows) {
+            uint4* at = ring + at_stage * stage_words;
+            X::copy(at, row_of<XT>(a.x, a.ldx, row), u0, T, units);
+            if (a.r) R::copy(at + X::words(), row_of<RT>(a.r, a.ldr, row), u0, T, units);
+        }
+        copies_commit();
+    };
+    for (int s = 0; s < S - 1; ++s) copy(first + s * every, s);
+    Raw8<WT> w[NV], b[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        float v[8];
+        vector8(a.w, a.wdt, a.w_aligned, a.cols, u0 + j * T, 1.f, v);
+        w[j] = narrow8<WT>(v);
+        vector8(a.b, a.bdt, a.b_aligned, a.cols, u0 + j * T, 0.f, v);
+        b[j] = narrow8<WT>(v);
+    }
+    int turn = 0, at_stage = 0;
+    for (int64_t row = first; row < a.rows; row += every, turn ^= 1) {
+        Raw8<RT> r[NV];
+        copy(row + (S - 1) * every, at_stage == 0 ? S - 1 : at_stage - 1);
+        copies_wait_all_but(S - 1);
+        if (XT == ZERO_F32 || RT == ZERO_F32) __syncwarp();
+        const uint4* at = ring + at_stage * stage_words;
+        at_stage = at_stage == S - 1 ? 0 : at_stage + 1;
+        char* H = a.h ? static_cast<char*>(a.h) + row * a.ldh * Elem<RT>::SIZE : nullptr;
+        // h as it is stored
+        uint64_t s2 = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int u = u0 + j * T;
+            Unit<XT, true> xu;
+            Unit<RT, true> ru;
+            xu.raw = X::read(at, j, u0, T, units);
+            if (a.r) ru.raw = R::read(at + X::words(), j, u0, T, units);
+            r[j] = (a.drop.on ? drop_add_unit<XT, RT, true>(xu, ru, a.r != nullptr, a.drop, step, row * units + u)
+                              : add_unit<XT, RT, true>(xu, ru, a.r != nullptr))
+                       .raw;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s2 = add2(s2, pair8<RT>(r[j], q));
+            if (H && u < units) put8<RT>(H, u, r[j], a.h32);
+        }
+        const float2 sp = unpack2(s2);
+        const float mw = warp_sum(sp.x + sp.y) * inv_mine;
+        const uint64_t mw2 = pack2(-mw, -mw);
+        uint64_t v2 = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (u0 + j * T < units)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint64_t d = add2(pair8<RT>(r[j], q), mw2);
+                    v2 = fma2(d, d, v2);
+                }
+        const float2 vp = unpack2(v2);
+        float m2 = warp_sum(vp.x + vp.y), mean = mw;
+        if (warps > 1) {
+            if (lane == 0) st.s[turn][warp] = make_float2(mw, m2);
+            row_barrier(group, T);
+            float sum = 0.f;
+#pragma unroll 4
+            for (int k = 0; k < warps; ++k) sum = fmaf(st.n[w0 + k], st.s[turn][w0 + k].x, sum);
+            mean = sum * inv_n;
+            m2 = 0.f;
+#pragma unroll 4
+            for (int k = 0; k < warps; ++k) {
+                const float2 p = st.s[turn][w0 + k];
+                const float d = p.x - mean;
+                m2 += fmaf(st.n[w0 + k] * d, d, p.y);
+            }
+        }
+        const float rstd = rsqrtf(fmaf(m2, inv_n, a.eps));
+        if (u0 == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        const uint64_t mm = pack2(-mean, -mean), rr = pack2(rstd, rstd);
+        char* Y = static_cast<char*>(a.y) + row * a.ldy * Elem<XT>::SIZE;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float y[8];
+            stay_packed(w[j]);
+            stay_packed(b[j]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 v = unpack2(fma2(mul2(add2(pair8<RT>(r[j], q), mm), rr), pair8<WT>(w[j], q), pair8<WT>(b[j], q)));
+                y[2 * q] = v.x;
+                y[2 * q + 1] = v.y;
+            }
+            if (u0 + j * T < units) put8<XT>(Y, u0 + j * T, narrow8<XT>(y), a.y32);
         }
     }
 }
@@ -227,28 +340,27 @@ __global__ void __launch_bounds__(NORM_THREADS) k_layernorm_forward_long(const _
     }
 }
 
-// w16: V8, and weight and bias in x's type.
 template <int XT, int RT>
-static const void* pick(bool v8, bool w16, int nv) {
-    switch (nv) {
-        case 2:
-            if (w16) return (const void*)k_layernorm_forward<XT, RT, XT, true, 2>;
-            return v8 ? (const void*)k_layernorm_forward<XT, RT, ZERO_F32, true, 2>
-                      : (const void*)k_layernorm_forward<XT, RT, ZERO_F32, false, 2>;
-        case 4:
-            if (w16) return (const void*)k_layernorm_forward<XT, RT, XT, true, 4>;
-            return v8 ? (const void*)k_layernorm_forward<XT, RT, ZERO_F32, true, 4>
-                      : (const void*)k_layernorm_forward<XT, RT, ZERO_F32, false, 4>;
-        default:
-            return v8 ? (const void*)k_layernorm_forward_long<XT, RT, true>
-                      : (const void*)k_layernorm_forward_long<XT, RT, false>;
-    }
+static const void* general(bool v8, int nv) {
+    if (nv == 2) return (const void*)k_layernorm_forward<XT, RT, 2>;
+    if (nv == 4) return (const void*)k_layernorm_forward<XT, RT, 4>;
+    return v8 ? (const void*)k_layernorm_forward_long<XT, RT, true> : (const void*)k_layernorm_forward_long<XT, RT, false>;
 }
-static const void* layernorm_forward_fn(int xt, int rt, bool v8, bool w16, int nv) {
-    if (xt == ZERO_F32) return pick<ZERO_F32, ZERO_F32>(v8, w16, nv);
-    if (xt == ZERO_BF16)
-        return rt == ZERO_F32 ? pick<ZERO_BF16, ZERO_F32>(v8, w16, nv) : pick<ZERO_BF16, ZERO_BF16>(v8, w16, nv);
-    return rt == ZERO_F32 ? pick<ZERO_F16, ZERO_F32>(v8, w16, nv) : pick<ZERO_F16, ZERO_F16>(v8, w16, nv);
+static const void* general_fn(int xt, int rt, bool v8, int nv) {
+    if (xt == ZERO_F32) return general<ZERO_F32, ZERO_F32>(v8, nv);
+    if (xt == ZERO_BF16) return rt == ZERO_F32 ? general<ZERO_BF16, ZERO_F32>(v8, nv) : general<ZERO_BF16, ZERO_BF16>(v8, nv);
+    return rt == ZERO_F32 ? general<ZERO_F16, ZERO_F32>(v8, nv) : general<ZERO_F16, ZERO_F16>(v8, nv);
+}
+// w16: weight and bias in x's type.
+template <int XT, int RT>
+static const void* rows_of(bool w16, int nv) {
+    if (nv == 4) return (const void*)k_layernorm_forward_rows<XT, RT, XT, 4>;
+    return w16 ? (const void*)k_layernorm_forward_rows<XT, RT, XT, 2> : (const void*)k_layernorm_forward_rows<XT, RT, ZERO_F32, 2>;
+}
+static const void* rows_fn(int xt, int rt, bool w16, int nv) {
+    if (xt == ZERO_F32) return (const void*)k_layernorm_forward_rows<ZERO_F32, ZERO_F32, ZERO_F32, 2>;
+    if (xt == ZERO_BF16) return rt == ZERO_F32 ? rows_of<ZERO_BF16, ZERO_F32>(w16, nv) : rows_of<ZERO_BF16, ZERO_BF16>(w16, nv);
+    return rt == ZERO_F32 ? rows_of<ZERO_F16, ZERO_F32>(w16, nv) : rows_of<ZERO_F16, ZERO_F16>(w16, nv);
 }
 
 }  // namespace zdp
@@ -306,17 +418,35 @@ extern "C" int zero_layernorm_forward(const zero_mat* x, const zero_mat* residua
     a.rstd = rstd;
     const bool v8 = cols % 8 == 0 && rows_aligned(*x, rows) && rows_aligned(*y, rows) &&
                     (!residual || rows_aligned(*residual, rows)) && (!h_out || rows_aligned(*h_out, rows));
-    const NormShape p = shape_of(cols, words_of(x->dtype) + words_of(rt), LN_FORWARD_THREADS);
-    a.stages = p.stages;
-    const int sms = sm_count();
+    const int sms = sm_count(), words = words_of(x->dtype) + words_of(rt);
     if (!sms) return ZERO_ECUDA;
-    const bool w16 = v8 && (!weight || weight->dtype == x->dtype) && (!bias || bias->dtype == x->dtype);
-    const void* f = layernorm_forward_fn(x->dtype, rt, v8, w16, p.nv);
+    void* args[] = {&a};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (v8) {
+        // units of 8 columns a thread: more than two in fp32, values or weights, do not fit its registers, and of rows of
+        // up to 512 columns four would leave half of a warp's lanes without any
+        const bool w16 = x->dtype != ZERO_F32 && (!weight || weight->dtype == x->dtype) && (!bias || bias->dtype == x->dtype);
+        const int nv = w16 && cols > 512 ? 4 : 2;
+        const RowsShape p = rows_shape(rows, cols, nv, words, sms);
+        if (p.threads) {
+            const void* f = rows_fn(x->dtype, rt, w16, nv);
+            a.h32 = h_out && rows_on_32(*h_out, rows);
+            a.y32 = rows_on_32(*y, rows);
+            a.stages = p.stages;
+            a.T = p.T;
+            rc = raise_smem(f, p.smem, "zero_layernorm_forward shared-memory size");
+            if (rc != ZERO_OK) return rc;
+            return cuda_fail(launch_after_previous(f, p.grid, p.threads, args, p.smem, s), "zero_layernorm_forward launch");
+        }
+    }
+    // rows on 16-byte boundaries that are too long for the registers are walked as any others that are
+    NormShape p = shape_of(cols, words, LN_FORWARD_THREADS);
+    if (v8) p = NormShape{0, NORM_THREADS, LN_FORWARD_THREADS / NORM_THREADS, 2, 0};
+    a.stages = p.stages;
+    const void* f = general_fn(x->dtype, rt, v8, p.nv);
     rc = raise_smem(f, p.smem, "zero_layernorm_forward shared-memory size");
     if (rc != ZERO_OK) return rc;
     const int64_t most = (int64_t)sms * p.per_sm * LN_FORWARD_OVER;
-    void* args[] = {&a};
-    return cuda_fail(launch_after_previous(f, (int)(rows < most ? rows : most), p.threads, args, p.smem,
-                                           static_cast<cudaStream_t>(stream)),
+    return cuda_fail(launch_after_previous(f, (int)(rows < most ? rows : most), p.threads, args, p.smem, s),
                      "zero_layernorm_forward launch");
 }

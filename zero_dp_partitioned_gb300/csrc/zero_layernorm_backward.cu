@@ -37,7 +37,10 @@ __device__ __forceinline__ float2 block_sum2(float x, float y, float2* s) {
 // The gradient of one unit stored: of r as it is, of x by the forward's mask.
 template <int XT, int RT, bool V8>
 __device__ __forceinline__ void store_gradients(const LayerNormArgs& a, uint32_t step, int64_t row, int u, float (&v)[8]) {
-    if (a.y) store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), u, a.cols, v);
+    if (a.y) {
+        if constexpr (!V8) store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), u, a.cols, v);
+        else if (u * 8 < a.cols) put8<RT>(row_of<RT>(a.y, a.ldy, row), u, narrow8<RT>(v), a.y32);
+    }
     if (!a.h) return;
     if (a.drop.on) {
         const uint4 bits = drop_bits(a.drop, step, row * a.units + u);
@@ -48,13 +51,16 @@ __device__ __forceinline__ void store_gradients(const LayerNormArgs& a, uint32_t
             v[2 * q + 1] = kept_high(w, a.drop.above) ? v[2 * q + 1] * a.drop.scale : 0.f;
         }
     }
-    store_unit<XT, V8>(row_of<XT>(a.h, a.ldh, row), u, a.cols, v);
+    if constexpr (!V8) store_unit<XT, V8>(row_of<XT>(a.h, a.ldh, row), u, a.cols, v);
+    else if (u * 8 < a.cols) put8<XT>(row_of<XT>(a.h, a.ldh, row), u, narrow8<XT>(v), a.h32);
 }
 
-// WT: the type in which the weight stays in registers, dy's where it is of it, or fp32.
-template <int XT, int RT, int WT, bool V8, int NV>
+// The general form, for rows that start anywhere and widths that are no multiple of 8.
+template <int XT, int RT, int NV>
 __global__ void __launch_bounds__(NORM_THREADS, 1) k_layernorm_backward(const __grid_constant__ LayerNormArgs a) {
     constexpr int E = Map::E;
+    constexpr bool V8 = false;
+    constexpr int WT = ZERO_F32;
     __shared__ __align__(16) float2 ssum[2][32];
     if (threadIdx.x < 64) ssum[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.f, 0.f);
     if (blockDim.x < 64 && threadIdx.x < 32) ssum[1][threadIdx.x] = make_float2(0.f, 0.f);
@@ -155,6 +161,157 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) k_layernorm_backward(const __
                     part[a.cols + c + e] = e % 2 ? q.y : q.x;
                 }
             }
+        }
+    }
+}
+
+// Rows on 16-byte boundaries (zero_layernorm.cuh).  WT: the type in which the
+// weight stays in registers, dy's where it is of it, or fp32.  The rows' mean
+// and rstd are read a row ahead; the block's G parts of dw and db are added in
+// order, so that a block writes one.
+template <int XT, int RT, int WT, int NV>
+__global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const __grid_constant__ LayerNormArgs a) {
+    __shared__ __align__(16) float2 ssum[2][32];
+    const int T = a.T, G = blockDim.x / T, group = threadIdx.x / T, u0 = threadIdx.x - group * T, units = a.units;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = T >> 5, w0 = group * warps;
+    pdl_wait();
+    pdl_launch_next();
+    const uint32_t step = drop_step(a.drop);
+    const float inv_n = 1.f / (float)a.cols;
+    extern __shared__ __align__(16) uint4 ring[];
+    using X = Lane<XT, NV>;
+    using R = Lane<RT, NV>;
+    const int S = a.stages, stage_words = X::words() + 2 * R::words();
+    const int64_t first = group * (int64_t)gridDim.x + blockIdx.x, every = (int64_t)G * gridDim.x;
+    const bool DH = a.r != nullptr;
+    auto copy = [&](int64_t row, int st) {
+        if (row < a.rows) {
+            uint4* at = ring + st * stage_words;
+            X::copy(at, row_of<XT>(a.x, a.ldx, row), u0, T, units);
+            R::copy(at + X::words(), row_of<RT>(a.hin, a.ldhin, row), u0, T, units);
+            if (DH) R::copy(at + X::words() + R::words(), row_of<RT>(a.r, a.ldr, row), u0, T, units);
+        }
+        copies_commit();
+    };
+    for (int s = 0; s < S - 1; ++s) copy(first + s * every, s);
+    Raw8<WT> w[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        float v[8];
+        vector8(a.w, a.wdt, a.w_aligned, a.cols, u0 + j * T, 1.f, v);
+        w[j] = narrow8<WT>(v);
+    }
+    uint64_t dw[NV][4] = {}, db[NV][4] = {};
+    float mean = 0.f, rstd = 0.f;
+    if (first < a.rows) {
+        mean = a.mean[first];
+        rstd = a.rstd[first];
+    }
+    int turn = 0, st = 0;
+    for (int64_t row = first; row < a.rows; row += every, turn ^= 1) {
+        copy(row + (S - 1) * every, st == 0 ? S - 1 : st - 1);
+        float next_mean = 0.f, next_rstd = 0.f;
+        if (row + every < a.rows) {
+            next_mean = a.mean[row + every];
+            next_rstd = a.rstd[row + every];
+        }
+        copies_wait_all_but(S - 1);
+        if (XT == ZERO_F32 || RT == ZERO_F32) __syncwarp();
+        const uint4* at = ring + st * stage_words;
+        st = st == S - 1 ? 0 : st + 1;
+        const uint64_t rr = pack2(rstd, rstd), mm = pack2(-mean, -mean);
+        uint64_t g2 = 0, d2 = 0;
+        // past the row's end dy is 0, and with it every term
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            stay_packed(w[j]);
+            const Raw8<XT> dy = X::read(at, j, u0, T, units);
+            const Raw8<RT> h = R::read(at + X::words(), j, u0, T, units);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint64_t xh = mul2(add2(pair8<RT>(h, q), mm), rr), g = pair8<XT>(dy, q), gw = mul2(g, pair8<WT>(w[j], q));
+                dw[j][q] = fma2(g, xh, dw[j][q]);
+                db[j][q] = add2(g, db[j][q]);
+                g2 = add2(g2, gw);
+                d2 = fma2(gw, xh, d2);
+            }
+        }
+        const float2 gp = unpack2(g2), dp = unpack2(d2);
+        float sx = warp_sum(gp.x + gp.y), sy = warp_sum(dp.x + dp.y);
+        if (warps > 1) {
+            if (lane == 0) ssum[turn][warp] = make_float2(sx, sy);
+            row_barrier(group, T);
+            sx = sy = 0.f;
+#pragma unroll 4
+            for (int k = 0; k < warps; ++k) {
+                const float2 p = ssum[turn][w0 + k];
+                sx += p.x;
+                sy += p.y;
+            }
+        }
+        asm volatile("" ::: "memory");
+        // dr = rstd g w + (dh - rstd c1 - xh rstd c2), the sum in the brackets first
+        const float c1 = -rstd * (sx * inv_n), c2 = -rstd * (sy * inv_n);
+        const uint64_t p1 = pack2(c1, c1), p2 = pack2(c2, c2);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int u = u0 + j * T;
+            stay_packed(w[j]);
+            // again from shared memory: registers hold the sums of dw and db and the weights
+            const Raw8<XT> dy = X::read(at, j, u0, T, units);
+            const Raw8<RT> h = R::read(at + X::words(), j, u0, T, units);
+            Raw8<RT> dh;
+            if (DH) dh = R::read(at + X::words() + R::words(), j, u0, T, units);
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint64_t xh = mul2(add2(pair8<RT>(h, q), mm), rr);
+                const uint64_t t = fma2(xh, p2, DH ? add2(pair8<RT>(dh, q), p1) : p1);
+                const float2 p = unpack2(fma2(mul2(pair8<XT>(dy, q), pair8<WT>(w[j], q)), rr, t));
+                v[2 * q] = p.x;
+                v[2 * q + 1] = p.y;
+            }
+            store_gradients<XT, RT, true>(a, step, row, u, v);
+        }
+        mean = next_mean;
+        rstd = next_rstd;
+        if (XT == ZERO_F32 || RT == ZERO_F32) __syncwarp();      // the next copies land in words that other lanes read
+    }
+    if (!a.part) return;
+    // the groups' parts by shared memory: 4 words of 4 columns for each unit of dw, then of db, threads side by side
+    copies_wait<0>();
+    __syncthreads();
+    float4* P = reinterpret_cast<float4*>(ring);
+    const int n = blockDim.x;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+            const float2 x = unpack2(dw[j][q]), y = unpack2(dw[j][q + 1]), s = unpack2(db[j][q]), t = unpack2(db[j][q + 1]);
+            P[(j * 4 + q / 2) * n + threadIdx.x] = make_float4(x.x, x.y, y.x, y.y);
+            P[(j * 4 + 2 + q / 2) * n + threadIdx.x] = make_float4(s.x, s.y, t.x, t.y);
+        }
+    __syncthreads();
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+    for (int i = threadIdx.x; i < NV * 4 * T; i += n) {
+        const int k = i / T, t = i - k * T, u = t + (k >> 2) * T;
+        if (u >= units) continue;
+        float4 sum = P[k * n + t];
+        for (int g = 1; g < G; ++g) {
+            const float4 p = P[k * n + g * T + t];
+            sum.x += p.x;
+            sum.y += p.y;
+            sum.z += p.z;
+            sum.w += p.w;
+        }
+        float* to = part + (k & 2 ? a.cols : 0) + u * 8 + (k & 1) * 4;
+        if (a.part16) {
+            *reinterpret_cast<float4*>(to) = sum;
+        } else {
+            to[0] = sum.x;
+            to[1] = sum.y;
+            to[2] = sum.z;
+            to[3] = sum.w;
         }
     }
 }
@@ -273,28 +430,27 @@ __global__ void __launch_bounds__(1024) k_layernorm_sums(const __grid_constant__
     st1_any(out, cc, t, dt);
 }
 
-// w16: V8, and the weight in dy's type.
 template <int XT, int RT>
-static const void* pick(bool v8, bool w16, int nv) {
-    switch (nv) {
-        case 2:
-            if (w16) return (const void*)k_layernorm_backward<XT, RT, XT, true, 2>;
-            return v8 ? (const void*)k_layernorm_backward<XT, RT, ZERO_F32, true, 2>
-                      : (const void*)k_layernorm_backward<XT, RT, ZERO_F32, false, 2>;
-        case 4:
-            if (w16) return (const void*)k_layernorm_backward<XT, RT, XT, true, 4>;
-            return v8 ? (const void*)k_layernorm_backward<XT, RT, ZERO_F32, true, 4>
-                      : (const void*)k_layernorm_backward<XT, RT, ZERO_F32, false, 4>;
-        default:
-            return v8 ? (const void*)k_layernorm_backward_long<XT, RT, true>
-                      : (const void*)k_layernorm_backward_long<XT, RT, false>;
-    }
+static const void* general(bool v8, int nv) {
+    if (nv == 2) return (const void*)k_layernorm_backward<XT, RT, 2>;
+    if (nv == 4) return (const void*)k_layernorm_backward<XT, RT, 4>;
+    return v8 ? (const void*)k_layernorm_backward_long<XT, RT, true> : (const void*)k_layernorm_backward_long<XT, RT, false>;
 }
-static const void* layernorm_backward_fn(int xt, int rt, bool v8, bool w16, int nv) {
-    if (xt == ZERO_F32) return pick<ZERO_F32, ZERO_F32>(v8, w16, nv);
-    if (xt == ZERO_BF16)
-        return rt == ZERO_F32 ? pick<ZERO_BF16, ZERO_F32>(v8, w16, nv) : pick<ZERO_BF16, ZERO_BF16>(v8, w16, nv);
-    return rt == ZERO_F32 ? pick<ZERO_F16, ZERO_F32>(v8, w16, nv) : pick<ZERO_F16, ZERO_F16>(v8, w16, nv);
+static const void* general_fn(int xt, int rt, bool v8, int nv) {
+    if (xt == ZERO_F32) return general<ZERO_F32, ZERO_F32>(v8, nv);
+    if (xt == ZERO_BF16) return rt == ZERO_F32 ? general<ZERO_BF16, ZERO_F32>(v8, nv) : general<ZERO_BF16, ZERO_BF16>(v8, nv);
+    return rt == ZERO_F32 ? general<ZERO_F16, ZERO_F32>(v8, nv) : general<ZERO_F16, ZERO_F16>(v8, nv);
+}
+// w16: the weight in dy's type.  nv 4: rows of more than 8192 columns, whose units do not all fit the registers.
+template <int XT, int RT>
+static const void* rows_of(bool w16, int nv) {
+    if (nv == 4) return (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 4>;
+    return w16 ? (const void*)k_layernorm_backward_rows<XT, RT, XT, 2> : (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 2>;
+}
+static const void* rows_fn(int xt, int rt, bool w16, int nv) {
+    if (xt == ZERO_F32) return rows_of<ZERO_F32, ZERO_F32>(w16, nv);
+    if (xt == ZERO_BF16) return rt == ZERO_F32 ? rows_of<ZERO_BF16, ZERO_F32>(w16, nv) : rows_of<ZERO_BF16, ZERO_BF16>(w16, nv);
+    return rt == ZERO_F32 ? rows_of<ZERO_F16, ZERO_F32>(w16, nv) : rows_of<ZERO_F16, ZERO_F16>(w16, nv);
 }
 static const void* sums_long_fn(int xt, int rt) {
     if (xt == ZERO_F32) return (const void*)k_layernorm_sums_long<ZERO_F32, ZERO_F32>;
@@ -371,36 +527,53 @@ int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_ma
     a.part16 = cols % 4 == 0 && aligned(workspace, 16);
     const bool v8 = cols % 8 == 0 && rows_aligned(*dy, rows) && rows_aligned(*h, rows) && (!dr || rows_aligned(*dr, rows)) &&
                     (!dx || rows_aligned(*dx, rows)) && (!dh || rows_aligned(*dh, rows));
-    const NormShape p = shape_of(cols, words_of(dy->dtype) + 2 * words_of(rt), LN_BACKWARD_THREADS);
-    a.stages = p.stages;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* args[] = {&a};
-    int64_t g = (int64_t)p.per_sm * sms;
-    if (g > NORM_MAX_GRID) g = NORM_MAX_GRID;
-    if (g > rows) g = rows;
-    const void* f = layernorm_backward_fn(dy->dtype, rt, v8, v8 && (!weight || weight->dtype == dy->dtype), p.nv);
-    rc = raise_smem(f, p.smem, "zero_layernorm_backward shared-memory size");
-    if (rc != ZERO_OK) return rc;
-    int parts = (int)g;
-    if (p.nv == 0 && a.part && rows > 0) {
-        // dw and db first: dr and dx may be written over dy or dh
-        const int64_t chunks = (cols + 127) / 128;
-        int64_t shares = (8 * (int64_t)sms + chunks - 1) / chunks;
-        if (shares > NORM_MAX_GRID) shares = NORM_MAX_GRID;
-        if (shares > rows) shares = rows;
-        parts = (int)shares;
-        const dim3 grid((unsigned)chunks, (unsigned)shares);
-        rc = cuda_fail(cudaLaunchKernel(sums_long_fn(dy->dtype, rt), grid, dim3(128), args, 0, s),
-                       "zero_layernorm_backward sums launch");
+    int parts = 0;
+    const int words = words_of(dy->dtype) + 2 * words_of(rt), nv = cols <= 8 * 2 * LN_THREADS ? 2 : 4;
+    const RowsShape rs = v8 && rows > 0 ? rows_shape(rows, cols, nv, words, sms) : RowsShape{};
+    if (rs.threads) {
+        const void* f = rows_fn(dy->dtype, rt, !weight || weight->dtype == dy->dtype, nv);
+        a.stages = rs.stages;
+        a.T = rs.T;
+        a.y32 = dr && rows_on_32(*dr, rows);
+        a.h32 = dx && rows_on_32(*dx, rows);
+        parts = rs.grid;
+        // at the end the parts of dw and db lie where the stages were
+        const size_t ends = (size_t)rs.threads * nv * 64, smem = rs.smem > ends ? rs.smem : ends;
+        rc = raise_smem(f, smem, "zero_layernorm_backward shared-memory size");
         if (rc != ZERO_OK) return rc;
-    }
-    if (rows > 0) {
+        rc = cuda_fail(launch_after_previous(f, rs.grid, rs.threads, args, smem, s), "zero_layernorm_backward launch");
+        if (rc != ZERO_OK) return rc;
+    } else if (rows > 0) {
+        NormShape p = shape_of(cols, words, LN_BACKWARD_THREADS);
+        if (v8) p = NormShape{0, NORM_THREADS, 1, 2, 0};
+        a.stages = p.stages;
+        int64_t g = (int64_t)p.per_sm * sms;
+        if (g > NORM_MAX_GRID) g = NORM_MAX_GRID;
+        if (g > rows) g = rows;
+        const void* f = general_fn(dy->dtype, rt, v8, p.nv);
+        rc = raise_smem(f, p.smem, "zero_layernorm_backward shared-memory size");
+        if (rc != ZERO_OK) return rc;
+        parts = (int)g;
+        if (p.nv == 0 && a.part) {
+            // dw and db first: dr and dx may be written over dy or dh
+            const int64_t chunks = (cols + 127) / 128;
+            int64_t shares = (8 * (int64_t)sms + chunks - 1) / chunks;
+            if (shares > NORM_MAX_GRID) shares = NORM_MAX_GRID;
+            if (shares > rows) shares = rows;
+            parts = (int)shares;
+            const dim3 grid((unsigned)chunks, (unsigned)shares);
+            rc = cuda_fail(cudaLaunchKernel(sums_long_fn(dy->dtype, rt), grid, dim3(128), args, 0, s),
+                           "zero_layernorm_backward sums launch");
+            if (rc != ZERO_OK) return rc;
+        }
         if (p.nv == 0) g = rows < 1 << 30 ? rows : 1 << 30;
         rc = cuda_fail(launch_after_previous(f, (int)g, p.threads, args, p.smem, s), "zero_layernorm_backward launch");
         if (rc != ZERO_OK) return rc;
     }
     if (!a.part) return ZERO_OK;
-    SumsArgs sums = {a.part, rows > 0 ? parts : 0, accumulate, cols, {dw ? dw->data : nullptr, db ? db->data : nullptr},
+    SumsArgs sums = {a.part, parts, accumulate, cols, {dw ? dw->data : nullptr, db ? db->data : nullptr},
                      {dw ? dw->dtype : 0, db ? db->dtype : 0}};
     void* sargs[] = {&sums};
     return cuda_fail(launch_after_previous((const void*)k_layernorm_sums, (int)((cols + 31) / 32) * 2, 1024, sargs, 0, s),
