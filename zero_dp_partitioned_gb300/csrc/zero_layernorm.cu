@@ -148,77 +148,85 @@ __global__ void __launch_bounds__(NORM_THREADS, 1)
     }
 }
 
-// Rows on 16-byte boundaries.  WT: the type in which weight and bias stay in
-// registers, x's where they are of it (half the registers) or fp32.
+// Rows on 16-byte boundaries.  WT: the type in which weight and bias lie in
+// shared memory.
 template <int XT, int RT, int WT, int NV>
 __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const __grid_constant__ LayerNormArgs a) {
     __shared__ __align__(16) WarpStats st;
-    const int T = a.T, G = blockDim.x / T, group = threadIdx.x / T, u0 = threadIdx.x - group * T, units = a.units;
+    using X = Lane<XT, NV>;
+    using R = Lane<RT, NV>;
+    using V = Vector<WT>;
+    constexpr int XS = 8 * Elem<XT>::SIZE, RS = 8 * Elem<RT>::SIZE;          // bytes of a unit
+    const int T = a.T, G = blockDim.x / T, group = threadIdx.x / T, units = a.units;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = T >> 5, w0 = group * warps;
-    int mine = 0;                                            // columns of this warp
-#pragma unroll
-    for (int j = 0; j < NV; ++j) mine += max(0, min(256, a.cols - ((u0 & ~31) + j * T) * 8));
+    const int uw = (warp - w0) * NV * 32, left = units - uw;                 // the warp's first unit, units from there
+    const int n = (left - lane + 31) >> 5;                                   // this lane's units (any number above NV: all)
+    const int mine = max(0, min(NV * 256, left * 8));                        // columns of this warp
     const float inv_mine = mine ? 1.f / (float)mine : 0.f, inv_n = 1.f / (float)a.cols;
     if (lane == 0) st.n[warp] = (float)mine;
-    __syncthreads();
     pdl_wait();
     pdl_launch_next();
     const uint32_t step = drop_step(a.drop);
     extern __shared__ __align__(16) uint4 ring[];
-    using X = Lane<XT, NV>;
-    using R = Lane<RT, NV>;
-    const int S = a.stages, stage_words = X::words() + R::words();
+    const int S = a.stages, xwords = (blockDim.x >> 5) * X::WORDS, stage_words = xwords + (blockDim.x >> 5) * R::WORDS;
     const int64_t first = group * (int64_t)gridDim.x + blockIdx.x, every = (int64_t)G * gridDim.x;
-    auto copy = [&](int64_t row, int at_stage) {
-        if (row < a.rows) {
-            uint4* at = ring + at_stage * stage_words;
-            X::copy(at, row_of<XT>(a.x, a.ldx, row), u0, T, units);
-            if (a.r) R::copy(at + X::words(), row_of<RT>(a.r, a.ldr, row), u0, T, units);
+    const uint4 *xat = ring + warp * X::WORDS, *rat = ring + xwords + warp * R::WORDS;
+    const uint32_t xat32 = (uint32_t)__cvta_generic_to_shared(xat), rat32 = (uint32_t)__cvta_generic_to_shared(rat);
+    // this warp's part of the row whose copy comes next, and of the row at hand
+    const char *cx = static_cast<const char*>(a.x) + first * a.ldx * Elem<XT>::SIZE + (int64_t)uw * XS;
+    const char* cr = static_cast<const char*>(a.r) + (a.r ? first * a.ldr * Elem<RT>::SIZE + (int64_t)uw * RS : 0);
+    char* H = static_cast<char*>(a.h) + (a.h ? first * a.ldh * Elem<RT>::SIZE + (int64_t)(uw + lane) * RS : 0);
+    char* Y = static_cast<char*>(a.y) + first * a.ldy * Elem<XT>::SIZE + (int64_t)(uw + lane) * XS;
+    const int64_t dx = every * a.ldx * Elem<XT>::SIZE, dr = every * a.ldr * Elem<RT>::SIZE, dh = every * a.ldh * Elem<RT>::SIZE,
+                  dy = every * a.ldy * Elem<XT>::SIZE;
+    int64_t crow = first, unit = first * units + uw + lane;
+    auto copy = [&](int at_stage) {
+        if (crow < a.rows) {
+            X::copy(xat32 + at_stage * stage_words * 16, cx, left);
+            if (a.r) R::copy(rat32 + at_stage * stage_words * 16, cr, left);
         }
         copies_commit();
+        crow += every;
+        cx += dx;
+        cr += dr;
     };
-    for (int s = 0; s < S - 1; ++s) copy(first + s * every, s);
-    Raw8<WT> w[NV], b[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        float v[8];
-        vector8(a.w, a.wdt, a.w_aligned, a.cols, u0 + j * T, 1.f, v);
-        w[j] = narrow8<WT>(v);
-        vector8(a.b, a.bdt, a.b_aligned, a.cols, u0 + j * T, 0.f, v);
-        b[j] = narrow8<WT>(v);
-    }
+    for (int s = 0; s < S - 1; ++s) copy(s);
+    uint4* const wat = ring + S * stage_words;
+    uint4* const bat = wat + V::W * units;
+    V::fill(wat, a.w, a.wdt, a.w_aligned, a.cols, units, 1.f);
+    V::fill(bat, a.b, a.bdt, a.b_aligned, a.cols, units, 0.f);
+    __syncthreads();
     int turn = 0, at_stage = 0;
-    for (int64_t row = first; row < a.rows; row += every, turn ^= 1) {
+    for (int64_t row = first; row < a.rows; row += every, turn ^= 1, unit += every * units, H += dh, Y += dy) {
         Raw8<RT> r[NV];
-        copy(row + (S - 1) * every, at_stage == 0 ? S - 1 : at_stage - 1);
+        copy(at_stage == 0 ? S - 1 : at_stage - 1);
         copies_wait_all_but(S - 1);
         if (XT == ZERO_F32 || RT == ZERO_F32) __syncwarp();
-        const uint4* at = ring + at_stage * stage_words;
+        const uint4 *xs = xat + at_stage * stage_words, *rs = rat + at_stage * stage_words;
         at_stage = at_stage == S - 1 ? 0 : at_stage + 1;
-        char* H = a.h ? static_cast<char*>(a.h) + row * a.ldh * Elem<RT>::SIZE : nullptr;
         // h as it is stored
         uint64_t s2 = 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int u = u0 + j * T;
-            Unit<XT, true> xu;
-            Unit<RT, true> ru;
-            xu.raw = X::read(at, j, u0, T, units);
-            if (a.r) ru.raw = R::read(at + X::words(), j, u0, T, units);
-            r[j] = (a.drop.on ? drop_add_unit<XT, RT, true>(xu, ru, a.r != nullptr, a.drop, step, row * units + u)
-                              : add_unit<XT, RT, true>(xu, ru, a.r != nullptr))
-                       .raw;
+        for (int j = 0; j < NV; ++j)
+            if (j < n) {
+                Unit<XT, true> xu;
+                Unit<RT, true> ru;
+                xu.raw = X::read(xs, j);
+                if (a.r) ru.raw = R::read(rs, j);
+                r[j] = (a.drop.on ? drop_add_unit<XT, RT, true>(xu, ru, a.r != nullptr, a.drop, step, unit + 32 * j)
+                                  : add_unit<XT, RT, true>(xu, ru, a.r != nullptr))
+                           .raw;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) s2 = add2(s2, pair8<RT>(r[j], q));
-            if (H && u < units) put8<RT>(H, u, r[j], a.h32);
-        }
+                for (int q = 0; q < 4; ++q) s2 = add2(s2, pair8<RT>(r[j], q));
+                if (a.h) put8<RT>(H, 32 * j, r[j], a.h32);
+            }
         const float2 sp = unpack2(s2);
         const float mw = warp_sum(sp.x + sp.y) * inv_mine;
         const uint64_t mw2 = pack2(-mw, -mw);
         uint64_t v2 = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (u0 + j * T < units)
+            if (j < n)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint64_t d = add2(pair8<RT>(r[j], q), mw2);
@@ -242,25 +250,24 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const 
             }
         }
         const float rstd = rsqrtf(fmaf(m2, inv_n, a.eps));
-        if (u0 == 0) {
+        if (warp == w0 && lane == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
         const uint64_t mm = pack2(-mean, -mean), rr = pack2(rstd, rstd);
-        char* Y = static_cast<char*>(a.y) + row * a.ldy * Elem<XT>::SIZE;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float y[8];
-            stay_packed(w[j]);
-            stay_packed(b[j]);
+        for (int j = 0; j < NV; ++j)
+            if (j < n) {
+                const Raw8<WT> w = V::read(wat, uw + lane + 32 * j, units), b = V::read(bat, uw + lane + 32 * j, units);
+                float y[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 v = unpack2(fma2(mul2(add2(pair8<RT>(r[j], q), mm), rr), pair8<WT>(w[j], q), pair8<WT>(b[j], q)));
-                y[2 * q] = v.x;
-                y[2 * q + 1] = v.y;
+                for (int q = 0; q < 4; ++q) {
+                    const float2 v = unpack2(fma2(mul2(add2(pair8<RT>(r[j], q), mm), rr), pair8<WT>(w, q), pair8<WT>(b, q)));
+                    y[2 * q] = v.x;
+                    y[2 * q + 1] = v.y;
+                }
+                put8<XT>(Y, 32 * j, narrow8<XT>(y), a.y32);
             }
-            if (u0 + j * T < units) put8<XT>(Y, u0 + j * T, narrow8<XT>(y), a.y32);
-        }
     }
 }
 
@@ -351,16 +358,16 @@ static const void* general_fn(int xt, int rt, bool v8, int nv) {
     if (xt == ZERO_BF16) return rt == ZERO_F32 ? general<ZERO_BF16, ZERO_F32>(v8, nv) : general<ZERO_BF16, ZERO_BF16>(v8, nv);
     return rt == ZERO_F32 ? general<ZERO_F16, ZERO_F32>(v8, nv) : general<ZERO_F16, ZERO_F16>(v8, nv);
 }
-// w16: weight and bias in x's type.
+// packed: weight and bias in shared memory in x's type, not in fp32.
 template <int XT, int RT>
-static const void* rows_of(bool w16, int nv) {
-    if (nv == 4) return (const void*)k_layernorm_forward_rows<XT, RT, XT, 4>;
-    return w16 ? (const void*)k_layernorm_forward_rows<XT, RT, XT, 2> : (const void*)k_layernorm_forward_rows<XT, RT, ZERO_F32, 2>;
+static const void* rows_of(bool packed, int nv) {
+    if (nv == 2) return (const void*)k_layernorm_forward_rows<XT, RT, ZERO_F32, 2>;
+    return packed ? (const void*)k_layernorm_forward_rows<XT, RT, XT, 4> : (const void*)k_layernorm_forward_rows<XT, RT, ZERO_F32, 4>;
 }
-static const void* rows_fn(int xt, int rt, bool w16, int nv) {
-    if (xt == ZERO_F32) return (const void*)k_layernorm_forward_rows<ZERO_F32, ZERO_F32, ZERO_F32, 2>;
-    if (xt == ZERO_BF16) return rt == ZERO_F32 ? rows_of<ZERO_BF16, ZERO_F32>(w16, nv) : rows_of<ZERO_BF16, ZERO_BF16>(w16, nv);
-    return rt == ZERO_F32 ? rows_of<ZERO_F16, ZERO_F32>(w16, nv) : rows_of<ZERO_F16, ZERO_F16>(w16, nv);
+static const void* rows_fn(int xt, int rt, bool packed, int nv) {
+    if (xt == ZERO_F32) return rows_of<ZERO_F32, ZERO_F32>(false, nv);
+    if (xt == ZERO_BF16) return rt == ZERO_F32 ? rows_of<ZERO_BF16, ZERO_F32>(packed, nv) : rows_of<ZERO_BF16, ZERO_BF16>(packed, nv);
+    return rt == ZERO_F32 ? rows_of<ZERO_F16, ZERO_F32>(packed, nv) : rows_of<ZERO_F16, ZERO_F16>(packed, nv);
 }
 
 }  // namespace zdp
@@ -423,13 +430,13 @@ extern "C" int zero_layernorm_forward(const zero_mat* x, const zero_mat* residua
     void* args[] = {&a};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (v8) {
-        // units of 8 columns a thread: more than two in fp32, values or weights, do not fit its registers, and of rows of
-        // up to 512 columns four would leave half of a warp's lanes without any
         const bool w16 = x->dtype != ZERO_F32 && (!weight || weight->dtype == x->dtype) && (!bias || bias->dtype == x->dtype);
-        const int nv = w16 && cols > 512 ? 4 : 2;
-        const RowsShape p = rows_shape(rows, cols, nv, words, sms);
+        int nv;
+        RowsShape p = rows_shape(rows, cols, words, 4, sms, &nv);
+        const bool packed = !p.threads && w16;
+        if (packed) p = rows_shape(rows, cols, nv = 4, words, 2, sms);
         if (p.threads) {
-            const void* f = rows_fn(x->dtype, rt, w16, nv);
+            const void* f = rows_fn(x->dtype, rt, packed, nv);
             a.h32 = h_out && rows_on_32(*h_out, rows);
             a.y32 = rows_on_32(*y, rows);
             a.stages = p.stages;

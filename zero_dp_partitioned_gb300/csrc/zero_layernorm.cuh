@@ -45,39 +45,35 @@ __device__ __forceinline__ Unit<RT, V8> drop_add_unit(const Unit<XT, V8>& x, con
 // ---------------------------------------------------------------- rows that all start on 16-byte boundaries
 // A block of up to 512 threads stays on its SM.  T of them (whole warps) share a
 // row: G = blockDim.x / T rows are under way at a time, each with its own
-// barrier, and what a block keeps in registers (weights, the weights'
-// gradients) it loads and writes once.  The rows that follow are on their way
-// to each thread's own slots of shared memory.  Against the general form, a
-// block a row and several times as many blocks: 8192 x 1600 bf16 forward 28 us
-// there (weights fetched for every 2 rows, 727 instructions a warp and row).
+// barrier.  A warp has NV * 32 neighbouring units of 8 columns, a lane every 32nd
+// of them, so that the places of its NV units differ by constants.  The rows that
+// follow are on their way to shared memory; weight and bias stay there, in fp32
+// (16-bit ones packed where rows are too long for that).  These kernels are
+// bound by the instructions they issue before HBM, so all that is not arithmetic
+// is done once a row, not once a unit: one block a row, its weights fetched for
+// every 2 rows, took 45 instructions an element and 28 us (8192 x 1600 bf16).
 constexpr int LN_THREADS = 512;
 
-// One matrix of a stage: NV units a thread.  16-bit units are one 16-byte word,
-// copied and read by the same thread.  fp32 units are two, and a thread that
-// copied its own two would touch every sector twice: a warp's lanes copy
-// neighbouring words instead, and read what other lanes copied.
+// One matrix of a stage.  16-bit units are one 16-byte word, copied and read by
+// the same lane.  fp32 units are two, and a lane that copied its own two would
+// touch every sector twice: the lanes copy neighbouring words instead, and read
+// what other lanes of the warp copied.
 template <int DT, int NV>
 struct Lane {
-    static constexpr int W = DT == ZERO_F32 ? 2 : 1;
-    static __device__ __forceinline__ int words() { return NV * W * blockDim.x; }
-    static __device__ __forceinline__ void copy(uint4* at, const void* row, int u0, int T, int units) {
+    static constexpr int W = DT == ZERO_F32 ? 2 : 1, WORDS = NV * W * 32;    // of a warp
+    // from: the warp's first unit of the row; left: units from there to the row's end
+    static __device__ __forceinline__ void copy(uint32_t at, const char* from, int left) {
         const int lane = threadIdx.x & 31;
+        left = left * W - lane;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                // word `from` of the warp's W * 32, which is of unit u
-                const int from = w * 32 + lane, u = u0 - lane + j * T + from / W;
-                if (u < units)
-                    copy16((uint32_t)__cvta_generic_to_shared(at + j * W * blockDim.x + (threadIdx.x - lane) * W + from),
-                           static_cast<const char*>(row) + ((int64_t)(u0 - lane + j * T) * W + from) * 16);
-            }
+        for (int k = 0; k < NV * W; ++k)
+            if (32 * k < left) copy16(at + (32 * k + lane) * 16, from + (32 * k + lane) * 16);
     }
-    static __device__ __forceinline__ Raw8<DT> read(const uint4* at, int j, int u0, int T, int units) {
+    static __device__ __forceinline__ Raw8<DT> read(const uint4* at, int j) {
+        const int lane = threadIdx.x & 31;
         Raw8<DT> v;
 #pragma unroll
-        for (int w = 0; w < W; ++w)
-            v.w[w] = u0 + j * T < units ? at[j * W * blockDim.x + threadIdx.x * W + w] : make_uint4(0, 0, 0, 0);
+        for (int w = 0; w < W; ++w) v.w[w] = at[(32 * j + lane) * W + w];
         return v;
     }
 };
@@ -92,44 +88,70 @@ __device__ __forceinline__ void put8(void* row, int u, const Raw8<DT>& r, bool o
     }
     st8<DT>(row, (int64_t)u * 8, r);
 }
-// Keeps what is computed of v's words inside the loop: the compiler would widen
-// 16-bit weights once, before it, and hold twice the registers.
-template <int DT>
-__device__ __forceinline__ void stay_packed(Raw8<DT>& v) {
-    if constexpr (DT != ZERO_F32) asm("" : "+r"(v.w[0].x), "+r"(v.w[0].y), "+r"(v.w[0].z), "+r"(v.w[0].w));
-}
+// A vector of all columns in shared memory: words w of the units side by side.
+template <int WT>
+struct Vector {
+    static constexpr int W = WT == ZERO_F32 ? 2 : 1;
+    static __device__ __forceinline__ void fill(uint4* to, const void* v, int dt, bool aligned16, int cols, int units, float none) {
+        for (int u = threadIdx.x; u < units; u += blockDim.x) {
+            float t[8];
+            vector8(v, dt, aligned16, cols, u, none, t);
+            const Raw8<WT> r = narrow8<WT>(t);
+#pragma unroll
+            for (int w = 0; w < W; ++w) to[w * units + u] = r.w[w];
+        }
+    }
+    static __device__ __forceinline__ Raw8<WT> read(const uint4* from, int u, int units) {
+        Raw8<WT> r;
+#pragma unroll
+        for (int w = 0; w < W; ++w) r.w[w] = from[w * units + u];
+        return r;
+    }
+};
 // Barrier of the T threads that share a row.
 __device__ __forceinline__ void row_barrier(int group, int T) {
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(T) : "memory");
 }
 
+inline bool rows_on_32(const zero_mat& m, int64_t rows) {
+    return aligned(m.data, 32) && (rows <= 1 || (m.ld * elem_size(m.dtype)) % 32 == 0);
+}
 // Threads a row, rows a block, blocks and stages.  words: 16-byte words of a
-// unit of all matrices read.  threads 0: the row does not fit NV units of 512
-// threads, or two stages of it shared memory.
+// unit of all matrices read; vectors: of all vectors.  threads 0: a row needs
+// more than 512 threads, or two stages of it more than shared memory.
 struct RowsShape {
     int threads, T, stages, grid;
     size_t smem;
 };
-inline bool rows_on_32(const zero_mat& m, int64_t rows) {
-    return aligned(m.data, 32) && (rows <= 1 || (m.ld * elem_size(m.dtype)) % 32 == 0);
-}
-inline RowsShape rows_shape(int64_t rows, int64_t cols, int nv, int words, int sms) {
+inline RowsShape rows_shape(int64_t rows, int64_t cols, int nv, int words, int vectors, int sms) {
     RowsShape s = {};
-    const int64_t units = cols / 8, t = ((units + nv - 1) / nv + 31) / 32 * 32;
+    const int64_t units = cols / 8, t = (units + 32 * nv - 1) / (32 * nv) * 32;
     if (t > LN_THREADS) return s;
     s.T = (int)t;
     int64_t g = (rows + sms - 1) / sms;
     if (g > LN_THREADS / t) g = LN_THREADS / t;
     const size_t stage = (size_t)words * nv * 16 * (size_t)t;      // of one row
-    while (g > 1 && 2 * stage * g > NORM_SM_SMEM) --g;
-    if (2 * stage * g > NORM_SM_SMEM) return s;
+    const size_t fixed = (size_t)vectors * 16 * (size_t)units;
+    while (g > 1 && 2 * stage * g + fixed > NORM_SM_SMEM) --g;
+    if (2 * stage * g + fixed > NORM_SM_SMEM) return s;
     s.threads = (int)(g * t);
     s.stages = 2;
-    while (s.stages < NORM_MAX_STAGES && (s.stages + 1) * stage * g <= NORM_SM_SMEM) ++s.stages;
-    s.smem = s.stages * stage * g;
+    while (s.stages < NORM_MAX_STAGES && (s.stages + 1) * stage * g + fixed <= NORM_SM_SMEM) ++s.stages;
+    s.smem = s.stages * stage * g + fixed;
     const int64_t blocks = (rows + g - 1) / g;
     s.grid = (int)(blocks < sms ? blocks : sms);
     return s;
+}
+
+// Four units a lane, so that what is done once a row counts less (backward 16384
+// x 3456 bf16 in 84 us, 92 with two); two where four leave the block fewer
+// threads: rows too wide to have as many under way (backward 8192 x 8192 bf16 in
+// 105 us, 129 with four; 8192 x 4096 fp32 in 86, 120), few rows, which then
+// have more threads each, and rows that four a lane would leave half a warp of.
+inline RowsShape rows_shape(int64_t rows, int64_t cols, int words, int vectors, int sms, int* nv) {
+    const RowsShape two = rows_shape(rows, cols, 2, words, vectors, sms), four = rows_shape(rows, cols, 4, words, vectors, sms);
+    *nv = cols > 512 && four.threads >= two.threads ? 4 : 2;
+    return *nv == 4 ? four : two;
 }
 
 }  // namespace zdp

@@ -165,42 +165,52 @@ __global__ void __launch_bounds__(NORM_THREADS, 1) k_layernorm_backward(const __
     }
 }
 
-// Rows on 16-byte boundaries (zero_layernorm.cuh).  WT: the type in which the
-// weight stays in registers, dy's where it is of it, or fp32.  The rows' mean
-// and rstd are read a row ahead; the block's G parts of dw and db are added in
-// order, so that a block writes one.
+// Rows on 16-byte boundaries (zero_layernorm.cuh).  Values are read from shared
+// memory for the sums and again for the gradients: registers hold the lane's
+// parts of dw and db.  The rows' mean and rstd are read a row ahead; the block's
+// G parts of dw and db are added in order, so that a block writes one.
 template <int XT, int RT, int WT, int NV>
 __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const __grid_constant__ LayerNormArgs a) {
     __shared__ __align__(16) float2 ssum[2][32];
-    const int T = a.T, G = blockDim.x / T, group = threadIdx.x / T, u0 = threadIdx.x - group * T, units = a.units;
+    using X = Lane<XT, NV>;
+    using R = Lane<RT, NV>;
+    using V = Vector<WT>;
+    constexpr int XS = 8 * Elem<XT>::SIZE, RS = 8 * Elem<RT>::SIZE;          // bytes of a unit
+    const int T = a.T, G = blockDim.x / T, group = threadIdx.x / T, units = a.units;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = T >> 5, w0 = group * warps;
+    const int uw = (warp - w0) * NV * 32, left = units - uw;                 // the warp's first unit, units from there
+    const int n = (left - lane + 31) >> 5;                                   // this lane's units (any number above NV: all)
     pdl_wait();
     pdl_launch_next();
     const uint32_t step = drop_step(a.drop);
     const float inv_n = 1.f / (float)a.cols;
     extern __shared__ __align__(16) uint4 ring[];
-    using X = Lane<XT, NV>;
-    using R = Lane<RT, NV>;
-    const int S = a.stages, stage_words = X::words() + 2 * R::words();
+    const int nw = blockDim.x >> 5, S = a.stages, xwords = nw * X::WORDS, rwords = nw * R::WORDS, stage_words = xwords + 2 * rwords;
     const int64_t first = group * (int64_t)gridDim.x + blockIdx.x, every = (int64_t)G * gridDim.x;
     const bool DH = a.r != nullptr;
-    auto copy = [&](int64_t row, int st) {
-        if (row < a.rows) {
-            uint4* at = ring + st * stage_words;
-            X::copy(at, row_of<XT>(a.x, a.ldx, row), u0, T, units);
-            R::copy(at + X::words(), row_of<RT>(a.hin, a.ldhin, row), u0, T, units);
-            if (DH) R::copy(at + X::words() + R::words(), row_of<RT>(a.r, a.ldr, row), u0, T, units);
+    const uint4 *gat = ring + warp * X::WORDS, *hat = ring + xwords + warp * R::WORDS, *uat = hat + rwords;
+    const uint32_t gat32 = (uint32_t)__cvta_generic_to_shared(gat), hat32 = (uint32_t)__cvta_generic_to_shared(hat), uat32 = hat32 + rwords * 16;
+    const char* cg = static_cast<const char*>(a.x) + first * a.ldx * Elem<XT>::SIZE + (int64_t)uw * XS;
+    const char* ch = static_cast<const char*>(a.hin) + first * a.ldhin * Elem<RT>::SIZE + (int64_t)uw * RS;
+    const char* cu = static_cast<const char*>(a.r) + (DH ? first * a.ldr * Elem<RT>::SIZE + (int64_t)uw * RS : 0);
+    const int64_t dg = every * a.ldx * Elem<XT>::SIZE, dh = every * a.ldhin * Elem<RT>::SIZE, du = every * a.ldr * Elem<RT>::SIZE;
+    int64_t crow = first;
+    auto copy = [&](int st) {
+        if (crow < a.rows) {
+            X::copy(gat32 + st * stage_words * 16, cg, left);
+            R::copy(hat32 + st * stage_words * 16, ch, left);
+            if (DH) R::copy(uat32 + st * stage_words * 16, cu, left);
         }
         copies_commit();
+        crow += every;
+        cg += dg;
+        ch += dh;
+        cu += du;
     };
-    for (int s = 0; s < S - 1; ++s) copy(first + s * every, s);
-    Raw8<WT> w[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        float v[8];
-        vector8(a.w, a.wdt, a.w_aligned, a.cols, u0 + j * T, 1.f, v);
-        w[j] = narrow8<WT>(v);
-    }
+    for (int s = 0; s < S - 1; ++s) copy(s);
+    uint4* const wat = ring + S * stage_words;
+    V::fill(wat, a.w, a.wdt, a.w_aligned, a.cols, units, 1.f);
+    __syncthreads();
     uint64_t dw[NV][4] = {}, db[NV][4] = {};
     float mean = 0.f, rstd = 0.f;
     if (first < a.rows) {
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
     }
     int turn = 0, st = 0;
     for (int64_t row = first; row < a.rows; row += every, turn ^= 1) {
-        copy(row + (S - 1) * every, st == 0 ? S - 1 : st - 1);
+        copy(st == 0 ? S - 1 : st - 1);
         float next_mean = 0.f, next_rstd = 0.f;
         if (row + every < a.rows) {
             next_mean = a.mean[row + every];
@@ -217,25 +227,25 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
         }
         copies_wait_all_but(S - 1);
         if (XT == ZERO_F32 || RT == ZERO_F32) __syncwarp();
-        const uint4* at = ring + st * stage_words;
+        const uint4 *gs = gat + st * stage_words, *hs = hat + st * stage_words, *us = uat + st * stage_words;
         st = st == S - 1 ? 0 : st + 1;
         const uint64_t rr = pack2(rstd, rstd), mm = pack2(-mean, -mean);
         uint64_t g2 = 0, d2 = 0;
-        // past the row's end dy is 0, and with it every term
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            stay_packed(w[j]);
-            const Raw8<XT> dy = X::read(at, j, u0, T, units);
-            const Raw8<RT> h = R::read(at + X::words(), j, u0, T, units);
+        for (int j = 0; j < NV; ++j)
+            if (j < n) {
+                const Raw8<XT> dy = X::read(gs, j);
+                const Raw8<RT> h = R::read(hs, j);
+                const Raw8<WT> w = V::read(wat, uw + lane + 32 * j, units);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint64_t xh = mul2(add2(pair8<RT>(h, q), mm), rr), g = pair8<XT>(dy, q), gw = mul2(g, pair8<WT>(w[j], q));
-                dw[j][q] = fma2(g, xh, dw[j][q]);
-                db[j][q] = add2(g, db[j][q]);
-                g2 = add2(g2, gw);
-                d2 = fma2(gw, xh, d2);
+                for (int q = 0; q < 4; ++q) {
+                    const uint64_t xh = mul2(add2(pair8<RT>(h, q), mm), rr), g = pair8<XT>(dy, q), gw = mul2(g, pair8<WT>(w, q));
+                    dw[j][q] = fma2(g, xh, dw[j][q]);
+                    db[j][q] = add2(g, db[j][q]);
+                    g2 = add2(g2, gw);
+                    d2 = fma2(gw, xh, d2);
+                }
             }
-        }
         const float2 gp = unpack2(g2), dp = unpack2(d2);
         float sx = warp_sum(gp.x + gp.y), sy = warp_sum(dp.x + dp.y);
         if (warps > 1) {
@@ -249,30 +259,29 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
                 sy += p.y;
             }
         }
-        asm volatile("" ::: "memory");
+        asm volatile("" ::: "memory");                       // the values are read again, not kept
         // dr = rstd g w + (dh - rstd c1 - xh rstd c2), the sum in the brackets first
         const float c1 = -rstd * (sx * inv_n), c2 = -rstd * (sy * inv_n);
         const uint64_t p1 = pack2(c1, c1), p2 = pack2(c2, c2);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int u = u0 + j * T;
-            stay_packed(w[j]);
-            // again from shared memory: registers hold the sums of dw and db and the weights
-            const Raw8<XT> dy = X::read(at, j, u0, T, units);
-            const Raw8<RT> h = R::read(at + X::words(), j, u0, T, units);
-            Raw8<RT> dh;
-            if (DH) dh = R::read(at + X::words() + R::words(), j, u0, T, units);
-            float v[8];
+        for (int j = 0; j < NV; ++j)
+            if (j < n) {
+                const Raw8<XT> dy = X::read(gs, j);
+                const Raw8<RT> h = R::read(hs, j);
+                const Raw8<WT> w = V::read(wat, uw + lane + 32 * j, units);
+                Raw8<RT> dh;
+                if (DH) dh = R::read(us, j);
+                float v[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint64_t xh = mul2(add2(pair8<RT>(h, q), mm), rr);
-                const uint64_t t = fma2(xh, p2, DH ? add2(pair8<RT>(dh, q), p1) : p1);
-                const float2 p = unpack2(fma2(mul2(pair8<XT>(dy, q), pair8<WT>(w[j], q)), rr, t));
-                v[2 * q] = p.x;
-                v[2 * q + 1] = p.y;
+                for (int q = 0; q < 4; ++q) {
+                    const uint64_t xh = mul2(add2(pair8<RT>(h, q), mm), rr);
+                    const uint64_t t = fma2(xh, p2, DH ? add2(pair8<RT>(dh, q), p1) : p1);
+                    const float2 p = unpack2(fma2(mul2(pair8<XT>(dy, q), pair8<WT>(w, q)), rr, t));
+                    v[2 * q] = p.x;
+                    v[2 * q + 1] = p.y;
+                }
+                store_gradients<XT, RT, true>(a, step, row, uw + lane + 32 * j, v);
             }
-            store_gradients<XT, RT, true>(a, step, row, u, v);
-        }
         mean = next_mean;
         rstd = next_rstd;
         if (XT == ZERO_F32 || RT == ZERO_F32) __syncwarp();      // the next copies land in words that other lanes read
@@ -282,23 +291,23 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
     copies_wait<0>();
     __syncthreads();
     float4* P = reinterpret_cast<float4*>(ring);
-    const int n = blockDim.x;
+    const int all = blockDim.x;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int q = 0; q < 4; q += 2) {
             const float2 x = unpack2(dw[j][q]), y = unpack2(dw[j][q + 1]), s = unpack2(db[j][q]), t = unpack2(db[j][q + 1]);
-            P[(j * 4 + q / 2) * n + threadIdx.x] = make_float4(x.x, x.y, y.x, y.y);
-            P[(j * 4 + 2 + q / 2) * n + threadIdx.x] = make_float4(s.x, s.y, t.x, t.y);
+            P[(j * 4 + q / 2) * all + threadIdx.x] = make_float4(x.x, x.y, y.x, y.y);
+            P[(j * 4 + 2 + q / 2) * all + threadIdx.x] = make_float4(s.x, s.y, t.x, t.y);
         }
     __syncthreads();
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
-    for (int i = threadIdx.x; i < NV * 4 * T; i += n) {
-        const int k = i / T, t = i - k * T, u = t + (k >> 2) * T;
+    for (int i = threadIdx.x; i < NV * 4 * T; i += all) {
+        const int k = i / T, t = i - k * T, u = (t >> 5) * NV * 32 + (k >> 2) * 32 + (t & 31);
         if (u >= units) continue;
-        float4 sum = P[k * n + t];
+        float4 sum = P[k * all + t];
         for (int g = 1; g < G; ++g) {
-            const float4 p = P[k * n + g * T + t];
+            const float4 p = P[k * all + g * T + t];
             sum.x += p.x;
             sum.y += p.y;
             sum.z += p.z;
@@ -441,16 +450,16 @@ static const void* general_fn(int xt, int rt, bool v8, int nv) {
     if (xt == ZERO_BF16) return rt == ZERO_F32 ? general<ZERO_BF16, ZERO_F32>(v8, nv) : general<ZERO_BF16, ZERO_BF16>(v8, nv);
     return rt == ZERO_F32 ? general<ZERO_F16, ZERO_F32>(v8, nv) : general<ZERO_F16, ZERO_F16>(v8, nv);
 }
-// w16: the weight in dy's type.  nv 4: rows of more than 8192 columns, whose units do not all fit the registers.
+// packed: the weight in shared memory in dy's type, not in fp32.
 template <int XT, int RT>
-static const void* rows_of(bool w16, int nv) {
-    if (nv == 4) return (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 4>;
-    return w16 ? (const void*)k_layernorm_backward_rows<XT, RT, XT, 2> : (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 2>;
+static const void* rows_of(bool packed, int nv) {
+    if (nv == 2) return (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 2>;
+    return packed ? (const void*)k_layernorm_backward_rows<XT, RT, XT, 4> : (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 4>;
 }
-static const void* rows_fn(int xt, int rt, bool w16, int nv) {
-    if (xt == ZERO_F32) return rows_of<ZERO_F32, ZERO_F32>(w16, nv);
-    if (xt == ZERO_BF16) return rt == ZERO_F32 ? rows_of<ZERO_BF16, ZERO_F32>(w16, nv) : rows_of<ZERO_BF16, ZERO_BF16>(w16, nv);
-    return rt == ZERO_F32 ? rows_of<ZERO_F16, ZERO_F32>(w16, nv) : rows_of<ZERO_F16, ZERO_F16>(w16, nv);
+static const void* rows_fn(int xt, int rt, bool packed, int nv) {
+    if (xt == ZERO_F32) return rows_of<ZERO_F32, ZERO_F32>(false, nv);
+    if (xt == ZERO_BF16) return rt == ZERO_F32 ? rows_of<ZERO_BF16, ZERO_F32>(packed, nv) : rows_of<ZERO_BF16, ZERO_BF16>(packed, nv);
+    return rt == ZERO_F32 ? rows_of<ZERO_F16, ZERO_F32>(packed, nv) : rows_of<ZERO_F16, ZERO_F16>(packed, nv);
 }
 static const void* sums_long_fn(int xt, int rt) {
     if (xt == ZERO_F32) return (const void*)k_layernorm_sums_long<ZERO_F32, ZERO_F32>;
@@ -530,10 +539,18 @@ int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_ma
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* args[] = {&a};
     int parts = 0;
-    const int words = words_of(dy->dtype) + 2 * words_of(rt), nv = cols <= 8 * 2 * LN_THREADS ? 2 : 4;
-    const RowsShape rs = v8 && rows > 0 ? rows_shape(rows, cols, nv, words, sms) : RowsShape{};
+    const int words = words_of(dy->dtype) + 2 * words_of(rt);
+    const bool w16 = dy->dtype != ZERO_F32 && (!weight || weight->dtype == dy->dtype);
+    RowsShape rs = {};
+    int nv = 4;
+    bool packed = false;
+    if (v8 && rows > 0) {
+        rs = rows_shape(rows, cols, words, 2, sms, &nv);
+        packed = !rs.threads && w16;
+        if (packed) rs = rows_shape(rows, cols, nv = 4, words, 1, sms);
+    }
     if (rs.threads) {
-        const void* f = rows_fn(dy->dtype, rt, !weight || weight->dtype == dy->dtype, nv);
+        const void* f = rows_fn(dy->dtype, rt, packed, nv);
         a.stages = rs.stages;
         a.T = rs.T;
         a.y32 = dr && rows_on_32(*dr, rows);
