@@ -922,7 +922,9 @@ size_t zero_gated_forward_workspace_bytes(const zero_mat* x, const zero_mat* gat
  *            once
  * workspace  zero_gated_backward_workspace_bytes of the same arguments (NULL for
  *            what is not read), as for the forward pass: copies of what the
- *            products read and whose rows do not start on 16-byte boundaries
+ *            products read and whose rows do not start on 16-byte boundaries,
+ *            and, where few rows and columns leave most of the GPU idle, fp32
+ *            parts of dx's sum (20 MB at most), which are added in order
  * With no rows dgate_w and dup_w are 0 (or unchanged), with ff = 0 dx is.
  * Errors as zero_gated_forward. */
 int zero_gated_backward(const zero_mat* dh, const zero_mat* gate, const zero_mat* up, const zero_mat* x,

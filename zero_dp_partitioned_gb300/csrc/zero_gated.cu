@@ -20,7 +20,7 @@
 //
 // A block stays and walks tiles.  Warp 0's first lane copies stages of 64
 // elements of k into shared memory (TMA, 128-byte swizzle), warp 1's first lane
-// (of the first block) issues the four products of a stage, warps 2 to 5 read
+// (of the first block) issues the four products of a stage, warps 2 to 9 read
 // the accumulator back and finish it; two accumulators of 256 columns fill the
 // tensor memory, so that one tile's end runs beside the next one's products.
 // Operands whose k runs along the rows (Wg, Wu in dx; all in dW) are read where
@@ -35,18 +35,23 @@
 
 namespace zdp {
 
-constexpr int GT_THREADS = 192;
-constexpr int GT_TILE = 256;                  // rows and columns of a pair's tile
-constexpr int GT_HALF = 128;                  // of a block's operands
+constexpr int GT_EPI_WARPS = 8;               // two for each 32 lanes of tensor memory, a half of the columns each
+constexpr int GT_THREADS = 64 + 32 * GT_EPI_WARPS;
+constexpr int GT_TILE = 256;                  // rows (and, but for few rows, columns) of a pair's tile
+constexpr int GT_HALF = 128;                  // rows of a block's A
 constexpr int GT_K = 64;                      // elements of k in a stage: 128 bytes
-constexpr int GT_OPERAND = GT_HALF * GT_K * 2;
+constexpr int GT_A = GT_HALF * GT_K * 2;      // bytes of a block's A in a stage
 constexpr int GT_CHUNK = GT_K * 128;          // 64 columns by 64 rows of an operand whose k runs along the rows
-constexpr int GT_STAGE = 2 * GT_OPERAND;
-constexpr int GT_STAGES = 6;
 constexpr int GT_HEADER = 1024;
-constexpr int GT_EPI = 4 * 32 * 17 * 4;       // a 32 x 16 piece for each epilogue warp, padded
-constexpr int GT_SMEM = GT_STAGES * GT_STAGE + 2048 + GT_EPI;
-static_assert(GT_SMEM <= 232448, "shared memory of a block");
+constexpr int GT_EPI = GT_EPI_WARPS * 32 * 17 * 4;      // a 32 x 16 piece for each of its warps, padded
+
+// N: rows of B of a pair, half of them in each block.
+template <int N>
+struct GtShape {
+    static constexpr int B = N / 2 * GT_K * 2, STAGE = GT_A + B, STAGES = N == 256 ? 6 : 8;
+    static constexpr int SMEM = STAGES * STAGE + 2048 + GT_EPI;
+    static_assert(SMEM <= 232448 && STAGE % 1024 == 0 && STAGES <= 8, "shared memory of a block");
+};
 
 enum { GT_FORWARD = 0, GT_DX = 1, GT_DW = 2 };
 
@@ -60,6 +65,8 @@ struct GatedArgs {
     int64_t rows, cols;                       // of an output
     int m_tiles, n_tiles, half_tiles;         // tiles; dW: m_tiles of dWg
     int k_steps, k_half;                      // stages of a tile; dx: of them with gate
+    int split;                                // dx: parts of its sum, each to rows of its own (the parts' outputs follow one another)
+    int a_rows;                               // rows of A's boxes: 128, or what few rows need (the second block then has none)
     int act, accumulate;
     int32_t* status;
     unsigned spin_limit, drain_limit;
@@ -141,10 +148,10 @@ __device__ __forceinline__ uint64_t gt_desc(uint32_t addr) {
 }
 // 16 elements of k further on, in the descriptor's units of 16 bytes
 template <bool K_ROWS> constexpr int GT_K16 = K_ROWS ? 16 * 128 >> 4 : 16 * 2 >> 4;
-// Instruction descriptor: 16-bit operands, fp32 accumulator, 256 x 256.
-template <int DT, bool A_ROWS, bool B_ROWS>
+// Instruction descriptor: 16-bit operands, fp32 accumulator, 256 x N.
+template <int DT, int N, bool A_ROWS, bool B_ROWS>
 constexpr uint32_t GT_IDESC = 1u << 4 | (DT == ZERO_BF16 ? 1u << 7 | 1u << 10 : 0u) | (A_ROWS ? 1u << 15 : 0u) |
-                              (B_ROWS ? 1u << 16 : 0u) | (uint32_t)(GT_TILE >> 3) << 17 | (uint32_t)(GT_TILE >> 4) << 24;
+                              (B_ROWS ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(GT_TILE >> 4) << 24;
 
 // ---------------------------------------------------------------- activations
 // Both are g times a sigmoid s; the slope is s + g s (1 - s) t' with t the
@@ -257,13 +264,16 @@ __device__ __forceinline__ void gt_tile(const GatedArgs& a, int t, int& m, int& 
     n = n0 + r % w;
 }
 
-template <int MODE, int DT>
+template <int MODE, int DT, int N>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     k_gated(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
             const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
             const __grid_constant__ GatedArgs a) {
     constexpr bool A_ROWS = MODE == GT_DW, B_ROWS = MODE != GT_FORWARD;      // k along the rows
-    constexpr int N_TILE = MODE == GT_FORWARD ? GT_HALF : GT_TILE;           // columns of the output
+    constexpr int N_TILE = MODE == GT_FORWARD ? N / 2 : N;                   // columns of the output
+    using S = GtShape<N>;
+    constexpr int STAGES = S::STAGES;
+    static_assert(!B_ROWS || N == 256, "two chunks of B");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023) & ~1023u;
     uint8_t* head = smem_raw + (base - raw);
@@ -277,16 +287,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3;                            // the 32 lanes of tensor memory this warp can reach
     const uint32_t rank = blockIdx.x & 1;                    // in the pair
-    float* epi = reinterpret_cast<float*>(head + GT_HEADER + GT_STAGES * GT_STAGE) + quarter * 32 * 17;
+    float* epi = reinterpret_cast<float*>(head + GT_HEADER + STAGES * S::STAGE) + (warp & 7) * 32 * 17;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < GT_STAGES; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(acc_full + 8 * s, 1);
-            mbar_init(acc_free + 8 * s, 8);
+            mbar_init(acc_free + 8 * s, 2 * GT_EPI_WARPS);
         }
         mbar_init(drained, 1);
         fence_mbar_init();
@@ -311,7 +321,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     pdl_wait();
     pdl_launch_next();
 
-    const int n_tiles = a.m_tiles * a.n_tiles, first = blockIdx.x >> 1, step = gridDim.x >> 1, K = a.k_steps;
+    // this pair's tiles, and the stages of the part of the sum that a tile stands for
+    const int n_parts = a.m_tiles * a.n_tiles, n_tiles = n_parts * a.split, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const auto part_of = [&](int t, int& tile, int& k0, int& k1) {
+        const int part = MODE == GT_DX ? t / n_parts : 0;
+        tile = MODE == GT_DX ? t - part * n_parts : t;
+        k0 = MODE == GT_DX ? (int)((int64_t)a.k_steps * part / a.split) : 0;
+        k1 = MODE == GT_DX ? (int)((int64_t)a.k_steps * (part + 1) / a.split) : a.k_steps;
+        return part;
+    };
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) {
@@ -319,13 +337,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
             int st = 0, count = 0;
             uint32_t phase = 0;
             for (int t = first; t < n_tiles && ok; t += step) {
-                int m, n;
-                gt_tile(a, t, m, n);
+                int m, n, tile, k0, k1;
+                part_of(t, tile, k0, k1);
+                gt_tile(a, tile, m, n);
                 const bool second = MODE == GT_DW && m >= a.half_tiles;
                 const int am = (second ? m - a.half_tiles : m) * GT_TILE + (int)rank * GT_HALF;
-                const int bn = MODE == GT_FORWARD ? n * GT_HALF : n * GT_TILE + (int)rank * GT_HALF;
-                for (int k = 0; k < K; ++k) {
-                    if (count >= GT_STAGES && !pair_wait<false>(empty + 8 * st, phase ^ 1, a.spin_limit, stop)) {
+                const int bn = MODE == GT_FORWARD ? n * N_TILE : n * N + (int)rank * (N / 2);
+                const uint32_t bytes = (a.a_rows < GT_HALF ? a.a_rows * (GT_K * 2) : 2 * GT_A) + 2 * S::B;
+                for (int k = k0; k < k1; ++k) {
+                    if (count >= STAGES && !pair_wait<false>(empty + 8 * st, phase ^ 1, a.spin_limit, stop)) {
                         ok = false;
                         break;
                     }
@@ -334,30 +354,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                     const CUtensorMap* A = second || up ? &a1 : &a0;
                     const CUtensorMap* B = (MODE == GT_FORWARD && rank) || up ? &b1 : &b0;
                     // rows and columns past the end read as 0
-                    const uint32_t bar = full0 + 8 * st, at = stages + st * GT_STAGE;
-                    if (rank == 0) mbar_expect_tx(full + 8 * st, 2 * GT_STAGE);
+                    const uint32_t bar = full0 + 8 * st, at = stages + st * S::STAGE;
+                    if (rank == 0) mbar_expect_tx(full + 8 * st, bytes);
                     if (A_ROWS) {
                         tma_pair(at, A, am, kk, bar);
                         tma_pair(at + GT_CHUNK, A, am + 64, kk, bar);
-                    } else {
+                    } else if (rank == 0 || a.a_rows == GT_HALF) {
+                        // of few rows only the boxes' are loaded; what else lies in A's place is multiplied, but not stored
                         tma_pair(at, A, kk, am, bar);
                     }
                     if (B_ROWS) {
-                        tma_pair(at + GT_OPERAND, B, bn, kk, bar);
-                        tma_pair(at + GT_OPERAND + GT_CHUNK, B, bn + 64, kk, bar);
+                        tma_pair(at + GT_A, B, bn, kk, bar);
+                        tma_pair(at + GT_A + GT_CHUNK, B, bn + 64, kk, bar);
                     } else {
-                        tma_pair(at + GT_OPERAND, B, kk, bn, bar);
+                        tma_pair(at + GT_A, B, kk, bn, bar);
                     }
                     *loaded = ++count;
-                    if (++st == GT_STAGES) {
+                    if (++st == STAGES) {
                         st = 0;
                         phase ^= 1;
                     }
                 }
             }
             // the last stages' releases come from the first block: this one does not leave before them
-            for (int c = max(0, count - GT_STAGES); c < count && ok; ++c)
-                ok = pair_wait<false>(empty + 8 * (c % GT_STAGES), (uint32_t)(c / GT_STAGES) & 1, a.spin_limit, stop);
+            for (int c = max(0, count - STAGES); c < count && ok; ++c)
+                ok = pair_wait<false>(empty + 8 * (c % STAGES), (uint32_t)(c / STAGES) & 1, a.spin_limit, stop);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
@@ -365,25 +386,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
             uint32_t phase = 0;
             for (int t = first; t < n_tiles && ok; t += step, ++n) {
                 const int acc = n & 1;
+                int tile, k0, k1;
+                part_of(t, tile, k0, k1);
                 if (n >= 2 && !pair_wait<true>(acc_free + 8 * acc, ((n - 2) >> 1) & 1, a.spin_limit, stop)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + acc * GT_TILE;
-                for (int k = 0; k < K; ++k) {
+                for (int k = k0; k < k1; ++k) {
                     if (!pair_wait<true>(full + 8 * st, phase, a.spin_limit, stop)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t at = stages + st * GT_STAGE;
-                    const uint64_t da = gt_desc<A_ROWS>(at), db = gt_desc<B_ROWS>(at + GT_OPERAND);
+                    const uint32_t at = stages + st * S::STAGE;
+                    const uint64_t da = gt_desc<A_ROWS>(at), db = gt_desc<B_ROWS>(at + GT_A);
 #pragma unroll
                     for (int q = 0; q < GT_K / 16; ++q)
-                        pair_mma(d, da + q * GT_K16<A_ROWS>, db + q * GT_K16<B_ROWS>, GT_IDESC<DT, A_ROWS, B_ROWS>, k > 0 || q > 0);
+                        pair_mma(d, da + q * GT_K16<A_ROWS>, db + q * GT_K16<B_ROWS>, GT_IDESC<DT, N, A_ROWS, B_ROWS>, k > k0 || q > 0);
                     pair_commit(empty + 8 * st);
-                    if (++st == GT_STAGES) {
+                    if (++st == STAGES) {
                         st = 0;
                         phase ^= 1;
                     }
@@ -394,10 +417,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
         }
     } else {
         const uint32_t free0 = block_addr(acc_free, 0);
+        constexpr int HALF = N_TILE / 2;
+        const int from = (warp - 2) / 4 * HALF;               // this warp's columns of the tile
         int n = 0;
         for (int t = first; t < n_tiles; t += step, ++n) {
-            int m, nt;
-            gt_tile(a, t, m, nt);
+            int m, nt, tile, k0, k1;
+            const int part = part_of(t, tile, k0, k1);
+            gt_tile(a, tile, m, nt);
             const int acc = n & 1;
             ok = pair_wait<false>(acc_full + 8 * acc, (n >> 1) & 1, a.spin_limit, stop);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -409,23 +435,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
             const bool second = MODE == GT_DW && m >= a.half_tiles;
             const int64_t row = (int64_t)(second ? m - a.half_tiles : m) * GT_TILE + (int)rank * GT_HALF + quarter * 32 + lane;
             const int64_t c0 = (int64_t)nt * N_TILE;
+            GatedOut o = a.o[MODE == GT_DW && second ? 1 : 0];
+            if (MODE == GT_DX && a.split > 1) o.p = static_cast<float*>(o.p) + part * a.rows * o.ld;
+            const auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(free0 + 8 * acc);
+            };
+            // a warp whose rows are all past the end has nothing to store
+            if (row - lane >= a.rows) {
+                release();
+                continue;
+            }
 #pragma unroll 1
-            for (int col = 0; col < N_TILE; col += 16) {
+            for (int col = from; col < from + HALF; col += MODE == GT_FORWARD ? 16 : 32) {
                 uint32_t v[16], w[16];
                 float f[16];
                 __syncwarp();
                 tc_ld16(d + col, v);
-                if (MODE == GT_FORWARD) tc_ld16(d + GT_HALF + col, w);
+                tc_ld16(d + col + (MODE == GT_FORWARD ? N / 2 : 16), w);
                 tc_wait_ld();
-                if (col + 16 == N_TILE) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_at(free0 + 8 * acc);
-                }
+                if (col + (MODE == GT_FORWARD ? 16 : 32) == from + HALF) release();
                 if (MODE == GT_FORWARD) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) f[e] = act_value(__uint_as_float(v[e]), a.act) * __uint_as_float(w[e]);
-                    gt_put16<DT>(a.o[0], a.rows, a.cols, row, c0 + col, f, false, epi);
+                    gt_put16<DT>(o, a.rows, a.cols, row, c0 + col, f, false, epi);
                     if (a.o[1].p) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(v[e]);
@@ -437,7 +471,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(v[e]);
-                    gt_put16<DT>(a.o[second], a.rows, a.cols, row, c0 + col, f, a.accumulate, epi);
+                    gt_put16<DT>(o, a.rows, a.cols, row, c0 + col, f, a.accumulate, epi);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(w[e]);
+                    gt_put16<DT>(o, a.rows, a.cols, row, c0 + col + 16, f, a.accumulate, epi);
                 }
             }
         }
@@ -456,8 +493,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     // after a stop of either block, the loads of both, which the first block's barriers count
     if (rank == 0 && threadIdx.x == 0 && (*stop || read_at(block_addr(base + 204, 1)))) {
         const int most = max(*loaded, read_at(block_addr(base + 208, 1)));
-        for (int c = max(0, most - GT_STAGES); c < most; ++c)
-            pair_wait<false>(full + 8 * (c % GT_STAGES), (uint32_t)(c / GT_STAGES) & 1, a.drain_limit, nullptr);
+        for (int c = max(0, most - STAGES); c < most; ++c)
+            pair_wait<false>(full + 8 * (c % STAGES), (uint32_t)(c / STAGES) & 1, a.drain_limit, nullptr);
     }
     __syncthreads();
     cluster_arrive();
@@ -561,6 +598,35 @@ __global__ void __launch_bounds__(256) k_gated_zero(void* d, int64_t ld, int64_t
     }
 }
 
+// The parts of a sum over k added in order and rounded.  A thread four columns of
+// a row; the parts' columns are padded to a multiple of 8.
+__global__ void __launch_bounds__(256) k_gated_join(const float* parts, int n, int64_t ldp, int64_t rows, int64_t cols, GatedOut o) {
+    pdl_wait();
+    pdl_launch_next();
+    const int64_t quads = ldp / 4;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * quads; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t row = i / quads, c = (i - row * quads) * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < n; ++p) {
+            const float4 v = *reinterpret_cast<const float4*>(parts + (p * rows + row) * ldp + c);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        const float f[4] = {s.x, s.y, s.z, s.w};
+        if (o.store && c + 4 <= cols) {
+            const uint2 w = o.dt == ZERO_BF16 ? make_uint2(Half16<ZERO_BF16>::narrow2(f[0], f[1]), Half16<ZERO_BF16>::narrow2(f[2], f[3]))
+                                              : make_uint2(Half16<ZERO_F16>::narrow2(f[0], f[1]), Half16<ZERO_F16>::narrow2(f[2], f[3]));
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(o.p) + row * o.ld + c) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < cols) st1_any(o.p, row * o.ld + c + e, f[e], o.dt);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- host
 constexpr unsigned GT_TYPES = 1u << ZERO_F16 | 1u << ZERO_BF16;
 constexpr int64_t GT_MOST = INT32_MAX / 2;
@@ -621,26 +687,52 @@ struct Maker {
         return {m.data, m.ld, m.dtype, on(32) ? 32 : on(16) ? 16 : 0};
     }
     void product(int mode, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1, GatedArgs& a,
-                 int32_t* status) {
+                 int32_t* status, int n = 256) {
         if (rc != ZERO_OK) return;
         a.status = status;
         const char* e = std::getenv("ZERO_GB300_SPIN_LIMIT");
         a.spin_limit = e ? (unsigned)std::strtoul(e, nullptr, 10) : SPIN_LIMIT;
         a.drain_limit = SPIN_LIMIT;
+        if (a.split < 1) a.split = 1;
+        if (!a.a_rows) a.a_rows = GT_HALF;
         const bool bf = dt == ZERO_BF16;
-        const void* f = mode == GT_FORWARD ? (bf ? (const void*)k_gated<GT_FORWARD, ZERO_BF16> : (const void*)k_gated<GT_FORWARD, ZERO_F16>)
-                        : mode == GT_DX    ? (bf ? (const void*)k_gated<GT_DX, ZERO_BF16> : (const void*)k_gated<GT_DX, ZERO_F16>)
-                                           : (bf ? (const void*)k_gated<GT_DW, ZERO_BF16> : (const void*)k_gated<GT_DW, ZERO_F16>);
-        rc = raise_smem(f, GT_SMEM, call);
+        const void* f = mode == GT_FORWARD
+                            ? (n == 256 ? (bf ? (const void*)k_gated<GT_FORWARD, ZERO_BF16, 256> : (const void*)k_gated<GT_FORWARD, ZERO_F16, 256>)
+                                        : (bf ? (const void*)k_gated<GT_FORWARD, ZERO_BF16, 128> : (const void*)k_gated<GT_FORWARD, ZERO_F16, 128>))
+                        : mode == GT_DX ? (bf ? (const void*)k_gated<GT_DX, ZERO_BF16, 256> : (const void*)k_gated<GT_DX, ZERO_F16, 256>)
+                                        : (bf ? (const void*)k_gated<GT_DW, ZERO_BF16, 256> : (const void*)k_gated<GT_DW, ZERO_F16, 256>);
+        const size_t smem = n == 256 ? GtShape<256>::SMEM : GtShape<128>::SMEM;
+        rc = raise_smem(f, smem, call);
         if (rc != ZERO_OK) return;
-        const int tiles = a.m_tiles * a.n_tiles, pairs = sms / 2;
+        const int tiles = a.m_tiles * a.n_tiles * a.split, pairs = sms / 2;
         void* args[] = {const_cast<CUtensorMap*>(&a0), const_cast<CUtensorMap*>(&a1), const_cast<CUtensorMap*>(&b0),
                         const_cast<CUtensorMap*>(&b1), &a};
-        rc = cuda_fail(launch_after_previous(f, 2 * (tiles < pairs ? tiles : pairs), GT_THREADS, args, GT_SMEM, s), call);
+        rc = cuda_fail(launch_after_previous(f, 2 * (tiles < pairs ? tiles : pairs), GT_THREADS, args, smem, s), call);
     }
 };
 
 static int tiles_of(int64_t n, int tile) { return (int)((n + tile - 1) / tile); }
+
+// Rows of A's boxes: of up to 128 rows the multiple of 8 that holds them.
+// Rows past the end cost the loads as much as others, and more (one token
+// through 4096 x 14336: 81 us with boxes of 128 rows, where 100 tokens took 52).
+static int boxes_of(int64_t rows) { return rows > GT_HALF ? GT_HALF : (int)((rows + 7) / 8 * 8); }
+
+// Parts of dx's sum where its tiles leave more than half of the pairs idle:
+// as many as all run at once, of 8 stages at least.  Counted in a GB300's 76 pairs,
+// whatever the device, since the workspace's size follows from it.
+constexpr int GT_PAIRS = 76;
+static int parts_of(int64_t rows, int64_t cols, int64_t ff) {
+    const int64_t tiles = (int64_t)tiles_of(rows, GT_TILE) * tiles_of(cols, GT_TILE), steps = 2 * (int64_t)tiles_of(ff, GT_K);
+    int64_t n = tiles < GT_PAIRS ? GT_PAIRS / tiles : 1;
+    if (n > steps / 8) n = steps / 8;
+    return n < 2 ? 1 : (int)n;
+}
+static int64_t parts_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
+static size_t parts_bytes(int64_t rows, int64_t cols, int64_t ff) {
+    const int n = parts_of(rows, cols, ff);
+    return n > 1 ? (size_t)n * (size_t)rows * (size_t)parts_ld(cols) * 4 : 0;
+}
 
 static int check_sizes(int64_t rows, int64_t cols, int64_t ff, int act, const char* call) {
     if (rows < 0 || cols < 0 || ff < 0) return refuse(ZERO_EINVAL, call, "rows, cols or ff", " negative");
@@ -701,7 +793,11 @@ int zero_gated_forward(const zero_mat* x, const zero_mat* gate_w, const zero_mat
         return mk.rc;
     }
     const zero_mat X = mk.packed(*x, rows, cols), G = mk.packed(*gate_w, ff, cols), U = mk.packed(*up_w, ff, cols);
-    const CUtensorMap xm = mk.map(X, rows, cols, GT_HALF), gm = mk.map(G, ff, cols, GT_HALF), um = mk.map(U, ff, cols, GT_HALF);
+    // Tiles of 128 columns, or, where all rows are in one tile and the weights' reads are what takes time, of 64 if that
+    // shares them out more evenly (14336 columns over 76 pairs: 3 rounds of half the size for 2)
+    const int pairs = sms / 2, wide = tiles_of(ff, GT_HALF), narrow = tiles_of(ff, GT_HALF / 2);
+    const int n = rows <= GT_TILE && (narrow + pairs - 1) / pairs < 2 * ((wide + pairs - 1) / pairs) ? 128 : 256;
+    const CUtensorMap xm = mk.map(X, rows, cols, boxes_of(rows)), gm = mk.map(G, ff, cols, n / 2), um = mk.map(U, ff, cols, n / 2);
     GatedArgs a = {};
     a.o[0] = Maker::out(*h, rows);
     if (gate) {
@@ -711,10 +807,11 @@ int zero_gated_forward(const zero_mat* x, const zero_mat* gate_w, const zero_mat
     a.rows = rows;
     a.cols = ff;
     a.m_tiles = tiles_of(rows, GT_TILE);
-    a.n_tiles = tiles_of(ff, GT_HALF);
+    a.n_tiles = n == 256 ? wide : narrow;
     a.k_steps = tiles_of(cols, GT_K);
+    a.a_rows = boxes_of(rows);
     a.act = act;
-    mk.product(GT_FORWARD, xm, xm, gm, um, a, status);
+    mk.product(GT_FORWARD, xm, xm, gm, um, a, status, n);
     return mk.rc;
 }
 
@@ -723,7 +820,7 @@ size_t zero_gated_backward_workspace_bytes(const zero_mat* x, const zero_mat* ga
                                            int64_t ff) {
     if (rows <= 0 || cols <= 0 || ff <= 0) return 0;
     return room_for(x, rows, cols) + room_for(gate_w, ff, cols) + room_for(up_w, ff, cols) + room_for(dgate, rows, ff) +
-           room_for(dup, rows, ff);
+           room_for(dup, rows, ff) + (gate_w && up_w ? parts_bytes(rows, cols, ff) : 0);
 }
 
 int zero_gated_backward(const zero_mat* dh, const zero_mat* gate, const zero_mat* up, const zero_mat* x,
@@ -810,15 +907,29 @@ int zero_gated_backward(const zero_mat* dh, const zero_mat* gate, const zero_mat
     if (dx) {
         const zero_mat G = mk.packed(*gate_w, ff, cols), U = mk.packed(*up_w, ff, cols);
         GatedArgs a = {};
-        a.o[0] = Maker::out(*dx, rows);
         a.rows = rows;
         a.cols = cols;
         a.m_tiles = tiles_of(rows, GT_TILE);
         a.n_tiles = tiles_of(cols, GT_TILE);
         a.k_half = tiles_of(ff, GT_K);
         a.k_steps = 2 * a.k_half;
-        mk.product(GT_DX, mk.map(DG, rows, ff, GT_HALF), mk.map(DU, rows, ff, GT_HALF), mk.map(G, ff, cols, GT_K),
+        a.a_rows = boxes_of(rows);
+        a.split = parts_of(rows, cols, ff);
+        const GatedOut to = Maker::out(*dx, rows);
+        const int64_t ldp = parts_ld(cols);
+        float* parts = reinterpret_cast<float*>(mk.ws);
+        if (a.split > 1) mk.ws += parts_bytes(rows, cols, ff);
+        a.o[0] = a.split > 1 ? GatedOut{parts, ldp, ZERO_F32, aligned(parts, 32) ? 32 : 16} : to;
+        mk.product(GT_DX, mk.map(DG, rows, ff, a.a_rows), mk.map(DU, rows, ff, a.a_rows), mk.map(G, ff, cols, GT_K),
                    mk.map(U, ff, cols, GT_K), a, status);
+        if (mk.rc == ZERO_OK && a.split > 1) {
+            int n = a.split;
+            int64_t r = rows, c = cols, ld = ldp;
+            GatedOut o = to;
+            void* jargs[] = {&parts, &n, &ld, &r, &c, &o};
+            const int64_t all = (rows * (ldp / 4) + 255) / 256, at_once = (int64_t)sms * 8;
+            mk.rc = cuda_fail(launch_after_previous((const void*)k_gated_join, (int)(all < at_once ? all : at_once), 256, jargs, 0, mk.s), me);
+        }
     }
     if (dgate_w) {
         const zero_mat X = mk.packed(*x, rows, cols);
