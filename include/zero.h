@@ -892,9 +892,10 @@ size_t zero_layernorm_workspace_bytes(int64_t cols);
  * act        ZERO_SILU: g / (1 + exp(-g)); ZERO_GELU_TANH: GELU's tanh form
  * gate, up   rows x ff, G and U rounded, for the backward pass; both or neither
  * workspace  zero_gated_forward_workspace_bytes of the same arguments, 16-byte
- *            aligned, contents irrelevant: 0 where the rows of x and of the
- *            weights start on 16-byte boundaries, else copies of those whose
- *            rows do not (NULL if 0)
+ *            aligned, contents irrelevant: 0 for up to 4 rows (of at most 12288
+ *            columns; fewer rows, more) and where the rows of x and of the weights
+ *            start on 16-byte boundaries, else copies of those whose rows do not
+ *            (NULL if 0)
  * status     device int32 the caller zero-fills; a block whose bounded wait runs
  *            out sets bit 0, and the outputs are then incomplete
  *            (ZERO_GB300_SPIN_LIMIT as for zero3_gather_bulk)

@@ -146,7 +146,7 @@ def test_layernorm_backward_refusals(Z):
 
 def test_gated_forward_refusals(Z):
     def call(code, **kw):
-        a = dict(x=m(Z), gate_w=m(Z), up_w=m(Z), rows=4, cols=64, ff=64, act=0, h=m(Z), gate=m(Z), up=m(Z),
+        a = dict(x=m(Z), gate_w=m(Z), up_w=m(Z), rows=9, cols=64, ff=64, act=0, h=m(Z), gate=m(Z), up=m(Z),
                  workspace=None, workspace_bytes=0, status=FAKE)
         a.update(kw)
         refused(Z, code, Z.zero_gated_forward, *a.values())
@@ -170,11 +170,12 @@ def test_gated_forward_refusals(Z):
     call(Z.ZERO_EINVAL, status=None)
     call(Z.ZERO_EINVAL, status=FAKE + 2)
     call(Z.ZERO_EWORKSPACE, x=m(Z, data=FAKE + 2))               # rows off 16 bytes need a copy
-    need = Z.zero_gated_forward_workspace_bytes(m(Z), m(Z, ld=65), m(Z), 4, 64, 64)
+    need = Z.zero_gated_forward_workspace_bytes(m(Z), m(Z, ld=65), m(Z), 9, 64, 64)
     assert need == 64 * 64 * 2
+    assert Z.zero_gated_forward_workspace_bytes(m(Z), m(Z, ld=65), m(Z), 4, 64, 64) == 0      # few rows: read where they lie
     call(Z.ZERO_EWORKSPACE, gate_w=m(Z, ld=65), workspace=FAKE, workspace_bytes=need - 1)
     call(Z.ZERO_EWORKSPACE, gate_w=m(Z, ld=65), workspace=FAKE + 8, workspace_bytes=need)
-    call(Z.ZERO_EINVAL, x=torch.zeros(4, 63, dtype=torch.bfloat16))
+    call(Z.ZERO_EINVAL, x=torch.zeros(9, 63, dtype=torch.bfloat16))
 
 
 def test_gated_backward_refusals(Z):

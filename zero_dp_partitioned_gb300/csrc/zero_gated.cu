@@ -37,21 +37,18 @@ namespace zdp {
 
 constexpr int GT_EPI_WARPS = 8;               // two for each 32 lanes of tensor memory, a half of the columns each
 constexpr int GT_THREADS = 64 + 32 * GT_EPI_WARPS;
-constexpr int GT_TILE = 256;                  // rows (and, but for few rows, columns) of a pair's tile
-constexpr int GT_HALF = 128;                  // rows of a block's A
+constexpr int GT_TILE = 256;                  // rows and columns of a pair's tile
+constexpr int GT_HALF = 128;                  // of a block's operands
 constexpr int GT_K = 64;                      // elements of k in a stage: 128 bytes
 constexpr int GT_A = GT_HALF * GT_K * 2;      // bytes of a block's A in a stage
 constexpr int GT_CHUNK = GT_K * 128;          // 64 columns by 64 rows of an operand whose k runs along the rows
 constexpr int GT_HEADER = 1024;
 constexpr int GT_EPI = GT_EPI_WARPS * 32 * 17 * 4;      // a 32 x 16 piece for each of its warps, padded
 
-// N: rows of B of a pair, half of them in each block.
-template <int N>
-struct GtShape {
-    static constexpr int B = N / 2 * GT_K * 2, STAGE = GT_A + B, STAGES = N == 256 ? 6 : 8;
-    static constexpr int SMEM = STAGES * STAGE + 2048 + GT_EPI;
-    static_assert(SMEM <= 232448 && STAGE % 1024 == 0 && STAGES <= 8, "shared memory of a block");
-};
+constexpr int GT_STAGE = 2 * GT_A;            // B has as many rows a block
+constexpr int GT_STAGES = 6;
+constexpr int GT_SMEM = GT_STAGES * GT_STAGE + 2048 + GT_EPI;
+static_assert(GT_SMEM <= 232448, "shared memory of a block");
 
 enum { GT_FORWARD = 0, GT_DX = 1, GT_DW = 2 };
 
@@ -148,10 +145,10 @@ __device__ __forceinline__ uint64_t gt_desc(uint32_t addr) {
 }
 // 16 elements of k further on, in the descriptor's units of 16 bytes
 template <bool K_ROWS> constexpr int GT_K16 = K_ROWS ? 16 * 128 >> 4 : 16 * 2 >> 4;
-// Instruction descriptor: 16-bit operands, fp32 accumulator, 256 x N.
-template <int DT, int N, bool A_ROWS, bool B_ROWS>
+// Instruction descriptor: 16-bit operands, fp32 accumulator, 256 x 256.
+template <int DT, bool A_ROWS, bool B_ROWS>
 constexpr uint32_t GT_IDESC = 1u << 4 | (DT == ZERO_BF16 ? 1u << 7 | 1u << 10 : 0u) | (A_ROWS ? 1u << 15 : 0u) |
-                              (B_ROWS ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(GT_TILE >> 4) << 24;
+                              (B_ROWS ? 1u << 16 : 0u) | (uint32_t)(GT_TILE >> 3) << 17 | (uint32_t)(GT_TILE >> 4) << 24;
 
 // ---------------------------------------------------------------- activations
 // Both are g times a sigmoid s; the slope is s + g s (1 - s) t' with t the
@@ -264,16 +261,13 @@ __device__ __forceinline__ void gt_tile(const GatedArgs& a, int t, int& m, int& 
     n = n0 + r % w;
 }
 
-template <int MODE, int DT, int N>
+template <int MODE, int DT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     k_gated(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
             const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
             const __grid_constant__ GatedArgs a) {
     constexpr bool A_ROWS = MODE == GT_DW, B_ROWS = MODE != GT_FORWARD;      // k along the rows
-    constexpr int N_TILE = MODE == GT_FORWARD ? N / 2 : N;                   // columns of the output
-    using S = GtShape<N>;
-    constexpr int STAGES = S::STAGES;
-    static_assert(!B_ROWS || N == 256, "two chunks of B");
+    constexpr int N_TILE = MODE == GT_FORWARD ? GT_HALF : GT_TILE;           // columns of the output
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023) & ~1023u;
     uint8_t* head = smem_raw + (base - raw);
@@ -287,10 +281,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3;                            // the 32 lanes of tensor memory this warp can reach
     const uint32_t rank = blockIdx.x & 1;                    // in the pair
-    float* epi = reinterpret_cast<float*>(head + GT_HEADER + STAGES * S::STAGE) + (warp & 7) * 32 * 17;
+    float* epi = reinterpret_cast<float*>(head + GT_HEADER + GT_STAGES * GT_STAGE) + (warp & 7) * 32 * 17;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (const CUtensorMap* m : {&a0, &a1, &b0, &b1}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+        for (int s = 0; s < GT_STAGES; ++s) {
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
         }
@@ -342,10 +337,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                 gt_tile(a, tile, m, n);
                 const bool second = MODE == GT_DW && m >= a.half_tiles;
                 const int am = (second ? m - a.half_tiles : m) * GT_TILE + (int)rank * GT_HALF;
-                const int bn = MODE == GT_FORWARD ? n * N_TILE : n * N + (int)rank * (N / 2);
-                const uint32_t bytes = (a.a_rows < GT_HALF ? a.a_rows * (GT_K * 2) : 2 * GT_A) + 2 * S::B;
+                const int bn = MODE == GT_FORWARD ? n * N_TILE : n * GT_TILE + (int)rank * GT_HALF;
+                const uint32_t bytes = (a.a_rows < GT_HALF ? a.a_rows * (GT_K * 2) : 2 * GT_A) + 2 * GT_A;
                 for (int k = k0; k < k1; ++k) {
-                    if (count >= STAGES && !pair_wait<false>(empty + 8 * st, phase ^ 1, a.spin_limit, stop)) {
+                    if (count >= GT_STAGES && !pair_wait<true>(empty + 8 * st, phase ^ 1, a.spin_limit, stop)) {
                         ok = false;
                         break;
                     }
@@ -354,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                     const CUtensorMap* A = second || up ? &a1 : &a0;
                     const CUtensorMap* B = (MODE == GT_FORWARD && rank) || up ? &b1 : &b0;
                     // rows and columns past the end read as 0
-                    const uint32_t bar = full0 + 8 * st, at = stages + st * S::STAGE;
+                    const uint32_t bar = full0 + 8 * st, at = stages + st * GT_STAGE;
                     if (rank == 0) mbar_expect_tx(full + 8 * st, bytes);
                     if (A_ROWS) {
                         tma_pair(at, A, am, kk, bar);
@@ -370,15 +365,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                         tma_pair(at + GT_A, B, kk, bn, bar);
                     }
                     *loaded = ++count;
-                    if (++st == STAGES) {
+                    if (++st == GT_STAGES) {
                         st = 0;
                         phase ^= 1;
                     }
                 }
             }
             // the last stages' releases come from the first block: this one does not leave before them
-            for (int c = max(0, count - STAGES); c < count && ok; ++c)
-                ok = pair_wait<false>(empty + 8 * (c % STAGES), (uint32_t)(c / STAGES) & 1, a.spin_limit, stop);
+            for (int c = max(0, count - GT_STAGES); c < count && ok; ++c)
+                ok = pair_wait<false>(empty + 8 * (c % GT_STAGES), (uint32_t)(c / GT_STAGES) & 1, a.spin_limit, stop);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
@@ -400,13 +395,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t at = stages + st * S::STAGE;
+                    const uint32_t at = stages + st * GT_STAGE;
                     const uint64_t da = gt_desc<A_ROWS>(at), db = gt_desc<B_ROWS>(at + GT_A);
 #pragma unroll
                     for (int q = 0; q < GT_K / 16; ++q)
-                        pair_mma(d, da + q * GT_K16<A_ROWS>, db + q * GT_K16<B_ROWS>, GT_IDESC<DT, N, A_ROWS, B_ROWS>, k > k0 || q > 0);
+                        pair_mma(d, da + q * GT_K16<A_ROWS>, db + q * GT_K16<B_ROWS>, GT_IDESC<DT, A_ROWS, B_ROWS>, k > k0 || q > 0);
                     pair_commit(empty + 8 * st);
-                    if (++st == STAGES) {
+                    if (++st == GT_STAGES) {
                         st = 0;
                         phase ^= 1;
                     }
@@ -447,16 +442,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                 release();
                 continue;
             }
+            if constexpr (MODE == GT_FORWARD) {
 #pragma unroll 1
-            for (int col = from; col < from + HALF; col += MODE == GT_FORWARD ? 16 : 32) {
-                uint32_t v[16], w[16];
-                float f[16];
-                __syncwarp();
-                tc_ld16(d + col, v);
-                tc_ld16(d + col + (MODE == GT_FORWARD ? N / 2 : 16), w);
-                tc_wait_ld();
-                if (col + (MODE == GT_FORWARD ? 16 : 32) == from + HALF) release();
-                if (MODE == GT_FORWARD) {
+                for (int col = from; col < from + HALF; col += 16) {
+                    uint32_t v[16], w[16];
+                    float f[16];
+                    __syncwarp();
+                    tc_ld16(d + col, v);
+                    tc_ld16(d + GT_HALF + col, w);
+                    tc_wait_ld();
+                    if (col + 16 == from + HALF) release();
 #pragma unroll
                     for (int e = 0; e < 16; ++e) f[e] = act_value(__uint_as_float(v[e]), a.act) * __uint_as_float(w[e]);
                     gt_put16<DT>(o, a.rows, a.cols, row, c0 + col, f, false, epi);
@@ -468,13 +463,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                         for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(w[e]);
                         gt_put16<DT>(a.o[2], a.rows, a.cols, row, c0 + col, f, false, epi);
                     }
-                } else {
+                }
+            } else {
+                // 64 columns at a time: a lane's stores fill whole lines of 128 bytes one behind the other
+#pragma unroll 1
+                for (int col = from; col < from + HALF; col += 64) {
+                    uint32_t v[4][16];
+                    __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(v[e]);
-                    gt_put16<DT>(o, a.rows, a.cols, row, c0 + col, f, a.accumulate, epi);
+                    for (int q = 0; q < 4; ++q) tc_ld16(d + col + 16 * q, v[q]);
+                    tc_wait_ld();
+                    if (col + 64 == from + HALF) release();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(w[e]);
-                    gt_put16<DT>(o, a.rows, a.cols, row, c0 + col + 16, f, a.accumulate, epi);
+                    for (int q = 0; q < 4; ++q) {
+                        float f[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(v[q][e]);
+                        gt_put16<DT>(o, a.rows, a.cols, row, c0 + col + 16 * q, f, a.accumulate, epi);
+                    }
                 }
             }
         }
@@ -493,8 +499,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     // after a stop of either block, the loads of both, which the first block's barriers count
     if (rank == 0 && threadIdx.x == 0 && (*stop || read_at(block_addr(base + 204, 1)))) {
         const int most = max(*loaded, read_at(block_addr(base + 208, 1)));
-        for (int c = max(0, most - STAGES); c < most; ++c)
-            pair_wait<false>(full + 8 * (c % STAGES), (uint32_t)(c / STAGES) & 1, a.drain_limit, nullptr);
+        for (int c = max(0, most - GT_STAGES); c < most; ++c)
+            pair_wait<false>(full + 8 * (c % GT_STAGES), (uint32_t)(c / GT_STAGES) & 1, a.drain_limit, nullptr);
     }
     __syncthreads();
     cluster_arrive();
@@ -507,6 +513,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     __syncwarp();
     cluster_arrive();
     cluster_wait();
+}
+
+// ---------------------------------------------------------------- few rows
+// Up to 4 rows: the weights are read once, and the sums are fp32 ones of the
+// ordinary units.  A warp has two columns of h, that is four rows of weights, of
+// which a lane reads every 32nd unit of 8; x lies in shared memory as it is.
+// Bound: HBM (the weights' bytes): through 4096 x 14336 bf16 one row in 35.7 us,
+// 6.57 TB/s (0.97 of the measured copy bandwidth), two in 36.1, four in 42.6.
+// The pairs above take 51 us for any number up to 256: 8.5 to start and end, two
+// rounds of tiles, the second on half of the SMs and bound by its products.
+// Eight rows here take 78: their sums leave half the registers for loads.
+constexpr int FEW_ROWS = 4, FEW_THREADS = 256;
+constexpr size_t FEW_SMEM = 96 * 1024;        // of x: two blocks an SM
+
+struct FewArgs {
+    const void *x, *wg, *wu;
+    int64_t ldx, ldg, ldu, ff;
+    int rows, cols, units, act;
+    GatedOut o[3];
+};
+
+template <int DT, int R, bool V8>
+__global__ void __launch_bounds__(FEW_THREADS, 2) k_gated_few(const __grid_constant__ FewArgs a) {
+    extern __shared__ __align__(16) uint4 xs[];              // [row][unit]
+    pdl_wait();
+    pdl_launch_next();
+    const Extent ex = extent_of<DT>(a.x, a.ldx, a.rows, a.cols), eg = extent_of<DT>(a.wg, a.ldg, a.ff, a.cols),
+                 eu = extent_of<DT>(a.wu, a.ldu, a.ff, a.cols);
+    for (int i = threadIdx.x; i < R * a.units; i += FEW_THREADS) {
+        const int r = i / a.units, u = i - r * a.units;
+        const uint16_t* row = static_cast<const uint16_t*>(a.x) + r * a.ldx;
+        xs[i] = r >= a.rows ? make_uint4(0, 0, 0, 0) : V8 ? ld8<DT>(row, u * 8).w[0] : ld8_shifted<DT>(row, u * 8, a.cols, ex).w[0];
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const int64_t pairs = (a.ff + 1) / 2, step = (int64_t)gridDim.x * (FEW_THREADS / 32);
+    for (int64_t p = (int64_t)blockIdx.x * (FEW_THREADS / 32) + (threadIdx.x >> 5); p < pairs; p += step) {
+        const int64_t f = 2 * p, f1 = f + 1 < a.ff ? f + 1 : f;          // an odd last column twice
+        const uint16_t* const w[4] = {static_cast<const uint16_t*>(a.wg) + f * a.ldg, static_cast<const uint16_t*>(a.wu) + f * a.ldu,
+                                      static_cast<const uint16_t*>(a.wg) + f1 * a.ldg, static_cast<const uint16_t*>(a.wu) + f1 * a.ldu};
+        uint64_t sum[4][R] = {};
+        constexpr int AT_ONCE = R <= 2 ? 4 : 2;              // units whose loads are under way, beside 8 R registers of sums
+        for (int u0 = lane; u0 < a.units; u0 += 32 * AT_ONCE) {
+            Raw8<DT> v[AT_ONCE][4];
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) {
+                const int u = u0 + 32 * j;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[j][q].w[0] = make_uint4(0, 0, 0, 0);
+                    if (u < a.units) {
+                        if (V8) v[j][q] = ld8_stream<DT>(w[q], u * 8);
+                        else v[j][q] = ld8_shifted<DT>(w[q], u * 8, a.cols, q & 1 ? eu : eg);
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) {
+                const int u = min(u0 + 32 * j, a.units - 1);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    Raw8<DT> x;
+                    x.w[0] = xs[r * a.units + u];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[q][r] = fma2(pair8<DT>(v[j][q], e), pair8<DT>(x, e), sum[q][r]);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float t[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 s = unpack2(sum[q][r]);
+                t[q] = warp_sum(s.x + s.y);
+            }
+            if (lane == 0 && r < a.rows) {
+                const int n = f1 > f ? 2 : 1;
+                for (int c = 0; c < n; ++c) {
+                    const float g = t[2 * c], u = t[2 * c + 1];
+                    st1<DT>(a.o[0].p, r * a.o[0].ld + f + c, act_value(g, a.act) * u);
+                    if (a.o[1].p) {
+                        st1<DT>(a.o[1].p, r * a.o[1].ld + f + c, g);
+                        st1<DT>(a.o[2].p, r * a.o[2].ld + f + c, u);
+                    }
+                }
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------------- the slopes
@@ -687,7 +784,7 @@ struct Maker {
         return {m.data, m.ld, m.dtype, on(32) ? 32 : on(16) ? 16 : 0};
     }
     void product(int mode, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1, GatedArgs& a,
-                 int32_t* status, int n = 256) {
+                 int32_t* status) {
         if (rc != ZERO_OK) return;
         a.status = status;
         const char* e = std::getenv("ZERO_GB300_SPIN_LIMIT");
@@ -696,22 +793,33 @@ struct Maker {
         if (a.split < 1) a.split = 1;
         if (!a.a_rows) a.a_rows = GT_HALF;
         const bool bf = dt == ZERO_BF16;
-        const void* f = mode == GT_FORWARD
-                            ? (n == 256 ? (bf ? (const void*)k_gated<GT_FORWARD, ZERO_BF16, 256> : (const void*)k_gated<GT_FORWARD, ZERO_F16, 256>)
-                                        : (bf ? (const void*)k_gated<GT_FORWARD, ZERO_BF16, 128> : (const void*)k_gated<GT_FORWARD, ZERO_F16, 128>))
-                        : mode == GT_DX ? (bf ? (const void*)k_gated<GT_DX, ZERO_BF16, 256> : (const void*)k_gated<GT_DX, ZERO_F16, 256>)
-                                        : (bf ? (const void*)k_gated<GT_DW, ZERO_BF16, 256> : (const void*)k_gated<GT_DW, ZERO_F16, 256>);
-        const size_t smem = n == 256 ? GtShape<256>::SMEM : GtShape<128>::SMEM;
-        rc = raise_smem(f, smem, call);
+        const void* f = mode == GT_FORWARD ? (bf ? (const void*)k_gated<GT_FORWARD, ZERO_BF16> : (const void*)k_gated<GT_FORWARD, ZERO_F16>)
+                        : mode == GT_DX    ? (bf ? (const void*)k_gated<GT_DX, ZERO_BF16> : (const void*)k_gated<GT_DX, ZERO_F16>)
+                                           : (bf ? (const void*)k_gated<GT_DW, ZERO_BF16> : (const void*)k_gated<GT_DW, ZERO_F16>);
+        rc = raise_smem(f, GT_SMEM, call);
         if (rc != ZERO_OK) return;
         const int tiles = a.m_tiles * a.n_tiles * a.split, pairs = sms / 2;
         void* args[] = {const_cast<CUtensorMap*>(&a0), const_cast<CUtensorMap*>(&a1), const_cast<CUtensorMap*>(&b0),
                         const_cast<CUtensorMap*>(&b1), &a};
-        rc = cuda_fail(launch_after_previous(f, 2 * (tiles < pairs ? tiles : pairs), GT_THREADS, args, smem, s), call);
+        rc = cuda_fail(launch_after_previous(f, 2 * (tiles < pairs ? tiles : pairs), GT_THREADS, args, GT_SMEM, s), call);
     }
 };
 
 static int tiles_of(int64_t n, int tile) { return (int)((n + tile - 1) / tile); }
+
+// Whether the few rows' kernel takes them: its x must fit shared memory.
+static int few_of(int64_t rows) { return rows <= 1 ? 1 : rows <= 2 ? 2 : 4; }
+static bool is_few(int64_t rows, int64_t cols) {
+    return rows <= FEW_ROWS && cols <= 1 << 20 && (size_t)few_of(rows) * (size_t)((cols + 7) / 8) * 16 <= FEW_SMEM;
+}
+template <int DT>
+static const void* few_fn(int r, bool v8) {
+    if (v8)
+        return r == 1 ? (const void*)k_gated_few<DT, 1, true> : r == 2 ? (const void*)k_gated_few<DT, 2, true>
+                                                                       : (const void*)k_gated_few<DT, 4, true>;
+    return r == 1 ? (const void*)k_gated_few<DT, 1, false> : r == 2 ? (const void*)k_gated_few<DT, 2, false>
+                                                                    : (const void*)k_gated_few<DT, 4, false>;
+}
 
 // Rows of A's boxes: of up to 128 rows the multiple of 8 that holds them.
 // Rows past the end cost the loads as much as others, and more (one token
@@ -761,7 +869,7 @@ extern "C" {
 
 size_t zero_gated_forward_workspace_bytes(const zero_mat* x, const zero_mat* gate_w, const zero_mat* up_w, int64_t rows,
                                           int64_t cols, int64_t ff) {
-    if (rows <= 0 || cols <= 0 || ff <= 0) return 0;
+    if (rows <= 0 || cols <= 0 || ff <= 0 || is_few(rows, cols)) return 0;
     return room_for(x, rows, cols) + room_for(gate_w, ff, cols) + room_for(up_w, ff, cols);
 }
 
@@ -792,12 +900,24 @@ int zero_gated_forward(const zero_mat* x, const zero_mat* gate_w, const zero_mat
             if (o) mk.zero(*o, rows, ff);
         return mk.rc;
     }
+    if (is_few(rows, cols)) {
+        FewArgs a = {x->data, gate_w->data, up_w->data, x->ld, gate_w->ld, up_w->ld, ff, (int)rows, (int)cols, (int)((cols + 7) / 8), act, {}};
+        a.o[0] = Maker::out(*h, rows);
+        if (gate) {
+            a.o[1] = Maker::out(*gate, rows);
+            a.o[2] = Maker::out(*up, rows);
+        }
+        const bool v8 = cols % 8 == 0 && rows_aligned(*x, rows) && rows_aligned(*gate_w, ff) && rows_aligned(*up_w, ff);
+        const void* f = dt == ZERO_BF16 ? few_fn<ZERO_BF16>(few_of(rows), v8) : few_fn<ZERO_F16>(few_of(rows), v8);
+        const size_t smem = (size_t)few_of(rows) * a.units * 16;
+        rc = raise_smem(f, smem, me);
+        if (rc != ZERO_OK) return rc;
+        const int64_t blocks = (ff + 2 * (FEW_THREADS / 32) - 1) / (2 * (FEW_THREADS / 32)), most = 2 * (int64_t)sms;
+        void* args[] = {&a};
+        return cuda_fail(launch_after_previous(f, (int)(blocks < most ? blocks : most), FEW_THREADS, args, smem, mk.s), me);
+    }
     const zero_mat X = mk.packed(*x, rows, cols), G = mk.packed(*gate_w, ff, cols), U = mk.packed(*up_w, ff, cols);
-    // Tiles of 128 columns, or, where all rows are in one tile and the weights' reads are what takes time, of 64 if that
-    // shares them out more evenly (14336 columns over 76 pairs: 3 rounds of half the size for 2)
-    const int pairs = sms / 2, wide = tiles_of(ff, GT_HALF), narrow = tiles_of(ff, GT_HALF / 2);
-    const int n = rows <= GT_TILE && (narrow + pairs - 1) / pairs < 2 * ((wide + pairs - 1) / pairs) ? 128 : 256;
-    const CUtensorMap xm = mk.map(X, rows, cols, boxes_of(rows)), gm = mk.map(G, ff, cols, n / 2), um = mk.map(U, ff, cols, n / 2);
+    const CUtensorMap xm = mk.map(X, rows, cols, boxes_of(rows)), gm = mk.map(G, ff, cols, GT_HALF), um = mk.map(U, ff, cols, GT_HALF);
     GatedArgs a = {};
     a.o[0] = Maker::out(*h, rows);
     if (gate) {
@@ -807,11 +927,11 @@ int zero_gated_forward(const zero_mat* x, const zero_mat* gate_w, const zero_mat
     a.rows = rows;
     a.cols = ff;
     a.m_tiles = tiles_of(rows, GT_TILE);
-    a.n_tiles = n == 256 ? wide : narrow;
+    a.n_tiles = tiles_of(ff, GT_HALF);
     a.k_steps = tiles_of(cols, GT_K);
     a.a_rows = boxes_of(rows);
     a.act = act;
-    mk.product(GT_FORWARD, xm, xm, gm, um, a, status, n);
+    mk.product(GT_FORWARD, xm, xm, gm, um, a, status);
     return mk.rc;
 }
 
