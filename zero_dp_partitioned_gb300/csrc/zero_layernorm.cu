@@ -17,9 +17,6 @@
 
 namespace zdp {
 
-constexpr int LN_FORWARD_THREADS = 1536;    // a multiprocessor, for the grid and the stages of the general form
-constexpr int LN_FORWARD_OVER = 2;
-
 // What a block keeps of its warps: the columns of each, and, in two sets used by
 // turns, mean and squares.
 struct WarpStats {
@@ -27,141 +24,20 @@ struct WarpStats {
     float2 s[2][32];
 };
 
-// valid columns of this warp's units
-__device__ __forceinline__ int warp_columns(int cols, int nv) {
-    int n = 0;
-    for (int j = 0; j < nv; ++j) {
-        const int c = ((int)(threadIdx.x & ~31u) + j * (int)blockDim.x) * 8;
-        n += max(0, min(256, cols - c));
-    }
-    return n;
-}
-
-// The general form, for rows that start anywhere and widths that are no multiple of 8.
-template <int XT, int RT, int NV>
-__global__ void __launch_bounds__(NORM_THREADS, 1)
-    k_layernorm_forward(const __grid_constant__ LayerNormArgs a) {
-    constexpr int E = Map::E;
-    constexpr bool V8 = false;
-    constexpr int WT = ZERO_F32;
-    __shared__ __align__(16) WarpStats st;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int mine = warp_columns(a.cols, NV);
-    const float inv_mine = mine ? 1.f / (float)mine : 0.f;
-    if (lane == 0) st.n[warp] = (float)mine;
-    __syncthreads();
-    pdl_wait();
-    pdl_launch_next();
-    const uint32_t step = drop_step(a.drop);
-    const float inv_n = 1.f / (float)a.cols;
-    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols);
-    extern __shared__ __align__(16) uint4 ring[];
-    using X = Slots<XT, NV, V8>;
-    using R = Slots<RT, NV, V8>;
-    const int S = a.stages, stage_words = X::words() + R::words();
-    auto copy = [&](int64_t row, int at_stage) {
-        if (row < a.rows) {
-            uint4* at = ring + at_stage * stage_words;
-            X{at}.copy(row_of<XT>(a.x, a.ldx, row), a.cols, ex);
-            if (a.r) R{at + X::words()}.copy(row_of<RT>(a.r, a.ldr, row), a.cols, er);
-        }
-        copies_commit();
-    };
-    for (int s = 0; s < S - 1; ++s) copy(blockIdx.x + (int64_t)s * gridDim.x, s);
-    Raw8<WT> w[NV], b[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        float v[E];
-        vector8(a.w, a.wdt, a.w_aligned, a.cols, Map::unit(j), 1.f, v);
-        w[j] = narrow8<WT>(v);
-        vector8(a.b, a.bdt, a.b_aligned, a.cols, Map::unit(j), 0.f, v);
-        b[j] = narrow8<WT>(v);
-    }
-    int turn = 0, at_stage = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        Unit<XT, V8> x[NV];
-        Unit<RT, V8> r[NV];
-        copy(row + (int64_t)(S - 1) * gridDim.x, at_stage == 0 ? S - 1 : at_stage - 1);
-        copies_wait_all_but(S - 1);
-        if (!V8) __syncthreads();
-        uint4* at = ring + at_stage * stage_words;
-        X{at}.read(x, row_of<XT>(a.x, a.ldx, row), a.cols);
-        if (a.r) R{at + X::words()}.read(r, row_of<RT>(a.r, a.ldr, row), a.cols);
-        at_stage = at_stage == S - 1 ? 0 : at_stage + 1;
-        // h as it is stored
-        uint64_t s2 = 0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            r[j] = a.drop.on ? drop_add_unit<XT, RT, V8>(x[j], r[j], a.r != nullptr, a.drop, step, row * a.units + Map::unit(j))
-                             : add_unit<XT, RT, V8>(x[j], r[j], a.r != nullptr);
-#pragma unroll
-            for (int q = 0; q < E / 2; ++q) s2 = add2(s2, r[j].pair(q));
-            if (a.h) r[j].store(row_of<RT>(a.h, a.ldh, row), Map::unit(j), a.cols);
-        }
-        const float2 sp = unpack2(s2);
-        const float mw = warp_sum(sp.x + sp.y) * inv_mine;
-        const uint64_t mw2 = pack2(-mw, -mw);
-        uint64_t v2 = 0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int left = a.cols - Map::unit(j) * 8;
-#pragma unroll
-            for (int q = 0; q < E / 2; ++q) {
-                uint64_t d = add2(r[j].pair(q), mw2);
-                const float2 p = unpack2(d);
-                d = pack2(2 * q < left ? p.x : 0.f, 2 * q + 1 < left ? p.y : 0.f);
-                v2 = fma2(d, d, v2);
-            }
-        }
-        const float2 vp = unpack2(v2);
-        float m2 = warp_sum(vp.x + vp.y), mean = mw;
-        if (warps > 1) {
-            if (lane == 0) st.s[turn][warp] = make_float2(mw, m2);
-            __syncthreads();
-            float sum = 0.f;
-            for (int k = 0; k < warps; ++k) sum = fmaf(st.n[k], st.s[turn][k].x, sum);
-            mean = sum * inv_n;
-            m2 = 0.f;
-            for (int k = 0; k < warps; ++k) {
-                const float2 p = st.s[turn][k];
-                const float d = p.x - mean;
-                m2 += fmaf(st.n[k] * d, d, p.y);
-            }
-        }
-        const float rstd = rsqrtf(fmaf(m2, inv_n, a.eps));
-        if (threadIdx.x == 0) {
-            if (a.mean) a.mean[row] = mean;
-            if (a.rstd) a.rstd[row] = rstd;
-        }
-        const uint64_t mm = pack2(-mean, -mean), rr = pack2(rstd, rstd);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float y[E];
-#pragma unroll
-            for (int q = 0; q < E / 2; ++q) {
-                const float2 v = unpack2(fma2(mul2(add2(r[j].pair(q), mm), rr), pair8<WT>(w[j], q), pair8<WT>(b[j], q)));
-                y[2 * q] = v.x;
-                y[2 * q + 1] = v.y;
-            }
-            store_unit<XT, V8>(row_of<XT>(a.y, a.ldy, row), Map::unit(j), a.cols, y);
-        }
-    }
-}
-
-// Rows on 16-byte boundaries.  WT: the type in which weight and bias lie in
-// shared memory.
-template <int XT, int RT, int WT, int NV>
+// WT: the type in which weight and bias lie in shared memory.
+template <int XT, int RT, int WT, int NV, bool SHIFT>
 __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const __grid_constant__ LayerNormArgs a) {
     __shared__ __align__(16) WarpStats st;
-    using X = Lane<XT, NV>;
-    using R = Lane<RT, NV>;
+    using X = Lane<XT, NV, SHIFT>;
+    using R = Lane<RT, NV, SHIFT>;
     using V = Vector<WT>;
     constexpr int XS = 8 * Elem<XT>::SIZE, RS = 8 * Elem<RT>::SIZE;          // bytes of a unit
     const int T = a.T, G = blockDim.x / T, group = threadIdx.x / T, units = a.units;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = T >> 5, w0 = group * warps;
     const int uw = (warp - w0) * NV * 32, left = units - uw;                 // the warp's first unit, units from there
-    const int n = (left - lane + 31) >> 5;                                   // this lane's units (any number above NV: all)
-    const int mine = max(0, min(NV * 256, left * 8));                        // columns of this warp
+    const int n = SHIFT ? (left + 31) >> 5 : (left - lane + 31) >> 5;        // the warp's js, or this lane's (any number above NV: all)
+    const int wcols = a.cols - uw * 8, lcols = wcols - lane * 8;             // columns from the warp's first on, from this lane's
+    const int mine = max(0, min(NV * 256, wcols));                           // columns of this warp
     const float inv_mine = mine ? 1.f / (float)mine : 0.f, inv_n = 1.f / (float)a.cols;
     if (lane == 0) st.n[warp] = (float)mine;
     pdl_wait();
@@ -170,20 +46,20 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const 
     extern __shared__ __align__(16) uint4 ring[];
     const int S = a.stages, xwords = (blockDim.x >> 5) * X::WORDS, stage_words = xwords + (blockDim.x >> 5) * R::WORDS;
     const int64_t first = group * (int64_t)gridDim.x + blockIdx.x, every = (int64_t)G * gridDim.x;
-    const uint4 *xat = ring + warp * X::WORDS, *rat = ring + xwords + warp * R::WORDS;
-    const uint32_t xat32 = (uint32_t)__cvta_generic_to_shared(xat), rat32 = (uint32_t)__cvta_generic_to_shared(rat);
+    uint4 *const xat = ring + warp * X::WORDS, *const rat = ring + xwords + warp * R::WORDS;
+    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols);
     // this warp's part of the row whose copy comes next, and of the row at hand
     const char *cx = static_cast<const char*>(a.x) + first * a.ldx * Elem<XT>::SIZE + (int64_t)uw * XS;
     const char* cr = static_cast<const char*>(a.r) + (a.r ? first * a.ldr * Elem<RT>::SIZE + (int64_t)uw * RS : 0);
-    char* H = static_cast<char*>(a.h) + (a.h ? first * a.ldh * Elem<RT>::SIZE + (int64_t)(uw + lane) * RS : 0);
-    char* Y = static_cast<char*>(a.y) + first * a.ldy * Elem<XT>::SIZE + (int64_t)(uw + lane) * XS;
+    char* H = static_cast<char*>(a.h) + (a.h ? first * a.ldh * Elem<RT>::SIZE + (int64_t)uw * RS : 0);
+    char* Y = static_cast<char*>(a.y) + first * a.ldy * Elem<XT>::SIZE + (int64_t)uw * XS;
     const int64_t dx = every * a.ldx * Elem<XT>::SIZE, dr = every * a.ldr * Elem<RT>::SIZE, dh = every * a.ldh * Elem<RT>::SIZE,
                   dy = every * a.ldy * Elem<XT>::SIZE;
     int64_t crow = first, unit = first * units + uw + lane;
     auto copy = [&](int at_stage) {
         if (crow < a.rows) {
-            X::copy(xat32 + at_stage * stage_words * 16, cx, left);
-            if (a.r) R::copy(rat32 + at_stage * stage_words * 16, cr, left);
+            X::copy(xat + at_stage * stage_words, cx, wcols, ex);
+            if (a.r) R::copy(rat + at_stage * stage_words, cr, wcols, er);
         }
         copies_commit();
         crow += every;
@@ -201,24 +77,27 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const 
         Raw8<RT> r[NV];
         copy(at_stage == 0 ? S - 1 : at_stage - 1);
         copies_wait_all_but(S - 1);
-        if (XT == ZERO_F32 || RT == ZERO_F32) __syncwarp();
+        if (X::SHARED || R::SHARED) __syncwarp();
+        const int xoff = SHIFT ? (int)(reinterpret_cast<uintptr_t>(cx - S * dx) & 15u) : 0,
+                  roff = SHIFT ? (int)(reinterpret_cast<uintptr_t>(cr - S * dr) & 15u) : 0;
         const uint4 *xs = xat + at_stage * stage_words, *rs = rat + at_stage * stage_words;
         at_stage = at_stage == S - 1 ? 0 : at_stage + 1;
         // h as it is stored
         uint64_t s2 = 0;
+        Put<RT, SHIFT> puth;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (j < n) {
                 Unit<XT, true> xu;
                 Unit<RT, true> ru;
-                xu.raw = X::read(xs, j);
-                if (a.r) ru.raw = R::read(rs, j);
+                xu.raw = X::read(xs, j, xoff, lcols - 256 * j);
+                if (a.r) ru.raw = R::read(rs, j, roff, lcols - 256 * j);
                 r[j] = (a.drop.on ? drop_add_unit<XT, RT, true>(xu, ru, a.r != nullptr, a.drop, step, unit + 32 * j)
                                   : add_unit<XT, RT, true>(xu, ru, a.r != nullptr))
                            .raw;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) s2 = add2(s2, pair8<RT>(r[j], q));
-                if (a.h) put8<RT>(H, 32 * j, r[j], a.h32);
+                if (a.h) puth.put(H, j, lcols - 256 * j, a.h32, j == NV - 1, r[j]);
             }
         const float2 sp = unpack2(s2);
         const float mw = warp_sum(sp.x + sp.y) * inv_mine;
@@ -226,12 +105,23 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const 
         uint64_t v2 = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (j < n)
+            if (j < n) {
+                const int here = lcols - 256 * j;
+                if (!SHIFT || here >= 8) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint64_t d = add2(pair8<RT>(r[j], q), mw2);
-                    v2 = fma2(d, d, v2);
+                    for (int q = 0; q < 4; ++q) {
+                        const uint64_t d = add2(pair8<RT>(r[j], q), mw2);
+                        v2 = fma2(d, d, v2);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 p = unpack2(add2(pair8<RT>(r[j], q), mw2));
+                        const uint64_t d = pack2(2 * q < here ? p.x : 0.f, 2 * q + 1 < here ? p.y : 0.f);
+                        v2 = fma2(d, d, v2);
+                    }
                 }
+            }
         const float2 vp = unpack2(v2);
         float m2 = warp_sum(vp.x + vp.y), mean = mw;
         if (warps > 1) {
@@ -255,10 +145,12 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const 
             if (a.rstd) a.rstd[row] = rstd;
         }
         const uint64_t mm = pack2(-mean, -mean), rr = pack2(rstd, rstd);
+        Put<XT, SHIFT> puty;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (j < n) {
-                const Raw8<WT> w = V::read(wat, uw + lane + 32 * j, units), b = V::read(bat, uw + lane + 32 * j, units);
+                const int u = SHIFT ? min(uw + lane + 32 * j, units - 1) : uw + lane + 32 * j;
+                const Raw8<WT> w = V::read(wat, u, units), b = V::read(bat, u, units);
                 float y[8];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -266,7 +158,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const 
                     y[2 * q] = v.x;
                     y[2 * q + 1] = v.y;
                 }
-                put8<XT>(Y, 32 * j, narrow8<XT>(y), a.y32);
+                puty.put(Y, j, lcols - 256 * j, a.y32, j == NV - 1, narrow8<XT>(y));
             }
     }
 }
@@ -347,27 +239,22 @@ __global__ void __launch_bounds__(NORM_THREADS) k_layernorm_forward_long(const _
     }
 }
 
+// packed: weight and bias in shared memory in x's type, not in fp32.
+template <int XT, int RT, bool SHIFT>
+static const void* rows_of(bool packed, int nv) {
+    if (nv == 2) return (const void*)k_layernorm_forward_rows<XT, RT, ZERO_F32, 2, SHIFT>;
+    return packed ? (const void*)k_layernorm_forward_rows<XT, RT, XT, 4, SHIFT> : (const void*)k_layernorm_forward_rows<XT, RT, ZERO_F32, 4, SHIFT>;
+}
 template <int XT, int RT>
-static const void* general(bool v8, int nv) {
-    if (nv == 2) return (const void*)k_layernorm_forward<XT, RT, 2>;
-    if (nv == 4) return (const void*)k_layernorm_forward<XT, RT, 4>;
+static const void* fn_of(bool v8, bool packed, int nv) {
+    if (nv) return v8 ? rows_of<XT, RT, false>(packed, nv) : rows_of<XT, RT, true>(packed, nv);
     return v8 ? (const void*)k_layernorm_forward_long<XT, RT, true> : (const void*)k_layernorm_forward_long<XT, RT, false>;
 }
-static const void* general_fn(int xt, int rt, bool v8, int nv) {
-    if (xt == ZERO_F32) return general<ZERO_F32, ZERO_F32>(v8, nv);
-    if (xt == ZERO_BF16) return rt == ZERO_F32 ? general<ZERO_BF16, ZERO_F32>(v8, nv) : general<ZERO_BF16, ZERO_BF16>(v8, nv);
-    return rt == ZERO_F32 ? general<ZERO_F16, ZERO_F32>(v8, nv) : general<ZERO_F16, ZERO_F16>(v8, nv);
-}
-// packed: weight and bias in shared memory in x's type, not in fp32.
-template <int XT, int RT>
-static const void* rows_of(bool packed, int nv) {
-    if (nv == 2) return (const void*)k_layernorm_forward_rows<XT, RT, ZERO_F32, 2>;
-    return packed ? (const void*)k_layernorm_forward_rows<XT, RT, XT, 4> : (const void*)k_layernorm_forward_rows<XT, RT, ZERO_F32, 4>;
-}
-static const void* rows_fn(int xt, int rt, bool packed, int nv) {
-    if (xt == ZERO_F32) return rows_of<ZERO_F32, ZERO_F32>(false, nv);
-    if (xt == ZERO_BF16) return rt == ZERO_F32 ? rows_of<ZERO_BF16, ZERO_F32>(packed, nv) : rows_of<ZERO_BF16, ZERO_BF16>(packed, nv);
-    return rt == ZERO_F32 ? rows_of<ZERO_F16, ZERO_F32>(packed, nv) : rows_of<ZERO_F16, ZERO_F16>(packed, nv);
+// nv 0: rows too long for the registers.
+static const void* forward_fn(int xt, int rt, bool v8, bool packed, int nv) {
+    if (xt == ZERO_F32) return fn_of<ZERO_F32, ZERO_F32>(v8, packed, nv);
+    if (xt == ZERO_BF16) return rt == ZERO_F32 ? fn_of<ZERO_BF16, ZERO_F32>(v8, packed, nv) : fn_of<ZERO_BF16, ZERO_BF16>(v8, packed, nv);
+    return rt == ZERO_F32 ? fn_of<ZERO_F16, ZERO_F32>(v8, packed, nv) : fn_of<ZERO_F16, ZERO_F16>(v8, packed, nv);
 }
 
 }  // namespace zdp
@@ -428,32 +315,24 @@ extern "C" int zero_layernorm_forward(const zero_mat* x, const zero_mat* residua
     const int sms = sm_count(), words = words_of(x->dtype) + words_of(rt);
     if (!sms) return ZERO_ECUDA;
     void* args[] = {&a};
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (v8) {
-        const bool w16 = x->dtype != ZERO_F32 && (!weight || weight->dtype == x->dtype) && (!bias || bias->dtype == x->dtype);
-        int nv;
-        RowsShape p = rows_shape(rows, cols, words, 4, sms, &nv);
-        const bool packed = !p.threads && w16;
-        if (packed) p = rows_shape(rows, cols, nv = 4, words, 2, sms);
-        if (p.threads) {
-            const void* f = rows_fn(x->dtype, rt, packed, nv);
-            a.h32 = h_out && rows_on_32(*h_out, rows);
-            a.y32 = rows_on_32(*y, rows);
-            a.stages = p.stages;
-            a.T = p.T;
-            rc = raise_smem(f, p.smem, "zero_layernorm_forward shared-memory size");
-            if (rc != ZERO_OK) return rc;
-            return cuda_fail(launch_after_previous(f, p.grid, p.threads, args, p.smem, s), "zero_layernorm_forward launch");
-        }
+    const bool w16 = x->dtype != ZERO_F32 && (!weight || weight->dtype == x->dtype) && (!bias || bias->dtype == x->dtype);
+    int nv;
+    RowsShape p = rows_shape(rows, cols, words, 4, sms, &nv);
+    const bool packed = !p.threads && w16;
+    if (packed) p = rows_shape(rows, cols, nv = 4, words, 2, sms);
+    if (p.threads) {
+        a.stages = p.stages;
+        a.T = p.T;
+        a.h32 = h_out && rows_on_32(*h_out, rows);
+        a.y32 = rows_on_32(*y, rows);
+    } else {
+        nv = 0;
+        const int64_t most = (int64_t)sms * 6;
+        p = RowsShape{NORM_THREADS, 0, 0, (int)(rows < most ? rows : most), 0};
     }
-    // rows on 16-byte boundaries that are too long for the registers are walked as any others that are
-    NormShape p = shape_of(cols, words, LN_FORWARD_THREADS);
-    if (v8) p = NormShape{0, NORM_THREADS, LN_FORWARD_THREADS / NORM_THREADS, 2, 0};
-    a.stages = p.stages;
-    const void* f = general_fn(x->dtype, rt, v8, p.nv);
+    const void* f = forward_fn(x->dtype, rt, v8, packed, nv);
     rc = raise_smem(f, p.smem, "zero_layernorm_forward shared-memory size");
     if (rc != ZERO_OK) return rc;
-    const int64_t most = (int64_t)sms * p.per_sm * LN_FORWARD_OVER;
-    return cuda_fail(launch_after_previous(f, (int)(rows < most ? rows : most), p.threads, args, p.smem, s),
+    return cuda_fail(launch_after_previous(f, p.grid, p.threads, args, p.smem, static_cast<cudaStream_t>(stream)),
                      "zero_layernorm_forward launch");
 }

@@ -14,8 +14,6 @@
 
 namespace zdp {
 
-constexpr int LN_BACKWARD_THREADS = 512;    // a multiprocessor: what the registers let run
-
 // Sums of two values over the block, the same in every thread and every run.
 // s: 32 pairs that no call in flight uses, zero beyond the block's warps.
 __device__ __forceinline__ float2 block_sum2(float x, float y, float2* s) {
@@ -34,152 +32,33 @@ __device__ __forceinline__ float2 block_sum2(float x, float y, float2* s) {
     return make_float2(tx, ty);
 }
 
-// The gradient of one unit stored: of r as it is, of x by the forward's mask.
-template <int XT, int RT, bool V8>
-__device__ __forceinline__ void store_gradients(const LayerNormArgs& a, uint32_t step, int64_t row, int u, float (&v)[8]) {
-    if (a.y) {
-        if constexpr (!V8) store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), u, a.cols, v);
-        else if (u * 8 < a.cols) put8<RT>(row_of<RT>(a.y, a.ldy, row), u, narrow8<RT>(v), a.y32);
-    }
-    if (!a.h) return;
-    if (a.drop.on) {
-        const uint4 bits = drop_bits(a.drop, step, row * a.units + u);
+// dropout of a unit's gradient, by the forward's mask
+__device__ __forceinline__ void dropped(const DropArgs& d, uint32_t step, int64_t unit, float (&v)[8]) {
+    const uint4 bits = drop_bits(d, step, unit);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t w = word_of(bits, q);
-            v[2 * q] = kept_low(w, a.drop.above) ? v[2 * q] * a.drop.scale : 0.f;
-            v[2 * q + 1] = kept_high(w, a.drop.above) ? v[2 * q + 1] * a.drop.scale : 0.f;
-        }
-    }
-    if constexpr (!V8) store_unit<XT, V8>(row_of<XT>(a.h, a.ldh, row), u, a.cols, v);
-    else if (u * 8 < a.cols) put8<XT>(row_of<XT>(a.h, a.ldh, row), u, narrow8<XT>(v), a.h32);
-}
-
-// The general form, for rows that start anywhere and widths that are no multiple of 8.
-template <int XT, int RT, int NV>
-__global__ void __launch_bounds__(NORM_THREADS, 1) k_layernorm_backward(const __grid_constant__ LayerNormArgs a) {
-    constexpr int E = Map::E;
-    constexpr bool V8 = false;
-    constexpr int WT = ZERO_F32;
-    __shared__ __align__(16) float2 ssum[2][32];
-    if (threadIdx.x < 64) ssum[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.f, 0.f);
-    if (blockDim.x < 64 && threadIdx.x < 32) ssum[1][threadIdx.x] = make_float2(0.f, 0.f);
-    __syncthreads();
-    pdl_wait();
-    pdl_launch_next();
-    const uint32_t step = drop_step(a.drop);
-    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols),
-                 eh = extent_of<RT>(a.hin, a.ldhin, a.rows, a.cols);
-    uint64_t dw[NV][E / 2] = {}, db[NV][E / 2] = {};
-    const float inv_n = 1.f / (float)a.cols;
-    extern __shared__ __align__(16) uint4 ring[];
-    using X = Slots<XT, NV, V8>;
-    using R = Slots<RT, NV, V8>;
-    const int S = a.stages, stage_words = X::words() + 2 * R::words();
-    const bool DH = a.r != nullptr;
-    auto copy = [&](int64_t row, int st) {
-        if (row < a.rows) {
-            uint4* at = ring + st * stage_words;
-            X{at}.copy(row_of<XT>(a.x, a.ldx, row), a.cols, ex);
-            R{at + X::words()}.copy(row_of<RT>(a.hin, a.ldhin, row), a.cols, eh);
-            if (DH) R{at + X::words() + R::words()}.copy(row_of<RT>(a.r, a.ldr, row), a.cols, er);
-        }
-        copies_commit();
-    };
-    for (int st = 0; st < S - 1; ++st) copy(blockIdx.x + (int64_t)st * gridDim.x, st);
-    Raw8<WT> w[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        float v[E];
-        vector8(a.w, a.wdt, a.w_aligned, a.cols, Map::unit(j), 1.f, v);
-        w[j] = narrow8<WT>(v);
-    }
-    int turn = 0, st = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const float rstd = a.rstd[row], mean = a.mean[row];
-        Unit<XT, V8> dy[NV];
-        Unit<RT, V8> h[NV], dh[NV];
-        copy(row + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
-        copies_wait_all_but(S - 1);
-        if (!V8) __syncthreads();
-        uint4* at = ring + st * stage_words;
-        X{at}.read(dy, row_of<XT>(a.x, a.ldx, row), a.cols);
-        R{at + X::words()}.read(h, row_of<RT>(a.hin, a.ldhin, row), a.cols);
-        if (DH) R{at + X::words() + R::words()}.read(dh, row_of<RT>(a.r, a.ldr, row), a.cols);
-        st = st == S - 1 ? 0 : st + 1;
-        const uint64_t rr = pack2(rstd, rstd), mm = pack2(-mean, -mean);
-        uint64_t g2 = 0, d2 = 0;
-        // past the row's end dy is 0, and with it every term
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int q = 0; q < E / 2; ++q) {
-                const uint64_t xh = mul2(add2(h[j].pair(q), mm), rr), g = dy[j].pair(q), gw = mul2(g, pair8<WT>(w[j], q));
-                dw[j][q] = fma2(g, xh, dw[j][q]);
-                db[j][q] = add2(g, db[j][q]);
-                g2 = add2(g2, gw);
-                d2 = fma2(gw, xh, d2);
-            }
-        const float2 gp = unpack2(g2), dp = unpack2(d2);
-        const float2 c = block_sum2(gp.x + gp.y, dp.x + dp.y, ssum[turn]);
-        // dr = rstd g w + (dh - rstd c1 - xh rstd c2), the sum in the brackets first
-        const float c1 = -rstd * (c.x * inv_n), c2 = -rstd * (c.y * inv_n);
-        const uint64_t p1 = pack2(c1, c1), p2 = pack2(c2, c2);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float v[E];
-#pragma unroll
-            for (int q = 0; q < E / 2; ++q) {
-                const uint64_t xh = mul2(add2(h[j].pair(q), mm), rr);
-                const uint64_t t = fma2(xh, p2, DH ? add2(dh[j].pair(q), p1) : p1);
-                const float2 p = unpack2(fma2(mul2(dy[j].pair(q), pair8<WT>(w[j], q)), rr, t));
-                v[2 * q] = p.x;
-                v[2 * q + 1] = p.y;
-            }
-            store_gradients<XT, RT, V8>(a, step, row, Map::unit(j), v);
-        }
-    }
-    if (!a.part) return;
-    float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = Map::unit(j) * 8;
-        if (a.part16 && c + 8 <= a.cols) {
-#pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-                const float2 x = unpack2(dw[j][q]), y = unpack2(dw[j][q + 1]);
-                *reinterpret_cast<float4*>(part + c + 2 * q) = make_float4(x.x, x.y, y.x, y.y);
-                const float2 s = unpack2(db[j][q]), t = unpack2(db[j][q + 1]);
-                *reinterpret_cast<float4*>(part + a.cols + c + 2 * q) = make_float4(s.x, s.y, t.x, t.y);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 p = unpack2(dw[j][e / 2]), q = unpack2(db[j][e / 2]);
-                if (c + e < a.cols) {
-                    part[c + e] = e % 2 ? p.y : p.x;
-                    part[a.cols + c + e] = e % 2 ? q.y : q.x;
-                }
-            }
-        }
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t w = word_of(bits, q);
+        v[2 * q] = kept_low(w, d.above) ? v[2 * q] * d.scale : 0.f;
+        v[2 * q + 1] = kept_high(w, d.above) ? v[2 * q + 1] * d.scale : 0.f;
     }
 }
 
-// Rows on 16-byte boundaries (zero_layernorm.cuh).  Values are read from shared
+// Values are read from shared
 // memory for the sums and again for the gradients: registers hold the lane's
 // parts of dw and db.  The rows' mean and rstd are read a row ahead; the block's
 // G parts of dw and db are added in order, so that a block writes one.
-template <int XT, int RT, int WT, int NV>
+template <int XT, int RT, int WT, int NV, bool SHIFT>
 __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const __grid_constant__ LayerNormArgs a) {
     __shared__ __align__(16) float2 ssum[2][32];
-    using X = Lane<XT, NV>;
-    using R = Lane<RT, NV>;
+    using X = Lane<XT, NV, SHIFT>;
+    using R = Lane<RT, NV, SHIFT>;
     using V = Vector<WT>;
     constexpr int XS = 8 * Elem<XT>::SIZE, RS = 8 * Elem<RT>::SIZE;          // bytes of a unit
     const int T = a.T, G = blockDim.x / T, group = threadIdx.x / T, units = a.units;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = T >> 5, w0 = group * warps;
     const int uw = (warp - w0) * NV * 32, left = units - uw;                 // the warp's first unit, units from there
-    const int n = (left - lane + 31) >> 5;                                   // this lane's units (any number above NV: all)
+    const int n = SHIFT ? (left + 31) >> 5 : (left - lane + 31) >> 5;        // the warp's js, or this lane's (any number above NV: all)
+    const int wcols = a.cols - uw * 8, lcols = wcols - lane * 8;             // columns from the warp's first on, from this lane's
     pdl_wait();
     pdl_launch_next();
     const uint32_t step = drop_step(a.drop);
@@ -188,18 +67,22 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
     const int nw = blockDim.x >> 5, S = a.stages, xwords = nw * X::WORDS, rwords = nw * R::WORDS, stage_words = xwords + 2 * rwords;
     const int64_t first = group * (int64_t)gridDim.x + blockIdx.x, every = (int64_t)G * gridDim.x;
     const bool DH = a.r != nullptr;
-    const uint4 *gat = ring + warp * X::WORDS, *hat = ring + xwords + warp * R::WORDS, *uat = hat + rwords;
-    const uint32_t gat32 = (uint32_t)__cvta_generic_to_shared(gat), hat32 = (uint32_t)__cvta_generic_to_shared(hat), uat32 = hat32 + rwords * 16;
+    uint4 *const gat = ring + warp * X::WORDS, *const hat = ring + xwords + warp * R::WORDS, *const uat = hat + rwords;
+    const Extent ex = extent_of<XT>(a.x, a.ldx, a.rows, a.cols), er = extent_of<RT>(a.r, a.ldr, a.rows, a.cols),
+                 eh = extent_of<RT>(a.hin, a.ldhin, a.rows, a.cols);
     const char* cg = static_cast<const char*>(a.x) + first * a.ldx * Elem<XT>::SIZE + (int64_t)uw * XS;
     const char* ch = static_cast<const char*>(a.hin) + first * a.ldhin * Elem<RT>::SIZE + (int64_t)uw * RS;
     const char* cu = static_cast<const char*>(a.r) + (DH ? first * a.ldr * Elem<RT>::SIZE + (int64_t)uw * RS : 0);
     const int64_t dg = every * a.ldx * Elem<XT>::SIZE, dh = every * a.ldhin * Elem<RT>::SIZE, du = every * a.ldr * Elem<RT>::SIZE;
+    char* DR = static_cast<char*>(a.y) + (a.y ? first * a.ldy * Elem<RT>::SIZE + (int64_t)uw * RS : 0);
+    char* DX = static_cast<char*>(a.h) + (a.h ? first * a.ldh * Elem<XT>::SIZE + (int64_t)uw * XS : 0);
+    const int64_t ddr = every * a.ldy * Elem<RT>::SIZE, ddx = every * a.ldh * Elem<XT>::SIZE;
     int64_t crow = first;
     auto copy = [&](int st) {
         if (crow < a.rows) {
-            X::copy(gat32 + st * stage_words * 16, cg, left);
-            R::copy(hat32 + st * stage_words * 16, ch, left);
-            if (DH) R::copy(uat32 + st * stage_words * 16, cu, left);
+            X::copy(gat + st * stage_words, cg, wcols, ex);
+            R::copy(hat + st * stage_words, ch, wcols, eh);
+            if (DH) R::copy(uat + st * stage_words, cu, wcols, er);
         }
         copies_commit();
         crow += every;
@@ -226,17 +109,27 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
             next_rstd = a.rstd[row + every];
         }
         copies_wait_all_but(S - 1);
-        if (XT == ZERO_F32 || RT == ZERO_F32) __syncwarp();
-        const uint4 *gs = gat + st * stage_words, *hs = hat + st * stage_words, *us = uat + st * stage_words;
+        if (X::SHARED || R::SHARED) __syncwarp();
+        const int goff = SHIFT ? (int)(reinterpret_cast<uintptr_t>(cg - S * dg) & 15u) : 0,
+                  hoff = SHIFT ? (int)(reinterpret_cast<uintptr_t>(ch - S * dh) & 15u) : 0,
+                  uoff = SHIFT ? (int)(reinterpret_cast<uintptr_t>(cu - S * du) & 15u) : 0;
+        uint4 *const gs = gat + st * stage_words, *const hs = hat + st * stage_words, *const us = uat + st * stage_words;
         st = st == S - 1 ? 0 : st + 1;
         const uint64_t rr = pack2(rstd, rstd), mm = pack2(-mean, -mean);
         uint64_t g2 = 0, d2 = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (j < n) {
-                const Raw8<XT> dy = X::read(gs, j);
-                const Raw8<RT> h = R::read(hs, j);
-                const Raw8<WT> w = V::read(wat, uw + lane + 32 * j, units);
+                const int u = SHIFT ? min(uw + lane + 32 * j, units - 1) : uw + lane + 32 * j;
+                // past the row's end dy and h are 0 (the next row's may be infinite), and with them every term
+                const Raw8<XT> dy = X::read(gs, j, goff, lcols - 256 * j);
+                const Raw8<RT> h = R::read(hs, j, hoff, lcols - 256 * j);
+                const Raw8<WT> w = V::read(wat, u, units);
+                if (SHIFT) {                                 // shifted once, not twice
+                    __syncwarp();
+                    X::write(gs, j, dy);
+                    R::write(hs, j, h);
+                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint64_t xh = mul2(add2(pair8<RT>(h, q), mm), rr), g = pair8<XT>(dy, q), gw = mul2(g, pair8<WT>(w, q));
@@ -263,28 +156,37 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
         // dr = rstd g w + (dh - rstd c1 - xh rstd c2), the sum in the brackets first
         const float c1 = -rstd * (sx * inv_n), c2 = -rstd * (sy * inv_n);
         const uint64_t p1 = pack2(c1, c1), p2 = pack2(c2, c2);
+        Put<RT, SHIFT> putr;
+        Put<XT, SHIFT> putx;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (j < n) {
-                const Raw8<XT> dy = X::read(gs, j);
-                const Raw8<RT> h = R::read(hs, j);
-                const Raw8<WT> w = V::read(wat, uw + lane + 32 * j, units);
-                Raw8<RT> dh;
-                if (DH) dh = R::read(us, j);
+                const int u = SHIFT ? min(uw + lane + 32 * j, units - 1) : uw + lane + 32 * j;
+                const Raw8<XT> dy = Lane<XT, NV, false>::read(gs, j, 0, 8);
+                const Raw8<RT> h = Lane<RT, NV, false>::read(hs, j, 0, 8);
+                const Raw8<WT> w = V::read(wat, u, units);
+                Raw8<RT> up;
+                if (DH) up = R::read(us, j, uoff, 8);
                 float v[8];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint64_t xh = mul2(add2(pair8<RT>(h, q), mm), rr);
-                    const uint64_t t = fma2(xh, p2, DH ? add2(pair8<RT>(dh, q), p1) : p1);
+                    const uint64_t t = fma2(xh, p2, DH ? add2(pair8<RT>(up, q), p1) : p1);
                     const float2 p = unpack2(fma2(mul2(pair8<XT>(dy, q), pair8<WT>(w, q)), rr, t));
                     v[2 * q] = p.x;
                     v[2 * q + 1] = p.y;
                 }
-                store_gradients<XT, RT, true>(a, step, row, uw + lane + 32 * j, v);
+                if (a.y) putr.put(DR, j, lcols - 256 * j, a.y32, j == NV - 1, narrow8<RT>(v));
+                if (a.h) {
+                    if (a.drop.on) dropped(a.drop, step, row * units + u, v);
+                    putx.put(DX, j, lcols - 256 * j, a.h32, j == NV - 1, narrow8<XT>(v));
+                }
             }
+        DR += ddr;
+        DX += ddx;
         mean = next_mean;
         rstd = next_rstd;
-        if (XT == ZERO_F32 || RT == ZERO_F32) __syncwarp();      // the next copies land in words that other lanes read
+        if (X::SHARED || R::SHARED) __syncwarp();            // the next copies land in words that other lanes read
     }
     if (!a.part) return;
     // the groups' parts by shared memory: 4 words of 4 columns for each unit of dw, then of db, threads side by side
@@ -304,7 +206,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
     for (int i = threadIdx.x; i < NV * 4 * T; i += all) {
         const int k = i / T, t = i - k * T, u = (t >> 5) * NV * 32 + (k >> 2) * 32 + (t & 31);
-        if (u >= units) continue;
+        if (u * 8 + (k & 1) * 4 >= a.cols) continue;
         float4 sum = P[k * all + t];
         for (int g = 1; g < G; ++g) {
             const float4 p = P[k * all + g * T + t];
@@ -315,12 +217,11 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
         }
         float* to = part + (k & 2 ? a.cols : 0) + u * 8 + (k & 1) * 4;
         if (a.part16) {
-            *reinterpret_cast<float4*>(to) = sum;
+            *reinterpret_cast<float4*>(to) = sum;            // columns a multiple of 4: all of them, or none
         } else {
-            to[0] = sum.x;
-            to[1] = sum.y;
-            to[2] = sum.z;
-            to[3] = sum.w;
+            const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+            for (int e = 0; e < 4; ++e)
+                if (u * 8 + (k & 1) * 4 + e < a.cols) to[e] = f[e];
         }
     }
 }
@@ -381,7 +282,11 @@ __global__ void __launch_bounds__(NORM_THREADS) k_layernorm_backward_long(const 
                 g[e] = rstd * (g[e] * w[e] - c1 - (v[e] - mean) * rstd * c2);
                 if (DH) g[e] += up[e];
             }
-            store_gradients<XT, RT, V8>(a, step, row, u, g);
+            if (a.y) store_unit<RT, V8>(row_of<RT>(a.y, a.ldy, row), u, a.cols, g);
+            if (a.h) {
+                if (a.drop.on) dropped(a.drop, step, row * a.units + u, g);
+                store_unit<XT, V8>(row_of<XT>(a.h, a.ldh, row), u, a.cols, g);
+            }
         }
     }
 }
@@ -439,27 +344,22 @@ __global__ void __launch_bounds__(1024) k_layernorm_sums(const __grid_constant__
     st1_any(out, cc, t, dt);
 }
 
+// packed: the weight in shared memory in dy's type, not in fp32.
+template <int XT, int RT, bool SHIFT>
+static const void* rows_of(bool packed, int nv) {
+    if (nv == 2) return (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 2, SHIFT>;
+    return packed ? (const void*)k_layernorm_backward_rows<XT, RT, XT, 4, SHIFT> : (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 4, SHIFT>;
+}
 template <int XT, int RT>
-static const void* general(bool v8, int nv) {
-    if (nv == 2) return (const void*)k_layernorm_backward<XT, RT, 2>;
-    if (nv == 4) return (const void*)k_layernorm_backward<XT, RT, 4>;
+static const void* fn_of(bool v8, bool packed, int nv) {
+    if (nv) return v8 ? rows_of<XT, RT, false>(packed, nv) : rows_of<XT, RT, true>(packed, nv);
     return v8 ? (const void*)k_layernorm_backward_long<XT, RT, true> : (const void*)k_layernorm_backward_long<XT, RT, false>;
 }
-static const void* general_fn(int xt, int rt, bool v8, int nv) {
-    if (xt == ZERO_F32) return general<ZERO_F32, ZERO_F32>(v8, nv);
-    if (xt == ZERO_BF16) return rt == ZERO_F32 ? general<ZERO_BF16, ZERO_F32>(v8, nv) : general<ZERO_BF16, ZERO_BF16>(v8, nv);
-    return rt == ZERO_F32 ? general<ZERO_F16, ZERO_F32>(v8, nv) : general<ZERO_F16, ZERO_F16>(v8, nv);
-}
-// packed: the weight in shared memory in dy's type, not in fp32.
-template <int XT, int RT>
-static const void* rows_of(bool packed, int nv) {
-    if (nv == 2) return (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 2>;
-    return packed ? (const void*)k_layernorm_backward_rows<XT, RT, XT, 4> : (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 4>;
-}
-static const void* rows_fn(int xt, int rt, bool packed, int nv) {
-    if (xt == ZERO_F32) return rows_of<ZERO_F32, ZERO_F32>(false, nv);
-    if (xt == ZERO_BF16) return rt == ZERO_F32 ? rows_of<ZERO_BF16, ZERO_F32>(packed, nv) : rows_of<ZERO_BF16, ZERO_BF16>(packed, nv);
-    return rt == ZERO_F32 ? rows_of<ZERO_F16, ZERO_F32>(packed, nv) : rows_of<ZERO_F16, ZERO_F16>(packed, nv);
+// nv 0: rows too long for the registers.
+static const void* backward_fn(int xt, int rt, bool v8, bool packed, int nv) {
+    if (xt == ZERO_F32) return fn_of<ZERO_F32, ZERO_F32>(v8, packed, nv);
+    if (xt == ZERO_BF16) return rt == ZERO_F32 ? fn_of<ZERO_BF16, ZERO_F32>(v8, packed, nv) : fn_of<ZERO_BF16, ZERO_BF16>(v8, packed, nv);
+    return rt == ZERO_F32 ? fn_of<ZERO_F16, ZERO_F32>(v8, packed, nv) : fn_of<ZERO_F16, ZERO_F16>(v8, packed, nv);
 }
 static const void* sums_long_fn(int xt, int rt) {
     if (xt == ZERO_F32) return (const void*)k_layernorm_sums_long<ZERO_F32, ZERO_F32>;
@@ -544,13 +444,22 @@ int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_ma
     RowsShape rs = {};
     int nv = 4;
     bool packed = false;
-    if (v8 && rows > 0) {
+    if (rows > 0) {
         rs = rows_shape(rows, cols, words, 2, sms, &nv);
+        // four units a lane and the shifts beside the sums do not fit the registers: only where two leave the block few threads
+        // (8192 x 4097, one row of 288 threads or three of 160)
+        if (!v8 && nv == 4) {
+            const RowsShape two = rows_shape(rows, cols, 2, words, 2, sms);
+            if (two.threads * 5 > rs.threads * 4) {
+                rs = two;
+                nv = 2;
+            }
+        }
         packed = !rs.threads && w16;
         if (packed) rs = rows_shape(rows, cols, nv = 4, words, 1, sms);
     }
     if (rs.threads) {
-        const void* f = rows_fn(dy->dtype, rt, packed, nv);
+        const void* f = backward_fn(dy->dtype, rt, v8, packed, nv);
         a.stages = rs.stages;
         a.T = rs.T;
         a.y32 = dr && rows_on_32(*dr, rows);
@@ -563,17 +472,7 @@ int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_ma
         rc = cuda_fail(launch_after_previous(f, rs.grid, rs.threads, args, smem, s), "zero_layernorm_backward launch");
         if (rc != ZERO_OK) return rc;
     } else if (rows > 0) {
-        NormShape p = shape_of(cols, words, LN_BACKWARD_THREADS);
-        if (v8) p = NormShape{0, NORM_THREADS, 1, 2, 0};
-        a.stages = p.stages;
-        int64_t g = (int64_t)p.per_sm * sms;
-        if (g > NORM_MAX_GRID) g = NORM_MAX_GRID;
-        if (g > rows) g = rows;
-        const void* f = general_fn(dy->dtype, rt, v8, p.nv);
-        rc = raise_smem(f, p.smem, "zero_layernorm_backward shared-memory size");
-        if (rc != ZERO_OK) return rc;
-        parts = (int)g;
-        if (p.nv == 0 && a.part) {
+        if (a.part) {
             // dw and db first: dr and dx may be written over dy or dh
             const int64_t chunks = (cols + 127) / 128;
             int64_t shares = (8 * (int64_t)sms + chunks - 1) / chunks;
@@ -585,8 +484,9 @@ int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_ma
                            "zero_layernorm_backward sums launch");
             if (rc != ZERO_OK) return rc;
         }
-        if (p.nv == 0) g = rows < 1 << 30 ? rows : 1 << 30;
-        rc = cuda_fail(launch_after_previous(f, (int)g, p.threads, args, p.smem, s), "zero_layernorm_backward launch");
+        const int g = (int)(rows < 1 << 30 ? rows : 1 << 30);
+        rc = cuda_fail(launch_after_previous(backward_fn(dy->dtype, rt, v8, false, 0), g, NORM_THREADS, args, 0, s),
+                       "zero_layernorm_backward launch");
         if (rc != ZERO_OK) return rc;
     }
     if (!a.part) return ZERO_OK;
