@@ -162,3 +162,14 @@ def test_another_stream_and_many_tiles(Z):
         Z.zero_dropout(x, None, rows, cols, Z.drop(0.1, 1, 2, 3), y)
     torch.cuda.current_stream().wait_stream(s)
     near(y, torch.where(B.keep(rows, cols, 0.1, 1, 2, 3), x.double() * B.scale(0.1), 0.0), BF16)
+
+
+@pytest.mark.parametrize("cols", [256, 257])
+def test_offsets_past_32_bits(Z, cols):
+    """Rows 2^29 elements apart: the last one's bytes lie past 2^32."""
+    g = gen(5)
+    wide = torch.empty(4 * (2 ** 29 + 8), device=DEV).view(4, 2 ** 29 + 8)
+    x, y = wide[:, :cols], wide[:, 4096:4096 + cols]
+    x.copy_(rnd(g, 4, cols))
+    Z.zero_dropout(x, None, 4, cols, Z.drop(0.3, 2), y)
+    near(y, torch.where(B.keep(4, cols, 0.3, 2, 0, 0), x.double() * B.scale(0.3), 0.0), F32)

@@ -347,3 +347,37 @@ def test_many_passes_one_behind_the_other(Z):
         out.append(o)
     assert int(b.status) == 0
     assert all(torch.equal(p, q) for p, q in zip(*out))
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("cols", [8, 300, 4104])
+def test_an_infinity_in_the_last_column_of_few_rows(Z, rows, cols):
+    """It meets its own column of the weights only: gate and up are infinite with the weights' signs, not NaN."""
+    g = gen(10)
+    b = Block(Z, rnd(g, rows, cols), rnd(g, 70, cols), rnd(g, 70, cols), 0)
+    b.x[0, -1] = float("inf")
+    gate, up = b.new(rows, 70), b.new(rows, 70)
+    b.forward(None, gate, up)
+    assert torch.equal(gate[0].double(), b.wg[:, -1].double() * float("inf"))
+    assert torch.equal(up[0].double(), b.wu[:, -1].double() * float("inf"))
+    assert torch.isfinite(gate[1:]).all()
+
+
+@pytest.mark.parametrize("rows", [2, 9])
+def test_offsets_past_32_bits(Z, rows):
+    """Rows 2^29 elements apart: the last one's bytes lie past 2^32."""
+    g = gen(11)
+    cols, ff, far = 136, 264, 2 ** 29 + 8
+    wide = torch.empty(rows * far, dtype=BF16, device=DEV).view(rows, far)
+    x, h = wide[:, 64:64 + cols], wide[:, 1024:1024 + ff]
+    x.copy_(rnd(g, rows, cols))
+    b = Block(Z, x, rnd(g, ff, cols, std=0.1), rnd(g, ff, cols, std=0.1), 0)
+    b.forward(h)
+    b.check_forward(h)
+    gate, up, dg, du, dx = (wide[:, k * 512:k * 512 + n] for k, n in ((4, ff), (5, ff), (6, ff), (7, ff), (8, cols)))
+    gate.copy_(rnd(g, rows, ff))
+    up.copy_(rnd(g, rows, ff))
+    dh, dwg, dwu = rnd(g, rows, ff), b.new(ff, cols), b.new(ff, cols)
+    b.backward(dh, gate, up, dg, du, dx, dwg, dwu)
+    b.check_slopes(dh, gate, up, dg, du)
+    b.check_products(dg, du, dx, dwg, dwu)

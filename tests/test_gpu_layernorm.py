@@ -303,3 +303,41 @@ def test_a_captured_pass(Z):
         assert all(torch.equal(p, q) for p, q in zip(o1, o2))
         k = B.keep(rows, cols, 0.1, 4, 1, step)
         near(o1[0], torch.where(k, x.double() * B.scale(0.1), 0.0) + r.double(), BF16, 8 * E)
+
+
+@pytest.mark.parametrize("cols", [264, 265, 20000])
+def test_offsets_past_32_bits(Z, cols):
+    """Rows 2^30 elements apart: the last one's bytes lie past 2^32."""
+    g = gen(13)
+    rows, far = 4, 2 ** 30 + 8
+    wide = torch.empty(rows * far, dtype=BF16, device=DEV).view(rows, far)
+    x, r, h, y, dy, dh, dr = (wide[:, k * 32768:k * 32768 + cols] for k in range(7))
+    for t in (x, r, dy, dh):
+        t.copy_(rnd(g, rows, cols, dtype=BF16))
+    w, b = rnd(g, cols, dtype=BF16, mean=1.0), rnd(g, cols, dtype=BF16)
+    mean, rstd, dw, db, ws = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV), torch.empty_like(w), torch.empty_like(w), workspace(Z, cols)
+    drop, k = Z.drop(0.2, 5), B.keep(rows, cols, 0.2, 5, 0, 0)
+    Z.zero_layernorm_forward(x, r, drop, w, b, rows, cols, EPS, h, y, mean, rstd)
+    xd = torch.where(k, x.double() * B.scale(0.2), 0.0)
+    near(h, xd + r.double(), BF16, 2 * E * (xd.abs() + r.double().abs()))
+    ref = Ref(h, w, b)
+    ref.check_forward(y, mean, rstd)
+    was = dy.clone()
+    Z.zero_layernorm_backward(dy, h, w, rows, cols, mean, rstd, dh, drop, dr, dy, dw, db, 0, ws, ws.numel())
+    ref.check_backward(was, dh, dr, dy, dw, db, k, 0.2)
+
+
+def test_a_bad_row_beside_rows_that_share_its_words(Z):
+    """Odd widths: a row's first and last 16 bytes hold the neighbouring rows' elements, which may be infinite."""
+    g = gen(14)
+    rows, cols = 9, 333
+    for dtype in (F16, BF16, F32):
+        x, dy = rnd(g, rows, cols, dtype=dtype), rnd(g, rows, cols, dtype=dtype)
+        x[4], dy[4] = float("inf"), float("nan")
+        y, dr, mean, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+        Z.zero_layernorm_forward(x, None, None, None, None, rows, cols, EPS, None, y, mean, rstd)
+        Z.zero_layernorm_backward(dy, x, None, rows, cols, mean, rstd, None, None, dr, None, None, None, 0, None, 0)
+        keep = [r for r in range(rows) if r != 4]
+        assert torch.isfinite(y[keep]).all() and torch.isfinite(dr[keep]).all()
+        Ref(x[keep], None, None).check_forward(y[keep], mean[keep], rstd[keep])
+        Ref(x[keep], None, None).check_backward(dy[keep], None, dr[keep], None, None, None)

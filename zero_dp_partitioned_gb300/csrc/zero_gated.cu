@@ -571,7 +571,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_gated_few(const __grid_const
             }
 #pragma unroll
             for (int j = 0; j < AT_ONCE; ++j) {
-                const int u = min(u0 + 32 * j, a.units - 1);
+                const int u = u0 + 32 * j;
+                if (u >= a.units) break;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     Raw8<DT> x;

@@ -78,13 +78,12 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const 
         copy(at_stage == 0 ? S - 1 : at_stage - 1);
         copies_wait_all_but(S - 1);
         if (X::SHARED || R::SHARED) __syncwarp();
-        const int xoff = SHIFT ? (int)(reinterpret_cast<uintptr_t>(cx - S * dx) & 15u) : 0,
-                  roff = SHIFT ? (int)(reinterpret_cast<uintptr_t>(cr - S * dr) & 15u) : 0;
-        const uint4 *xs = xat + at_stage * stage_words, *rs = rat + at_stage * stage_words;
+        const int xoff = X::off(cx - S * dx), roff = R::off(cr - S * dr);
+        uint4 *const xs = xat + at_stage * stage_words, *const rs = rat + at_stage * stage_words;
         at_stage = at_stage == S - 1 ? 0 : at_stage + 1;
         // h as it is stored
+        Put<RT, NV, SHIFT> puth;
         uint64_t s2 = 0;
-        Put<RT, SHIFT> puth;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (j < n) {
@@ -97,8 +96,15 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const 
                            .raw;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) s2 = add2(s2, pair8<RT>(r[j], q));
-                if (a.h) puth.put(H, j, lcols - 256 * j, a.h32, j == NV - 1, r[j]);
+                if (!SHIFT && a.h) puth.put(H, rs, j, lcols - 256 * j, a.h32, r[j]);
             }
+        if (SHIFT && a.h) {
+            __syncwarp();                                    // all lanes have read the residual's units
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (j < n) puth.put(H, rs, j, lcols - 256 * j, false, r[j]);
+            puth.end(H, rs, wcols);
+        }
         const float2 sp = unpack2(s2);
         const float mw = warp_sum(sp.x + sp.y) * inv_mine;
         const uint64_t mw2 = pack2(-mw, -mw);
@@ -145,7 +151,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const 
             if (a.rstd) a.rstd[row] = rstd;
         }
         const uint64_t mm = pack2(-mean, -mean), rr = pack2(rstd, rstd);
-        Put<XT, SHIFT> puty;
+        Put<XT, NV, SHIFT> puty;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (j < n) {
@@ -158,8 +164,10 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_forward_rows(const 
                     y[2 * q] = v.x;
                     y[2 * q + 1] = v.y;
                 }
-                puty.put(Y, j, lcols - 256 * j, a.y32, j == NV - 1, narrow8<XT>(y));
+                puty.put(Y, xs, j, lcols - 256 * j, a.y32, narrow8<XT>(y));
             }
+        puty.end(Y, xs, wcols);
+        if (SHIFT) __syncwarp();                             // the next copies land in these words
     }
 }
 

@@ -53,13 +53,21 @@ __device__ __forceinline__ Unit<RT, V8> drop_add_unit(const Unit<XT, V8>& x, con
 // is done once a row, not once a unit: one block a row, its weights fetched for
 // every 2 rows, took 45 instructions an element and 28 us (8192 x 1600 bf16).
 //
-// SHIFT: rows that start anywhere, or widths that are no multiple of 8.  Memory
-// is still read and written in aligned 16-byte words: a warp copies the words
-// that its columns lie in, a lane takes the words that its unit touches and
-// shifts them, and gives what it stores the end of the unit before it (from the
-// neighbouring lane, or lane 31's last unit); only a warp's first and last
-// words of a row, which it shares, go element by element.
+// SHIFT: rows that start anywhere, or widths that are no multiple of 8.  fp32
+// rows are copied by words of 4 bytes, neighbouring lanes neighbouring ones, so
+// that they lie aligned in shared memory, and stored the same way from there.
+// 16-bit rows are copied and stored in aligned 16-byte words: a lane takes the
+// words that its unit touches and shifts them, and gives what it stores the end
+// of the unit before it (from the neighbouring lane, or lane 31's last unit);
+// only a warp's first and last words of a row, which it shares, go element by
+// element.  Each the other way was slower (8192 x 4097, forward and backward:
+// bf16 92 and 167 us, by 4 bytes 109 and 191; fp32 134 and 168, by shifts 159 and
+// 224).
 constexpr int LN_THREADS = 512;
+
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 
 // One matrix of a stage.  Without SHIFT, 16-bit units are one 16-byte word, copied
 // and read by the same lane.  fp32 units are two, and a lane that copied its own
@@ -67,68 +75,79 @@ constexpr int LN_THREADS = 512;
 // and read what other lanes of the warp copied.
 template <int DT, int NV, bool SHIFT>
 struct Lane {
-    static constexpr int W = DT == ZERO_F32 ? 2 : 1, N = 4 * W, SIZE = Elem<DT>::SIZE;
-    static constexpr int WORDS = NV * W * 32 + SHIFT;                        // of a warp
-    static constexpr bool SHARED = SHIFT || DT == ZERO_F32;                 // lanes read what others copied
+    static constexpr bool F32 = DT == ZERO_F32;
+    static constexpr int W = F32 ? 2 : 1, SIZE = Elem<DT>::SIZE;
+    static constexpr int WORDS = NV * W * 32 + (SHIFT && !F32);              // of a warp
+    static constexpr bool SHARED = SHIFT || F32;                            // lanes read what others copied
+    // The byte in its first word at which a row lies in shared memory.
+    static __device__ __forceinline__ int off(const char* row) {
+        return SHIFT && !F32 ? (int)(reinterpret_cast<uintptr_t>(row) & 15u) : 0;
+    }
     // from: the warp's first column of the row; cols: columns from there to the row's end; x: what may be read
     static __device__ __forceinline__ void copy(uint4* to, const char* from, int cols, const Extent& x) {
         const int lane = threadIdx.x & 31;
         const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-        if (!SHIFT) {
+        if constexpr (!SHIFT) {
             const int left = cols / 8 * W - lane;
 #pragma unroll
             for (int k = 0; k < NV * W; ++k)
                 if (32 * k < left) copy16(at + (32 * k + lane) * 16, from + (32 * k + lane) * 16);
-            return;
-        }
-        if (cols <= 0) return;
-        const int off = (int)(reinterpret_cast<uintptr_t>(from) & 15u), all = min(cols, NV * 256) * SIZE + off;
-        const int words = (all + 15) / 16, left = words - lane;              // words from this lane's first
-        from -= off;
-        const bool edge = from < x.lo || from + words * 16 > x.hi;
+        } else if constexpr (F32) {
+            const int left = min(cols, NV * 256) - lane;
 #pragma unroll
-        for (int k = 0; k < NV * W + 1; ++k)
-            if (32 * k < left) {
-                const char* p = from + (32 * k + lane) * 16;
-                if (!edge || (p >= x.lo && p + 16 <= x.hi)) {
-                    copy16(at + (32 * k + lane) * 16, p);
-                } else {
-                    // partly outside the matrix: element by element
+            for (int k = 0; k < NV * 8; ++k)
+                if (32 * k < left) copy4(at + (32 * k + lane) * 4, from + (32 * k + lane) * 4);
+        } else {
+            if (cols <= 0) return;
+            const int o = off(from), words = (min(cols, NV * 256) * SIZE + o + 15) / 16, left = words - lane;
+            from -= o;
+            const bool edge = from < x.lo || from + words * 16 > x.hi;
+#pragma unroll
+            for (int k = 0; k < NV + 1; ++k)
+                if (32 * k < left) {
+                    const char* p = from + (32 * k + lane) * 16;
+                    if (!edge || (p >= x.lo && p + 16 <= x.hi)) {
+                        copy16(at + (32 * k + lane) * 16, p);
+                    } else {
+                        // partly outside the matrix: element by element
 #pragma unroll 1
-                    for (int e = 0; e < 16 / SIZE; ++e) {
-                        const char* q = p + e * SIZE;
-                        const bool in = q >= x.lo && q + SIZE <= x.hi;
-                        if constexpr (DT == ZERO_F32)
-                            reinterpret_cast<uint32_t*>(to + 32 * k + lane)[e] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
-                        else
-                            reinterpret_cast<uint16_t*>(to + 32 * k + lane)[e] = in ? *reinterpret_cast<const uint16_t*>(q) : (uint16_t)0;
+                        for (int e = 0; e < 8; ++e) {
+                            const char* q = p + e * SIZE;
+                            reinterpret_cast<uint16_t*>(to + 32 * k + lane)[e] =
+                                q >= x.lo && q + SIZE <= x.hi ? *reinterpret_cast<const uint16_t*>(q) : (uint16_t)0;
+                        }
                     }
                 }
-            }
+        }
     }
-    // This lane's j-th unit.  SHIFT: off: the row's byte in its first word; cols: columns from the unit on, what follows reads as 0.
-    static __device__ __forceinline__ Raw8<DT> read(const uint4* at, int j, int off, int cols) {
+    // This lane's j-th unit.  SHIFT: o: off() of the row; cols: columns from the unit on, what follows reads as 0.
+    static __device__ __forceinline__ Raw8<DT> read(const uint4* at, int j, int o, int cols) {
         const int lane = threadIdx.x & 31;
         Raw8<DT> v;
-        if constexpr (!SHIFT) {
 #pragma unroll
-            for (int w = 0; w < W; ++w) v.w[w] = at[(32 * j + lane) * W + w];
-        } else {
-            uint32_t u[N + 4];
+        for (int w = 0; w < W; ++w) v.w[w] = at[(32 * j + lane) * W + w];
+        if constexpr (SHIFT) {
+            uint32_t u[4 * W + 4];
 #pragma unroll
-            for (int k = 0; k < W + 1; ++k) {
-                const uint4 t = at[(32 * j + lane) * W + k];
-                u[4 * k] = t.x;
-                u[4 * k + 1] = t.y;
-                u[4 * k + 2] = t.z;
-                u[4 * k + 3] = t.w;
+            for (int k = 0; k < W; ++k) {
+                u[4 * k] = v.w[k].x;
+                u[4 * k + 1] = v.w[k].y;
+                u[4 * k + 2] = v.w[k].z;
+                u[4 * k + 3] = v.w[k].w;
             }
-            shift_words<N>(u, off);
+            if constexpr (!F32) {
+                const uint4 t = at[32 * j + lane + 1];
+                u[4] = t.x;
+                u[5] = t.y;
+                u[6] = t.z;
+                u[7] = t.w;
+                shift_words<4>(u, o);
+            }
             if (cols < 8)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (e >= cols) {
-                        if constexpr (DT == ZERO_F32) u[e] = 0;
+                        if constexpr (F32) u[e] = 0;
                         else u[e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
                     }
 #pragma unroll
@@ -136,7 +155,7 @@ struct Lane {
         }
         return v;
     }
-    // The unit shifted into place, in the stead of what read() took; all lanes have read their j-th (and no earlier) before.
+    // A unit into its lane's place: what no lane reads any more.
     static __device__ __forceinline__ void write(uint4* at, int j, const Raw8<DT>& v) {
 #pragma unroll
         for (int w = 0; w < W; ++w) at[(32 * j + (threadIdx.x & 31)) * W + w] = v.w[w];
@@ -144,66 +163,67 @@ struct Lane {
 };
 
 // A warp's units of a row, stored one j after the other; the whole warp calls
-// put() where any of its lanes has a unit.
-template <int DT, bool SHIFT>
+// put() where any of its lanes has a unit, and with SHIFT end() at the end.
+template <int DT, int NV, bool SHIFT>
 struct Put {
-    static constexpr int N = DT == ZERO_F32 ? 8 : 4, SIZE = Elem<DT>::SIZE;
-    uint32_t last[4];                                                        // of the unit before: its last 16 bytes
-    // row: the warp's first column of it; on32: rows start on 32-byte boundaries; cols: columns from this lane's unit to the
-    // row's end (none: at most 0); lasts: the warp's last j
-    __device__ __forceinline__ void put(char* row, int j, int cols, bool on32, bool lasts, const Raw8<DT>& r) {
+    static constexpr bool F32 = DT == ZERO_F32;
+    static constexpr int SIZE = Elem<DT>::SIZE;
+    uint32_t last[4];                                                        // of the unit before: its 16 bytes
+    // row: the warp's first column of it; at: the warp's part of a stage, of which no lane reads its j-th units any more; on32:
+    // rows start on 32-byte boundaries; cols: columns from this lane's unit to the row's end (none: at most 0)
+    __device__ __forceinline__ void put(char* row, uint4* at, int j, int cols, bool on32, const Raw8<DT>& r) {
         const int lane = threadIdx.x & 31;
+        char* p = row + (32 * j + lane) * (8 * SIZE);
         if constexpr (!SHIFT) {
-            if (cols <= 0) return;
-            char* p = row + (32 * j + lane) * (8 * SIZE);
-            if constexpr (DT == ZERO_F32) {
+            if constexpr (F32) {
                 if (on32) {
                     st32(p, r.w[0], r.w[1]);
                     return;
                 }
             }
             st8<DT>(p, 0, r);
+        } else if constexpr (F32) {
+            Lane<DT, NV, SHIFT>::write(at, j, r);
         } else {
-            uint32_t v[N], w[N + 4];
-#pragma unroll
-            for (int k = 0; k < N / 4; ++k) {
-                v[4 * k] = r.w[k].x;
-                v[4 * k + 1] = r.w[k].y;
-                v[4 * k + 2] = r.w[k].z;
-                v[4 * k + 3] = r.w[k].w;
-            }
-            char* p = row + (32 * j + lane) * (8 * SIZE);
-            const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15u), cut = 8 - off / SIZE;      // elements up to the last word
+            const uint32_t v[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+            uint32_t w[8];
+            const int o = (int)(reinterpret_cast<uintptr_t>(p) & 15u), cut = 8 - o / SIZE;          // elements up to the last word
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                w[i] = __shfl_sync(0xFFFFFFFFu, lane == 31 ? last[i] : v[N - 4 + i], (lane + 31) & 31);
-                last[i] = v[N - 4 + i];
+                w[i] = __shfl_sync(0xFFFFFFFFu, lane == 31 ? last[i] : v[i], (lane + 31) & 31);
+                last[i] = v[i];
+                w[4 + i] = v[i];
             }
-#pragma unroll
-            for (int i = 0; i < N; ++i) w[4 + i] = v[i];
             if (cols <= 0) return;
-            const bool whole = cols >= 8, before = j > 0 || lane > 0, after = cols >= 16 && !(lasts && lane == 31);
+            const bool whole = cols >= 8, before = j > 0 || lane > 0, after = cols >= 16 && !(j == NV - 1 && lane == 31);
             int from = 0;
-            if (whole && (before || off == 0)) {
-                if (off) {
-                    shift_words<N>(w, 16 - off);
+            if (whole && (before || o == 0)) {
+                if (o) {
+                    shift_words<4>(w, 16 - o);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) w[i] = v[i];
+                    for (int i = 0; i < 4; ++i) w[i] = v[i];
                 }
-#pragma unroll
-                for (int k = 0; k < N / 4; ++k)
-                    reinterpret_cast<uint4*>(p - off)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                *reinterpret_cast<uint4*>(p - o) = make_uint4(w[0], w[1], w[2], w[3]);
                 from = cut;
             }
             const int to = whole && after ? cut : min(cols, 8);
             if (from < to)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (e >= from && e < to) {
-                        if constexpr (DT == ZERO_F32) reinterpret_cast<uint32_t*>(p)[e] = v[e];
-                        else reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
-                    }
+                    if (e >= from && e < to) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+        }
+    }
+    // cols: columns from the warp's first to the row's end
+    __device__ __forceinline__ void end(char* row, const uint4* at, int cols) const {
+        if constexpr (SHIFT && F32) {
+            __syncwarp();
+            const int lane = threadIdx.x & 31, left = min(cols, NV * 256) - lane;
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(at) + lane;
+            uint32_t* p = reinterpret_cast<uint32_t*>(row) + lane;
+#pragma unroll
+            for (int k = 0; k < NV * 8; ++k)
+                if (32 * k < left) p[32 * k] = u[32 * k];
         }
     }
 };

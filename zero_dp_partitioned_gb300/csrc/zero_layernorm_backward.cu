@@ -110,9 +110,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
         }
         copies_wait_all_but(S - 1);
         if (X::SHARED || R::SHARED) __syncwarp();
-        const int goff = SHIFT ? (int)(reinterpret_cast<uintptr_t>(cg - S * dg) & 15u) : 0,
-                  hoff = SHIFT ? (int)(reinterpret_cast<uintptr_t>(ch - S * dh) & 15u) : 0,
-                  uoff = SHIFT ? (int)(reinterpret_cast<uintptr_t>(cu - S * du) & 15u) : 0;
+        const int goff = X::off(cg - S * dg), hoff = R::off(ch - S * dh), uoff = R::off(cu - S * du);
         uint4 *const gs = gat + st * stage_words, *const hs = hat + st * stage_words, *const us = uat + st * stage_words;
         st = st == S - 1 ? 0 : st + 1;
         const uint64_t rr = pack2(rstd, rstd), mm = pack2(-mean, -mean);
@@ -156,8 +154,8 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
         // dr = rstd g w + (dh - rstd c1 - xh rstd c2), the sum in the brackets first
         const float c1 = -rstd * (sx * inv_n), c2 = -rstd * (sy * inv_n);
         const uint64_t p1 = pack2(c1, c1), p2 = pack2(c2, c2);
-        Put<RT, SHIFT> putr;
-        Put<XT, SHIFT> putx;
+        Put<RT, NV, SHIFT> putr;
+        Put<XT, NV, SHIFT> putx;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (j < n) {
@@ -176,12 +174,14 @@ __global__ void __launch_bounds__(LN_THREADS, 1) k_layernorm_backward_rows(const
                     v[2 * q] = p.x;
                     v[2 * q + 1] = p.y;
                 }
-                if (a.y) putr.put(DR, j, lcols - 256 * j, a.y32, j == NV - 1, narrow8<RT>(v));
+                if (a.y) putr.put(DR, hs, j, lcols - 256 * j, a.y32, narrow8<RT>(v));
                 if (a.h) {
                     if (a.drop.on) dropped(a.drop, step, row * units + u, v);
-                    putx.put(DX, j, lcols - 256 * j, a.h32, j == NV - 1, narrow8<XT>(v));
+                    putx.put(DX, gs, j, lcols - 256 * j, a.h32, narrow8<XT>(v));
                 }
             }
+        if (a.y) putr.end(DR, hs, wcols);
+        if (a.h) putx.end(DX, gs, wcols);
         DR += ddr;
         DX += ddx;
         mean = next_mean;
