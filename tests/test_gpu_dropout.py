@@ -1,13 +1,12 @@
 """zero_dropout against the mask of the generator's definition and the formula
 in 64 bits.
 
-Tolerances.  x scale (+ residual) is one fp32 operation, off by 2^-24 of the
-product or sum, then one rounding to the type (u = eps / 2): u + 2 * 2^-24 of
-the value, or half a step of fp16's subnormals.  The scale itself is an fp32
-value, off by 2^-24 of itself at most: the product is off by as much of itself,
-also where a residual cancels it (x scale = 7.5, r = -7.4: the sum of 0.1 may be
-off by 7.5 * 2^-24, 75 * 2^-24 of itself), so 2^-24 |x scale| is added, times
-1 + u for the last rounding."""
+Tolerances.  The scale is an fp32 value, off by 2^-24 of itself at most, and so
+are the product x scale and the sum with the residual once each; then one
+rounding to the type (u = eps / 2): u + 2 * 2^-24 of the value, or half a step of
+fp16's subnormals, and 2 * 2^-24 of the product, also where a residual cancels it
+(x scale = 7.5, r = -7.4: the sum of 0.1 may be off by 15 * 2^-24), times 1 + u
+for the last rounding."""
 import pytest
 import torch
 
@@ -39,7 +38,7 @@ def rnd(g, *shape, dtype=F32, std=1.0, off=0, pad=0):
 
 def near(got, ref, dtype, product=0.0):
     err = (got.double() - ref).abs()
-    lim = ref.abs() * (U[dtype] + 2 * E) + TINY[dtype] + product * E * (1 + U[dtype])
+    lim = ref.abs() * (U[dtype] + 2 * E) + TINY[dtype] + product * 2 * E * (1 + U[dtype])
     assert bool((err <= lim).all()), float((err - lim).max())
 
 

@@ -381,3 +381,33 @@ def test_offsets_past_32_bits(Z, rows):
     b.backward(dh, gate, up, dg, du, dx, dwg, dwu)
     b.check_slopes(dh, gate, up, dg, du)
     b.check_products(dg, du, dx, dwg, dwu)
+
+
+def test_two_streams_at_once(Z):
+    """Passes of two sizes on two streams, beside one another, each with its own buffers and workspace."""
+    g = gen(12)
+    blocks = []
+    for rows, cols, ff in ((700, 264, 1000), (90, 512, 3000)):
+        b = Block(Z, rnd(g, rows, cols), rnd(g, ff, cols, std=0.05), rnd(g, ff, cols, std=0.05), 1)
+        dh = rnd(g, rows, ff)
+        ws = b.ws(Z.zero_gated_backward_workspace_bytes(b.x, b.wg, b.wu, dh, dh, rows, cols, ff))
+        outs = [[b.new(rows, ff) for _ in range(5)] + [b.new(rows, cols), b.new(ff, cols), b.new(ff, cols)] for _ in range(2)]
+        blocks.append((b, dh, ws, outs))
+
+    def passes(b, dh, ws, o):
+        h, gate, up, dg, du, dx, dwg, dwu = o
+        Z.zero_gated_forward(b.x, b.wg, b.wu, b.rows, b.cols, b.ff, 1, h, gate, up, None, 0, b.status)
+        Z.zero_gated_backward(dh, gate, up, b.x, b.wg, b.wu, b.rows, b.cols, b.ff, 1, dg, du, dx, dwg, dwu, 0, *ws, b.status)
+
+    for b, dh, ws, outs in blocks:
+        passes(b, dh, ws, outs[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in blocks]
+    for _ in range(100):
+        for s, (b, dh, ws, outs) in zip(streams, blocks):
+            with torch.cuda.stream(s):
+                passes(b, dh, ws, outs[1])
+    torch.cuda.synchronize()
+    for b, dh, ws, outs in blocks:
+        assert int(b.status) == 0
+        assert all(torch.equal(p, q) for p, q in zip(*outs))

@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(DROP_THREADS) k_dropout(const __grid_constant_
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint64_t k = a.drop.on ? drop2(pair8<DT>(x[j], q), bits, q, a.drop.above) : pair8<DT>(x[j], q);
-                const float2 p = unpack2(RES ? fma2(k, s, pair8<DT>(r[j], q)) : mul2(k, s));
+                const uint64_t d = mul2(k, s);
+                const float2 p = unpack2(RES ? add2(d, pair8<DT>(r[j], q)) : d);
                 v[2 * q] = p.x;
                 v[2 * q + 1] = p.y;
             }
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(DROP_THREADS) k_dropout_any(const __grid_const
         for (int j = 0; j < 8; ++j) {
             const bool kept = __shfl_sync(0xFFFFFFFFu, keep, 4 * j + (lane >> 3)) >> (lane & 7) & 1u;
             const float v = kept ? x[j] : 0.f;
-            if (32 * j < left) st1<DT>(Y, 32 * j, RES ? fmaf(v, a.drop.scale, r[j]) : v * a.drop.scale);
+            if (32 * j < left) st1<DT>(Y, 32 * j, RES ? __fadd_rn(__fmul_rn(v, a.drop.scale), r[j]) : v * a.drop.scale);
         }
     }
 }

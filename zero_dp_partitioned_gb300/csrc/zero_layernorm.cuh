@@ -23,7 +23,9 @@ struct LayerNormArgs {
     DropArgs drop;
 };
 
-// dropout(x) + r of one unit, rounded to the type h is stored in.
+// dropout(x) + r of one unit, rounded to the type h is stored in: the product and
+// the sum each to fp32, as zero_dropout and any other form in fp32 does, so that h
+// has the same bits.
 template <int XT, int RT, bool V8>
 __device__ __forceinline__ Unit<RT, V8> drop_add_unit(const Unit<XT, V8>& x, const Unit<RT, V8>& r, bool has_r,
                                                       const DropArgs& d, uint32_t step, int64_t unit) {
@@ -34,7 +36,8 @@ __device__ __forceinline__ Unit<RT, V8> drop_add_unit(const Unit<XT, V8>& x, con
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const uint64_t k = drop2(x.pair(q), bits, q, d.above);
-        const float2 p = unpack2(has_r ? fma2(k, s, r.pair(q)) : mul2(k, s));
+        const uint64_t d = mul2(k, s);
+        const float2 p = unpack2(has_r ? add2(d, r.pair(q)) : d);
         v[2 * q] = p.x;
         v[2 * q + 1] = p.y;
     }
@@ -51,7 +54,8 @@ __device__ __forceinline__ Unit<RT, V8> drop_add_unit(const Unit<XT, V8>& x, con
 // (16-bit ones packed where rows are too long for that).  These kernels are
 // bound by the instructions they issue before HBM, so all that is not arithmetic
 // is done once a row, not once a unit: one block a row, its weights fetched for
-// every 2 rows, took 45 instructions an element and 28 us (8192 x 1600 bf16).
+// every 2 rows, took 58 instructions an element and 28 us (8192 x 1600 bf16; 20 us
+// now).
 //
 // SHIFT: rows that start anywhere, or widths that are no multiple of 8.  fp32
 // rows are copied by words of 4 bytes, neighbouring lanes neighbouring ones, so

@@ -15,8 +15,8 @@
 // bandwidth): 16384 x 3456 bf16 in 84 us (0.80), behind a dropout, with dx too, 117
 // (0.72); fp16 with an fp32 stream 120 (0.98); 8192 x 4096 fp32 88 (0.90); 8192 x
 // 1600 bf16 28 (0.55: five of them the sums' launch), behind a dropout 37.
-// 16-bit rows are bound by the instructions they issue (43 an element behind a
-// dropout, 25 of them the generator's and dx's).  Rows that start anywhere: 8192
+// 16-bit rows are bound by the instructions they issue (36 an element, with the
+// generator's and dx's 56).  Rows that start anywhere: 8192
 // x 4097 bf16 155 (0.26), fp32 167 (0.47).  Rows past 16384 columns (fp32: 8192)
 // are walked twice and their columns' sums taken by a pass of its own: 2048 x
 // 20480 bf16 in 215 (0.23).
