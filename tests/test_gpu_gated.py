@@ -118,7 +118,7 @@ class Block:
                 near(dw, a + o, ta + 2.0 ** -23 * (a + o).abs(), "dw")
 
 
-SIZES = [(1, 8, 8), (2, 1000, 77), (4, 4100, 300), (3, 12288, 131), (4, 12296, 40), (5, 4096, 2051), (2, 24576, 9), (3, 40, 24), (1, 1600, 640), (1, 256, 9000), (9, 130, 9728), (121, 264, 520), (129, 72, 10000), (2, 129, 65), (17, 64, 128), (100, 136, 304), (257, 200, 129), (300, 1337, 257),
+SIZES = [(1, 8, 8), (2, 1000, 77), (4, 4100, 300), (3, 12288, 131), (4, 12296, 40), (5, 4096, 2051), (2, 24576, 9), (3, 40, 24), (1, 1600, 640), (1, 256, 9000), (9, 130, 9728), (121, 264, 520), (129, 72, 10000), (100, 72, 10000), (128, 200, 20000), (5, 1000, 9800), (2, 129, 65), (17, 64, 128), (100, 136, 304), (257, 200, 129), (300, 1337, 257),
          (513, 520, 1000), (255, 72, 2047)]
 
 
@@ -316,11 +316,11 @@ def test_another_stream_a_captured_pass_and_the_same_bits(Z):
 
 def test_a_wait_that_runs_out_is_reported(Z, monkeypatch):
     g = gen(8)
-    for rows in (9, 300):
-        b = Block(Z, rnd(g, rows, 1000), rnd(g, 700, 1000), rnd(g, 700, 1000), 0)
+    for rows, ff in ((9, 700), (9, 9800), (300, 700)):
+        b = Block(Z, rnd(g, rows, 1000), rnd(g, ff, 1000), rnd(g, ff, 1000), 0)
         monkeypatch.setenv("ZERO_GB300_SPIN_LIMIT", "0")
-        h = b.new(rows, 700)
-        Z.zero_gated_forward(b.x, b.wg, b.wu, rows, 1000, 700, 0, h, None, None, None, 0, b.status)
+        h = b.new(rows, ff)
+        Z.zero_gated_forward(b.x, b.wg, b.wu, rows, 1000, ff, 0, h, None, None, None, 0, b.status)
         torch.cuda.synchronize()
         assert int(b.status) == 1
         monkeypatch.delenv("ZERO_GB300_SPIN_LIMIT")

@@ -30,12 +30,14 @@
 // (the measured burst rate of a library product), 1.03 to 1.15 where the card
 // holds its power limit, 1.87 to 1.67 (measured sustained: 1.72); with gate and up
 // stored 1.11 to 1.16; dx and dW 1.10 to 1.17 each; the slopes 183 us, 6.4 TB/s.
-// 512 rows in 72 us, up to 256 in 51 to 53: 8.5 to start and end, then two rounds
-// of 112 tiles on 76 pairs, the first bound by HBM, the second by its 36 pairs'
-// products.  A stage takes 512 cycles of products whatever the rows, and whether
-// B has 256 rows or 128 (tiles of 64 columns were slower: 63 us), so shorter
-// rounds do not help.  Weights asked for ahead towards L2, and sums that start at
-// different places of k, made it slower (56 to 67 us; 56).
+// 512 rows in 72 us, 129 to 256 in 53: 8.5 to start and end, then two rounds of 112
+// tiles on 76 pairs, the first bound by HBM, the second by its 36 pairs' products.
+// A stage takes 512 cycles of products whatever the rows, and whether B has 256
+// rows or 128 (tiles of 64 columns: 63 us), so shorter rounds do not help.  With up
+// to 128 rows a block alone has a tile where that takes fewer rounds (one of 112
+// blocks): 43 to 44 us for the 51 to 52 of pairs, HBM at 0.80.  Weights asked for
+// ahead towards L2, and sums that start at different places of k, made it slower
+// (56 to 67 us; 56).
 //
 // Every wait is bounded.  A block whose wait runs out sets bit 0 of *status, its
 // roles stop, what the pair has in flight is waited for (bounded again), the
@@ -56,10 +58,13 @@ constexpr int GT_CHUNK = GT_K * 128;          // 64 columns by 64 rows of an ope
 constexpr int GT_HEADER = 1024;
 constexpr int GT_EPI = GT_EPI_WARPS * 32 * 17 * 4;      // a 32 x 16 piece for each of its warps, padded
 
-constexpr int GT_STAGE = 2 * GT_A;            // B has as many rows a block
-constexpr int GT_STAGES = 6;
-constexpr int GT_SMEM = GT_STAGES * GT_STAGE + 2048 + GT_EPI;
-static_assert(GT_SMEM <= 232448, "shared memory of a block");
+// Alone, a block has all 256 rows of B.
+template <bool PAIR>
+struct GtShape {
+    static constexpr int B = PAIR ? GT_A : 2 * GT_A, STAGE = GT_A + B, STAGES = PAIR ? 6 : 4;
+    static constexpr int SMEM = STAGES * STAGE + 2048 + GT_EPI;
+    static_assert(SMEM <= 232448 && STAGES <= 8, "shared memory of a block");
+};
 
 enum { GT_FORWARD = 0, GT_DX = 1, GT_DW = 2 };
 
@@ -82,26 +87,52 @@ struct GatedArgs {
 
 // ---------------------------------------------------------------- PTX
 // A tile to this block's shared memory, its bytes counted by a barrier of the pair's first block.
-__device__ __forceinline__ void tma_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            dst),
-        "l"(map), "r"(x), "r"(y), "r"(bar)
-        : "memory");
+template <bool PAIR>
+__device__ __forceinline__ void gt_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        tma_tile(dst, map, x, y, bar);
 }
-// Arrives at the barrier of both blocks once what was issued before is done.
-__device__ __forceinline__ void pair_commit(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
+// All threads of the pair, or of the block.
+template <bool PAIR>
+__device__ __forceinline__ void gt_meet() {
+    if constexpr (PAIR) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
 }
-__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((int)add)
-        : "memory");
+// Arrives at the barrier (of both blocks) once what was issued before is done.
+template <bool PAIR>
+__device__ __forceinline__ void gt_commit(uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void gt_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((int)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((int)add)
+            : "memory");
 }
 __device__ __forceinline__ uint32_t block_addr(uint32_t local, uint32_t rank) {
     uint32_t r;
@@ -156,10 +187,10 @@ __device__ __forceinline__ uint64_t gt_desc(uint32_t addr) {
 }
 // 16 elements of k further on, in the descriptor's units of 16 bytes
 template <bool K_ROWS> constexpr int GT_K16 = K_ROWS ? 16 * 128 >> 4 : 16 * 2 >> 4;
-// Instruction descriptor: 16-bit operands, fp32 accumulator, 256 x 256.
-template <int DT, bool A_ROWS, bool B_ROWS>
+// Instruction descriptor: 16-bit operands, fp32 accumulator, 256 columns and 256 rows, or 128.
+template <int DT, bool PAIR, bool A_ROWS, bool B_ROWS>
 constexpr uint32_t GT_IDESC = 1u << 4 | (DT == ZERO_BF16 ? 1u << 7 | 1u << 10 : 0u) | (A_ROWS ? 1u << 15 : 0u) |
-                              (B_ROWS ? 1u << 16 : 0u) | (uint32_t)(GT_TILE >> 3) << 17 | (uint32_t)(GT_TILE >> 4) << 24;
+                              (B_ROWS ? 1u << 16 : 0u) | (uint32_t)(GT_TILE >> 3) << 17 | (uint32_t)((PAIR ? GT_TILE : GT_HALF) >> 4) << 24;
 
 // ---------------------------------------------------------------- activations
 // Both are g times a sigmoid s; the slope is s + g s (1 - s) t' with t the
@@ -272,11 +303,13 @@ __device__ __forceinline__ void gt_tile(const GatedArgs& a, int t, int& m, int& 
     n = n0 + r % w;
 }
 
-template <int MODE, int DT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
-    k_gated(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
-            const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
-            const __grid_constant__ GatedArgs a) {
+// PAIR: two blocks a tile of 256 rows; else (forward, up to 128 rows) one.
+template <int MODE, int DT, bool PAIR>
+__device__ __forceinline__ void gated(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
+                                      const GatedArgs& a) {
+    using S = GtShape<PAIR>;
+    constexpr int STAGES = S::STAGES;
+    static_assert(PAIR || MODE == GT_FORWARD, "one block a tile");
     constexpr bool A_ROWS = MODE == GT_DW, B_ROWS = MODE != GT_FORWARD;      // k along the rows
     constexpr int N_TILE = MODE == GT_FORWARD ? GT_HALF : GT_TILE;           // columns of the output
     extern __shared__ uint8_t smem_raw[];
@@ -291,18 +324,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     const uint32_t stages = base + GT_HEADER;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3;                            // the 32 lanes of tensor memory this warp can reach
-    const uint32_t rank = blockIdx.x & 1;                    // in the pair
-    float* epi = reinterpret_cast<float*>(head + GT_HEADER + GT_STAGES * GT_STAGE) + (warp & 7) * 32 * 17;
+    const uint32_t rank = PAIR ? blockIdx.x & 1 : 0;         // in the pair
+    float* epi = reinterpret_cast<float*>(head + GT_HEADER + STAGES * S::STAGE) + (warp & 7) * 32 * 17;
 
     if (threadIdx.x == 0) {
         for (const CUtensorMap* m : {&a0, &a1, &b0, &b1}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
-        for (int s = 0; s < GT_STAGES; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(acc_full + 8 * s, 1);
-            mbar_init(acc_free + 8 * s, 2 * GT_EPI_WARPS);
+            mbar_init(acc_free + 8 * s, (PAIR ? 2 : 1) * GT_EPI_WARPS);
         }
         mbar_init(drained, 1);
         fence_mbar_init();
@@ -312,23 +345,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     // Both blocks run before either allocates, and neither leaves before both have freed: the allocation is the pair's.
     // Without the first barrier, a block that had started well before its partner (beside a kernel whose blocks were still
     // on the partner's SM) was through, and the partner's allocation never returned.
-    cluster_arrive();
-    cluster_wait();
+    gt_meet<PAIR>();
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + 200) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + 200) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + 200) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
-    cluster_arrive();
-    cluster_wait();                                          // both blocks' barriers stand
+    gt_meet<PAIR>();                                          // both blocks' barriers stand
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
     pdl_launch_next();
 
     // this pair's tiles, and the stages of the part of the sum that a tile stands for
-    const int n_parts = a.m_tiles * a.n_tiles, n_tiles = n_parts * a.split, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int n_parts = a.m_tiles * a.n_tiles, n_tiles = n_parts * a.split, first = PAIR ? blockIdx.x >> 1 : blockIdx.x,
+              step = PAIR ? gridDim.x >> 1 : gridDim.x;
     const auto part_of = [&](int t, int& tile, int& k0, int& k1) {
         const int part = MODE == GT_DX ? t / n_parts : 0;
         tile = MODE == GT_DX ? t - part * n_parts : t;
@@ -339,7 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) {
-            const uint32_t full0 = block_addr(full, 0);
+            const uint32_t full0 = PAIR ? block_addr(full, 0) : full;
             int st = 0, count = 0;
             uint32_t phase = 0;
             for (int t = first; t < n_tiles && ok; t += step) {
@@ -349,9 +386,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                 const bool second = MODE == GT_DW && m >= a.half_tiles;
                 const int am = (second ? m - a.half_tiles : m) * GT_TILE + (int)rank * GT_HALF;
                 const int bn = MODE == GT_FORWARD ? n * N_TILE : n * GT_TILE + (int)rank * GT_HALF;
-                const uint32_t bytes = (a.a_rows < GT_HALF ? a.a_rows * (GT_K * 2) : 2 * GT_A) + 2 * GT_A;
+                const uint32_t bytes = (a.a_rows < GT_HALF ? a.a_rows * (GT_K * 2) : (PAIR ? 2 : 1) * GT_A) + 2 * GT_A;
                 for (int k = k0; k < k1; ++k) {
-                    if (count >= GT_STAGES && !pair_wait<true>(empty + 8 * st, phase ^ 1, a.spin_limit, stop)) {
+                    if (count >= STAGES && !pair_wait<true>(empty + 8 * st, phase ^ 1, a.spin_limit, stop)) {
                         ok = false;
                         break;
                     }
@@ -360,31 +397,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                     const CUtensorMap* A = second || up ? &a1 : &a0;
                     const CUtensorMap* B = (MODE == GT_FORWARD && rank) || up ? &b1 : &b0;
                     // rows and columns past the end read as 0
-                    const uint32_t bar = full0 + 8 * st, at = stages + st * GT_STAGE;
+                    const uint32_t bar = full0 + 8 * st, at = stages + st * S::STAGE;
                     if (rank == 0) mbar_expect_tx(full + 8 * st, bytes);
                     if (A_ROWS) {
-                        tma_pair(at, A, am, kk, bar);
-                        tma_pair(at + GT_CHUNK, A, am + 64, kk, bar);
+                        gt_load<PAIR>(at, A, am, kk, bar);
+                        gt_load<PAIR>(at + GT_CHUNK, A, am + 64, kk, bar);
                     } else if (rank == 0 || a.a_rows == GT_HALF) {
                         // of few rows only the boxes' are loaded; what else lies in A's place is multiplied, but not stored
-                        tma_pair(at, A, kk, am, bar);
+                        gt_load<PAIR>(at, A, kk, am, bar);
                     }
                     if (B_ROWS) {
-                        tma_pair(at + GT_A, B, bn, kk, bar);
-                        tma_pair(at + GT_A + GT_CHUNK, B, bn + 64, kk, bar);
+                        gt_load<PAIR>(at + GT_A, B, bn, kk, bar);
+                        gt_load<PAIR>(at + GT_A + GT_CHUNK, B, bn + 64, kk, bar);
                     } else {
-                        tma_pair(at + GT_A, B, kk, bn, bar);
+                        gt_load<PAIR>(at + GT_A, B, kk, bn, bar);
+                        if (!PAIR) gt_load<PAIR>(at + 2 * GT_A, &b1, kk, bn, bar);
                     }
                     *loaded = ++count;
-                    if (++st == GT_STAGES) {
+                    if (++st == STAGES) {
                         st = 0;
                         phase ^= 1;
                     }
                 }
             }
             // the last stages' releases come from the first block: this one does not leave before them
-            for (int c = max(0, count - GT_STAGES); c < count && ok; ++c)
-                ok = pair_wait<false>(empty + 8 * (c % GT_STAGES), (uint32_t)(c / GT_STAGES) & 1, a.spin_limit, stop);
+            for (int c = max(0, count - STAGES); c < count && ok; ++c)
+                ok = pair_wait<false>(empty + 8 * (c % STAGES), (uint32_t)(c / STAGES) & 1, a.spin_limit, stop);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
@@ -406,23 +444,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t at = stages + st * GT_STAGE;
+                    const uint32_t at = stages + st * S::STAGE;
                     const uint64_t da = gt_desc<A_ROWS>(at), db = gt_desc<B_ROWS>(at + GT_A);
 #pragma unroll
                     for (int q = 0; q < GT_K / 16; ++q)
-                        pair_mma(d, da + q * GT_K16<A_ROWS>, db + q * GT_K16<B_ROWS>, GT_IDESC<DT, A_ROWS, B_ROWS>, k > k0 || q > 0);
-                    pair_commit(empty + 8 * st);
-                    if (++st == GT_STAGES) {
+                        gt_mma<PAIR>(d, da + q * GT_K16<A_ROWS>, db + q * GT_K16<B_ROWS>, GT_IDESC<DT, PAIR, A_ROWS, B_ROWS>, k > k0 || q > 0);
+                    gt_commit<PAIR>(empty + 8 * st);
+                    if (++st == STAGES) {
                         st = 0;
                         phase ^= 1;
                     }
                 }
-                if (ok) pair_commit(acc_full + 8 * acc);
+                if (ok) gt_commit<PAIR>(acc_full + 8 * acc);
             }
-            pair_commit(drained);
+            gt_commit<PAIR>(drained);
         }
     } else {
-        const uint32_t free0 = block_addr(acc_free, 0);
+        const uint32_t free0 = PAIR ? block_addr(acc_free, 0) : acc_free;
         constexpr int HALF = N_TILE / 2;
         const int from = (warp - 2) / 4 * HALF;               // this warp's columns of the tile
         int n = 0;
@@ -505,25 +543,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
     if (threadIdx.x == 32) pair_wait<false>(drained, 0, a.drain_limit, nullptr);
     tc_fence_before();
     __syncthreads();
-    cluster_arrive();
-    cluster_wait();
+    gt_meet<PAIR>();
     // after a stop of either block, the loads of both, which the first block's barriers count
-    if (rank == 0 && threadIdx.x == 0 && (*stop || read_at(block_addr(base + 204, 1)))) {
-        const int most = max(*loaded, read_at(block_addr(base + 208, 1)));
-        for (int c = max(0, most - GT_STAGES); c < most; ++c)
-            pair_wait<false>(full + 8 * (c % GT_STAGES), (uint32_t)(c / GT_STAGES) & 1, a.drain_limit, nullptr);
+    if (rank == 0 && threadIdx.x == 0 && (*stop || (PAIR && read_at(block_addr(base + 204, 1))))) {
+        const int most = PAIR ? max(*loaded, read_at(block_addr(base + 208, 1))) : *loaded;
+        for (int c = max(0, most - STAGES); c < most; ++c)
+            pair_wait<false>(full + 8 * (c % STAGES), (uint32_t)(c / STAGES) & 1, a.drain_limit, nullptr);
     }
     __syncthreads();
-    cluster_arrive();
-    cluster_wait();
+    gt_meet<PAIR>();
     tc_fence_after();
     if (warp == 1) {
         __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
     __syncwarp();
-    cluster_arrive();
-    cluster_wait();
+    gt_meet<PAIR>();
+}
+
+template <int MODE, int DT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
+    k_gated(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
+            const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
+            const __grid_constant__ GatedArgs a) {
+    gated<MODE, DT, true>(a0, a1, b0, b1, a);
+}
+// Up to 128 rows, where one block a tile needs fewer rounds (112 tiles: one of 152 blocks, two of 76 pairs).
+template <int DT>
+__global__ void __launch_bounds__(GT_THREADS, 1)
+    k_gated_alone(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
+                  const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
+                  const __grid_constant__ GatedArgs a) {
+    gated<GT_FORWARD, DT, false>(a0, a1, b0, b1, a);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -532,9 +584,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
 // which a lane reads every 32nd unit of 8; x lies in shared memory as it is.
 // Bound: HBM (the weights' bytes): through 4096 x 14336 bf16 one row in 35.7 us,
 // 6.57 TB/s (0.97 of the measured copy bandwidth), two in 36.1, four in 42.6.
-// The pairs above take 51 us for any number up to 256: 8.5 to start and end, two
-// rounds of tiles, the second on half of the SMs and bound by its products.
-// Eight rows here take 78: their sums leave half the registers for loads.
+// The products above take 43 us for any number up to 128.  Eight rows here take
+// 78: their sums leave half the registers for loads.
 constexpr int FEW_ROWS = 4, FEW_THREADS = 256;
 constexpr size_t FEW_SMEM = 96 * 1024;        // of x: two blocks an SM
 
@@ -796,7 +847,7 @@ struct Maker {
         return {m.data, m.ld, m.dtype, on(32) ? 32 : on(16) ? 16 : 0};
     }
     void product(int mode, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1, GatedArgs& a,
-                 int32_t* status) {
+                 int32_t* status, bool alone = false) {
         if (rc != ZERO_OK) return;
         a.status = status;
         const char* e = std::getenv("ZERO_GB300_SPIN_LIMIT");
@@ -808,12 +859,14 @@ struct Maker {
         const void* f = mode == GT_FORWARD ? (bf ? (const void*)k_gated<GT_FORWARD, ZERO_BF16> : (const void*)k_gated<GT_FORWARD, ZERO_F16>)
                         : mode == GT_DX    ? (bf ? (const void*)k_gated<GT_DX, ZERO_BF16> : (const void*)k_gated<GT_DX, ZERO_F16>)
                                            : (bf ? (const void*)k_gated<GT_DW, ZERO_BF16> : (const void*)k_gated<GT_DW, ZERO_F16>);
-        rc = raise_smem(f, GT_SMEM, call);
+        if (alone) f = bf ? (const void*)k_gated_alone<ZERO_BF16> : (const void*)k_gated_alone<ZERO_F16>;
+        const size_t smem = alone ? GtShape<false>::SMEM : GtShape<true>::SMEM;
+        rc = raise_smem(f, smem, call);
         if (rc != ZERO_OK) return;
-        const int tiles = a.m_tiles * a.n_tiles * a.split, pairs = sms / 2;
+        const int tiles = a.m_tiles * a.n_tiles * a.split, at_once = alone ? sms : sms / 2;
         void* args[] = {const_cast<CUtensorMap*>(&a0), const_cast<CUtensorMap*>(&a1), const_cast<CUtensorMap*>(&b0),
                         const_cast<CUtensorMap*>(&b1), &a};
-        rc = cuda_fail(launch_after_previous(f, 2 * (tiles < pairs ? tiles : pairs), GT_THREADS, args, GT_SMEM, s), call);
+        rc = cuda_fail(launch_after_previous(f, (alone ? 1 : 2) * (tiles < at_once ? tiles : at_once), GT_THREADS, args, smem, s), call);
     }
 };
 
@@ -943,7 +996,9 @@ int zero_gated_forward(const zero_mat* x, const zero_mat* gate_w, const zero_mat
     a.k_steps = tiles_of(cols, GT_K);
     a.a_rows = boxes_of(rows);
     a.act = act;
-    mk.product(GT_FORWARD, xm, xm, gm, um, a, status);
+    const int pairs = sms / 2;
+    const bool alone = rows <= GT_HALF && (a.n_tiles + sms - 1) / sms < (a.n_tiles + pairs - 1) / pairs;
+    mk.product(GT_FORWARD, xm, xm, gm, um, a, status, alone);
     return mk.rc;
 }
 
