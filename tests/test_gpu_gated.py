@@ -411,3 +411,78 @@ def test_two_streams_at_once(Z):
     for b, dh, ws, outs in blocks:
         assert int(b.status) == 0
         assert all(torch.equal(p, q) for p, q in zip(*outs))
+
+
+# Gates far below zero, where the activation is 10^-8 to 10^-39: SiLU's argument t is the gate, GELU's about 1.6 g (1 + 0.045 g^2).
+FAR = {0: [-16.0 - 0.75 * i for i in range(108)], 1: [-3.5 - 0.0625 * i for i in range(118)]}
+
+
+def far_gates(act, dtype):
+    return torch.tensor(FAR[act], device=DEV).to(dtype)
+
+
+def far_reference(g, act):
+    """act(g), its slope, and what either may be off by before its rounding, for g < 0.
+
+    exp(t) is off by (2 + 1.2 |t|) ulps of 2^-23 (its documented error), GELU's t
+    by five roundings of 2^-24, which exp turns into |t| 2.5 ulps more; quotient,
+    products and d: 8 more.  Below 2^-126 fp32 has steps of 2^-149: half a one in
+    exp, in the quotient and in each product, all times |g|, |g d| or what it is
+    multiplied with."""
+    g = g.double()
+    if act == 0:
+        t, d = g, torch.ones_like(g)
+    else:
+        a, b = 2 * math.sqrt(2 / math.pi), 0.044715
+        t, d = a * (g + b * g ** 3), a * (1 + 3 * b * g * g)
+    s = torch.exp(t) / (1 + torch.exp(t))
+    rel, grain = (10 + 4 * t.abs()) * 2.0 ** -23, 2.0 ** -149
+    size = s * (1 + (g * d).abs())
+    return (g * s, (g * s).abs() * rel + (2 + g.abs()) * grain,
+            s + g * s * (1 - s) * d, size * rel + (2 + (g * d).abs()) * 2 * grain)
+
+
+def near_far(got, ref, tol, what):
+    """Half a step of the type, of the smallest ones at least."""
+    least = {F16: 2.0 ** -25, BF16: 2.0 ** -134}[got.dtype]
+    err, lim = (got.double() - ref).abs(), (ref.abs() + tol) * U[got.dtype] + least + tol
+    assert bool((err <= lim).all()), (what, int((err > lim).sum()), float((err / lim).max()))
+
+
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_slopes_of_gates_far_below_zero(Z, act, dtype):
+    """Against relative bounds, down to the type's smallest numbers, rows that start on 16 bytes and not."""
+    for off in (0, 1):
+        gate = far_gates(act, dtype)
+        n = gate.numel() // 8 * 8
+        wide = torch.empty(3, n + 8, dtype=dtype, device=DEV)
+        g = wide[:, off:off + n]
+        g.copy_(gate[:n])
+        up, dh = torch.full_like(g, 0.75), torch.full_like(g, 1.5)
+        b = Block(Z, torch.ones(3, 8, dtype=dtype, device=DEV), torch.ones(n, 8, dtype=dtype, device=DEV),
+                  torch.ones(n, 8, dtype=dtype, device=DEV), act)
+        dg, du = torch.empty_like(g), torch.empty_like(g)
+        b.backward(dh, g, up, dg, du, None, None, None)
+        v, tv, slope, ts = far_reference(g, act)
+        near_far(du, 1.5 * v, 1.5 * tv, "dup")
+        near_far(dg, 1.125 * slope, 1.125 * ts, "dgate")
+
+
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("rows", [1, 3, 9, 300])
+def test_activations_of_gates_far_below_zero(Z, act, dtype, rows):
+    """Weights that make every gate one of the list, exactly, and every up 0.75; few rows, a block alone and pairs."""
+    gate = far_gates(act, dtype)
+    ff = gate.numel()
+    x = torch.zeros(rows, 16, dtype=dtype, device=DEV)
+    wg, wu = (torch.zeros(ff, 16, dtype=dtype, device=DEV) for _ in range(2))
+    x[:, 0], x[:, 9] = 1, 1
+    wg[:, 0], wu[:, 9] = gate, 0.75
+    b = Block(Z, x, wg, wu, act)
+    h, g, u = b.new(rows, ff), b.new(rows, ff), b.new(rows, ff)
+    b.forward(h, g, u)
+    assert torch.equal(g, gate.expand(rows, ff)) and bool((u == 0.75).all())
+    v, tv, _, _ = far_reference(g, act)
+    near_far(h, 0.75 * v, 0.75 * tv, "h")

@@ -194,20 +194,30 @@ constexpr uint32_t GT_IDESC = 1u << 4 | (DT == ZERO_BF16 ? 1u << 7 | 1u << 10 : 
 
 // ---------------------------------------------------------------- activations
 // Both are g times a sigmoid s; the slope is s + g s (1 - s) t' with t the
-// sigmoid's argument.  exp and the quotient are the fast ones: off by some
-// 2^-20, of a result with 8 or 11 bits.
+// sigmoid's argument.  s and 1 - s are taken from exp(-|t|), which is at most 1:
+// far below zero s is exp(t) down to the smallest number (by 1 / (1 + exp(-t)) it
+// was 0 from t = -87.4 on, where __fdividef's divisor passes 2^126, and bf16 holds
+// g s down to t = -96).  exp and the quotient are the fast ones: s is off by some
+// (4 + 1.2 |t|) 2^-23 of itself (exp's error grows with its argument), GELU's t by
+// |t| 2^-22 more, of a result with 8 or 11 bits.
 struct Act {
     float value, slope;
 };
+struct Sigmoid {
+    float s, rest;                            // rest: 1 - s
+};
 constexpr float GELU_A = 1.5957691216057308f, GELU_B = 0.044715f;       // 2 sqrt(2 / pi)
-__device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.f, 1.f + __expf(-t)); }
+__device__ __forceinline__ Sigmoid sigmoid(float t) {
+    const float e = __expf(-fabsf(t)), most = __fdividef(1.f, 1.f + e), least = e * most;
+    return t < 0.f ? Sigmoid{least, most} : Sigmoid{most, least};
+}
 __device__ __forceinline__ float act_value(float g, int act) {
     float t = g;
     if (act == ZERO_GELU_TANH) {
         const float c = fminf(fmaxf(g, -100.f), 100.f);     // beyond, s is 0 or 1, and g^3 stays finite
         t = GELU_A * c * fmaf(GELU_B * c, c, 1.f);
     }
-    return g * sigmoid(t);
+    return g * sigmoid(t).s;
 }
 __device__ __forceinline__ Act act_both(float g, int act) {
     float t = g, d = 1.f;
@@ -216,8 +226,9 @@ __device__ __forceinline__ Act act_both(float g, int act) {
         t = GELU_A * c * fmaf(GELU_B * c, c, 1.f);
         d = GELU_A * fmaf(3.f * GELU_B * c, c, 1.f);
     }
-    const float s = sigmoid(t), v = g * s;
-    return {v, fmaf(v * (1.f - s), d, s)};
+    const Sigmoid s = sigmoid(t);
+    const float v = g * s.s;
+    return {v, fmaf(v * s.rest, d, s.s)};
 }
 
 // ---------------------------------------------------------------- the end of a tile
