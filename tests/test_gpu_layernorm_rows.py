@@ -1,0 +1,122 @@
+"""zero_layernorm_forward / zero_layernorm_backward at the shapes that training
+gives them: several rows under way in a block, four units a lane, rows whose
+weights lie packed in shared memory, and rounds in which only some of a block's
+groups have a row.  Formulas and tolerances are test_gpu_layernorm.py's; the
+restated rule of the launches (layernorm_rule.py) says that the sizes reach
+every kernel there is."""
+import pytest
+import torch
+
+import block_helpers as B
+import layernorm_rule as R
+import test_gpu_layernorm as T
+
+NAMES = {T.F16: "f16", T.BF16: "bf16", T.F32: "f32"}
+TYPES = [(T.F16, T.F16), (T.BF16, T.BF16), (T.F32, T.F32), (T.F16, T.F32), (T.BF16, T.F32)]
+# 1300 and 2500 rows: the last round of 152 blocks of 8, 5, 4 or 3 groups is a part of one
+SIZES = [(1300, 1600), (2500, 1600), (700, 3456), (1300, 1337), (500, 4097), (3, 8200), (3, 9200), (3, 12288), (3, 14336)]
+
+
+@pytest.fixture(scope="module")
+def Z():
+    import zero_dp_partitioned_gb300 as Z
+    return Z
+
+
+def reached(sizes, backward, sms=152):
+    """(rows, cols) of `sizes` by the kernel that they reach: {template: [(groups, blocks, rule, rows)]}."""
+    found = {}
+    for rows, cols in sizes:
+        for xt, rt in TYPES:
+            for off in (0, 1):
+                k, g, blocks, rule = R.kernel(backward, rows, cols, NAMES[xt], NAMES[rt], NAMES[xt], not off and cols % 8 == 0, sms)
+                found.setdefault(k, []).append((g, blocks, rule, rows))
+    return found
+
+
+def every_kernel(backward):
+    way = "backward" if backward else "forward"
+    for xt, rt in TYPES:
+        x, r = NAMES[xt], NAMES[rt]
+        for shift in (False, True):
+            yield way, x, r, 2, False, shift
+            yield way, x, r, "long", False, shift
+            # a backward pass of fp32 rows never takes four units a lane: shared memory holds more threads of two
+            if not (backward and x == "f32"):
+                yield way, x, r, 4, False, shift
+            if x != "f32":
+                yield way, x, r, 4, True, shift
+
+
+@pytest.mark.parametrize("backward", [0, 1])
+def test_the_sizes_reach_every_kernel(backward):
+    found = reached(T.SIZES + SIZES, backward)
+    assert set(found) == set(every_kernel(backward))
+    for way, x, r, nv, packed, shift in found:
+        calls = found[way, x, r, nv, packed, shift]
+        groups = max(c[0] for c in calls)
+        # several groups a block, and a last round that not all of them have a row in, where any shape has several groups
+        part = any(g > 1 and rows % (g * blocks) > 0 and rows > g * blocks for g, blocks, _, rows in calls)
+        if nv == 4 and not packed and not (backward and r == "f32"):
+            assert groups > 1 or x == "f32"
+            if not backward and x != "f32":
+                assert groups == 8 and part
+            if backward:
+                assert groups >= (3 if shift else 8)
+    if backward:
+        assert any(rule == "two for their threads" for calls in found.values() for _, _, rule, _ in calls)
+
+
+@pytest.mark.parametrize("backward", [0, 1])
+def test_four_units_of_fp32_rows(backward):
+    """What no shape reaches: a backward pass of fp32 rows with four units a lane, whatever its rows and columns."""
+    four = {(rows, cols) for rows in (1, 2, 151, 153, 400, 700, 1300, 9000) for cols in range(1, 20001, 3)
+            if R.kernel(backward, rows, cols, "f32", "f32", "f32", cols % 8 == 0, 152)[0][3] == 4}
+    assert bool(four) == (not backward)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", SIZES)
+@pytest.mark.parametrize("xt,rt", TYPES)
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("p", [0.0, 0.2])
+def test_forward_and_backward(Z, rows, cols, xt, rt, off, p):
+    T.test_forward_and_backward(Z, rows, cols, xt, rt, off, p)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(1300, 1600), (3, 14336), (1300, 1337)])
+def test_weights_of_another_type(Z, rows, cols):
+    """fp32 weights beside 16-bit rows: rows that packed weights would fit are walked instead."""
+    g = T.gen(rows + cols)
+    x, dy = T.rnd(g, rows, cols, dtype=T.BF16), T.rnd(g, rows, cols, dtype=T.BF16)
+    w, b = T.rnd(g, cols, mean=1.0), T.rnd(g, cols)
+    y, dr, mean, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device=T.DEV), torch.empty(rows, device=T.DEV)
+    Z.zero_layernorm_forward(x, None, None, w, b, rows, cols, T.EPS, None, y, mean, rstd)
+    ref = T.Ref(x, w, b)
+    ref.check_forward(y, mean, rstd)
+    dw, db, ws = torch.empty_like(w), torch.empty_like(b), T.workspace(Z, cols)
+    Z.zero_layernorm_backward(dy, x, w, rows, cols, mean, rstd, None, None, dr, None, dw, db, 0, ws, ws.numel())
+    ref.check_backward(dy, None, dr, None, dw, db)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(1300, 1600), (1300, 1337), (700, 3456), (500, 4097)])
+def test_sums_added_and_the_same_bits(Z, rows, cols):
+    """dw and db added to what a bucket holds, twice with the same bits, dr over dh and dx over dy."""
+    g = T.gen(rows - cols)
+    h, dy, dh = (T.rnd(g, rows, cols, dtype=T.BF16) for _ in range(3))
+    w, drop, k = T.rnd(g, cols, dtype=T.BF16, mean=1.0), Z.drop(0.1, 21, 2, 3), B.keep(rows, cols, 0.1, 21, 2, 3)
+    y, mean, rstd = torch.empty_like(h), torch.empty(rows, device=T.DEV), torch.empty(rows, device=T.DEV)
+    Z.zero_layernorm_forward(h, None, None, w, None, rows, cols, T.EPS, None, y, mean, rstd)
+    ref, old, out = T.Ref(h, w, None), T.rnd(g, 2 * cols), []
+    for _ in range(2):
+        bucket, dr, dx, ws = old.clone(), dh.clone(), dy.clone(), T.workspace(Z, cols)
+        Z.zero_layernorm_backward(dx, h, w, rows, cols, mean, rstd, dr, drop, dr, dx, bucket[:cols], bucket[cols:], 1, ws, ws.numel())
+        out.append((bucket, dr, dx))
+    assert all(torch.equal(p, q) for p, q in zip(*out))
+    ref.check_backward(dy, dh, dr, dx, None, None, k, 0.1)
+    _, _, rw, sw, rb, sb = ref.gradients(dy, dh)
+    was = old.double()
+    T.near(bucket[:cols], was[:cols] + rw, T.F32, (rows + 256) * T.E * (sw + was[:cols].abs()), "dw")
+    T.near(bucket[cols:], was[cols:] + rb, T.F32, (rows + 256) * T.E * (sb + was[cols:].abs()), "db")
