@@ -69,8 +69,8 @@ def test_the_sizes_reach_every_kernel(backward):
 
 @pytest.mark.parametrize("backward", [0, 1])
 def test_four_units_of_fp32_rows(backward):
-    """What no shape reaches: a backward pass of fp32 rows with four units a lane, whatever its rows and columns."""
-    four = {(rows, cols) for rows in (1, 2, 151, 153, 400, 700, 1300, 9000) for cols in range(1, 20001, 3)
+    """What no shape would take: a backward pass of fp32 rows with four units a lane, whatever its rows and columns."""
+    four = {(rows, cols) for rows in (1, 153, 400, 1300, 9000) for cols in range(1, 20001, 8)
             if R.kernel(backward, rows, cols, "f32", "f32", "f32", cols % 8 == 0, 152)[0][3] == 4}
     assert bool(four) == (not backward)
 

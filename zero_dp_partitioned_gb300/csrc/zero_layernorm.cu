@@ -12,8 +12,9 @@
 // (0.83); 8192 x 4096 fp32 94 (0.85); 8192 x 1600 bf16 19.8 (0.78: 3 rows a
 // group), with dropout 25.7 (the generator's products beside those of the norm);
 // 4096 x 12288 bf16 67 (0.89).  Rows that start anywhere: 8192 x 4097 bf16 94
-// (0.42), fp32 134 (0.59).  Rows past 16384 columns (fp32: 8192) are walked three
-// times: 2048 x 20480 bf16 in 84 (0.59).
+// (0.42), fp32 134 (0.59).  Rows past 16384 columns (with a weight or bias of
+// another type 13312; onto an fp32 stream 13312 and 10616; fp32 9104) are walked
+// three times: 2048 x 20480 bf16 in 84 (0.59).
 //
 // The mean and the squares about it come with one barrier: a warp takes the
 // mean of its own columns, then the squares about that mean from its registers,

@@ -17,9 +17,10 @@
 // 1600 bf16 28 (0.55: five of them the sums' launch), behind a dropout 37.
 // 16-bit rows are bound by the instructions they issue (36 an element, with the
 // generator's and dx's 56).  Rows that start anywhere: 8192
-// x 4097 bf16 155 (0.26), fp32 167 (0.47).  Rows past 16384 columns (fp32: 8192)
-// are walked twice and their columns' sums taken by a pass of its own: 2048 x
-// 20480 bf16 in 215 (0.23).
+// x 4097 bf16 155 (0.26), fp32 167 (0.47).  Rows past 15360 columns (with a weight
+// of another type 13312; onto an fp32 stream 9216 and 9000; fp32 7680) are walked
+// twice and their columns' sums taken by a pass of its own: 2048 x 20480 bf16 in 215
+// (0.23).
 #include "zero_layernorm.cuh"
 
 namespace zdp {
@@ -357,8 +358,11 @@ __global__ void __launch_bounds__(1024) k_layernorm_sums(const __grid_constant__
 // packed: the weight in shared memory in dy's type, not in fp32.
 template <int XT, int RT, bool SHIFT>
 static const void* rows_of(bool packed, int nv) {
-    if (nv == 2) return (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 2, SHIFT>;
-    return packed ? (const void*)k_layernorm_backward_rows<XT, RT, XT, 4, SHIFT> : (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 4, SHIFT>;
+    if constexpr (XT != ZERO_F32)
+        if (nv == 4)
+            return packed ? (const void*)k_layernorm_backward_rows<XT, RT, XT, 4, SHIFT>
+                          : (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 4, SHIFT>;
+    return (const void*)k_layernorm_backward_rows<XT, RT, ZERO_F32, 2, SHIFT>;
 }
 template <int XT, int RT>
 static const void* fn_of(bool v8, bool packed, int nv) {
@@ -455,7 +459,8 @@ int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_ma
     int nv = 4;
     bool packed = false;
     if (rows > 0) {
-        rs = rows_shape(rows, cols, words, 2, sms, &nv);
+        // of fp32 rows shared memory holds more threads with two units each, whatever the sizes
+        rs = dy->dtype == ZERO_F32 ? rows_shape(rows, cols, nv = 2, words, 2, sms) : rows_shape(rows, cols, words, 2, sms, &nv);
         // four units a lane and the shifts beside the sums do not fit the registers: only where two leave the block few threads
         // (8192 x 4097, one row of 288 threads or three of 160)
         if (!v8 && nv == 4) {
