@@ -203,3 +203,13 @@ def test_gated_backward_refusals(Z):
     call(Z.ZERO_EWORKSPACE, dgate=m(Z, ld=65))
     assert Z.zero_gated_backward_workspace_bytes(None, None, None, m(Z), m(Z, ld=70), 4, 64, 100) == 4 * 128 * 2
     assert Z.zero_gated_backward_workspace_bytes(m(Z), m(Z), m(Z), m(Z), m(Z), 4, 64, 64) == 0
+
+
+def test_the_layernorm_workspace_holds_what_a_launch_writes(Z):
+    """A partial dw and db of each of 152 blocks at most; rows that are walked have the few shares of them that fill the GPU."""
+    for cols in (1, 1600, 4097, 16384):
+        assert Z.zero_layernorm_workspace_bytes(cols) == 152 * cols * 8
+    for cols in (16385, 20000, 200000, 1 << 20):
+        shares = -(-8 * 152 // -(-cols // 128))
+        assert Z.zero_layernorm_workspace_bytes(cols) == shares * cols * 8
+    assert Z.zero_layernorm_workspace_bytes((1 << 20) + 1) == 0

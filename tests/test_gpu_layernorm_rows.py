@@ -120,3 +120,24 @@ def test_sums_added_and_the_same_bits(Z, rows, cols):
     was = old.double()
     T.near(bucket[:cols], was[:cols] + rw, T.F32, (rows + 256) * T.E * (sw + was[:cols].abs()), "dw")
     T.near(bucket[cols:], was[cols:] + rb, T.F32, (rows + 256) * T.E * (sb + was[cols:].abs()), "db")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(1300, 1600), (2500, 333), (700, 8200), (300, 15000), (300, 16384), (300, 16385), (200, 20001), (20, 200000), (3, 1 << 20)])
+@pytest.mark.parametrize("dtype", [T.BF16, T.F32])
+def test_nothing_behind_the_workspace_is_written(Z, rows, cols, dtype):
+    """Sums right and the bytes behind them as they were.  A thread of a walked row adds cols / 512 terms one after the
+    other, for the mean and again for the squares: cols / 256 roundings more than test_gpu_layernorm.py counts."""
+    g = T.gen(cols)
+    h, dy = T.rnd(g, rows, cols, dtype=dtype), T.rnd(g, rows, cols, dtype=dtype)
+    y, dr = torch.empty_like(h), torch.empty_like(h)
+    mean, rstd = torch.empty(rows, device=T.DEV), torch.empty(rows, device=T.DEV)
+    Z.zero_layernorm_forward(h, None, None, None, None, rows, cols, T.EPS, None, y, mean, rstd)
+    n = Z.zero_layernorm_workspace_bytes(cols)
+    ws = torch.full((n + 4 * cols,), 0x5A, dtype=torch.uint8, device=T.DEV)
+    dw, db = torch.empty(cols, device=T.DEV), torch.empty(cols, device=T.DEV)
+    Z.zero_layernorm_backward(dy, h, None, rows, cols, mean, rstd, None, None, dr, None, dw, db, 0, ws[:n], n)
+    _, _, rw, sw, rb, sb = T.Ref(h, None, None).gradients(dy, None)
+    T.near(dw, rw, T.F32, (rows + 256 + cols // 256) * T.E * sw, "dw")
+    T.near(db, rb, T.F32, (rows + 256) * T.E * sb, "db")
+    assert bool((ws[n:] == 0x5A).all())

@@ -355,6 +355,17 @@ __global__ void __launch_bounds__(1024) k_layernorm_sums(const __grid_constant__
     st1_any(out, cc, t, dt);
 }
 
+// Partial rows of dw and db: one of each block, of which an SM has one.  Counted in
+// a GB300's 152 SMs, whatever the device, since the workspace's size follows from it.
+constexpr int LN_PARTS = 152;
+constexpr int64_t LN_ROWS_COLS = (int64_t)LN_THREADS * 4 * 8;            // past these a row is walked, whatever its type
+// Shares of the rows where they are walked: eight blocks an SM, of 128 columns each.
+static int64_t long_shares(int64_t cols) {
+    const int64_t chunks = (cols + 127) / 128;
+    return (8 * LN_PARTS + chunks - 1) / chunks;
+}
+static_assert(8 * LN_PARTS / (7680 / 128) < LN_PARTS, "rows that are walked though shorter than LN_ROWS_COLS have fewer shares than blocks");
+
 // packed: the weight in shared memory in dy's type, not in fp32.
 template <int XT, int RT, bool SHIFT>
 static const void* rows_of(bool packed, int nv) {
@@ -391,7 +402,8 @@ using namespace zdp;
 extern "C" {
 
 size_t zero_layernorm_workspace_bytes(int64_t cols) {
-    return cols > 0 && cols <= NORM_MAX_COLS ? (size_t)NORM_MAX_GRID * (size_t)cols * 8 : 0;
+    if (cols <= 0 || cols > NORM_MAX_COLS) return 0;
+    return (size_t)(cols > LN_ROWS_COLS ? long_shares(cols) : LN_PARTS) * (size_t)cols * 8;
 }
 
 int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_mat* weight, int64_t rows, int64_t cols,
@@ -424,7 +436,7 @@ int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_ma
     LayerNormArgs a = {};
     rc = check_drop(drop, a.drop, me);
     if (rc != ZERO_OK || cols == 0) return rc;
-    const int sms = sm_count();
+    const int all = sm_count(), sms = all < LN_PARTS ? all : LN_PARTS;
     if (!sms) return ZERO_ECUDA;
     a.x = dy->data;
     a.ldx = dy->ld;
@@ -489,10 +501,7 @@ int zero_layernorm_backward(const zero_mat* dy, const zero_mat* h, const zero_ma
     } else if (rows > 0) {
         if (a.part) {
             // dw and db first: dr and dx may be written over dy or dh
-            const int64_t chunks = (cols + 127) / 128;
-            int64_t shares = (8 * (int64_t)sms + chunks - 1) / chunks;
-            if (shares > NORM_MAX_GRID) shares = NORM_MAX_GRID;
-            if (shares > rows) shares = rows;
+            const int64_t chunks = (cols + 127) / 128, most = long_shares(cols), shares = rows < most ? rows : most;
             parts = (int)shares;
             const dim3 grid((unsigned)chunks, (unsigned)shares);
             rc = cuda_fail(cudaLaunchKernel(sums_long_fn(dy->dtype, rt), grid, dim3(128), args, 0, s),
