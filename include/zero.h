@@ -816,11 +816,15 @@ int zero_mx4_matmul(const zero_mx4* a, const zero_mx4* b, float alpha, const zer
  * unit = r ceil(cols / 8) + c / 8.  The same zero_drop and sizes give the same
  * mask in the forward and in the backward pass, whatever the row distances.
  * seed     of the run (and rank: ranks with different data want different ones)
- * site     which dropout of the model; two that share it drop the same elements
+ * site     which dropout of the step: of the model, and of the micro-batch where
+ *          several add to one step's gradients; two that share it drop the same
+ *          elements
  * p        0 .. 1; below 2^-17 nothing is dropped, from 1 - 2^-17 all is
  * chain    not NULL: the low word of chain->step, read on the device when the
  *          kernel runs, so that a captured step draws a new mask each time it is
- *          replayed and a skipped one keeps its mask; `step` is then not used */
+ *          replayed and a skipped one keeps its mask; `step` is then not used.
+ *          chain->step moves once an applied step, so the micro-batches of a step
+ *          need sites (or seeds) of their own */
 typedef struct {
     uint64_t seed;
     uint32_t site;

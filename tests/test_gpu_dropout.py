@@ -172,3 +172,29 @@ def test_offsets_past_32_bits(Z, cols):
     x.copy_(rnd(g, 4, cols))
     Z.zero_dropout(x, None, 4, cols, Z.drop(0.3, 2), y)
     near(y, torch.where(B.keep(4, cols, 0.3, 2, 0, 0), x.double() * B.scale(0.3), 0.0), F32)
+
+
+def test_micro_batches_of_one_step(Z):
+    """A chain's step is the same for all micro-batches of a step: sites or seeds of their own draw them masks of their
+    own, in a captured step too, and the next step draws others again."""
+    chain = torch.frombuffer(bytearray(bytes(Z.chain(step=4))), dtype=torch.uint8).to(DEV)
+    x, ys = torch.ones(50, 160, device=DEV), [torch.empty(50, 160, device=DEV) for _ in range(4)]
+    drops = [Z.drop(0.25, seed, site=site, chain_dev=chain) for seed, site in ((9, 3), (9, 3 + 8), (10, 3), (9, 3))]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        for d, y in zip(drops, ys):
+            Z.zero_dropout(x, None, 50, 160, d, y)
+    masks = []
+    for step in (4, 5):
+        chain.copy_(torch.frombuffer(bytearray(bytes(Z.chain(step=step))), dtype=torch.uint8))
+        graph.replay()
+        torch.cuda.synchronize()
+        for y, (seed, site) in zip(ys, ((9, 3), (9, 11), (10, 3), (9, 3))):
+            assert torch.equal(y > 0, B.keep(50, 160, 0.25, seed, site, step))
+        assert torch.equal(ys[0], ys[3])                     # the same seed and site: the same elements
+        masks += [y > 0 for y in ys[:3]]
+    for i in range(6):
+        for j in range(i):
+            assert not torch.equal(masks[i], masks[j])

@@ -660,7 +660,9 @@ def zero_mx4_matmul(a, b, alpha, d, status, stream=None):
 def drop(p, seed, site=0, step=0, chain_dev=None) -> zero_drop:
     """A dropout: the probability of dropping, the run's 64-bit seed, the place in
     the model, and the step, or the device zero_chain whose step is taken when
-    the kernel runs."""
+    the kernel runs.  A chain's step moves once an applied step: micro-batches
+    that add to one step's gradients need sites (or seeds) of their own, or they
+    drop the same elements."""
     d = zero_drop(int(seed) & 0xFFFFFFFFFFFFFFFF, int(site) & 0xFFFFFFFF, p, int(step),
                   _buf(chain_dev, ctypes.sizeof(zero_chain), "chain_dev"))
     if hasattr(chain_dev, "data_ptr"):
