@@ -198,3 +198,20 @@ def test_micro_batches_of_one_step(Z):
     for i in range(6):
         for j in range(i):
             assert not torch.equal(masks[i], masks[j])
+
+
+@pytest.mark.parametrize("rows,cols,off", [(5, 1600, 0), (300, 640, 0), (77, 2568, 0), (77, 2568, 1), (77, 2569, 0)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("p", [0.1, 0.25])
+def test_product_and_sum_are_each_rounded_to_fp32(Z, rows, cols, off, dtype, p):
+    """The bits of the same steps in fp32, one after the other: with p = 1/4 x 4/3 often falls on half a step of bf16 once it
+    is rounded, which a product kept whole into the sum would always pass."""
+    g = gen(rows + cols)
+    x, r = rnd(g, rows, cols, dtype=dtype, off=off), rnd(g, rows, cols, dtype=dtype, std=2.0, off=off)
+    y, k = torch.empty_like(x), B.keep(rows, cols, p, 13, 5, 7)
+    product = torch.where(k, x.float() * torch.tensor(B.scale(p), dtype=F32, device=DEV), torch.zeros((), device=DEV))
+    d = Z.drop(p, 13, 5, 7)
+    Z.zero_dropout(x, r, rows, cols, d, y)
+    assert torch.equal(y, (product + r.float()).to(dtype)), int((y != (product + r.float()).to(dtype)).sum())
+    Z.zero_dropout(x, None, rows, cols, d, y)
+    assert torch.equal(y, product.to(dtype))

@@ -141,3 +141,20 @@ def test_nothing_behind_the_workspace_is_written(Z, rows, cols, dtype):
     T.near(dw, rw, T.F32, (rows + 256 + cols // 256) * T.E * sw, "dw")
     T.near(db, rb, T.F32, (rows + 256) * T.E * sb, "db")
     assert bool((ws[n:] == 0x5A).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(5, 1600), (300, 640), (77, 2568), (77, 2569), (1300, 1600), (3, 14336), (3, 20000), (3, 20001)])
+@pytest.mark.parametrize("xt,rt", TYPES)
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("p", [0.1, 0.25])
+def test_h_has_the_bits_of_the_fp32_form(Z, rows, cols, xt, rt, off, p):
+    """dropout(x) and its sum with the residual each rounded to fp32, as zero_dropout and the elementary operations do."""
+    g = T.gen(rows + cols)
+    x, r = T.rnd(g, rows, cols, dtype=xt, std=0.5, off=off), T.rnd(g, rows, cols, dtype=rt, std=2.0, mean=0.25, off=off)
+    h, y = torch.empty_like(r), torch.empty_like(x)
+    Z.zero_layernorm_forward(x, r, Z.drop(p, 13, 5, 7), None, None, rows, cols, T.EPS, h, y, None, None)
+    k = B.keep(rows, cols, p, 13, 5, 7)
+    product = torch.where(k, x.float() * torch.tensor(B.scale(p), dtype=T.F32, device=T.DEV), torch.zeros((), device=T.DEV))
+    want = (product + r.float()).to(rt)
+    assert torch.equal(h, want), int((h != want).sum())

@@ -3,7 +3,7 @@
 //
 // Bound: HBM (x and the residual read, y written) where rows start on 16 bytes:
 // 32768 x 4096 bf16 in 87 us, 6.2 TB/s (0.91 of the measured copy bandwidth),
-// onto a residual in 123 (0.97); fp32 rows that start anywhere too (4095 x 6401
+// onto a residual in 125 (0.95); fp32 rows that start anywhere too (4095 x 6401
 // onto a residual in 49, 0.95).  16-bit rows that start anywhere are bound by
 // their instructions, an access an element: 16384 x 4097 bf16 in 74 us (0.53),
 // onto a residual in 90 (0.66).
@@ -50,13 +50,11 @@ __global__ void __launch_bounds__(DROP_THREADS) k_dropout(const __grid_constant_
             const int64_t u = u0 + j * DROP_THREADS;
             if (u >= a.units) break;
             const uint4 bits = drop_bits(a.drop, step, row * a.units + u);
-            const uint64_t s = pack2(a.drop.scale, a.drop.scale);
             float v[8];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint64_t k = a.drop.on ? drop2(pair8<DT>(x[j], q), bits, q, a.drop.above) : pair8<DT>(x[j], q);
-                const uint64_t d = mul2(k, s);
-                const float2 p = unpack2(RES ? add2(d, pair8<DT>(r[j], q)) : d);
+                const float2 p = unpack2(RES ? scaled_onto2(k, a.drop, pair8<DT>(r[j], q)) : mul2(k, pack2(a.drop.scale, a.drop.scale)));
                 v[2 * q] = p.x;
                 v[2 * q + 1] = p.y;
             }
@@ -115,7 +113,7 @@ static const void* dropout_fn(bool v8, bool res) {
 
 int check_drop(const zero_drop* d, DropArgs& a, const char* call) {
     a = {};
-    a.scale = 1.f;
+    a.scale = a.one = 1.f;
     if (!d) return ZERO_OK;
     if (!(d->p >= 0.f) || !(d->p <= 1.f)) return refuse(ZERO_EINVAL, call, "drop", ": p must be in 0 .. 1");
     if (!aligned(d->chain, 8)) return refuse(ZERO_EALIGN, call, "drop", ": chain not 8-byte aligned");

@@ -8,9 +8,9 @@
 // how rows are shared out stands in zero_layernorm.cuh.
 //
 // Measured (GB300; in brackets the share of the measured copy bandwidth): 16384 x
-// 3456 bf16 in 81 us (0.83), with dropout 83; fp16 onto an fp32 stream 120
+// 3456 bf16 in 81 us (0.83), with dropout 84; fp16 onto an fp32 stream 120
 // (0.83); 8192 x 4096 fp32 94 (0.85); 8192 x 1600 bf16 19.8 (0.78: 3 rows a
-// group), with dropout 25.7 (the generator's products beside those of the norm);
+// group), with dropout 26.0 (the generator's products beside those of the norm);
 // 4096 x 12288 bf16 67 (0.89).  Rows that start anywhere: 8192 x 4097 bf16 94
 // (0.42), fp32 134 (0.59).  Rows past 16384 columns (with a weight or bias of
 // another type 13312; onto an fp32 stream 13312 and 10616; fp32 9104) are walked

@@ -23,21 +23,18 @@ struct LayerNormArgs {
     DropArgs drop;
 };
 
-// dropout(x) + r of one unit, rounded to the type h is stored in: the product and
-// the sum each to fp32, as zero_dropout and any other form in fp32 does, so that h
-// has the same bits.
+// dropout(x) + r of one unit, rounded to the type h is stored in: the bits of
+// zero_dropout.
 template <int XT, int RT, bool V8>
 __device__ __forceinline__ Unit<RT, V8> drop_add_unit(const Unit<XT, V8>& x, const Unit<RT, V8>& r, bool has_r,
                                                       const DropArgs& d, uint32_t step, int64_t unit) {
     const uint4 bits = drop_bits(d, step, unit);
-    const uint64_t s = pack2(d.scale, d.scale);
     Unit<RT, V8> h;
     float v[8];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const uint64_t k = drop2(x.pair(q), bits, q, d.above);
-        const uint64_t d = mul2(k, s);
-        const float2 p = unpack2(has_r ? add2(d, r.pair(q)) : d);
+        const float2 p = unpack2(has_r ? scaled_onto2(k, d, r.pair(q)) : mul2(k, pack2(d.scale, d.scale)));
         v[2 * q] = p.x;
         v[2 * q + 1] = p.y;
     }
