@@ -158,3 +158,28 @@ def test_h_has_the_bits_of_the_fp32_form(Z, rows, cols, xt, rt, off, p):
     product = torch.where(k, x.float() * torch.tensor(B.scale(p), dtype=T.F32, device=T.DEV), torch.zeros((), device=T.DEV))
     want = (product + r.float()).to(rt)
     assert torch.equal(h, want), int((h != want).sum())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,off", [(700, 1600, 0), (700, 1337, 0), (700, 1600, 1), (5, 16400, 0), (5, 16403, 1)])
+@pytest.mark.parametrize("dtype", [T.BF16, T.F32])
+def test_gradients_over_each_other_s_places(Z, rows, cols, off, dtype):
+    """dr over dy with dx over dh, dx alone over dh, dr alone over dy: the bits of outputs of their own."""
+    g = T.gen(cols)
+    h, dy, dh = (T.rnd(g, rows, cols, dtype=dtype, off=off) for _ in range(3))
+    w, drop = T.rnd(g, cols, dtype=dtype, mean=1.0), Z.drop(0.1, 21, 2, 3)
+    y, mean, rstd = torch.empty_like(h), torch.empty(rows, device=T.DEV), torch.empty(rows, device=T.DEV)
+    Z.zero_layernorm_forward(h, None, None, w, None, rows, cols, T.EPS, None, y, mean, rstd)
+
+    def backward(dy, dh, dr, dx):
+        dw, db, ws = torch.empty(cols, device=T.DEV), torch.empty(cols, device=T.DEV), T.workspace(Z, cols)
+        Z.zero_layernorm_backward(dy, h, w, rows, cols, mean, rstd, dh, drop, dr, dx, dw, db, 0, ws, ws.numel())
+        return dr, dx, dw, db
+
+    new = lambda t: T.rnd(g, rows, cols, dtype=dtype, off=off).copy_(t)
+    want = backward(dy, dh, torch.empty_like(h), torch.empty_like(h))
+    for over_dy, over_dh in (("dr", "dx"), (None, "dx"), ("dr", None)):
+        a, b = new(dy), new(dh)
+        got = backward(a, b, a if over_dy else None, b if over_dh else None)
+        for p, q in zip(got, want):
+            assert p is None or torch.equal(p, q)

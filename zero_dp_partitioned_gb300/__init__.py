@@ -711,7 +711,8 @@ def zero_layernorm_backward(dy, h, weight, rows, cols, mean, rstd, dh, drop, dr,
 
 
 def zero_gated_forward_workspace_bytes(x, gate_w, up_w, rows, cols, ff):
-    """0 where the rows of x and of the weights start on 16-byte boundaries."""
+    """0 for few rows, and where the rows of x and of the weights start on 16-byte
+    boundaries."""
     return lib.zero_gated_forward_workspace_bytes(_mat(x, rows, cols, "x"), _mat(gate_w, ff, cols, "gate_w"),
                                                   _mat(up_w, ff, cols, "up_w"), rows, cols, ff)
 
@@ -729,7 +730,9 @@ def zero_gated_forward(x, gate_w, up_w, rows, cols, ff, act, h, gate, up, worksp
 
 
 def zero_gated_backward_workspace_bytes(x, gate_w, up_w, dgate, dup, rows, cols, ff):
-    """0 where the rows of all of them start on 16-byte boundaries."""
+    """Room for copies of those whose rows do not start on 16-byte boundaries, and
+    for the parts of dx's sum where few rows and columns leave most of the GPU
+    idle."""
     return lib.zero_gated_backward_workspace_bytes(_mat(x, rows, cols, "x"), _mat(gate_w, ff, cols, "gate_w"),
                                                    _mat(up_w, ff, cols, "up_w"), _mat(dgate, rows, ff, "dgate"),
                                                    _mat(dup, rows, ff, "dup"), rows, cols, ff)

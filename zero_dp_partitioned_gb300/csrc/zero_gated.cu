@@ -26,22 +26,31 @@
 // Operands whose k runs along the rows (Wg, Wu in dx; all in dW) are read where
 // they lie, as chunks of 64 columns by 64 rows (the "MN-major" layout).
 //
-// Measured (GB300, bf16, through 4096 x 14336): 8192 rows in 1.00 ms, 1.92 PFLOP/s
-// (the measured burst rate of a library product), 1.03 to 1.15 where the card
-// holds its power limit, 1.87 to 1.67 (measured sustained: 1.72); with gate and up
-// stored 1.11 to 1.16; dx and dW 1.10 to 1.17 each; the slopes 183 us, 6.4 TB/s.
-// 512 rows in 72 us, 129 to 256 in 53: 8.5 to start and end, then two rounds of 112
+// Measured (GB300, bf16, through 4096 x 14336): 8192 rows in 1.09 to 1.18 ms, 1.77 to
+// 1.64 PFLOP/s, at the card's power limit (a library product: 1.71 sustained, 1.87 in
+// a burst); 1.00 where the limit does not hold yet; with gate and up stored 1.20; dx
+// and dW 1.18 and 1.20 each, dW added to a bucket 1.21, in fp32 1.25, added in fp32
+// 1.26; the slopes 186 us, 6.3 TB/s.
+// 512 rows in 73 us, 129 to 256 in 53: 8.5 to start and end, then two rounds of 112
 // tiles on 76 pairs, the first bound by HBM, the second by its 36 pairs' products.
 // A stage takes 512 cycles of products whatever the rows, and whether B has 256
 // rows or 128 (tiles of 64 columns: 63 us), so shorter rounds do not help.  With up
 // to 128 rows a block alone has a tile where that takes fewer rounds (one of 112
-// blocks): 43 to 44 us for the 51 to 52 of pairs, HBM at 0.80.  Weights asked for
+// blocks): 44 us for the 51 to 52 of pairs, HBM at 0.80.  Weights asked for
 // ahead towards L2, and sums that start at different places of k, made it slower
-// (56 to 67 us; 56).
+// (56 to 67 us; 56).  Outputs whose rows start on 16 bytes but not on 32 are stored
+// half a sector at a time: with gate and up 2001 x 1600 x 4264 takes 56 us, 2048 x
+// 1600 x 4352 44.  Odd widths are copied first: 2001 x 1601 x 4263 in 65 us, 94
+// with gate and up, its slopes, dx and dW in 25, 70 and 65.
 //
-// Every wait is bounded.  A block whose wait runs out sets bit 0 of *status, its
-// roles stop, what the pair has in flight is waited for (bounded again), the
-// tensor memory is freed, and both leave; the outputs are then incomplete.
+// Every wait on an mbarrier is bounded.  A block whose wait runs out sets bit 0 of
+// *status, its roles stop, what the pair has in flight is waited for (bounded again),
+// the tensor memory is freed, and both leave; the outputs are then incomplete.  The
+// cluster barriers and the tensor-memory allocation have no limit of their own.
+// They end because a cluster's blocks are scheduled together and each of their
+// threads reaches every barrier, bounded waits in between; and because a block's 216
+// KB of shared memory keep any other of these kernels, or of the 4-bit product's,
+// off its SM while it holds tensor memory.
 #include <cstdlib>
 
 #include "zero_tc.cuh"

@@ -48,11 +48,13 @@ __device__ __forceinline__ Unit<RT, V8> drop_add_unit(const Unit<XT, V8>& x, con
 // barrier.  A warp has NV * 32 neighbouring units of 8 columns, a lane every 32nd
 // of them, so that the places of its NV units differ by constants.  The rows that
 // follow are on their way to shared memory; weight and bias stay there, in fp32
-// (16-bit ones packed where rows are too long for that).  These kernels are
-// bound by the instructions they issue before HBM, so all that is not arithmetic
+// (16-bit ones packed where rows are too long for that).  What is not arithmetic
 // is done once a row, not once a unit: one block a row, its weights fetched for
 // every 2 rows, took 58 instructions an element and 28 us (8192 x 1600 bf16; 20 us
-// now).
+// now).  Wide rows are bound by HBM; narrow ones by latency: 8192 x 1600 fills half
+// of the issue slots, and its four warps a scheduler wait for fixed latencies, the
+// row's barrier and shared memory (200 units on 64 lanes of four leave 22 % of the
+// places empty).
 //
 // SHIFT: rows that start anywhere, or widths that are no multiple of 8.  fp32
 // rows are copied by words of 4 bytes, neighbouring lanes neighbouring ones, so

@@ -15,11 +15,11 @@
 // bandwidth): 16384 x 3456 bf16 in 84 us (0.80), behind a dropout, with dx too, 117
 // (0.72); fp16 with an fp32 stream 120 (0.98); 8192 x 4096 fp32 88 (0.90); 8192 x
 // 1600 bf16 28 (0.55: five of them the sums' launch), behind a dropout 37.
-// 16-bit rows are bound by the instructions they issue (36 an element, with the
-// generator's and dx's 56).  Rows that start anywhere: 8192
-// x 4097 bf16 155 (0.26), fp32 167 (0.47).  Rows past 15360 columns (with a weight
+// 16-bit rows take 36 instructions an element (with the generator's and dx's 56),
+// and narrow ones are bound by latency: 8192 x 1600 fills half of the issue slots.
+// Rows that start anywhere: 8192 x 4097 bf16 155 (0.26), fp32 167 (0.47).  Rows past 15360 columns (with a weight
 // of another type 13312; onto an fp32 stream 9216 and 9000; fp32 7680) are walked
-// twice and their columns' sums taken by a pass of its own: 2048 x 20480 bf16 in 215
+// twice and their columns' sums taken by a pass of its own: 2048 x 20480 bf16 in 220
 // (0.23).
 #include "zero_layernorm.cuh"
 
